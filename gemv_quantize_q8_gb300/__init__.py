@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(HERE, "_build", "libkq.so")
 
 Q4_K, Q6_K, Q8_0, Q8_K, Q8_1, Q5_K = 1, 2, 3, 4, 5, 6
 DTYPES = {"q4_k": Q4_K, "q5_k": Q5_K, "q6_k": Q6_K, "q8_0": Q8_0, "q8_k": Q8_K, "q8_1": Q8_1}
+F32, F16, BF16 = 16, 17, 18  # element types of plain rows
 STATUS = {0: "KQ_OK", 1: "KQ_ERR_INVALID_ARG", 2: "KQ_ERR_UNSUPPORTED_DTYPE", 3: "KQ_ERR_ALIGNMENT",
           4: "KQ_ERR_WORKSPACE", 5: "KQ_ERR_CUDA", 6: "KQ_ERR_DEVICE_FLAG"}
 
@@ -73,6 +74,13 @@ _SIGS = {
     "kq_gemm_f32_ex": ([_I32, _P, _P, _I64, _I64, _I64, _I64, _P, _I64, ctypes.c_uint, _P, _SZ, _P], _I32),
     "kq_debug_tc_sums": ([_I32, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _SZ, _P], _I32),
     "kq_debug_tc_sums_grouped": ([_I32, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _SZ, _P], _I32),
+    "kq_quantize_i8": ([_I32, _P, _I64, _I64, _I64, _P, _I64, _P, _P], _I32),
+    "kq_gemm_i8_workspace_bytes": ([_I64, _I64, _I64], _SZ),
+    "kq_gemm_i8": ([_P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _I32, _P, _I64, _P, _SZ, _P], _I32),
+    "kq_gemm_i8_dyn": ([_I32, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I32, _P, _I64, _P, _SZ, _P], _I32),
+    "kq_qk_norm_rope": ([_I32, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _P, _I64,
+                         _I64, _I32, _I32, _P, _I64, _P, _I64, _P], _I32),
+    "kq_logprobs": ([_I32, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P, _P], _I32),
     "kq_debug_tc_wait_timeout": ([_I32, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _SZ, _P], _I32),
 }
 
@@ -252,6 +260,42 @@ def kq_read_device_flag(workspace, stream=None) -> int:
 
 def kq_moe_weighted_sum(y_slots, w, M, top_k, N, out, stream=None):
     _check(lib().kq_moe_weighted_sum(_ptr(y_slots), _ptr(w), M, top_k, N, _ptr(out), _stream(stream)))
+
+
+def kq_quantize_i8(xt, x, M, K, ldx, q, ldq, scale, stream=None):
+    """Rows of type xt (F32, F16, BF16) to int8 codes with one scale a row."""
+    _check(lib().kq_quantize_i8(xt, _ptr(x), M, K, ldx, _ptr(q), ldq, _ptr(scale), _stream(stream)))
+
+
+def kq_gemm_i8_workspace_bytes(M, N, K) -> int:
+    return int(lib().kq_gemm_i8_workspace_bytes(M, N, K))
+
+
+def kq_gemm_i8(q, ldq, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, workspace, ws_bytes, stream=None):
+    """int8 product with scales per token (sx) and per channel (sw); bias may be None."""
+    _check(lib().kq_gemm_i8(_ptr(q), ldq, _ptr(sx), _ptr(w), ldw, _ptr(sw), _ptr(bias), M, N, K, yt, _ptr(y), ldy,
+                            _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def kq_gemm_i8_dyn(xt, x, ldx, w, ldw, sw, bias, M, N, K, yt, y, ldy, workspace, ws_bytes, stream=None):
+    """kq_gemm_i8 from rows of type xt, quantised on the way as kq_quantize_i8 does."""
+    _check(lib().kq_gemm_i8_dyn(xt, _ptr(x), ldx, _ptr(w), ldw, _ptr(sw), _ptr(bias), M, N, K, yt, _ptr(y), ldy,
+                                _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def kq_qk_norm_rope(xt, q, ldq, k, ldk, M, n_q, n_k, D, q_gamma, k_gamma, eps, positions, cos_tab, sin_tab, n_pos, rot,
+                    pairs, yt, q_out, ldqo, k_out, ldko, stream=None):
+    """Per-head RMS norm of queries and keys and the position rotation, in one pass."""
+    _check(lib().kq_qk_norm_rope(xt, _ptr(q), ldq, _ptr(k), ldk, M, n_q, n_k, D, _ptr(q_gamma), _ptr(k_gamma),
+                                 float(eps), _ptr(positions), _ptr(cos_tab), _ptr(sin_tab), n_pos, rot, pairs, yt,
+                                 _ptr(q_out), ldqo, _ptr(k_out), ldko, _stream(stream)))
+
+
+def kq_logprobs(xt, logits, ldx, M, V, targets, n_targets, logprob, entropy, top_k=0, top_ids=None, top_logprob=None,
+                stream=None):
+    """Log probabilities of the given tokens, the entropy and the top alternatives of every row of logits."""
+    _check(lib().kq_logprobs(xt, _ptr(logits), ldx, M, V, _ptr(targets), n_targets, _ptr(logprob), _ptr(entropy),
+                             top_k, _ptr(top_ids), _ptr(top_logprob), _stream(stream)))
 
 
 def kq_debug_partials(wt, w, xq, M, N, K, partials, stream=None):

@@ -10,7 +10,8 @@ namespace kq {
 
 static thread_local char g_last_error[512] = "";
 static std::atomic<int64_t> g_launches[R_COUNT];
-static const char *kRouteNames[R_COUNT] = {"quantize", "repack", "gemv", "mmq_exact", "mmq_tc", "route", "weighted_sum"};
+static const char *kRouteNames[R_COUNT] = {"quantize", "repack", "gemv", "mmq_exact", "mmq_tc", "route", "weighted_sum",
+                                              "i8", "qk_norm_rope", "logprobs"};
 
 void count_launch(Route r, int kernels) { g_launches[r].fetch_add(kernels, std::memory_order_relaxed); }
 
@@ -43,6 +44,9 @@ const char *dtype_name(kq_dtype d) {
     case KQ_Q8_0: return "Q8_0";
     case KQ_Q8_K: return "Q8_K";
     case KQ_Q8_1: return "Q8_1";
+    case KQ_F32: return "F32";
+    case KQ_F16: return "F16";
+    case KQ_BF16: return "BF16";
     default: return "unknown";
     }
 }

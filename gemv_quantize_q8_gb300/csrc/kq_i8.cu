@@ -1,0 +1,231 @@
+// kq_i8.cu -- int8 products with one scale per token and one per output channel, and their quantizer.
+//
+// y[m][n] = ((float)(sum_k q[m][k]*w[n][k]) * sx[m]) * sw[n] (+ bias[n]); the sum is exact in int32, so the
+// order in which a kernel adds it up is free and every kernel gives the same bits.
+#include <algorithm>
+
+#include "kq_value.cuh"
+
+namespace kq {
+
+// ---------------------------------------------------------------- quantizer
+constexpr int kI8QuantThreads = 256;
+
+// One block per row: the row's largest magnitude, then its codes.
+template <typename T>
+__global__ void __launch_bounds__(kI8QuantThreads)
+    i8_quant_kernel(const T *__restrict__ x, int64_t ldx, int K, int8_t *__restrict__ q, int64_t ldq,
+                    float *__restrict__ scale) {
+    __shared__ float red[kI8QuantThreads / 32];
+    const int64_t m = blockIdx.x;
+    const T *xr = x + m * ldx;
+    float amax = 0.0f;
+    for (int i = threadIdx.x; i < K; i += kI8QuantThreads) amax = fmaxf(amax, fabsf(to_f32(xr[i])));
+#pragma unroll
+    for (int s = 16; s; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, s));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+    __syncthreads();
+    amax = red[0];
+#pragma unroll
+    for (int w = 1; w < kI8QuantThreads / 32; ++w) amax = fmaxf(amax, red[w]);
+    float inv = __fdiv_rn(127.0f, amax);
+    const bool zero = isinf(inv);
+    if (zero) inv = 0.0f;
+    if (threadIdx.x == 0) scale[m] = zero ? 0.0f : __fdiv_rn(amax, 127.0f);
+    int8_t *qr = q + m * ldq;
+    const int Kp = (K + 15) & ~15;
+    for (int i = threadIdx.x; i < Kp; i += kI8QuantThreads) {
+        const float v = i < K ? __fmul_rn(to_f32(xr[i]), inv) : 0.0f;
+        qr[i] = (int8_t)(isnan(v) ? 0 : __float2int_rn(v));
+    }
+}
+
+// ---------------------------------------------------------------- product
+// 64 x 64 outputs a block, four by four a thread, K in steps of 16 codes through shared memory.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    i8_gemm_kernel(const int8_t *__restrict__ q, int64_t ldq, const float *__restrict__ sx,
+                   const int8_t *__restrict__ w, int64_t ldw, const float *__restrict__ sw,
+                   const float *__restrict__ bias, int M, int64_t N, int K, T *__restrict__ y, int64_t ldy) {
+    __shared__ int sq[4][64], sww[4][64];
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 64;
+    const int m0 = blockIdx.y * 64;
+    int acc[4][4] = {};
+    for (int k0 = 0; k0 < K; k0 += 16) {
+        const int r = tid >> 2, c = tid & 3, k = k0 + 4 * c;
+        // the word's bytes past K are cleared: they are not the caller's
+        const int valid = min(4, max(0, K - k));
+        const unsigned mask = valid == 4 ? ~0u : (1u << (8 * valid)) - 1u;
+        sq[c][r] = m0 + r < M && valid ? (int)(*reinterpret_cast<const unsigned *>(q + (int64_t)(m0 + r) * ldq + k) & mask) : 0;
+        sww[c][r] = n0 + r < N && valid ? (int)(*reinterpret_cast<const unsigned *>(w + (n0 + r) * ldw + k) & mask) : 0;
+        __syncthreads();
+#pragma unroll
+        for (int c2 = 0; c2 < 4; ++c2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = dp4a(sq[c2][ty * 4 + i], sww[c2][tx + 16 * j], acc[i][j]);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int m = m0 + ty * 4 + i;
+            const int64_t n = n0 + tx + 16 * j;
+            if (m >= M || n >= N) continue;
+            float v = __fmul_rn(__fmul_rn((float)acc[i][j], sx[m]), sw[n]);
+            if (bias) v = __fadd_rn(v, bias[n]);
+            y[(int64_t)m * ldy + n] = from_f32<T>(v);
+        }
+}
+
+// ---------------------------------------------------------------- host
+constexpr int64_t kI8MaxK = 131071;  // 2^14 * K below 2^31: any sum of K products of two int8 fits 32 bits
+constexpr int64_t kI8MaxDim = 0x7fffff00;
+
+static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+
+// The workspace: device flag, the dynamic form's scales, its codes.
+struct I8Workspace {
+    size_t scale, codes, total;
+    int64_t ld;
+};
+static I8Workspace i8_workspace(int64_t M, int64_t K) {
+    I8Workspace l;
+    l.scale = 256;
+    l.codes = l.scale + (size_t)up(M * 4, 256);
+    l.ld = up(K, 16);
+    l.total = l.codes + (size_t)up(M * l.ld, 256);
+    return l;
+}
+
+static kq_status i8_quant(const char *fn, kq_dtype xt, const void *x, int64_t M, int64_t K, int64_t ldx, int8_t *q,
+                          int64_t ldq, float *scale, cudaStream_t st) {
+    return with_type(xt, [&](auto t) {
+        using T = decltype(t);
+        i8_quant_kernel<T><<<(unsigned)M, kI8QuantThreads, 0, st>>>(static_cast<const T *>(x), ldx, (int)K, q, ldq, scale);
+        kq_status s = check_launch(fn);
+        if (s == KQ_OK) count_launch(R_I8);
+        return s;
+    });
+}
+
+static kq_status i8_check_rows(const char *fn, kq_dtype xt, const void *x, int64_t M, int64_t K, int64_t ldx) {
+    if (!is_value_type(xt))
+        return fail(KQ_ERR_UNSUPPORTED_DTYPE, "%s: x type %s is not F32, F16 or BF16", fn, dtype_name(xt));
+    if (!x) return fail(KQ_ERR_INVALID_ARG, "%s: null x", fn);
+    if (M <= 0 || M > kI8MaxDim || K <= 0 || K > kI8MaxK || ldx < K)
+        return fail(KQ_ERR_INVALID_ARG, "%s: need M > 0, 0 < K <= %lld and ldx >= K (M=%lld K=%lld ldx=%lld)", fn,
+                    (long long)kI8MaxK, (long long)M, (long long)K, (long long)ldx);
+    if (!aligned(x, value_bytes(xt))) return fail(KQ_ERR_ALIGNMENT, "%s: x must be aligned to its elements", fn);
+    return KQ_OK;
+}
+
+static kq_status i8_check_codes(const char *fn, const char *name, const void *p, int64_t K, int64_t ld) {
+    if (!p) return fail(KQ_ERR_INVALID_ARG, "%s: null %s", fn, name);
+    if (ld < K) return fail(KQ_ERR_INVALID_ARG, "%s: ld%s=%lld is less than K=%lld", fn, name, (long long)ld, (long long)K);
+    if (!aligned(p, 16) || ld % 16)
+        return fail(KQ_ERR_ALIGNMENT, "%s: %s must be 16-byte aligned and ld%s a multiple of 16", fn, name, name);
+    return KQ_OK;
+}
+
+static kq_status i8_check_product(const char *fn, const int8_t *w, int64_t ldw, const float *sw, const float *bias,
+                                  int64_t M, int64_t N, int64_t K, kq_dtype yt, const void *y, int64_t ldy,
+                                  const void *ws, size_t ws_bytes) {
+    if (!is_value_type(yt))
+        return fail(KQ_ERR_UNSUPPORTED_DTYPE, "%s: y type %s is not F32, F16 or BF16", fn, dtype_name(yt));
+    if (!sw || !y) return fail(KQ_ERR_INVALID_ARG, "%s: null %s", fn, sw ? "y" : "sw");
+    if (M <= 0 || M > kI8MaxDim || N <= 0 || N > kI8MaxDim || K <= 0 || K > kI8MaxK || ldy < N)
+        return fail(KQ_ERR_INVALID_ARG, "%s: need M, N > 0, 0 < K <= %lld and ldy >= N (M=%lld N=%lld K=%lld ldy=%lld)",
+                    fn, (long long)kI8MaxK, (long long)M, (long long)N, (long long)K, (long long)ldy);
+    kq_status s = i8_check_codes(fn, "w", w, K, ldw);
+    if (s != KQ_OK) return s;
+    if (!aligned(sw, 4) || (bias && !aligned(bias, 4)) || !aligned(y, value_bytes(yt)))
+        return fail(KQ_ERR_ALIGNMENT, "%s: sw, bias and y must be aligned to their elements", fn);
+    const size_t need = i8_workspace(M, K).total;
+    if (!ws || ws_bytes < need)
+        return fail(KQ_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws ? ws_bytes : (size_t)0, need);
+    if (!aligned(ws, 256)) return fail(KQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", fn);
+    return KQ_OK;
+}
+
+static kq_status i8_product(const char *fn, const int8_t *q, int64_t ldq, const float *sx, const int8_t *w, int64_t ldw,
+                            const float *sw, const float *bias, int64_t M, int64_t N, int64_t K, kq_dtype yt, void *y,
+                            int64_t ldy, cudaStream_t st) {
+    return with_type(yt, [&](auto t) {
+        using T = decltype(t);
+        // grid.y holds 65535 tiles of 64 rows at most: longer batches go in slabs
+        for (int64_t m0 = 0; m0 < M; m0 += 65535 * 64) {
+            const int64_t mn = std::min<int64_t>(M - m0, 65535 * 64);
+            i8_gemm_kernel<T><<<dim3((unsigned)((N + 63) / 64), (unsigned)((mn + 63) / 64)), 256, 0, st>>>(
+                q + m0 * ldq, ldq, sx + m0, w, ldw, sw, bias, (int)mn, N, (int)K, static_cast<T *>(y) + m0 * ldy, ldy);
+            kq_status s = check_launch(fn);
+            if (s != KQ_OK) return s;
+            count_launch(R_I8);
+        }
+        return KQ_OK;
+    });
+}
+
+static kq_status i8_clear_flag(const char *fn, void *ws, cudaStream_t st) {
+    const cudaError_t e = cudaMemsetAsync(ws, 0, 8, st);
+    return e == cudaSuccess ? KQ_OK : fail(KQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+}
+
+}  // namespace kq
+
+using namespace kq;
+
+extern "C" {
+
+kq_status kq_quantize_i8(kq_dtype xt, const void *x, int64_t M, int64_t K, int64_t ldx, int8_t *q, int64_t ldq,
+                         float *scale, kq_stream_t stream) {
+    const char *fn = "kq_quantize_i8";
+    kq_status s = i8_check_rows(fn, xt, x, M, K, ldx);
+    if (s == KQ_OK) s = i8_check_codes(fn, "q", q, K, ldq);
+    if (s != KQ_OK) return s;
+    if (!scale) return fail(KQ_ERR_INVALID_ARG, "%s: null scale", fn);
+    if (!aligned(scale, 4)) return fail(KQ_ERR_ALIGNMENT, "%s: scale must be 4-byte aligned", fn);
+    return i8_quant(fn, xt, x, M, K, ldx, q, ldq, scale, (cudaStream_t)stream);
+}
+
+size_t kq_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || M > kI8MaxDim || N <= 0 || N > kI8MaxDim || K <= 0 || K > kI8MaxK) return 0;
+    return i8_workspace(M, K).total;
+}
+
+kq_status kq_gemm_i8(const int8_t *q, int64_t ldq, const float *sx, const int8_t *w, int64_t ldw, const float *sw,
+                     const float *bias, int64_t M, int64_t N, int64_t K, kq_dtype yt, void *y, int64_t ldy,
+                     void *workspace, size_t ws_bytes, kq_stream_t stream) {
+    const char *fn = "kq_gemm_i8";
+    kq_status s = i8_check_product(fn, w, ldw, sw, bias, M, N, K, yt, y, ldy, workspace, ws_bytes);
+    if (s == KQ_OK) s = i8_check_codes(fn, "q", q, K, ldq);
+    if (s != KQ_OK) return s;
+    if (!sx) return fail(KQ_ERR_INVALID_ARG, "%s: null sx", fn);
+    if (!aligned(sx, 4)) return fail(KQ_ERR_ALIGNMENT, "%s: sx must be 4-byte aligned", fn);
+    s = i8_clear_flag(fn, workspace, (cudaStream_t)stream);
+    if (s != KQ_OK) return s;
+    return i8_product(fn, q, ldq, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, (cudaStream_t)stream);
+}
+
+kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const int8_t *w, int64_t ldw, const float *sw,
+                         const float *bias, int64_t M, int64_t N, int64_t K, kq_dtype yt, void *y, int64_t ldy,
+                         void *workspace, size_t ws_bytes, kq_stream_t stream) {
+    const char *fn = "kq_gemm_i8_dyn";
+    kq_status s = i8_check_rows(fn, xt, x, M, K, ldx);
+    if (s == KQ_OK) s = i8_check_product(fn, w, ldw, sw, bias, M, N, K, yt, y, ldy, workspace, ws_bytes);
+    if (s != KQ_OK) return s;
+    s = i8_clear_flag(fn, workspace, (cudaStream_t)stream);
+    if (s != KQ_OK) return s;
+    const I8Workspace l = i8_workspace(M, K);
+    uint8_t *b = static_cast<uint8_t *>(workspace);
+    int8_t *q = reinterpret_cast<int8_t *>(b + l.codes);
+    float *sx = reinterpret_cast<float *>(b + l.scale);
+    s = i8_quant(fn, xt, x, M, K, ldx, q, l.ld, sx, (cudaStream_t)stream);
+    if (s != KQ_OK) return s;
+    return i8_product(fn, q, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, (cudaStream_t)stream);
+}
+
+}  // extern "C"

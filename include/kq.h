@@ -27,8 +27,8 @@
  *     KQ_ERR_CUDA.  Unsupported dtypes are rejected, never routed elsewhere.
  *   - Results are deterministic: no atomics in any reduction.
  *   - Sizes are elements unless named *_bytes.  K must be a multiple of 256
- *     for every path (all K-quant super-blocks, and Q8_0 rows are grouped in
- *     256-element chunks in the native layout).
+ *     for every path of the block formats (all K-quant super-blocks, and Q8_0
+ *     rows are grouped in 256-element chunks in the native layout).
  *
  * Canonical (GGUF-style) block layouts, little-endian:
  *   Q4_K (144 B / 256): f16 d, f16 dmin, 12 bytes of packed 6-bit sub-block
@@ -82,7 +82,10 @@ extern "C" {
 struct CUstream_st;
 typedef struct CUstream_st *kq_stream_t; /* same handle as cudaStream_t */
 
-typedef enum { KQ_Q4_K = 1, KQ_Q6_K = 2, KQ_Q8_0 = 3, KQ_Q8_K = 4, KQ_Q8_1 = 5, KQ_Q5_K = 6 } kq_dtype;
+typedef enum {
+    KQ_Q4_K = 1, KQ_Q6_K = 2, KQ_Q8_0 = 3, KQ_Q8_K = 4, KQ_Q8_1 = 5, KQ_Q5_K = 6, /* block formats */
+    KQ_F32 = 16, KQ_F16 = 17, KQ_BF16 = 18 /* element types of plain rows, where an entry point takes one */
+} kq_dtype;
 
 typedef enum {
     KQ_OK = 0,
@@ -311,9 +314,88 @@ KQ_API kq_status kq_read_device_flag(void *workspace, int64_t *n_bad, kq_stream_
 KQ_API kq_status kq_moe_weighted_sum(const float *y_slots, const float *w, int64_t M, int64_t top_k, int64_t N, float *out,
                               kq_stream_t stream);
 
+/* ---- int8 products with one scale per token and one per output channel ----
+ *
+ * The other common int8 scheme beside the block formats: activations carry one scale a row, weights one
+ * scale an output channel, and both stay plain row-major int8 (no repack).  Rows of codes start on
+ * 16-byte boundaries (q and w 16-byte aligned, ldq and ldw multiples of 16); K itself is free (1 to
+ * 131071, so that any sum of K products fits 32 bits), and the bytes from K to the end of a row are
+ * never used.
+ *
+ *   y[m][n] = ((float)(sum_k q[m][k]*w[n][k]) * sx[m]) * sw[n] + bias[n]
+ *
+ * The sum is exact in 32-bit integers for every int8 input, then rounded once to fp32; the two products
+ * and the sum with the bias are each rounded (no fused multiply-add), and an f16 or bf16 output is
+ * rounded once more.  So y does not depend on which kernel a size takes, nor on the other rows of the
+ * batch. */
+
+/* Quantise rows to int8 with one scale a row: amax = max |x[m][.]| (NaN never wins), scale[m] = amax/127,
+ * q = nearest-even(x * (127/amax)) with both divisions IEEE; a NaN product gives code 0.  A row whose
+ * 127/amax is not finite (amax below 3.74e-37, an all-zero row among them) is the zero row: scale 0,
+ * codes 0.  A row with an infinity has scale infinity and codes 0 (its products are NaN).
+ * x: [M][ldx] of type xt (KQ_F32, KQ_F16 or KQ_BF16), element-aligned; ldx >= K.  q: int8 [M][ldq], 16-byte
+ * aligned, ldq >= K a multiple of 16; bytes K .. K rounded up to 16 of a row are written as 0, those beyond
+ * are left.  scale: fp32 [M]. */
+KQ_API kq_status kq_quantize_i8(kq_dtype xt, const void *x, int64_t M, int64_t K, int64_t ldx, int8_t *q, int64_t ldq,
+                                float *scale, kq_stream_t stream);
+
+/* Workspace bytes of kq_gemm_i8 and kq_gemm_i8_dyn for this shape (never 0). */
+KQ_API size_t kq_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* The product from quantised rows.  q: int8 [M][ldq], sx: fp32 [M]; w: int8 [N][ldw], sw: fp32 [N]; bias:
+ * fp32 [N] or NULL; y: [M][ldy] of type yt (KQ_F32, KQ_F16 or KQ_BF16), ldy >= N, element-aligned.
+ * workspace: kq_gemm_i8_workspace_bytes(M, N, K) bytes, 256-byte aligned; kq_read_device_flag applies to
+ * it (a tensor-core pipeline wait that timed out). */
+KQ_API kq_status kq_gemm_i8(const int8_t *q, int64_t ldq, const float *sx, const int8_t *w, int64_t ldw,
+                            const float *sw, const float *bias, int64_t M, int64_t N, int64_t K, kq_dtype yt, void *y,
+                            int64_t ldy, void *workspace, size_t ws_bytes, kq_stream_t stream);
+
+/* The product from rows of type xt, quantised on the way ("dynamic" scales): bit-identical to
+ * kq_quantize_i8 followed by kq_gemm_i8.  x and ldx as kq_quantize_i8, the rest as kq_gemm_i8. */
+KQ_API kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const int8_t *w, int64_t ldw, const float *sw,
+                                const float *bias, int64_t M, int64_t N, int64_t K, kq_dtype yt, void *y, int64_t ldy,
+                                void *workspace, size_t ws_bytes, kq_stream_t stream);
+
+/* ---- what reads a product's rows ---- */
+
+/* Per-head RMS norm of queries and keys with the position rotation in the same pass.  For every token t
+ * and head h:  v = x * (1 / sqrt(sum x^2 / D + eps)) * gamma  (fp32; the factor 1 when gamma is NULL means
+ * no norm at all), then the first `rot` elements are rotated in pairs by the angle of position p =
+ * positions[t]:  (a, b) -> (a*c - b*s, b*c + a*s), c = cos_tab[p][i], s = sin_tab[p][i], i = 0 .. rot/2-1.
+ * pairs = 0: a = v[i], b = v[i + rot/2] (halves); pairs = 1: a = v[2i], b = v[2i+1] (neighbours).  The
+ * elements from rot to D are normed only.
+ * q: [M][ldq] of type xt, n_q heads of D elements side by side from q + t*ldq; k likewise with n_k heads
+ * (both may be column ranges of one product's rows); n_q or n_k may be 0 (its pointers are then unused).
+ * q_gamma, k_gamma: fp32 [D] or NULL.  cos_tab, sin_tab: fp32 [n_pos][rot/2] (unused when rot = 0).
+ * q_out, k_out: of type yt, row strides ldqo and ldko; an output may be its own input (same pointer, type
+ * and stride), so a cache row can be written directly.  D is even, 2 .. 1024; rot is even, 0 .. D.  A
+ * position outside [0, n_pos) has no angle: its token's rows are written as NaN. */
+KQ_API kq_status kq_qk_norm_rope(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, int64_t M,
+                                 int64_t n_q, int64_t n_k, int64_t D, const float *q_gamma, const float *k_gamma,
+                                 float eps, const int32_t *positions, const float *cos_tab, const float *sin_tab,
+                                 int64_t n_pos, int64_t rot, int pairs, kq_dtype yt, void *q_out, int64_t ldqo,
+                                 void *k_out, int64_t ldko, kq_stream_t stream);
+
+/* Log probabilities of given tokens, with the entropy and the top alternatives of every row, in one pass
+ * over the logits.  For a row x of V logits: m = max x, S = sum exp(x - m),
+ *   logprob[j] = (x[targets[j]] - m) - log S,  entropy = log S - (sum exp(x - m)*(x - m)) / S,
+ *   top_ids[0 .. top_k-1] the ids of the largest logits, largest first, the lowest id first among equals;
+ *   top_logprob their log probabilities.
+ * logits: [M][ldx] of type xt; targets: int32 [M][n_targets] (NULL when n_targets = 0); logprob: fp32
+ * [M][n_targets]; entropy: fp32 [M] or NULL; top_ids: int32 [M][top_k], top_logprob: fp32 [M][top_k]
+ * (unused when top_k = 0).  top_k is 0 .. 32 and at most V; V at most 2^30.
+ * Logits of -inf (masked tokens) have probability 0, log probability -inf and no share in the entropy.  A
+ * row with nothing but -inf gives log probabilities -inf, entropy 0 and the ids 0 .. top_k-1.  A row with
+ * a NaN or +inf gives NaN for its log probabilities and entropy; its ids rank +inf first and NaN with
+ * -inf.  A negative target stands for "no token": its logprob is 0.  A target >= V gives NaN. */
+KQ_API kq_status kq_logprobs(kq_dtype xt, const void *logits, int64_t ldx, int64_t M, int64_t V, const int32_t *targets,
+                             int64_t n_targets, float *logprob, float *entropy, int64_t top_k, int32_t *top_ids,
+                             float *top_logprob, kq_stream_t stream);
+
 /* Routing witness (host-side dispatch counters): number of kernel launches made by this library
  * since load, in total (route = NULL) or for one route: "quantize", "repack", "gemv", "mmq_exact",
- * "mmq_tc", "route", "weighted_sum".  Unknown route names return -1.  Thread-safe. */
+ * "mmq_tc", "route", "weighted_sum", "i8" (the int8 products), "qk_norm_rope", "logprobs".  Unknown
+ * route names return -1.  Thread-safe. */
 KQ_API int64_t kq_launch_count(const char *route);
 
 /* Debug: the integer sub-block dots of kq_gemm, partials[m][n][j] (int32)
