@@ -4,20 +4,24 @@
 // order in which a kernel adds it up is free and every kernel gives the same bits.
 #include <algorithm>
 
-#include "kq_value.cuh"
+#include "kq_i8_tc.cuh"
+#include "kq_sm100.cuh"
 
 namespace kq {
 
 // ---------------------------------------------------------------- quantizer
 constexpr int kI8QuantThreads = 256;
 
-// One block per row: the row's largest magnitude, then its codes.
-template <typename T>
+// One block per row: the row's largest magnitude, then its codes, as int8 or (the tensor-core product's
+// panel) as f16; the row's end is filled with zeros up to `fill`.  Clears the device flag where given one.
+template <typename T, typename TQ>
 __global__ void __launch_bounds__(kI8QuantThreads)
-    i8_quant_kernel(const T *__restrict__ x, int64_t ldx, int K, int8_t *__restrict__ q, int64_t ldq,
-                    float *__restrict__ scale) {
+    i8_quant_kernel(const T *__restrict__ x, int64_t ldx, int K, TQ *__restrict__ q, int64_t ldq, int fill,
+                    float *__restrict__ scale, unsigned long long *__restrict__ err) {
     __shared__ float red[kI8QuantThreads / 32];
+    sm100::grid_launch_dependents();
     const int64_t m = blockIdx.x;
+    if (err && m == 0 && threadIdx.x == 0) *err = 0ull;
     const T *xr = x + m * ldx;
     float amax = 0.0f;
     for (int i = threadIdx.x; i < K; i += kI8QuantThreads) amax = fmaxf(amax, fabsf(to_f32(xr[i])));
@@ -32,12 +36,34 @@ __global__ void __launch_bounds__(kI8QuantThreads)
     const bool zero = isinf(inv);
     if (zero) inv = 0.0f;
     if (threadIdx.x == 0) scale[m] = zero ? 0.0f : __fdiv_rn(amax, 127.0f);
-    int8_t *qr = q + m * ldq;
-    const int Kp = (K + 15) & ~15;
-    for (int i = threadIdx.x; i < Kp; i += kI8QuantThreads) {
+    TQ *qr = q + m * ldq;
+    for (int i = threadIdx.x; i < fill; i += kI8QuantThreads) {
         const float v = i < K ? __fmul_rn(to_f32(xr[i]), inv) : 0.0f;
-        qr[i] = (int8_t)(isnan(v) ? 0 : __float2int_rn(v));
+        const int c = isnan(v) ? 0 : __float2int_rn(v);
+        if constexpr (sizeof(TQ) == 1) qr[i] = (int8_t)c;
+        else qr[i] = __int2half_rn(c);
     }
+}
+
+// The tensor-core product's panel from int8 rows: f16 codes, zeros from K to ldp.  One thread a 16-code piece.
+__global__ void __launch_bounds__(256)
+    i8_panel_kernel(const int8_t *__restrict__ q, int64_t ldq, int64_t M, int K, __half *__restrict__ panel, int64_t ldp,
+                    unsigned long long *__restrict__ err) {
+    sm100::grid_launch_dependents();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, pieces = ldp / 16;
+    if (i == 0) *err = 0ull;
+    if (i >= M * pieces) return;
+    const int64_t m = i / pieces;
+    const int k = (int)(i % pieces) * 16;
+    __half h[16];
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (k < K) v = *reinterpret_cast<const uint4 *>(q + m * ldq + k);  // rows are 16-byte pieces up to ldq
+    const int8_t *c = reinterpret_cast<const int8_t *>(&v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) h[j] = __int2half_rn(k + j < K ? c[j] : 0);
+    uint4 *o = reinterpret_cast<uint4 *>(panel + m * ldp + k);
+    o[0] = reinterpret_cast<const uint4 *>(h)[0];
+    o[1] = reinterpret_cast<const uint4 *>(h)[1];
 }
 
 // ---------------------------------------------------------------- product
@@ -87,7 +113,10 @@ constexpr int64_t kI8MaxDim = 0x7fffff00;
 
 static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-// The workspace: device flag, the dynamic form's scales, its codes.
+// Tokens up to which the product streams the weights once through dp4a; more take the tensor cores.
+constexpr int64_t kI8FewTokens = 8;
+
+// The workspace: device flag, the dynamic form's scales, and its codes (few tokens) or the f16 panel.
 struct I8Workspace {
     size_t scale, codes, total;
     int64_t ld;
@@ -96,16 +125,18 @@ static I8Workspace i8_workspace(int64_t M, int64_t K) {
     I8Workspace l;
     l.scale = 256;
     l.codes = l.scale + (size_t)up(M * 4, 256);
-    l.ld = up(K, 16);
-    l.total = l.codes + (size_t)up(M * l.ld, 256);
+    l.ld = up(K, M > kI8FewTokens ? 64 : 16);
+    l.total = l.codes + (size_t)up(M * l.ld * (M > kI8FewTokens ? 2 : 1), 256);
     return l;
 }
 
-static kq_status i8_quant(const char *fn, kq_dtype xt, const void *x, int64_t M, int64_t K, int64_t ldx, int8_t *q,
-                          int64_t ldq, float *scale, cudaStream_t st) {
+template <typename TQ>
+static kq_status i8_quant(const char *fn, kq_dtype xt, const void *x, int64_t M, int64_t K, int64_t ldx, TQ *q, int64_t ldq,
+                          int64_t fill, float *scale, unsigned long long *err, cudaStream_t st) {
     return with_type(xt, [&](auto t) {
         using T = decltype(t);
-        i8_quant_kernel<T><<<(unsigned)M, kI8QuantThreads, 0, st>>>(static_cast<const T *>(x), ldx, (int)K, q, ldq, scale);
+        i8_quant_kernel<T, TQ><<<(unsigned)M, kI8QuantThreads, 0, st>>>(static_cast<const T *>(x), ldx, (int)K, q, ldq,
+                                                                        (int)fill, scale, err);
         kq_status s = check_launch(fn);
         if (s == KQ_OK) count_launch(R_I8);
         return s;
@@ -188,7 +219,7 @@ kq_status kq_quantize_i8(kq_dtype xt, const void *x, int64_t M, int64_t K, int64
     if (s != KQ_OK) return s;
     if (!scale) return fail(KQ_ERR_INVALID_ARG, "%s: null scale", fn);
     if (!aligned(scale, 4)) return fail(KQ_ERR_ALIGNMENT, "%s: scale must be 4-byte aligned", fn);
-    return i8_quant(fn, xt, x, M, K, ldx, q, ldq, scale, (cudaStream_t)stream);
+    return i8_quant(fn, xt, x, M, K, ldx, q, ldq, up(K, 16), scale, nullptr, (cudaStream_t)stream);
 }
 
 size_t kq_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
@@ -205,9 +236,21 @@ kq_status kq_gemm_i8(const int8_t *q, int64_t ldq, const float *sx, const int8_t
     if (s != KQ_OK) return s;
     if (!sx) return fail(KQ_ERR_INVALID_ARG, "%s: null sx", fn);
     if (!aligned(sx, 4)) return fail(KQ_ERR_ALIGNMENT, "%s: sx must be 4-byte aligned", fn);
-    s = i8_clear_flag(fn, workspace, (cudaStream_t)stream);
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (M <= kI8FewTokens) {
+        s = i8_clear_flag(fn, workspace, st);
+        return s != KQ_OK ? s : i8_product(fn, q, ldq, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, st);
+    }
+    const I8Workspace l = i8_workspace(M, K);
+    __half *panel = reinterpret_cast<__half *>(static_cast<uint8_t *>(workspace) + l.codes);
+    unsigned long long *err = static_cast<unsigned long long *>(workspace);
+    const int64_t blocks = (M * (l.ld / 16) + 255) / 256;
+    if (blocks > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: M=%lld is too large", fn, (long long)M);
+    i8_panel_kernel<<<(unsigned)blocks, 256, 0, st>>>(q, ldq, M, (int)K, panel, l.ld, err);
+    s = check_launch(fn);
     if (s != KQ_OK) return s;
-    return i8_product(fn, q, ldq, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, (cudaStream_t)stream);
+    count_launch(R_I8);
+    return i8_tc_product(fn, {panel, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err}, st);
 }
 
 kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const int8_t *w, int64_t ldw, const float *sw,
@@ -217,15 +260,19 @@ kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const int8_t *
     kq_status s = i8_check_rows(fn, xt, x, M, K, ldx);
     if (s == KQ_OK) s = i8_check_product(fn, w, ldw, sw, bias, M, N, K, yt, y, ldy, workspace, ws_bytes);
     if (s != KQ_OK) return s;
-    s = i8_clear_flag(fn, workspace, (cudaStream_t)stream);
-    if (s != KQ_OK) return s;
+    const cudaStream_t st = (cudaStream_t)stream;
     const I8Workspace l = i8_workspace(M, K);
     uint8_t *b = static_cast<uint8_t *>(workspace);
-    int8_t *q = reinterpret_cast<int8_t *>(b + l.codes);
     float *sx = reinterpret_cast<float *>(b + l.scale);
-    s = i8_quant(fn, xt, x, M, K, ldx, q, l.ld, sx, (cudaStream_t)stream);
-    if (s != KQ_OK) return s;
-    return i8_product(fn, q, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, (cudaStream_t)stream);
+    unsigned long long *err = static_cast<unsigned long long *>(workspace);
+    if (M <= kI8FewTokens) {
+        int8_t *q = reinterpret_cast<int8_t *>(b + l.codes);
+        s = i8_quant(fn, xt, x, M, K, ldx, q, l.ld, l.ld, sx, err, st);
+        return s != KQ_OK ? s : i8_product(fn, q, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, st);
+    }
+    __half *panel = reinterpret_cast<__half *>(b + l.codes);
+    s = i8_quant(fn, xt, x, M, K, ldx, panel, l.ld, l.ld, sx, err, st);
+    return s != KQ_OK ? s : i8_tc_product(fn, {panel, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err}, st);
 }
 
 }  // extern "C"

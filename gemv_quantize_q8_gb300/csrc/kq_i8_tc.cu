@@ -1,0 +1,582 @@
+// kq_i8_tc.cu -- tensor-core int8 product with one scale per token and per output channel.
+//
+// sm_103a has no int8 tcgen05 MMA, so the integer sum is carried exactly on the f16 tensor pipe: codes of
+// -128..127 are exact in f16, their products in fp32, and a sum of 1024 products stays within
+// 1024 * 2^14 = 2^24, where fp32 still holds every integer.  So an accumulator in tensor memory runs over
+// 1024 elements of K at most (a chunk) and is then added to int32 sums in the epilogue's registers.
+//   * weights (int8 rows) reach shared memory by TMA; converter warps turn 128 rows x 64 codes into f16
+//     and store them into tensor memory, where the MMA reads them as its A operand.
+//   * activations come as an f16 panel (written once by a prologue), by TMA, as the B operand.
+//   * outputs: weight rows = TMEM lanes, tokens = columns.
+// Large products: a pair of CTAs (cta_group::2) computes 256 rows x 256 tokens; each CTA converts its own
+// 128 rows and loads half of the tokens.  The accumulator's two 128-token halves are filled in turn, four
+// k-steps (of 64) each, so that one half's chunk is read out while the other half computes.
+// Small products: one CTA, 128 rows x 32, 64 or 128 tokens, two accumulators taking turns chunk by chunk.
+// Few tiles split K over a cluster; its CTAs exchange their int32 sums through distributed shared memory,
+// which is exact in any order.
+//
+// Roles: EPI warps read accumulators (TMEM lane quarter = warp % 4), CONV warps convert weights, then one
+// warp each loads weights, loads activations, and issues MMAs (in the pair: the first CTA's only).
+// Every wait is bounded; on expiry the CTA counts an error in the device flag and leaves in order.
+#include <algorithm>
+#include <cooperative_groups.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "kq_i8_tc.cuh"
+#include "kq_sm100.cuh"
+
+namespace kq {
+
+using namespace sm100;
+
+constexpr int I8_ROWS = 128;      // weight rows per CTA
+constexpr int I8_KS = 64;         // K per k-step: one activation tile, one TMEM stage of A
+constexpr int I8_UNIT = 128;      // K per weight tile: two k-steps
+constexpr int I8_CHUNK = 8;       // units per chunk: 1024 elements, the longest exact fp32 accumulation
+constexpr int I8_STAGES = 8;      // k-steps in flight (activation tiles and TMEM stages)
+constexpr int I8_WT = I8_ROWS * I8_UNIT;  // weight tile bytes
+constexpr unsigned long long kI8WaitNs = 2000000000ull;
+
+template <int CG_, int NT_, int EPI_, int CONV_, int WSTAGES_>
+struct I8Cfg {
+    static constexpr int CG = CG_;                // CTAs per tile
+    static constexpr int NT = NT_;                // tokens per tile
+    static constexpr int H = NT > 128 ? 2 : 1;    // halves of a tile's tokens, filled in turn
+    static constexpr int NM = NT / H;             // N of one MMA
+    static constexpr int EPI = EPI_, CONV = CONV_;
+    static constexpr int COLS = NT / (EPI / 4);   // accumulator columns of an epilogue thread
+    static constexpr int WSTAGES = WSTAGES_;
+    static constexpr int BT = NT / CG * I8_KS * 2;  // activation tile bytes of one CTA
+    static constexpr int W_PROD = EPI + CONV, W_ACT = W_PROD + 1, W_MMA = W_ACT + 1;
+    static constexpr int THREADS = (W_MMA + 1) * 32;
+    static constexpr uint32_t TM_A = 256;         // TMEM: accumulators below, A stages (32 columns each) above
+    static constexpr int W_OFF = I8_STAGES * BT;
+    static constexpr int BAR_OFF = W_OFF + WSTAGES * I8_WT;
+    static constexpr int RED_LD = I8_ROWS + 4;    // int32 per token of a parked split-K tile
+    static constexpr int BARS = 2 * I8_STAGES + 2 * WSTAGES + 5;
+    static constexpr int DATA = BAR_OFF > NT * RED_LD * 4 ? BAR_OFF : NT * RED_LD * 4;
+    static constexpr int TOTAL = ((DATA + 15) & ~15) + BARS * 8 + 16 + 1024;  // + slack to align the base
+    static_assert(TOTAL <= 227 * 1024, "shared memory");
+    static_assert(2 * NM <= (int)TM_A && TM_A + I8_STAGES * 32 <= 512, "TMEM");
+    static_assert(CONV % 4 == 0 && EPI % 4 == 0 && COLS % 8 == 0, "roles");
+};
+using I8Pair = I8Cfg<2, 256, 16, 4, 4>;
+using I8One128 = I8Cfg<1, 128, 8, 8, 4>;
+using I8One64 = I8Cfg<1, 64, 4, 8, 6>;
+using I8One32 = I8Cfg<1, 32, 4, 8, 8>;
+
+struct I8TcParams {
+    const float *sx, *sw, *bias;
+    void *y;
+    int64_t ldy;
+    int M, N, n_tiles, tiles;
+    int units, units_per_split, nsplit;  // K in units of 128
+    unsigned long long *err;
+};
+
+// ---------------------------------------------------------------- cta_group forms
+template <int CG>
+__device__ __forceinline__ void cg_alloc(uint32_t *dst) {
+    if (CG == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void cg_dealloc(uint32_t taddr) {
+    if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+}
+// Four MMAs over the 64 K of one k-step; the first accumulates iff acc0.
+template <int CG>
+__device__ __forceinline__ void cg_mma4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc0) {
+    if (CG == 1) {
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %9, 0;\n setp.eq.u32 q, %9, %9;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %10, p;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %10, q;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %10, q;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %10, q;\n}" ::"r"(d), "r"(a), "r"(a + 8), "r"(a + 16),
+            "r"(a + 24), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "r"(acc0), "r"(idesc)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %9, 0;\n setp.eq.u32 q, %9, %9;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %5, %10, p;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%2], %6, %10, q;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%3], %7, %10, q;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%4], %8, %10, q;\n}" ::"r"(d), "r"(a), "r"(a + 8), "r"(a + 16),
+            "r"(a + 24), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "r"(acc0), "r"(idesc)
+            : "memory");
+    }
+}
+// Arrive on `bar` (in both CTAs of a pair) when this thread's MMAs so far have completed.
+template <int CG>
+__device__ __forceinline__ void cg_commit(uint64_t *bar, uint16_t mask) {
+    if (CG == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                     : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"(mask)
+            : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+// TMA load into this CTA whose bytes count on the barrier of the pair's first CTA.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const void *tmap, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+// Arrive (release, cluster scope) at a barrier given by its cluster address.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 20000;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Bounded wait, acquire at cluster scope (arrivals may come from the other CTA); each try sleeps up to 20 us.
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > kI8WaitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+// A wait that a whole warp makes succeeds for all its lanes or for none, so that the warp stays together.
+__device__ __forceinline__ bool all_lanes(bool ok) { return __all_sync(~0u, ok); }
+
+// Four codes to four f16: the byte under a 0x64 high byte is 1024 + byte, so with the sign bit flipped
+// (0x6400 | (c ^ 0x80)) = 1152 + c, and one subtraction gives c exactly.
+__device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    w ^= 0x80808080u;
+    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
+template <typename C, typename TY>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, I8TcParams P) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *sB = sm, *sW = sm + C::W_OFF;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + ((C::DATA + 15) & ~15));
+    // k_full/k_empty: one k-step's activation tile and converted weights; k_full and acc_empty are waited on
+    // in the pair's first CTA only, and every arrival goes there
+    uint64_t *k_full = bars, *k_empty = k_full + I8_STAGES;
+    uint64_t *w_full = k_empty + I8_STAGES, *w_empty = w_full + C::WSTAGES;
+    uint64_t *acc_full = w_empty + C::WSTAGES, *acc_empty = acc_full + 2, *mma_done = acc_empty + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t crank = cooperative_groups::this_cluster().block_rank();
+    const int r = C::CG == 2 ? (int)(crank & 1) : 0;       // place in the pair
+    const uint32_t lead = C::CG == 2 ? crank & ~1u : crank;  // the pair's first CTA
+    const int z = blockIdx.z;                              // split-K rank
+    const int u0 = z * P.units_per_split, nu = min(P.units, u0 + P.units_per_split) - u0;
+    const int tile0 = blockIdx.x / C::CG, tstride = gridDim.x / C::CG;
+
+    if (tid == 0) {
+        for (int i = 0; i < I8_STAGES; ++i) { mbar_init(&k_full[i], 1 + 4 * C::CG); mbar_init(&k_empty[i], 1); }
+        for (int i = 0; i < C::WSTAGES; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_empty[i], C::CONV); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], C::EPI / C::H * C::CG); }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::W_MMA) cg_alloc<C::CG>(tmem_holder);
+    if (warp == C::W_PROD && lane == 0) prefetch_tmap(&tmW);
+    if (warp == C::W_ACT && lane == 0) prefetch_tmap(&tmX);
+    tc_fence_before();
+    __syncthreads();
+    cooperative_groups::this_cluster().sync();  // the pair's barriers are ready
+    tc_fence_after();
+    const uint32_t tbase = *tmem_holder;
+    int acc[C::COLS];  // epilogue: this thread's sums, one weight row
+
+    if (warp == C::W_PROD) {
+        // ------------------------------------------------------------ weight tiles
+        if (lane == 0) {
+            bool ok = true;
+            int g = 0;
+            for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
+                const int n0 = (tile % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS;
+                for (int u = 0; u < nu; ++u, ++g) {
+                    const int s = g % C::WSTAGES, ph = (g / C::WSTAGES) & 1;
+                    if (!(ok = mbar_wait_sleep(&w_empty[s], ph ^ 1, abort_flag, kI8WaitNs))) break;
+                    mbar_arrive_expect_tx(&w_full[s], I8_WT);
+                    tma_load_2d(sW + s * I8_WT, &tmW, &w_full[s], (u0 + u) * I8_UNIT, n0);
+                }
+            }
+            // leaving early: the copies in flight land first (bounded)
+            for (int i = 0; i < C::WSTAGES && !ok; ++i) {
+                const int last = g - 1 - i;
+                volatile int no_abort = 0;
+                if (last >= 0) mbar_wait(&w_full[last % C::WSTAGES], (last / C::WSTAGES) & 1, &no_abort, 100000000ull);
+            }
+        }
+    } else if (warp == C::W_ACT) {
+        // ------------------------------------------------------------ activation tiles
+        if (lane == 0) {
+            bool ok = true;
+            int g = 0;
+            grid_dependency_wait();  // the panel is the output of the kernel before this one
+            for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
+                const int m0 = (tile / P.n_tiles) * C::NT + r * (C::NT / C::CG);
+                for (int ks = 0; ks < 2 * nu; ++ks, ++g) {
+                    const int s = g % I8_STAGES, ph = (g / I8_STAGES) & 1;
+                    if (!(ok = wait_cluster(&k_empty[s], ph ^ 1, abort_flag))) break;
+                    const int x = u0 * I8_UNIT + ks * I8_KS;
+                    if (r == 0) mbar_arrive_expect_tx(&k_full[s], C::CG * C::BT);
+                    if (C::CG == 1) tma_load_2d(sB + s * C::BT, &tmX, &k_full[s], x, m0);
+                    else tma_load_2d_pair(sB + s * C::BT, &tmX, cluster_addr(&k_full[s], lead), x, m0);
+                }
+            }
+            if (!ok) {
+                // leaving early: give the copies in flight far more time than they need; their barrier may
+                // be the other CTA's or wait for converters that have left, so time alone bounds this
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 10000000ull) {}
+            }
+        }
+    } else if (warp == C::W_MMA) {
+        // ------------------------------------------------------------ MMAs
+        if (lane == 0 && r == 0) {
+            constexpr uint32_t idesc = idesc_f16_f32(I8_ROWS * C::CG, C::NM);
+            const uint64_t dB = smem_desc(smem_u32(sB), 1024, 2);
+            const uint16_t mask = (uint16_t)(3u << lead);
+            constexpr uint64_t half_rows = (uint64_t)(C::BT / C::H) >> 4;  // a half's rows in an activation tile
+            bool ok = true;
+            int g = 0, job = 0;  // k-steps, and accumulator fills of a half, so far
+            for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
+                for (int c0 = 0; c0 < nu && ok; c0 += I8_CHUNK, ++job) {
+                    const int ks_n = 2 * min(I8_CHUNK, nu - c0);
+                    // groups of four k-steps: the first half's MMAs over all of them, then the second half's
+                    for (int k0 = 0; k0 < ks_n && ok; k0 += 4) {
+                        const int kn = min(4, ks_n - k0);
+                        for (int h = 0; h < C::H && ok; ++h) {
+                            const int buf = C::H == 2 ? h : job & 1;
+                            const uint32_t use = C::H == 2 ? job : job >> 1;
+                            if (k0 == 0) {
+                                if (!(ok = wait_cluster(&acc_empty[buf], (use & 1) ^ 1, abort_flag))) break;
+                                tc_fence_after();
+                            }
+                            const uint32_t d = tbase + buf * C::NM;
+                            for (int k = 0; k < kn; ++k) {
+                                const int gs = g + k0 + k, s = gs % I8_STAGES;
+                                if (h == 0) {
+                                    if (!(ok = wait_cluster(&k_full[s], (gs / I8_STAGES) & 1, abort_flag))) break;
+                                    tc_fence_after();
+                                }
+                                cg_mma4<C::CG>(d, tbase + C::TM_A + s * 32, dB + (uint64_t)(s * (C::BT >> 4)) + h * half_rows,
+                                               idesc, (k0 + k) != 0);
+                                if (h == C::H - 1) cg_commit<C::CG>(&k_empty[s], mask);
+                            }
+                            if (ok && k0 + 4 >= ks_n) cg_commit<C::CG>(&acc_full[buf], mask);
+                        }
+                    }
+                    g += ks_n;
+                }
+            }
+            // every MMA issued has finished before tensor memory is freed
+            cg_commit<C::CG>(mma_done, (uint16_t)(1u << lead));
+            volatile int no_abort = 0;
+            mbar_wait(mma_done, 0, &no_abort, 100000000ull);
+        }
+    } else if (warp >= C::EPI) {
+        // ------------------------------------------------------------ weight converters
+        // Each group of four warps converts every (CONV/4)-th k-step: a thread's 64 codes of its row.
+        const int grp = (warp - C::EPI) >> 2, q = warp & 3, row = 32 * q + lane;
+        constexpr int GROUPS = C::CONV / 4;
+        const uint32_t ta = tbase + ((uint32_t)(32 * q) << 16) + C::TM_A;
+        bool ok = true;
+        int g = 0;  // units so far
+        for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
+            for (int u = 0; u < nu && ok; ++u, ++g) {
+                const int ws = g % C::WSTAGES;
+                if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, kI8WaitNs)))) break;
+                const uint8_t *wr = sW + ws * I8_WT + row * I8_UNIT;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (GROUPS == 2 && j != grp) continue;
+                    uint32_t o[32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // 16-byte piece p of row `row` sits at piece p ^ (row & 7) (128-byte swizzle)
+                        const uint4 v = *reinterpret_cast<const uint4 *>(wr + (((4 * j + i) ^ (row & 7)) << 4));
+                        i8x4_to_f16(v.x, o[8 * i], o[8 * i + 1]);
+                        i8x4_to_f16(v.y, o[8 * i + 2], o[8 * i + 3]);
+                        i8x4_to_f16(v.z, o[8 * i + 4], o[8 * i + 5]);
+                        i8x4_to_f16(v.w, o[8 * i + 6], o[8 * i + 7]);
+                    }
+                    const int gs = 2 * g + j, s = gs % I8_STAGES;
+                    if (!(ok = all_lanes(wait_cluster(&k_empty[s], ((gs / I8_STAGES) & 1) ^ 1, abort_flag)))) break;
+                    tc_fence_after();
+                    tmem_st32(ta + s * 32, o);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (C::CG == 1) mbar_arrive(&k_full[s]);
+                        else mbar_arrive_cluster(cluster_addr(&k_full[s], lead));
+                    }
+                }
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(&w_empty[ws]);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3, col0 = (warp >> 2) * C::COLS, row = 32 * q + lane;
+        const uint32_t lane_base = tbase + ((uint32_t)(32 * q) << 16);
+        const int h = C::H == 2 ? col0 / C::NM : 0;
+        // the token of column col0 (columns of a pair's half: 64 tokens of the first CTA, 64 of the second)
+        const int tok0 = C::CG == 1 ? col0 : (col0 % C::NM) / (C::NM / 2) * (C::NT / 2) + h * (C::NM / 2) + col0 % (C::NM / 2);
+        bool ok = true;
+        int job = 0;
+        for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
+            for (int c0 = 0; c0 < nu; c0 += I8_CHUNK, ++job) {
+                const int buf = C::H == 2 ? h : job & 1;
+                const uint32_t use = C::H == 2 ? job : job >> 1;
+                if (!(ok = all_lanes(wait_cluster(&acc_full[buf], use & 1, abort_flag)))) break;
+                tc_fence_after();
+                const uint32_t t = lane_base + (C::H == 2 ? col0 : buf * C::NM + col0);
+#pragma unroll
+                for (int c = 0; c < C::COLS; c += 8) {
+                    float v[8];
+                    tmem_ld8(t + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[c + i] = (c0 ? acc[c + i] : 0) + __float2int_rn(v[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (C::CG == 1) mbar_arrive(&acc_empty[buf]);
+                    else mbar_arrive_cluster(cluster_addr(&acc_empty[buf], lead));
+                }
+            }
+            if (!ok || P.nsplit > 1) break;  // a split tile (one a cluster) is summed below
+            if (tile == tile0) grid_dependency_wait();  // scales may be the output of the kernel before this one
+            const int n = (tile % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS + row;
+            const int m0 = (tile / P.n_tiles) * C::NT + tok0;
+            if (n < P.N) {
+                const float sw = P.sw[n], b = P.bias ? P.bias[n] : 0.0f;
+                TY *y = static_cast<TY *>(P.y) + (int64_t)m0 * P.ldy + n;
+#pragma unroll
+                for (int i = 0; i < C::COLS; ++i) {
+                    if (m0 + i < P.M) {
+                        float v = __fmul_rn(__fmul_rn((float)acc[i], P.sx[m0 + i]), sw);
+                        if (P.bias) v = __fadd_rn(v, b);
+                        y[(int64_t)i * P.ldy] = from_f32<TY>(v);
+                    }
+                }
+            }
+        }
+    }
+
+    __syncthreads();
+    if (P.nsplit > 1) {
+        // Split K: every CTA parks its int32 tile in its (now idle) shared memory, then sums a slice of
+        // tokens over the cluster's splits and stores it.
+        int *red = reinterpret_cast<int *>(sm);
+        if (warp < C::EPI) {
+            const int row = 32 * (warp & 3) + lane, col0 = (warp >> 2) * C::COLS;
+#pragma unroll
+            for (int i = 0; i < C::COLS; ++i) red[(col0 + i) * C::RED_LD + row] = acc[i];
+        }
+        cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        grid_dependency_wait();
+        const int per = (C::NT + P.nsplit - 1) / P.nsplit;
+        const int c_end = min(C::NT, (z + 1) * per);
+        const int n0 = (tile0 % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS, m0 = (tile0 / P.n_tiles) * C::NT;
+        for (int i = tid; i < (c_end - z * per) * I8_ROWS; i += C::THREADS) {
+            const int c = z * per + i / I8_ROWS, row = i % I8_ROWS, hh = c / C::NM, cm = c % C::NM;
+            const int m = m0 + (C::CG == 1 ? c : cm / (C::NM / 2) * (C::NT / 2) + hh * (C::NM / 2) + cm % (C::NM / 2));
+            const int n = n0 + row;
+            if (m >= P.M || n >= P.N) continue;
+            int sum = 0;
+            for (int k = 0; k < P.nsplit; ++k) sum += cluster.map_shared_rank(red, k * C::CG + r)[c * C::RED_LD + row];
+            float v = __fmul_rn(__fmul_rn((float)sum, P.sx[m]), P.sw[n]);
+            if (P.bias) v = __fadd_rn(v, P.bias[n]);
+            static_cast<TY *>(P.y)[(int64_t)m * P.ldy + n] = from_f32<TY>(v);
+        }
+    }
+    if (tid == 0 && *abort_flag) {
+        grid_dependency_wait();  // the kernel before this one clears the flag
+        atomicAdd(P.err, 1ull);
+    }
+    tc_fence_before();
+    cooperative_groups::this_cluster().sync();  // nobody still reads or signals the other CTA's memory
+    if (warp == C::W_MMA) {
+        tc_fence_after();
+        cg_dealloc<C::CG>(tbase);
+    }
+}
+
+// ---------------------------------------------------------------- host
+static PFN_cuTensorMapEncodeTiled_v12000 i8_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *p = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+static int i8_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        n <= 0) {
+        cudaGetLastError();
+        n = 152;
+    }
+    return n;
+}
+
+// Tiles (groups of CG CTAs) of this form that the current device holds at once.  Looked up once a device.
+template <typename C>
+static int i8_resident() {
+    static int cache[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return i8_sms() / C::CG;
+    }
+    if (!cache[dev]) {
+        auto kern = i8_tc_kernel<C, float>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(C::CG);
+        cfg.blockDim = dim3(C::THREADS);
+        cfg.dynamicSmemBytes = C::TOTAL;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = C::CG;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+            cudaGetLastError();
+            n = i8_sms() / C::CG;
+        }
+        cache[dev] = n;
+    }
+    return cache[dev];
+}
+
+template <typename C, typename TY>
+static kq_status i8_launch(const char *fn, const I8TcArgs &a, int splits, cudaStream_t st) {
+    auto encode = i8_encoder();
+    if (!encode) return fail(KQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", fn);
+    CUtensorMap tmW, tmX;
+    const cuuint32_t es[2] = {1, 1};
+    {
+        const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.N}, strides[1] = {(cuuint64_t)a.ldw};
+        const cuuint32_t box[2] = {I8_UNIT, I8_ROWS};
+        const CUresult e = encode(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(a.w), dims, strides, box, es,
+                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (e != CUDA_SUCCESS) return fail(KQ_ERR_CUDA, "%s: tensor map of w failed (%d)", fn, (int)e);
+    }
+    {
+        const cuuint64_t dims[2] = {(cuuint64_t)a.ldp, (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)a.ldp * 2};
+        const cuuint32_t box[2] = {I8_KS, C::NT / C::CG};
+        const CUresult e = encode(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half *>(a.panel), dims, strides, box,
+                                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (e != CUDA_SUCCESS) return fail(KQ_ERR_CUDA, "%s: tensor map of the panel failed (%d)", fn, (int)e);
+    }
+    I8TcParams p{};
+    p.sx = a.sx; p.sw = a.sw; p.bias = a.bias; p.y = a.y; p.ldy = a.ldy;
+    p.M = (int)a.M; p.N = (int)a.N;
+    p.n_tiles = (int)((a.N + I8_ROWS * C::CG - 1) / (I8_ROWS * C::CG));
+    const int64_t tiles = (int64_t)p.n_tiles * ((a.M + C::NT - 1) / C::NT);
+    if (tiles > 0x7fffffff / C::CG) return fail(KQ_ERR_INVALID_ARG, "%s: too many tiles", fn);
+    p.tiles = (int)tiles;
+    p.units = (int)((a.K + I8_UNIT - 1) / I8_UNIT);
+    p.units_per_split = (p.units + splits - 1) / splits;
+    p.nsplit = splits;
+    p.err = a.err;
+    auto kern = i8_tc_kernel<C, TY>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
+    if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    const int64_t groups = splits > 1 ? tiles : std::min<int64_t>(tiles, i8_resident<C>());
+    cfg.gridDim = dim3((unsigned)(groups * C::CG), 1, (unsigned)splits);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::TOTAL;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C::CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = (unsigned)splits;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // starts beside the panel's kernel
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, tmW, tmX, p);
+    if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+    count_launch(R_I8);
+    return KQ_OK;
+}
+
+// Splits of K for `tiles` tiles of CG CTAs: doubled while the CTAs still fit the device at once and every
+// split keeps four units (512 elements).
+static int i8_splits(int64_t tiles, int cg, int64_t units) {
+    const int sms = i8_sms();
+    int s = 1;
+    while (s < 8 / cg && tiles * cg * s * 2 <= sms && units >= 4 * s * 2 && (units + 2 * s - 1) / (2 * s) * (2 * s - 1) < units) s *= 2;
+    return s;
+}
+
+kq_status i8_tc_product(const char *fn, const I8TcArgs &a, cudaStream_t st) {
+    return with_type(a.yt, [&](auto t) {
+        using TY = decltype(t);
+        const int64_t units = (a.K + I8_UNIT - 1) / I8_UNIT, rows = (a.N + 127) / 128;
+        if (a.M <= 32) return i8_launch<I8One32, TY>(fn, a, i8_splits(rows, 1, units), st);
+        if (a.M <= 64) return i8_launch<I8One64, TY>(fn, a, i8_splits(rows, 1, units), st);
+        if (a.M <= 128) return i8_launch<I8One128, TY>(fn, a, i8_splits(rows, 1, units), st);
+        return i8_launch<I8Pair, TY>(fn, a, i8_splits((rows + 1) / 2 * ((a.M + 255) / 256), 2, units), st);
+    });
+}
+
+}  // namespace kq
