@@ -9,8 +9,8 @@
 //   * activations come as an f16 panel (written once by a prologue), by TMA, as the B operand.
 //   * outputs: weight rows = TMEM lanes, tokens = columns.
 // Large products: a pair of CTAs (cta_group::2) computes 256 rows x 256 tokens; each CTA converts its own
-// 128 rows and loads half of the tokens.  The accumulator's two 128-token halves are filled in turn, four
-// k-steps (of 64) each, so that one half's chunk is read out while the other half computes.
+// 128 rows and loads half of the tokens.  The accumulator's two 128-token halves are filled in turn, two
+// units (of 128 K) each, so that one half's chunk is read out while the other half computes.
 // Small products: one CTA, 128 rows x 32, 64 or 128 tokens, two accumulators taking turns chunk by chunk.
 // Few tiles split K over a cluster; its CTAs exchange their int32 sums through distributed shared memory,
 // which is exact in any order.
@@ -31,10 +31,10 @@ namespace kq {
 using namespace sm100;
 
 constexpr int I8_ROWS = 128;      // weight rows per CTA
-constexpr int I8_KS = 64;         // K per k-step: one activation tile, one TMEM stage of A
-constexpr int I8_UNIT = 128;      // K per weight tile: two k-steps
+constexpr int I8_KS = 64;         // K per activation tile (a 128-byte swizzled row of f16)
+constexpr int I8_UNIT = 128;      // K per unit: a weight tile, two activation tiles, one TMEM stage of A
 constexpr int I8_CHUNK = 8;       // units per chunk: 1024 elements, the longest exact fp32 accumulation
-constexpr int I8_STAGES = 8;      // k-steps in flight (activation tiles and TMEM stages)
+constexpr int I8_STAGES = 4;      // units in flight (activation tiles and TMEM stages)
 constexpr int I8_WT = I8_ROWS * I8_UNIT;  // weight tile bytes
 constexpr unsigned long long kI8WaitNs = 2000000000ull;
 
@@ -47,18 +47,18 @@ struct I8Cfg {
     static constexpr int EPI = EPI_, CONV = CONV_;
     static constexpr int COLS = NT / (EPI / 4);   // accumulator columns of an epilogue thread
     static constexpr int WSTAGES = WSTAGES_;
-    static constexpr int BT = NT / CG * I8_KS * 2;  // activation tile bytes of one CTA
+    static constexpr int BT = NT / CG * I8_KS * 2;  // activation tile bytes of one CTA (two tiles a unit)
     static constexpr int W_PROD = EPI + CONV, W_ACT = W_PROD + 1, W_MMA = W_ACT + 1;
     static constexpr int THREADS = (W_MMA + 1) * 32;
-    static constexpr uint32_t TM_A = 256;         // TMEM: accumulators below, A stages (32 columns each) above
-    static constexpr int W_OFF = I8_STAGES * BT;
+    static constexpr uint32_t TM_A = 256;         // TMEM: accumulators below, A stages (64 columns each) above
+    static constexpr int W_OFF = I8_STAGES * 2 * BT;
     static constexpr int BAR_OFF = W_OFF + WSTAGES * I8_WT;
     static constexpr int RED_LD = I8_ROWS + 4;    // int32 per token of a parked split-K tile
     static constexpr int BARS = 2 * I8_STAGES + 2 * WSTAGES + 5;
     static constexpr int DATA = BAR_OFF > NT * RED_LD * 4 ? BAR_OFF : NT * RED_LD * 4;
     static constexpr int TOTAL = ((DATA + 15) & ~15) + BARS * 8 + 16 + 1024;  // + slack to align the base
     static_assert(TOTAL <= 227 * 1024, "shared memory");
-    static_assert(2 * NM <= (int)TM_A && TM_A + I8_STAGES * 32 <= 512, "TMEM");
+    static_assert(2 * NM <= (int)TM_A && TM_A + I8_STAGES * 64 <= 512, "TMEM");
     static_assert(CONV % 4 == 0 && EPI % 4 == 0 && COLS % 8 == 0, "roles");
 };
 using I8Pair = I8Cfg<2, 256, 16, 4, 4>;
@@ -91,26 +91,43 @@ __device__ __forceinline__ void cg_dealloc(uint32_t taddr) {
     if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
     else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
 }
-// Four MMAs over the 64 K of one k-step; the first accumulates iff acc0.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+// Eight MMAs over the 128 K of a unit (B tiles of 64 K at b and b2); the first accumulates iff acc0.
 template <int CG>
-__device__ __forceinline__ void cg_mma4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc0) {
+__device__ __forceinline__ void cg_mma8(uint32_t d, uint32_t a, uint64_t b, uint64_t b2, uint32_t idesc, uint32_t acc0) {
     if (CG == 1) {
         asm volatile(
-            "{\n .reg .pred p, q;\n setp.ne.u32 p, %9, 0;\n setp.eq.u32 q, %9, %9;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %10, p;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %10, q;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %10, q;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %10, q;\n}" ::"r"(d), "r"(a), "r"(a + 8), "r"(a + 16),
-            "r"(a + 24), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "r"(acc0), "r"(idesc)
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %17, 0;\n setp.eq.u32 q, %17, %17;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %9, %18, p;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %10, %18, q;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %11, %18, q;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %12, %18, q;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %13, %18, q;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%6], %14, %18, q;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %15, %18, q;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%8], %16, %18, q;\n}"
+            ::"r"(d),
+            "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "r"(a + 32), "r"(a + 40), "r"(a + 48), "r"(a + 56), "l"(b), "l"(b + 2),
+            "l"(b + 4), "l"(b + 6), "l"(b2), "l"(b2 + 2), "l"(b2 + 4), "l"(b2 + 6), "r"(acc0), "r"(idesc)
             : "memory");
     } else {
         asm volatile(
-            "{\n .reg .pred p, q;\n setp.ne.u32 p, %9, 0;\n setp.eq.u32 q, %9, %9;\n"
-            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %5, %10, p;\n"
-            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%2], %6, %10, q;\n"
-            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%3], %7, %10, q;\n"
-            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%4], %8, %10, q;\n}" ::"r"(d), "r"(a), "r"(a + 8), "r"(a + 16),
-            "r"(a + 24), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "r"(acc0), "r"(idesc)
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %17, 0;\n setp.eq.u32 q, %17, %17;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %9, %18, p;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%2], %10, %18, q;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%3], %11, %18, q;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%4], %12, %18, q;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%5], %13, %18, q;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%6], %14, %18, q;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%7], %15, %18, q;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], [%8], %16, %18, q;\n}"
+            ::"r"(d),
+            "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "r"(a + 32), "r"(a + 40), "r"(a + 48), "r"(a + 56), "l"(b), "l"(b + 2),
+            "l"(b + 4), "l"(b + 6), "l"(b2), "l"(b2 + 2), "l"(b2 + 4), "l"(b2 + 6), "r"(acc0), "r"(idesc)
             : "memory");
     }
 }
@@ -140,32 +157,11 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const void *tmap, ui
         "l"(tmap), "r"(bar), "r"(c0), "r"(c1)
         : "memory");
 }
-// Arrive (release, cluster scope) at a barrier given by its cluster address.
+// Arrive at a barrier given by its cluster address.  Relaxed: what it announces went to (or was read from)
+// tensor memory and is ordered by the tcgen05 fences around it.  A release at cluster scope in its place
+// cost the converters 940 cycles a k-step.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 20000;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Bounded wait, acquire at cluster scope (arrivals may come from the other CTA); each try sleeps up to 20 us.
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (*abort) return false;
-        if (globaltimer_ns() - t0 > kI8WaitNs) {
-            *abort = 1;
-            return false;
-        }
-    }
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // A wait that a whole warp makes succeeds for all its lanes or for none, so that the warp stays together.
@@ -190,7 +186,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *sB = sm, *sW = sm + C::W_OFF;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + ((C::DATA + 15) & ~15));
-    // k_full/k_empty: one k-step's activation tile and converted weights; k_full and acc_empty are waited on
+    // k_full/k_empty: one unit's activation tiles and converted weights; k_full and acc_empty are waited on
     // in the pair's first CTA only, and every arrival goes there
     uint64_t *k_full = bars, *k_empty = k_full + I8_STAGES;
     uint64_t *w_full = k_empty + I8_STAGES, *w_empty = w_full + C::WSTAGES;
@@ -207,7 +203,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int tile0 = blockIdx.x / C::CG, tstride = gridDim.x / C::CG;
 
     if (tid == 0) {
-        for (int i = 0; i < I8_STAGES; ++i) { mbar_init(&k_full[i], 1 + 4 * C::CG); mbar_init(&k_empty[i], 1); }
+        for (int i = 0; i < I8_STAGES; ++i) { mbar_init(&k_full[i], 1 + C::CONV * C::CG); mbar_init(&k_empty[i], 1); }
         for (int i = 0; i < C::WSTAGES; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_empty[i], C::CONV); }
         for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], C::EPI / C::H * C::CG); }
         mbar_init(mma_done, 1);
@@ -221,7 +217,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __syncthreads();
     cooperative_groups::this_cluster().sync();  // the pair's barriers are ready
     tc_fence_after();
-    const uint32_t tbase = *tmem_holder;
+    // all 512 columns are this kernel's, so the allocation starts at column 0 of lane 0
+    constexpr uint32_t tbase = 0;
     int acc[C::COLS];  // epilogue: this thread's sums, one weight row
 
     if (warp == C::W_PROD) {
@@ -253,13 +250,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             grid_dependency_wait();  // the panel is the output of the kernel before this one
             for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
                 const int m0 = (tile / P.n_tiles) * C::NT + r * (C::NT / C::CG);
-                for (int ks = 0; ks < 2 * nu; ++ks, ++g) {
+                for (int u = 0; u < nu; ++u, ++g) {
                     const int s = g % I8_STAGES, ph = (g / I8_STAGES) & 1;
-                    if (!(ok = wait_cluster(&k_empty[s], ph ^ 1, abort_flag))) break;
-                    const int x = u0 * I8_UNIT + ks * I8_KS;
-                    if (r == 0) mbar_arrive_expect_tx(&k_full[s], C::CG * C::BT);
-                    if (C::CG == 1) tma_load_2d(sB + s * C::BT, &tmX, &k_full[s], x, m0);
-                    else tma_load_2d_pair(sB + s * C::BT, &tmX, cluster_addr(&k_full[s], lead), x, m0);
+                    if (!(ok = mbar_wait_sleep(&k_empty[s], ph ^ 1, abort_flag, kI8WaitNs))) break;
+                    const int x = (u0 + u) * I8_UNIT;
+                    if (r == 0) mbar_arrive_expect_tx(&k_full[s], C::CG * 2 * C::BT);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint8_t *dst = sB + (2 * s + j) * C::BT;
+                        if (C::CG == 1) tma_load_2d(dst, &tmX, &k_full[s], x + j * I8_KS, m0);
+                        else tma_load_2d_pair(dst, &tmX, cluster_addr(&k_full[s], lead), x + j * I8_KS, m0);
+                    }
                 }
             }
             if (!ok) {
@@ -271,51 +272,59 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
     } else if (warp == C::W_MMA) {
         // ------------------------------------------------------------ MMAs
-        if (lane == 0 && r == 0) {
+        // The whole warp walks the loop, so that the operands stay in uniform registers; one lane issues.
+        if (r == 0) {
+            const bool one = elect_one();
             constexpr uint32_t idesc = idesc_f16_f32(I8_ROWS * C::CG, C::NM);
             const uint64_t dB = smem_desc(smem_u32(sB), 1024, 2);
             const uint16_t mask = (uint16_t)(3u << lead);
             constexpr uint64_t half_rows = (uint64_t)(C::BT / C::H) >> 4;  // a half's rows in an activation tile
             bool ok = true;
-            int g = 0, job = 0;  // k-steps, and accumulator fills of a half, so far
+            int s = 0, job = 0;  // stage, and accumulator fills so far
+            uint32_t ph = 0;     // phase of stage s's barriers
             for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
                 for (int c0 = 0; c0 < nu && ok; c0 += I8_CHUNK, ++job) {
-                    const int ks_n = 2 * min(I8_CHUNK, nu - c0);
-                    // groups of four k-steps: the first half's MMAs over all of them, then the second half's
-                    for (int k0 = 0; k0 < ks_n && ok; k0 += 4) {
-                        const int kn = min(4, ks_n - k0);
+                    const int un = min(I8_CHUNK, nu - c0);
+                    // two units at a time: the first half's MMAs over both, then the second half's
+                    for (int u = 0; u < un && ok; u += 2) {
+                        const int kn = min(2, un - u);
                         for (int h = 0; h < C::H && ok; ++h) {
                             const int buf = C::H == 2 ? h : job & 1;
                             const uint32_t use = C::H == 2 ? job : job >> 1;
-                            if (k0 == 0) {
-                                if (!(ok = wait_cluster(&acc_empty[buf], (use & 1) ^ 1, abort_flag))) break;
+                            if (u == 0) {
+                                if (!(ok = all_lanes(mbar_wait_sleep(&acc_empty[buf], (use & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
                                 tc_fence_after();
                             }
-                            const uint32_t d = tbase + buf * C::NM;
                             for (int k = 0; k < kn; ++k) {
-                                const int gs = g + k0 + k, s = gs % I8_STAGES;
+                                const int sk = (s + k) % I8_STAGES;
                                 if (h == 0) {
-                                    if (!(ok = wait_cluster(&k_full[s], (gs / I8_STAGES) & 1, abort_flag))) break;
+                                    const uint32_t phk = s + k < I8_STAGES ? ph : ph ^ 1;
+                                    if (!(ok = all_lanes(mbar_wait_sleep(&k_full[sk], phk, abort_flag, kI8WaitNs)))) break;
                                     tc_fence_after();
                                 }
-                                cg_mma4<C::CG>(d, tbase + C::TM_A + s * 32, dB + (uint64_t)(s * (C::BT >> 4)) + h * half_rows,
-                                               idesc, (k0 + k) != 0);
-                                if (h == C::H - 1) cg_commit<C::CG>(&k_empty[s], mask);
+                                const uint64_t b = dB + (uint64_t)(sk * (2 * C::BT >> 4)) + h * half_rows;
+                                if (one) {
+                                    cg_mma8<C::CG>(buf * C::NM, C::TM_A + sk * 64, b, b + (C::BT >> 4), idesc, u + k);
+                                    if (h == C::H - 1) cg_commit<C::CG>(&k_empty[sk], mask);
+                                }
+                                __syncwarp();
                             }
-                            if (ok && k0 + 4 >= ks_n) cg_commit<C::CG>(&acc_full[buf], mask);
+                            if (ok && one && u + 2 >= un) cg_commit<C::CG>(&acc_full[buf], mask);
                         }
+                        s += kn;
+                        if (s >= I8_STAGES) { s -= I8_STAGES; ph ^= 1; }
                     }
-                    g += ks_n;
                 }
             }
             // every MMA issued has finished before tensor memory is freed
-            cg_commit<C::CG>(mma_done, (uint16_t)(1u << lead));
+            if (one) cg_commit<C::CG>(mma_done, (uint16_t)(1u << lead));
+            __syncwarp();
             volatile int no_abort = 0;
             mbar_wait(mma_done, 0, &no_abort, 100000000ull);
         }
     } else if (warp >= C::EPI) {
         // ------------------------------------------------------------ weight converters
-        // Each group of four warps converts every (CONV/4)-th k-step: a thread's 64 codes of its row.
+        // A thread converts its row's codes of a unit; with eight warps, four take each half of the unit.
         const int grp = (warp - C::EPI) >> 2, q = warp & 3, row = 32 * q + lane;
         constexpr int GROUPS = C::CONV / 4;
         const uint32_t ta = tbase + ((uint32_t)(32 * q) << 16) + C::TM_A;
@@ -326,6 +335,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int ws = g % C::WSTAGES;
                 if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, kI8WaitNs)))) break;
                 const uint8_t *wr = sW + ws * I8_WT + row * I8_UNIT;
+                const int s = g % I8_STAGES;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     if (GROUPS == 2 && j != grp) continue;
@@ -339,20 +349,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         i8x4_to_f16(v.z, o[8 * i + 4], o[8 * i + 5]);
                         i8x4_to_f16(v.w, o[8 * i + 6], o[8 * i + 7]);
                     }
-                    const int gs = 2 * g + j, s = gs % I8_STAGES;
-                    if (!(ok = all_lanes(wait_cluster(&k_empty[s], ((gs / I8_STAGES) & 1) ^ 1, abort_flag)))) break;
-                    tc_fence_after();
-                    tmem_st32(ta + s * 32, o);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (C::CG == 1) mbar_arrive(&k_full[s]);
-                        else mbar_arrive_cluster(cluster_addr(&k_full[s], lead));
+                    if (j == 0 || GROUPS == 2) {
+                        if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / I8_STAGES) & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
+                        tc_fence_after();
                     }
+                    tmem_st32(ta + s * 64 + j * 32, o);
                 }
+                if (!ok) break;
+                tmem_wait_st();
+                tc_fence_before();
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(&w_empty[ws]);
+                if (lane == 0) {
+                    if (C::CG == 1) mbar_arrive(&k_full[s]);
+                    else mbar_arrive_cluster(cluster_addr(&k_full[s], lead));
+                    mbar_arrive(&w_empty[ws]);
+                }
             }
         }
     } else {
@@ -368,7 +379,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int c0 = 0; c0 < nu; c0 += I8_CHUNK, ++job) {
                 const int buf = C::H == 2 ? h : job & 1;
                 const uint32_t use = C::H == 2 ? job : job >> 1;
-                if (!(ok = all_lanes(wait_cluster(&acc_full[buf], use & 1, abort_flag)))) break;
+                if (!(ok = all_lanes(mbar_wait_sleep(&acc_full[buf], use & 1, abort_flag, kI8WaitNs)))) break;
                 tc_fence_after();
                 const uint32_t t = lane_base + (C::H == 2 ? col0 : buf * C::NM + col0);
 #pragma unroll
@@ -441,7 +452,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     cooperative_groups::this_cluster().sync();  // nobody still reads or signals the other CTA's memory
     if (warp == C::W_MMA) {
         tc_fence_after();
-        cg_dealloc<C::CG>(tbase);
+        cg_dealloc<C::CG>(*tmem_holder);
     }
 }
 
