@@ -1,9 +1,9 @@
 // kq_i8.cu -- int8 products with one scale per token and one per output channel, and their quantizer.
 //
 // y[m][n] = ((float)(sum_k q[m][k]*w[n][k]) * sx[m]) * sw[n] (+ bias[n]); the sum is exact in int32, so the
-// order in which a kernel adds it up is free and every kernel gives the same bits.
-#include <algorithm>
-
+// order in which a kernel adds it up is free and every kernel gives the same bits.  Up to eight tokens take
+// kq_i8_gemv.cu (bound by the weights' bytes), more the tensor cores (kq_i8_tc.cu).
+#include "kq_i8_gemv.cuh"
 #include "kq_i8_tc.cuh"
 #include "kq_sm100.cuh"
 
@@ -66,55 +66,11 @@ __global__ void __launch_bounds__(256)
     o[1] = reinterpret_cast<const uint4 *>(h)[1];
 }
 
-// ---------------------------------------------------------------- product
-// 64 x 64 outputs a block, four by four a thread, K in steps of 16 codes through shared memory.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    i8_gemm_kernel(const int8_t *__restrict__ q, int64_t ldq, const float *__restrict__ sx,
-                   const int8_t *__restrict__ w, int64_t ldw, const float *__restrict__ sw,
-                   const float *__restrict__ bias, int M, int64_t N, int K, T *__restrict__ y, int64_t ldy) {
-    __shared__ int sq[4][64], sww[4][64];
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 64;
-    const int m0 = blockIdx.y * 64;
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += 16) {
-        const int r = tid >> 2, c = tid & 3, k = k0 + 4 * c;
-        // the word's bytes past K are cleared: they are not the caller's
-        const int valid = min(4, max(0, K - k));
-        const unsigned mask = valid == 4 ? ~0u : (1u << (8 * valid)) - 1u;
-        sq[c][r] = m0 + r < M && valid ? (int)(*reinterpret_cast<const unsigned *>(q + (int64_t)(m0 + r) * ldq + k) & mask) : 0;
-        sww[c][r] = n0 + r < N && valid ? (int)(*reinterpret_cast<const unsigned *>(w + (n0 + r) * ldw + k) & mask) : 0;
-        __syncthreads();
-#pragma unroll
-        for (int c2 = 0; c2 < 4; ++c2)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = dp4a(sq[c2][ty * 4 + i], sww[c2][tx + 16 * j], acc[i][j]);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty * 4 + i;
-            const int64_t n = n0 + tx + 16 * j;
-            if (m >= M || n >= N) continue;
-            float v = __fmul_rn(__fmul_rn((float)acc[i][j], sx[m]), sw[n]);
-            if (bias) v = __fadd_rn(v, bias[n]);
-            y[(int64_t)m * ldy + n] = from_f32<T>(v);
-        }
-}
-
 // ---------------------------------------------------------------- host
 constexpr int64_t kI8MaxK = 131071;  // 2^14 * K below 2^31: any sum of K products of two int8 fits 32 bits
 constexpr int64_t kI8MaxDim = 0x7fffff00;
 
 static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
-
-// Tokens up to which the product streams the weights once through dp4a; more take the tensor cores.
-constexpr int64_t kI8FewTokens = 8;
 
 // The workspace: device flag, the dynamic form's scales, and its codes (few tokens) or the f16 panel.
 struct I8Workspace {
@@ -182,29 +138,6 @@ static kq_status i8_check_product(const char *fn, const int8_t *w, int64_t ldw, 
     return KQ_OK;
 }
 
-static kq_status i8_product(const char *fn, const int8_t *q, int64_t ldq, const float *sx, const int8_t *w, int64_t ldw,
-                            const float *sw, const float *bias, int64_t M, int64_t N, int64_t K, kq_dtype yt, void *y,
-                            int64_t ldy, cudaStream_t st) {
-    return with_type(yt, [&](auto t) {
-        using T = decltype(t);
-        // grid.y holds 65535 tiles of 64 rows at most: longer batches go in slabs
-        for (int64_t m0 = 0; m0 < M; m0 += 65535 * 64) {
-            const int64_t mn = std::min<int64_t>(M - m0, 65535 * 64);
-            i8_gemm_kernel<T><<<dim3((unsigned)((N + 63) / 64), (unsigned)((mn + 63) / 64)), 256, 0, st>>>(
-                q + m0 * ldq, ldq, sx + m0, w, ldw, sw, bias, (int)mn, N, (int)K, static_cast<T *>(y) + m0 * ldy, ldy);
-            kq_status s = check_launch(fn);
-            if (s != KQ_OK) return s;
-            count_launch(R_I8);
-        }
-        return KQ_OK;
-    });
-}
-
-static kq_status i8_clear_flag(const char *fn, void *ws, cudaStream_t st) {
-    const cudaError_t e = cudaMemsetAsync(ws, 0, 8, st);
-    return e == cudaSuccess ? KQ_OK : fail(KQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-}
-
 }  // namespace kq
 
 using namespace kq;
@@ -237,13 +170,10 @@ kq_status kq_gemm_i8(const int8_t *q, int64_t ldq, const float *sx, const int8_t
     if (!sx) return fail(KQ_ERR_INVALID_ARG, "%s: null sx", fn);
     if (!aligned(sx, 4)) return fail(KQ_ERR_ALIGNMENT, "%s: sx must be 4-byte aligned", fn);
     const cudaStream_t st = (cudaStream_t)stream;
-    if (M <= kI8FewTokens) {
-        s = i8_clear_flag(fn, workspace, st);
-        return s != KQ_OK ? s : i8_product(fn, q, ldq, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, st);
-    }
+    unsigned long long *err = static_cast<unsigned long long *>(workspace);
+    if (M <= kI8FewTokens) return i8_gemv(fn, {q, ldq, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, false}, st);
     const I8Workspace l = i8_workspace(M, K);
     __half *panel = reinterpret_cast<__half *>(static_cast<uint8_t *>(workspace) + l.codes);
-    unsigned long long *err = static_cast<unsigned long long *>(workspace);
     const int64_t blocks = (M * (l.ld / 16) + 255) / 256;
     if (blocks > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: M=%lld is too large", fn, (long long)M);
     i8_panel_kernel<<<(unsigned)blocks, 256, 0, st>>>(q, ldq, M, (int)K, panel, l.ld, err);
@@ -267,8 +197,8 @@ kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const int8_t *
     unsigned long long *err = static_cast<unsigned long long *>(workspace);
     if (M <= kI8FewTokens) {
         int8_t *q = reinterpret_cast<int8_t *>(b + l.codes);
-        s = i8_quant(fn, xt, x, M, K, ldx, q, l.ld, l.ld, sx, err, st);
-        return s != KQ_OK ? s : i8_product(fn, q, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, st);
+        s = i8_quant(fn, xt, x, M, K, ldx, q, l.ld, l.ld, sx, static_cast<unsigned long long *>(nullptr), st);
+        return s != KQ_OK ? s : i8_gemv(fn, {q, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, true}, st);
     }
     __half *panel = reinterpret_cast<__half *>(b + l.codes);
     s = i8_quant(fn, xt, x, M, K, ldx, panel, l.ld, l.ld, sx, err, st);
