@@ -72,7 +72,7 @@ constexpr int64_t kI8MaxDim = 0x7fffff00;
 
 static int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-// The workspace: device flag, the dynamic form's scales, and its codes (few tokens) or the f16 panel.
+// The workspace: device flag, the dynamic form's scales, and its codes (up to kI8DirectTokens) or the f16 panel.
 struct I8Workspace {
     size_t scale, codes, total;
     int64_t ld;
@@ -81,8 +81,8 @@ static I8Workspace i8_workspace(int64_t M, int64_t K) {
     I8Workspace l;
     l.scale = 256;
     l.codes = l.scale + (size_t)up(M * 4, 256);
-    l.ld = up(K, M > kI8FewTokens ? 64 : 16);
-    l.total = l.codes + (size_t)up(M * l.ld * (M > kI8FewTokens ? 2 : 1), 256);
+    l.ld = up(K, M > kI8DirectTokens ? 64 : 16);
+    l.total = l.codes + (size_t)up(M * l.ld * (M > kI8DirectTokens ? 2 : 1), 256);
     return l;
 }
 
@@ -172,6 +172,8 @@ kq_status kq_gemm_i8(const int8_t *q, int64_t ldq, const float *sx, const int8_t
     const cudaStream_t st = (cudaStream_t)stream;
     unsigned long long *err = static_cast<unsigned long long *>(workspace);
     if (M <= kI8FewTokens) return i8_gemv(fn, {q, ldq, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, false}, st);
+    if (M <= kI8DirectTokens)
+        return i8_tc_product(fn, {q, ldq, nullptr, 0, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, false}, st);
     const I8Workspace l = i8_workspace(M, K);
     __half *panel = reinterpret_cast<__half *>(static_cast<uint8_t *>(workspace) + l.codes);
     const int64_t blocks = (M * (l.ld / 16) + 255) / 256;
@@ -180,7 +182,7 @@ kq_status kq_gemm_i8(const int8_t *q, int64_t ldq, const float *sx, const int8_t
     s = check_launch(fn);
     if (s != KQ_OK) return s;
     count_launch(R_I8);
-    return i8_tc_product(fn, {panel, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err}, st);
+    return i8_tc_product(fn, {nullptr, 0, panel, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, true}, st);
 }
 
 kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const int8_t *w, int64_t ldw, const float *sw,
@@ -195,14 +197,17 @@ kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const int8_t *
     uint8_t *b = static_cast<uint8_t *>(workspace);
     float *sx = reinterpret_cast<float *>(b + l.scale);
     unsigned long long *err = static_cast<unsigned long long *>(workspace);
-    if (M <= kI8FewTokens) {
+    if (M <= kI8DirectTokens) {
         int8_t *q = reinterpret_cast<int8_t *>(b + l.codes);
         s = i8_quant(fn, xt, x, M, K, ldx, q, l.ld, l.ld, sx, static_cast<unsigned long long *>(nullptr), st);
-        return s != KQ_OK ? s : i8_gemv(fn, {q, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, true}, st);
+        if (s != KQ_OK) return s;
+        if (M > kI8FewTokens)
+            return i8_tc_product(fn, {q, l.ld, nullptr, 0, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, true}, st);
+        return i8_gemv(fn, {q, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, true}, st);
     }
     __half *panel = reinterpret_cast<__half *>(b + l.codes);
     s = i8_quant(fn, xt, x, M, K, ldx, panel, l.ld, l.ld, sx, err, st);
-    return s != KQ_OK ? s : i8_tc_product(fn, {panel, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err}, st);
+    return s != KQ_OK ? s : i8_tc_product(fn, {nullptr, 0, panel, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, true}, st);
 }
 
 }  // extern "C"

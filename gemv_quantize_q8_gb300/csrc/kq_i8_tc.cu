@@ -11,12 +11,13 @@
 // Large products: a pair of CTAs (cta_group::2) computes 256 rows x 256 tokens; each CTA converts its own
 // 128 rows and loads half of the tokens.  The accumulator's two 128-token halves are filled in turn, two
 // units (of 128 K) each, so that one half's chunk is read out while the other half computes.
-// Small products: one CTA, 128 rows x 32, 64 or 128 tokens, two accumulators taking turns chunk by chunk.
+// Small products: one CTA, 128 rows x 32, 64 or 128 tokens, two CTAs an SM (one computes while the other
+// starts, ends or waits); up to 64 tokens are converted from int8 by the CTA itself, without a panel.
 // Few tiles split K over a cluster; its CTAs exchange their int32 sums through distributed shared memory,
 // which is exact in any order.
 //
-// Roles: EPI warps read accumulators (TMEM lane quarter = warp % 4), CONV warps convert weights, then one
-// warp each loads weights, loads activations, and issues MMAs (in the pair: the first CTA's only).
+// Roles: EPI warps read accumulators (TMEM lane quarter = warp % 4), CONV warps convert weights, one warp
+// loads weights, ACT warps load or convert activations, one issues MMAs (in the pair: the first CTA's only).
 // Every wait is bounded; on expiry the CTA counts an error in the device flag and leaves in order.
 #include <algorithm>
 #include <cooperative_groups.h>
@@ -34,37 +35,44 @@ constexpr int I8_ROWS = 128;      // weight rows per CTA
 constexpr int I8_KS = 64;         // K per activation tile (a 128-byte swizzled row of f16)
 constexpr int I8_UNIT = 128;      // K per unit: a weight tile, two activation tiles, one TMEM stage of A
 constexpr int I8_CHUNK = 8;       // units per chunk: 1024 elements, the longest exact fp32 accumulation
-constexpr int I8_STAGES = 4;      // units in flight (activation tiles and TMEM stages)
-constexpr int I8_WT = I8_ROWS * I8_UNIT;  // weight tile bytes
+constexpr int I8_MAX_SPLIT = 8;  // CTAs that share a tile's K (portable cluster size)
 constexpr unsigned long long kI8WaitNs = 2000000000ull;
 
-template <int CG_, int NT_, int EPI_, int CONV_, int WSTAGES_>
+template <int CG_, int NT_, int EPI_, int STAGES_, int WSTAGES_, int PER_SM_>
 struct I8Cfg {
     static constexpr int CG = CG_;                // CTAs per tile
     static constexpr int NT = NT_;                // tokens per tile
     static constexpr int H = NT > 128 ? 2 : 1;    // halves of a tile's tokens, filled in turn
     static constexpr int NM = NT / H;             // N of one MMA
-    static constexpr int EPI = EPI_, CONV = CONV_;
+    static constexpr int NACC = 2;  // accumulators of NM columns
+    static constexpr int EPI = EPI_, CONV = 4;
     static constexpr int COLS = NT / (EPI / 4);   // accumulator columns of an epilogue thread
-    static constexpr int WSTAGES = WSTAGES_;
+    static constexpr int STAGES = STAGES_;        // units in flight (activation tiles and TMEM stages)
+    static constexpr int WSTAGES = WSTAGES_;      // weight tiles in flight
+    static constexpr int PER_SM = PER_SM_;        // CTAs of an SM
+    // Up to 64 tokens: no f16 panel; ACT warps turn int8 codes into the B tiles themselves
+    static constexpr bool DIRECT = NT <= kI8DirectTokens;
+    static constexpr int ACT = DIRECT ? NT / 8 : 1;  // eight tokens a warp: with 32 it was the slowest role, 0.58 us a unit
     static constexpr int BT = NT / CG * I8_KS * 2;  // activation tile bytes of one CTA (two tiles a unit)
-    static constexpr int W_PROD = EPI + CONV, W_ACT = W_PROD + 1, W_MMA = W_ACT + 1;
+    static constexpr int W_PROD = EPI + CONV, W_ACT = W_PROD + 1, W_MMA = W_ACT + ACT;
     static constexpr int THREADS = (W_MMA + 1) * 32;
-    static constexpr uint32_t TM_A = 256;         // TMEM: accumulators below, A stages (64 columns each) above
-    static constexpr int W_OFF = I8_STAGES * 2 * BT;
-    static constexpr int BAR_OFF = W_OFF + WSTAGES * I8_WT;
+    static constexpr uint32_t TM_A = NACC * NM;   // TMEM: accumulators, then A stages (64 columns each)
+    static constexpr uint32_t TM_COLS = 512 / PER_SM;
+    static constexpr int W_OFF = STAGES * 2 * BT;
+    static constexpr int WT = (I8_ROWS + (DIRECT ? NT : 0)) * I8_UNIT;  // a unit's codes: weight rows, then (direct) tokens
+    static constexpr int BAR_OFF = W_OFF + WSTAGES * WT;
     static constexpr int RED_LD = I8_ROWS + 4;    // int32 per token of a parked split-K tile
-    static constexpr int BARS = 2 * I8_STAGES + 2 * WSTAGES + 5;
+    static constexpr int BARS = 2 * STAGES + 2 * WSTAGES + 5;
     static constexpr int DATA = BAR_OFF > NT * RED_LD * 4 ? BAR_OFF : NT * RED_LD * 4;
     static constexpr int TOTAL = ((DATA + 15) & ~15) + BARS * 8 + 16 + 1024;  // + slack to align the base
-    static_assert(TOTAL <= 227 * 1024, "shared memory");
-    static_assert(2 * NM <= (int)TM_A && TM_A + I8_STAGES * 64 <= 512, "TMEM");
-    static_assert(CONV % 4 == 0 && EPI % 4 == 0 && COLS % 8 == 0, "roles");
+    static_assert(TOTAL <= 227 * 1024 / PER_SM - (PER_SM > 1 ? 1024 : 0), "shared memory");
+    static_assert(TM_A + STAGES * 64 <= TM_COLS, "TMEM");
+    static_assert(EPI % 4 == 0 && COLS % 8 == 0, "roles");
 };
-using I8Pair = I8Cfg<2, 256, 16, 4, 4>;
-using I8One128 = I8Cfg<1, 128, 8, 8, 4>;
-using I8One64 = I8Cfg<1, 64, 4, 8, 6>;
-using I8One32 = I8Cfg<1, 32, 4, 8, 8>;
+using I8Pair = I8Cfg<2, 256, 16, 4, 4, 1>;
+using I8One128 = I8Cfg<1, 128, 8, 4, 5, 1>;
+using I8One64 = I8Cfg<1, 64, 8, 4, 6, 1>;
+using I8One32 = I8Cfg<1, 32, 4, 4, 9, 1>;
 
 struct I8TcParams {
     const float *sx, *sw, *bias;
@@ -76,20 +84,20 @@ struct I8TcParams {
 };
 
 // ---------------------------------------------------------------- cta_group forms
-template <int CG>
+template <int CG, uint32_t COLS>
 __device__ __forceinline__ void cg_alloc(uint32_t *dst) {
     if (CG == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "n"(COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     } else {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "n"(COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
 }
-template <int CG>
+template <int CG, uint32_t COLS>
 __device__ __forceinline__ void cg_dealloc(uint32_t taddr) {
-    if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
-    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+    if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(COLS) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(COLS) : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -180,7 +188,7 @@ __device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &
 }
 
 template <typename C, typename TY>
-__global__ void __launch_bounds__(C::THREADS, 1)
+__global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, I8TcParams P) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -188,8 +196,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + ((C::DATA + 15) & ~15));
     // k_full/k_empty: one unit's activation tiles and converted weights; k_full and acc_empty are waited on
     // in the pair's first CTA only, and every arrival goes there
-    uint64_t *k_full = bars, *k_empty = k_full + I8_STAGES;
-    uint64_t *w_full = k_empty + I8_STAGES, *w_empty = w_full + C::WSTAGES;
+    uint64_t *k_full = bars, *k_empty = k_full + C::STAGES;
+    uint64_t *w_full = k_empty + C::STAGES, *w_empty = w_full + C::WSTAGES;
     uint64_t *acc_full = w_empty + C::WSTAGES, *acc_empty = acc_full + 2, *mma_done = acc_empty + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -203,36 +211,51 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int tile0 = blockIdx.x / C::CG, tstride = gridDim.x / C::CG;
 
     if (tid == 0) {
-        for (int i = 0; i < I8_STAGES; ++i) { mbar_init(&k_full[i], 1 + C::CONV * C::CG); mbar_init(&k_empty[i], 1); }
-        for (int i = 0; i < C::WSTAGES; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_empty[i], C::CONV); }
+        for (int i = 0; i < C::STAGES; ++i) { mbar_init(&k_full[i], C::ACT + C::CONV * C::CG); mbar_init(&k_empty[i], 1); }
+        for (int i = 0; i < C::WSTAGES; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_empty[i], C::CONV + (C::DIRECT ? C::ACT : 0)); }
         for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], C::EPI / C::H * C::CG); }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == C::W_MMA) cg_alloc<C::CG>(tmem_holder);
+    if (warp == C::W_MMA) cg_alloc<C::CG, C::TM_COLS>(tmem_holder);
     if (warp == C::W_PROD && lane == 0) prefetch_tmap(&tmW);
     if (warp == C::W_ACT && lane == 0) prefetch_tmap(&tmX);
+    // the direct form's flag: an error is counted two seconds later at the earliest
+    if (C::DIRECT && tid == 0 && blockIdx.x == 0 && z == 0) *P.err = 0ull;
     tc_fence_before();
     __syncthreads();
-    cooperative_groups::this_cluster().sync();  // the pair's barriers are ready
+    if (C::CG > 1) cooperative_groups::this_cluster().sync();  // the pair's barriers are ready
     tc_fence_after();
-    // all 512 columns are this kernel's, so the allocation starts at column 0 of lane 0
-    constexpr uint32_t tbase = 0;
+    // in a uniform register (the reduction leaves it in one), which the MMAs take their operands from
+    const uint32_t tbase = C::PER_SM == 1 ? 0 : __reduce_or_sync(~0u, *tmem_holder);
     int acc[C::COLS];  // epilogue: this thread's sums, one weight row
 
     if (warp == C::W_PROD) {
         // ------------------------------------------------------------ weight tiles
         if (lane == 0) {
             bool ok = true;
-            int g = 0;
+            int g = 0, ahead = 0;
+            if (C::DIRECT) {
+                // the weights of the first units start before the codes, which the kernel before this one
+                // may still be writing
+                ahead = min(C::WSTAGES, nu);
+                for (int u = 0; u < ahead; ++u) {
+                    mbar_arrive_expect_tx(&w_full[u], C::WT);
+                    tma_load_2d(sW + u * C::WT, &tmW, &w_full[u], (u0 + u) * I8_UNIT, (tile0 % P.n_tiles) * I8_ROWS);
+                }
+                grid_dependency_wait();
+            }
             for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
                 const int n0 = (tile % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS;
                 for (int u = 0; u < nu; ++u, ++g) {
                     const int s = g % C::WSTAGES, ph = (g / C::WSTAGES) & 1;
-                    if (!(ok = mbar_wait_sleep(&w_empty[s], ph ^ 1, abort_flag, kI8WaitNs))) break;
-                    mbar_arrive_expect_tx(&w_full[s], I8_WT);
-                    tma_load_2d(sW + s * I8_WT, &tmW, &w_full[s], (u0 + u) * I8_UNIT, n0);
+                    if (g >= ahead) {
+                        if (!(ok = mbar_wait_sleep(&w_empty[s], ph ^ 1, abort_flag, kI8WaitNs))) break;
+                        mbar_arrive_expect_tx(&w_full[s], C::WT);
+                        tma_load_2d(sW + s * C::WT, &tmW, &w_full[s], (u0 + u) * I8_UNIT, n0);
+                    }
+                    if (C::DIRECT) tma_load_2d(sW + s * C::WT + I8_ROWS * I8_UNIT, &tmX, &w_full[s], (u0 + u) * I8_UNIT, 0);
                 }
             }
             // leaving early: the copies in flight land first (bounded)
@@ -242,8 +265,48 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (last >= 0) mbar_wait(&w_full[last % C::WSTAGES], (last / C::WSTAGES) & 1, &no_abort, 100000000ull);
             }
         }
-    } else if (warp == C::W_ACT) {
-        // ------------------------------------------------------------ activation tiles
+    } else if (C::DIRECT && warp >= C::W_ACT && warp < C::W_MMA) {
+        // ------------------------------------------------------------ activation tiles from int8 codes
+        // Eight lanes take a token's 128 codes of a unit, four tokens a pass, and write them as f16 in the
+        // 128-byte swizzle.  (Read from global memory here instead, under the weights' stream, a unit's codes
+        // took 3000 cycles to come.)
+        const int row0 = (warp - C::W_ACT) * 8 + (lane >> 3), c = lane & 7;
+        bool ok = true;
+        int g = 0;
+        for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
+            for (int u = 0; u < nu; ++u, ++g) {
+                const int s = g % C::STAGES, ws = g % C::WSTAGES;
+                if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, kI8WaitNs)))) break;
+                const uint8_t *xt = sW + ws * C::WT + I8_ROWS * I8_UNIT;
+                uint4 v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = row0 + 4 * i;
+                    v[i] = *reinterpret_cast<const uint4 *>(xt + row * I8_UNIT + ((c ^ (row & 7)) << 4));
+                }
+                if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / C::STAGES) & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
+                uint8_t *bt = sB + (2 * s + (c >> 2)) * C::BT;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = row0 + 4 * i, pc = 2 * (c & 3);
+                    uint4 a, b;
+                    i8x4_to_f16(v[i].x, a.x, a.y);
+                    i8x4_to_f16(v[i].y, a.z, a.w);
+                    i8x4_to_f16(v[i].z, b.x, b.y);
+                    i8x4_to_f16(v[i].w, b.z, b.w);
+                    *reinterpret_cast<uint4 *>(bt + row * 128 + ((pc ^ (row & 7)) << 4)) = a;
+                    *reinterpret_cast<uint4 *>(bt + row * 128 + (((pc + 1) ^ (row & 7)) << 4)) = b;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&k_full[s]);
+                    mbar_arrive(&w_empty[ws]);
+                }
+            }
+        }
+    } else if (!C::DIRECT && warp == C::W_ACT) {
+        // ------------------------------------------------------------ activation tiles from the panel
         if (lane == 0) {
             bool ok = true;
             int g = 0;
@@ -251,7 +314,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
                 const int m0 = (tile / P.n_tiles) * C::NT + r * (C::NT / C::CG);
                 for (int u = 0; u < nu; ++u, ++g) {
-                    const int s = g % I8_STAGES, ph = (g / I8_STAGES) & 1;
+                    const int s = g % C::STAGES, ph = (g / C::STAGES) & 1;
                     if (!(ok = mbar_wait_sleep(&k_empty[s], ph ^ 1, abort_flag, kI8WaitNs))) break;
                     const int x = (u0 + u) * I8_UNIT;
                     if (r == 0) mbar_arrive_expect_tx(&k_full[s], C::CG * 2 * C::BT);
@@ -289,22 +352,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int u = 0; u < un && ok; u += 2) {
                         const int kn = min(2, un - u);
                         for (int h = 0; h < C::H && ok; ++h) {
-                            const int buf = C::H == 2 ? h : job & 1;
-                            const uint32_t use = C::H == 2 ? job : job >> 1;
+                            const int buf = C::H == 2 ? h : job % C::NACC;
+                            const uint32_t use = C::H == 2 ? job : job / C::NACC;
                             if (u == 0) {
                                 if (!(ok = all_lanes(mbar_wait_sleep(&acc_empty[buf], (use & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
                                 tc_fence_after();
                             }
                             for (int k = 0; k < kn; ++k) {
-                                const int sk = (s + k) % I8_STAGES;
+                                const int sk = (s + k) % C::STAGES;
                                 if (h == 0) {
-                                    const uint32_t phk = s + k < I8_STAGES ? ph : ph ^ 1;
+                                    const uint32_t phk = s + k < C::STAGES ? ph : ph ^ 1;
                                     if (!(ok = all_lanes(mbar_wait_sleep(&k_full[sk], phk, abort_flag, kI8WaitNs)))) break;
                                     tc_fence_after();
                                 }
                                 const uint64_t b = dB + (uint64_t)(sk * (2 * C::BT >> 4)) + h * half_rows;
                                 if (one) {
-                                    cg_mma8<C::CG>(buf * C::NM, C::TM_A + sk * 64, b, b + (C::BT >> 4), idesc, u + k);
+                                    cg_mma8<C::CG>(tbase + buf * C::NM, tbase + C::TM_A + sk * 64, b, b + (C::BT >> 4), idesc, u + k);
                                     if (h == C::H - 1) cg_commit<C::CG>(&k_empty[sk], mask);
                                 }
                                 __syncwarp();
@@ -312,7 +375,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             if (ok && one && u + 2 >= un) cg_commit<C::CG>(&acc_full[buf], mask);
                         }
                         s += kn;
-                        if (s >= I8_STAGES) { s -= I8_STAGES; ph ^= 1; }
+                        if (s >= C::STAGES) { s -= C::STAGES; ph ^= 1; }
                     }
                 }
             }
@@ -324,9 +387,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
     } else if (warp >= C::EPI) {
         // ------------------------------------------------------------ weight converters
-        // A thread converts its row's codes of a unit; with eight warps, four take each half of the unit.
-        const int grp = (warp - C::EPI) >> 2, q = warp & 3, row = 32 * q + lane;
-        constexpr int GROUPS = C::CONV / 4;
+        // A thread converts its row's 128 codes of a unit, half of them at a time.
+        const int q = warp & 3, row = 32 * q + lane;
         const uint32_t ta = tbase + ((uint32_t)(32 * q) << 16) + C::TM_A;
         bool ok = true;
         int g = 0;  // units so far
@@ -334,11 +396,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int u = 0; u < nu && ok; ++u, ++g) {
                 const int ws = g % C::WSTAGES;
                 if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, kI8WaitNs)))) break;
-                const uint8_t *wr = sW + ws * I8_WT + row * I8_UNIT;
-                const int s = g % I8_STAGES;
+                const uint8_t *wr = sW + ws * C::WT + row * I8_UNIT;
+                const int s = g % C::STAGES;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if (GROUPS == 2 && j != grp) continue;
                     uint32_t o[32];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -349,8 +410,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         i8x4_to_f16(v.z, o[8 * i + 4], o[8 * i + 5]);
                         i8x4_to_f16(v.w, o[8 * i + 6], o[8 * i + 7]);
                     }
-                    if (j == 0 || GROUPS == 2) {
-                        if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / I8_STAGES) & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
+                    if (j == 0) {
+                        if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / C::STAGES) & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
                         tc_fence_after();
                     }
                     tmem_st32(ta + s * 64 + j * 32, o);
@@ -375,10 +436,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int tok0 = C::CG == 1 ? col0 : (col0 % C::NM) / (C::NM / 2) * (C::NT / 2) + h * (C::NM / 2) + col0 % (C::NM / 2);
         bool ok = true;
         int job = 0;
+        grid_dependency_wait();  // scales may be the output of the kernel before this one
         for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
+            // this tile's scales, on their way while it is computed: lane l keeps the tokens l, l + 32
+            const int n = (tile % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS + row;
+            const int m0 = (tile / P.n_tiles) * C::NT + tok0;
+            float sx[(C::COLS + 31) / 32];
+#pragma unroll
+            for (int j = 0; j < (C::COLS + 31) / 32; ++j) sx[j] = m0 + lane + 32 * j < P.M ? P.sx[m0 + lane + 32 * j] : 0.0f;
+            const float sw = n < P.N ? P.sw[n] : 0.0f, b = P.bias && n < P.N ? P.bias[n] : 0.0f;
             for (int c0 = 0; c0 < nu; c0 += I8_CHUNK, ++job) {
-                const int buf = C::H == 2 ? h : job & 1;
-                const uint32_t use = C::H == 2 ? job : job >> 1;
+                const int buf = C::H == 2 ? h : job % C::NACC;
+                const uint32_t use = C::H == 2 ? job : job / C::NACC;
                 if (!(ok = all_lanes(mbar_wait_sleep(&acc_full[buf], use & 1, abort_flag, kI8WaitNs)))) break;
                 tc_fence_after();
                 const uint32_t t = lane_base + (C::H == 2 ? col0 : buf * C::NM + col0);
@@ -398,20 +467,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
             }
             if (!ok || P.nsplit > 1) break;  // a split tile (one a cluster) is summed below
-            if (tile == tile0) grid_dependency_wait();  // scales may be the output of the kernel before this one
-            const int n = (tile % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS + row;
-            const int m0 = (tile / P.n_tiles) * C::NT + tok0;
-            if (n < P.N) {
-                const float sw = P.sw[n], b = P.bias ? P.bias[n] : 0.0f;
-                TY *y = static_cast<TY *>(P.y) + (int64_t)m0 * P.ldy + n;
+            TY *y = static_cast<TY *>(P.y) + (int64_t)m0 * P.ldy + n;
 #pragma unroll
-                for (int i = 0; i < C::COLS; ++i) {
-                    if (m0 + i < P.M) {
-                        float v = __fmul_rn(__fmul_rn((float)acc[i], P.sx[m0 + i]), sw);
-                        if (P.bias) v = __fadd_rn(v, b);
-                        y[(int64_t)i * P.ldy] = from_f32<TY>(v);
-                    }
-                }
+            for (int i = 0; i < C::COLS; ++i) {
+                float v = __fmul_rn(__fmul_rn((float)acc[i], __shfl_sync(~0u, sx[i / 32], i % 32)), sw);
+                if (P.bias) v = __fadd_rn(v, b);
+                if (n < P.N && m0 + i < P.M) *y = from_f32<TY>(v);
+                // one addition a token: left to itself the compiler multiplies 64 offsets out (3.8 us for 128
+                // tokens against 1.2)
+                y += P.ldy;
+                asm volatile("" : "+l"(y));
             }
         }
     }
@@ -426,33 +491,57 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < C::COLS; ++i) red[(col0 + i) * C::RED_LD + row] = acc[i];
         }
+        // four rows a thread, the same in every round, and all splits' loads at once
+        const int n = (tile0 % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS + lane * 4;
+        float sw[4], bias[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sw[j] = n + j < P.N ? P.sw[n + j] : 0.0f;
+            bias[j] = P.bias && n + j < P.N ? P.bias[n + j] : 0.0f;
+        }
         cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
         cluster.sync();
         grid_dependency_wait();
         const int per = (C::NT + P.nsplit - 1) / P.nsplit;
         const int c_end = min(C::NT, (z + 1) * per);
-        const int n0 = (tile0 % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS, m0 = (tile0 / P.n_tiles) * C::NT;
-        for (int i = tid; i < (c_end - z * per) * I8_ROWS; i += C::THREADS) {
-            const int c = z * per + i / I8_ROWS, row = i % I8_ROWS, hh = c / C::NM, cm = c % C::NM;
+        const int m0 = (tile0 / P.n_tiles) * C::NT;
+        const int *peer[I8_MAX_SPLIT];
+#pragma unroll
+        for (int k = 0; k < I8_MAX_SPLIT; ++k) peer[k] = cluster.map_shared_rank(red, min(k, P.nsplit - 1) * C::CG + r);
+        for (int c = z * per + warp; c < c_end; c += C::THREADS / 32) {
+            const int hh = c / C::NM, cm = c % C::NM;
             const int m = m0 + (C::CG == 1 ? c : cm / (C::NM / 2) * (C::NT / 2) + hh * (C::NM / 2) + cm % (C::NM / 2));
-            const int n = n0 + row;
-            if (m >= P.M || n >= P.N) continue;
-            int sum = 0;
-            for (int k = 0; k < P.nsplit; ++k) sum += cluster.map_shared_rank(red, k * C::CG + r)[c * C::RED_LD + row];
-            float v = __fmul_rn(__fmul_rn((float)sum, P.sx[m]), P.sw[n]);
-            if (P.bias) v = __fadd_rn(v, P.bias[n]);
-            static_cast<TY *>(P.y)[(int64_t)m * P.ldy + n] = from_f32<TY>(v);
+            if (m >= P.M) continue;
+            const float sx = P.sx[m];
+            int4 v[I8_MAX_SPLIT];
+#pragma unroll
+            for (int k = 0; k < I8_MAX_SPLIT; ++k)
+                v[k] = k < P.nsplit ? *reinterpret_cast<const int4 *>(peer[k] + c * C::RED_LD + lane * 4) : make_int4(0, 0, 0, 0);
+            int sum[4] = {};
+#pragma unroll
+            for (int k = 0; k < I8_MAX_SPLIT; ++k) {
+                sum[0] += v[k].x; sum[1] += v[k].y; sum[2] += v[k].z; sum[3] += v[k].w;
+            }
+            TY *y = static_cast<TY *>(P.y) + (int64_t)m * P.ldy + n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float f = __fmul_rn(__fmul_rn((float)sum[j], sx), sw[j]);
+                if (P.bias) f = __fadd_rn(f, bias[j]);
+                if (n + j < P.N) y[j] = from_f32<TY>(f);
+            }
         }
     }
     if (tid == 0 && *abort_flag) {
-        grid_dependency_wait();  // the kernel before this one clears the flag
+        grid_dependency_wait();  // the panel's kernel clears the flag
         atomicAdd(P.err, 1ull);
     }
     tc_fence_before();
-    cooperative_groups::this_cluster().sync();  // nobody still reads or signals the other CTA's memory
+    // nobody still reads or signals another CTA's memory
+    if (C::CG > 1 || P.nsplit > 1) cooperative_groups::this_cluster().sync();
+    else __syncthreads();
     if (warp == C::W_MMA) {
         tc_fence_after();
-        cg_dealloc<C::CG>(*tmem_holder);
+        cg_dealloc<C::CG, C::TM_COLS>(*tmem_holder);
     }
 }
 
@@ -527,7 +616,14 @@ static kq_status i8_launch(const char *fn, const I8TcArgs &a, int splits, cudaSt
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (e != CUDA_SUCCESS) return fail(KQ_ERR_CUDA, "%s: tensor map of w failed (%d)", fn, (int)e);
     }
-    {
+    if (C::DIRECT) {
+        const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)a.ldq};
+        const cuuint32_t box[2] = {I8_UNIT, C::NT};
+        const CUresult e = encode(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(a.q), dims, strides, box, es,
+                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (e != CUDA_SUCCESS) return fail(KQ_ERR_CUDA, "%s: tensor map of q failed (%d)", fn, (int)e);
+    } else {
         const cuuint64_t dims[2] = {(cuuint64_t)a.ldp, (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)a.ldp * 2};
         const cuuint32_t box[2] = {I8_KS, C::NT / C::CG};
         const CUresult e = encode(&tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half *>(a.panel), dims, strides, box,
@@ -560,22 +656,24 @@ static kq_status i8_launch(const char *fn, const I8TcArgs &a, int splits, cudaSt
     attr[0].val.clusterDim.x = C::CG;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = (unsigned)splits;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // starts beside the panel's kernel
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // starts beside the panel's or the quantizer's kernel
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = a.after_prologue ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, tmW, tmX, p);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
     count_launch(R_I8);
     return KQ_OK;
 }
 
-// Splits of K for `tiles` tiles of CG CTAs: doubled while the CTAs still fit the device at once and every
-// split keeps four units (512 elements).
-static int i8_splits(int64_t tiles, int cg, int64_t units) {
-    const int sms = i8_sms();
+// Splits of K for `tiles` tiles of CG CTAs, PER_SM of which share an SM: doubled while all CTAs still run
+// at once and every split keeps two units (256 elements).
+template <typename C>
+static int i8_splits(int64_t tiles, int64_t units) {
+    const int64_t room = (int64_t)i8_sms() * C::PER_SM;
     int s = 1;
-    while (s < 8 / cg && tiles * cg * s * 2 <= sms && units >= 4 * s * 2 && (units + 2 * s - 1) / (2 * s) * (2 * s - 1) < units) s *= 2;
+    while (s < I8_MAX_SPLIT / C::CG && tiles * C::CG * s * 2 <= room && units >= 2 * s * 2 && (units + 2 * s - 1) / (2 * s) * (2 * s - 1) < units)
+        s *= 2;
     return s;
 }
 
@@ -583,10 +681,10 @@ kq_status i8_tc_product(const char *fn, const I8TcArgs &a, cudaStream_t st) {
     return with_type(a.yt, [&](auto t) {
         using TY = decltype(t);
         const int64_t units = (a.K + I8_UNIT - 1) / I8_UNIT, rows = (a.N + 127) / 128;
-        if (a.M <= 32) return i8_launch<I8One32, TY>(fn, a, i8_splits(rows, 1, units), st);
-        if (a.M <= 64) return i8_launch<I8One64, TY>(fn, a, i8_splits(rows, 1, units), st);
-        if (a.M <= 128) return i8_launch<I8One128, TY>(fn, a, i8_splits(rows, 1, units), st);
-        return i8_launch<I8Pair, TY>(fn, a, i8_splits((rows + 1) / 2 * ((a.M + 255) / 256), 2, units), st);
+        if (a.M <= 32) return i8_launch<I8One32, TY>(fn, a, i8_splits<I8One32>(rows, units), st);
+        if (a.M <= 64) return i8_launch<I8One64, TY>(fn, a, i8_splits<I8One64>(rows, units), st);
+        if (a.M <= 128) return i8_launch<I8One128, TY>(fn, a, i8_splits<I8One128>(rows, units), st);
+        return i8_launch<I8Pair, TY>(fn, a, i8_splits<I8Pair>((rows + 1) / 2 * ((a.M + 255) / 256), units), st);
     });
 }
 

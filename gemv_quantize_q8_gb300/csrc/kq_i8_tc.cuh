@@ -4,9 +4,13 @@
 
 namespace kq {
 
-// One product over an f16 panel of activation codes (exact: |code| <= 128).
+// Tokens up to which the kernel takes int8 codes as they are; more come as an f16 panel.
+constexpr int kI8DirectTokens = 64;
+
 struct I8TcArgs {
-    const __half *panel;  // [M][ldp] codes as f16, ldp a multiple of 64, zeros from K to ldp
+    const int8_t *q;      // M <= kI8DirectTokens: codes [M][ldq], ldq a multiple of 16
+    int64_t ldq;
+    const __half *panel;  // M above that: codes as f16 [M][ldp], ldp a multiple of 64, zeros from K to ldp
     int64_t ldp;
     const float *sx;      // [M]
     const int8_t *w;      // [N][ldw]
@@ -16,7 +20,8 @@ struct I8TcArgs {
     kq_dtype yt;
     void *y;
     int64_t ldy;
-    unsigned long long *err;  // device flag, cleared by the kernel before this one
+    unsigned long long *err;  // device flag: cleared here (int8 codes) or by the panel's kernel
+    bool after_prologue;      // the kernel just before is this library's own (quantizer or panel): start beside it
 };
 kq_status i8_tc_product(const char *fn, const I8TcArgs &a, cudaStream_t st);
 
