@@ -55,15 +55,21 @@ __global__ void __launch_bounds__(256)
     if (i >= M * pieces) return;
     const int64_t m = i / pieces;
     const int k = (int)(i % pieces) * 16;
-    __half h[16];
-    uint4 v = make_uint4(0, 0, 0, 0);
+    uint4 v = make_uint4(0, 0, 0, 0), o[2];
     if (k < K) v = *reinterpret_cast<const uint4 *>(q + m * ldq + k);  // rows are 16-byte pieces up to ldq
-    const int8_t *c = reinterpret_cast<const int8_t *>(&v);
+    if (k + 16 > K && k < K) {  // the last piece's bytes past K are not codes
+        int8_t *c = reinterpret_cast<int8_t *>(&v);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) h[j] = __int2half_rn(k + j < K ? c[j] : 0);
-    uint4 *o = reinterpret_cast<uint4 *>(panel + m * ldp + k);
-    o[0] = reinterpret_cast<const uint4 *>(h)[0];
-    o[1] = reinterpret_cast<const uint4 *>(h)[1];
+        for (int j = 0; j < 16; ++j)
+            if (k + j >= K) c[j] = 0;
+    }
+    i8x4_to_f16(v.x, o[0].x, o[0].y);
+    i8x4_to_f16(v.y, o[0].z, o[0].w);
+    i8x4_to_f16(v.z, o[1].x, o[1].y);
+    i8x4_to_f16(v.w, o[1].z, o[1].w);
+    uint4 *dst = reinterpret_cast<uint4 *>(panel + m * ldp + k);
+    dst[0] = o[0];
+    dst[1] = o[1];
 }
 
 // ---------------------------------------------------------------- host

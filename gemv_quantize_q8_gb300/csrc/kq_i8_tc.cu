@@ -11,8 +11,8 @@
 // Large products: a pair of CTAs (cta_group::2) computes 256 rows x 256 tokens; each CTA converts its own
 // 128 rows and loads half of the tokens.  The accumulator's two 128-token halves are filled in turn, two
 // units (of 128 K) each, so that one half's chunk is read out while the other half computes.
-// Small products: one CTA, 128 rows x 32, 64 or 128 tokens, two CTAs an SM (one computes while the other
-// starts, ends or waits); up to 64 tokens are converted from int8 by the CTA itself, without a panel.
+// Small products: one CTA, up to 128 rows x 32, 64 or 128 tokens, two accumulators taking turns chunk by
+// chunk; up to 64 tokens are converted from int8 by the CTA itself, without a panel.
 // Few tiles split K over a cluster; its CTAs exchange their int32 sums through distributed shared memory,
 // which is exact in any order.
 //
@@ -31,33 +31,33 @@ namespace kq {
 
 using namespace sm100;
 
-constexpr int I8_ROWS = 128;      // weight rows per CTA
+constexpr int I8_ROWS = 128;      // weight rows of an MMA; a CTA's tile may have fewer
 constexpr int I8_KS = 64;         // K per activation tile (a 128-byte swizzled row of f16)
 constexpr int I8_UNIT = 128;      // K per unit: a weight tile, two activation tiles, one TMEM stage of A
 constexpr int I8_CHUNK = 8;       // units per chunk: 1024 elements, the longest exact fp32 accumulation
 constexpr int I8_MAX_SPLIT = 8;  // CTAs that share a tile's K (portable cluster size)
 constexpr unsigned long long kI8WaitNs = 2000000000ull;
 
-template <int CG_, int NT_, int EPI_, int STAGES_, int WSTAGES_, int PER_SM_>
+template <int CG_, int NT_, int EPI_, int CONV_, int STAGES_, int WSTAGES_>
 struct I8Cfg {
     static constexpr int CG = CG_;                // CTAs per tile
     static constexpr int NT = NT_;                // tokens per tile
     static constexpr int H = NT > 128 ? 2 : 1;    // halves of a tile's tokens, filled in turn
     static constexpr int NM = NT / H;             // N of one MMA
     static constexpr int NACC = 2;  // accumulators of NM columns
-    static constexpr int EPI = EPI_, CONV = 4;
+    static constexpr int EPI = EPI_, CONV = CONV_;
     static constexpr int COLS = NT / (EPI / 4);   // accumulator columns of an epilogue thread
     static constexpr int STAGES = STAGES_;        // units in flight (activation tiles and TMEM stages)
     static constexpr int WSTAGES = WSTAGES_;      // weight tiles in flight
-    static constexpr int PER_SM = PER_SM_;        // CTAs of an SM
     // Up to 64 tokens: no f16 panel; ACT warps turn int8 codes into the B tiles themselves
     static constexpr bool DIRECT = NT <= kI8DirectTokens;
-    static constexpr int ACT = DIRECT ? NT / 8 : 1;  // eight tokens a warp: with 32 it was the slowest role, 0.58 us a unit
+    static constexpr int ACT = DIRECT ? NT / 8 : 1;
+    static constexpr int GROUPS = CONV / 4;       // converters (and ACT warps) in groups that take units in turn
+    static constexpr int ACT_G = DIRECT ? ACT / GROUPS : 1, ACT_TOK = NT / ACT_G;  // ACT warps of a unit, tokens of one
     static constexpr int BT = NT / CG * I8_KS * 2;  // activation tile bytes of one CTA (two tiles a unit)
     static constexpr int W_PROD = EPI + CONV, W_ACT = W_PROD + 1, W_MMA = W_ACT + ACT;
     static constexpr int THREADS = (W_MMA + 1) * 32;
     static constexpr uint32_t TM_A = NACC * NM;   // TMEM: accumulators, then A stages (64 columns each)
-    static constexpr uint32_t TM_COLS = 512 / PER_SM;
     static constexpr int W_OFF = STAGES * 2 * BT;
     static constexpr int WT = (I8_ROWS + (DIRECT ? NT : 0)) * I8_UNIT;  // a unit's codes: weight rows, then (direct) tokens
     static constexpr int BAR_OFF = W_OFF + WSTAGES * WT;
@@ -65,39 +65,40 @@ struct I8Cfg {
     static constexpr int BARS = 2 * STAGES + 2 * WSTAGES + 5;
     static constexpr int DATA = BAR_OFF > NT * RED_LD * 4 ? BAR_OFF : NT * RED_LD * 4;
     static constexpr int TOTAL = ((DATA + 15) & ~15) + BARS * 8 + 16 + 1024;  // + slack to align the base
-    static_assert(TOTAL <= 227 * 1024 / PER_SM - (PER_SM > 1 ? 1024 : 0), "shared memory");
-    static_assert(TM_A + STAGES * 64 <= TM_COLS, "TMEM");
-    static_assert(EPI % 4 == 0 && COLS % 8 == 0, "roles");
+    static_assert(TOTAL <= 227 * 1024, "shared memory");
+    static_assert(TM_A + STAGES * 64 <= 512, "TMEM");
+    static_assert(EPI % 4 == 0 && (CONV == 4 || CONV == 8) && COLS % 8 == 0, "roles");
 };
-using I8Pair = I8Cfg<2, 256, 16, 4, 4, 1>;
-using I8One128 = I8Cfg<1, 128, 8, 4, 5, 1>;
-using I8One64 = I8Cfg<1, 64, 8, 4, 6, 1>;
-using I8One32 = I8Cfg<1, 32, 4, 4, 9, 1>;
+using I8Pair = I8Cfg<2, 256, 16, 4, 4, 4>;
+using I8One128 = I8Cfg<1, 128, 8, 8, 4, 5>;
+using I8One64 = I8Cfg<1, 64, 8, 8, 4, 6>;
+using I8One32 = I8Cfg<1, 32, 4, 8, 4, 9>;
 
 struct I8TcParams {
     const float *sx, *sw, *bias;
     void *y;
     int64_t ldy;
     int M, N, n_tiles, tiles;
+    int rows;                            // weight rows of a CTA's tile, a multiple of 8 up to I8_ROWS
     int units, units_per_split, nsplit;  // K in units of 128
     unsigned long long *err;
 };
 
 // ---------------------------------------------------------------- cta_group forms
-template <int CG, uint32_t COLS>
+template <int CG>
 __device__ __forceinline__ void cg_alloc(uint32_t *dst) {
     if (CG == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "n"(COLS) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     } else {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "n"(COLS) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
 }
-template <int CG, uint32_t COLS>
+template <int CG>
 __device__ __forceinline__ void cg_dealloc(uint32_t taddr) {
-    if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(COLS) : "memory");
-    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(COLS) : "memory");
+    if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -175,20 +176,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
 // A wait that a whole warp makes succeeds for all its lanes or for none, so that the warp stays together.
 __device__ __forceinline__ bool all_lanes(bool ok) { return __all_sync(~0u, ok); }
 
-// Four codes to four f16: the byte under a 0x64 high byte is 1024 + byte, so with the sign bit flipped
-// (0x6400 | (c ^ 0x80)) = 1152 + c, and one subtraction gives c exactly.
-__device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-    w ^= 0x80808080u;
-    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), bias);
-    lo = *reinterpret_cast<const uint32_t *>(&x);
-    hi = *reinterpret_cast<const uint32_t *>(&y);
-}
-
 template <typename C, typename TY>
-__global__ void __launch_bounds__(C::THREADS, C::PER_SM)
+__global__ void __launch_bounds__(C::THREADS, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, I8TcParams P) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -211,14 +200,14 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     const int tile0 = blockIdx.x / C::CG, tstride = gridDim.x / C::CG;
 
     if (tid == 0) {
-        for (int i = 0; i < C::STAGES; ++i) { mbar_init(&k_full[i], C::ACT + C::CONV * C::CG); mbar_init(&k_empty[i], 1); }
-        for (int i = 0; i < C::WSTAGES; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_empty[i], C::CONV + (C::DIRECT ? C::ACT : 0)); }
+        for (int i = 0; i < C::STAGES; ++i) { mbar_init(&k_full[i], C::ACT_G + 4 * C::CG); mbar_init(&k_empty[i], 1); }
+        for (int i = 0; i < C::WSTAGES; ++i) { mbar_init(&w_full[i], 1); mbar_init(&w_empty[i], 4 + (C::DIRECT ? C::ACT_G : 0)); }
         for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], C::EPI / C::H * C::CG); }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == C::W_MMA) cg_alloc<C::CG, C::TM_COLS>(tmem_holder);
+    if (warp == C::W_MMA) cg_alloc<C::CG>(tmem_holder);
     if (warp == C::W_PROD && lane == 0) prefetch_tmap(&tmW);
     if (warp == C::W_ACT && lane == 0) prefetch_tmap(&tmX);
     // the direct form's flag: an error is counted two seconds later at the earliest
@@ -227,8 +216,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     __syncthreads();
     if (C::CG > 1) cooperative_groups::this_cluster().sync();  // the pair's barriers are ready
     tc_fence_after();
-    // in a uniform register (the reduction leaves it in one), which the MMAs take their operands from
-    const uint32_t tbase = C::PER_SM == 1 ? 0 : __reduce_or_sync(~0u, *tmem_holder);
+    // all 512 columns are this kernel's, so the allocation starts at column 0 of lane 0
+    constexpr uint32_t tbase = 0;
     int acc[C::COLS];  // epilogue: this thread's sums, one weight row
 
     if (warp == C::W_PROD) {
@@ -236,26 +225,38 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         if (lane == 0) {
             bool ok = true;
             int g = 0, ahead = 0;
+            const uint32_t unit_bytes = (P.rows + (C::DIRECT ? C::NT : 0)) * I8_UNIT;
             if (C::DIRECT) {
                 // the weights of the first units start before the codes, which the kernel before this one
                 // may still be writing
                 ahead = min(C::WSTAGES, nu);
                 for (int u = 0; u < ahead; ++u) {
-                    mbar_arrive_expect_tx(&w_full[u], C::WT);
-                    tma_load_2d(sW + u * C::WT, &tmW, &w_full[u], (u0 + u) * I8_UNIT, (tile0 % P.n_tiles) * I8_ROWS);
+                    mbar_arrive_expect_tx(&w_full[u], unit_bytes);
+                    tma_load_2d(sW + u * C::WT, &tmW, &w_full[u], (u0 + u) * I8_UNIT, (tile0 % P.n_tiles) * P.rows);
                 }
                 grid_dependency_wait();
             }
             for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
-                const int n0 = (tile % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS;
-                for (int u = 0; u < nu; ++u, ++g) {
-                    const int s = g % C::WSTAGES, ph = (g / C::WSTAGES) & 1;
-                    if (g >= ahead) {
-                        if (!(ok = mbar_wait_sleep(&w_empty[s], ph ^ 1, abort_flag, kI8WaitNs))) break;
-                        mbar_arrive_expect_tx(&w_full[s], C::WT);
-                        tma_load_2d(sW + s * C::WT, &tmW, &w_full[s], (u0 + u) * I8_UNIT, n0);
+                const int n0 = (tile % P.n_tiles) * (P.rows * C::CG) + r * P.rows;
+                // two neighbouring units at a time: 256 consecutive bytes of every row, which device memory
+                // gives faster than 128 (4.7 against 4.1 TB/s, copies alone)
+                for (int u = 0; u < nu && ok; u += 2) {
+                    const int kn = min(2, nu - u);
+                    for (int k = 0; k < kn && ok; ++k) {
+                        const int gk = g + k;
+                        if (gk >= ahead)
+                            ok = mbar_wait_sleep(&w_empty[gk % C::WSTAGES], ((gk / C::WSTAGES) & 1) ^ 1, abort_flag, kI8WaitNs);
                     }
-                    if (C::DIRECT) tma_load_2d(sW + s * C::WT + I8_ROWS * I8_UNIT, &tmX, &w_full[s], (u0 + u) * I8_UNIT, 0);
+                    if (!ok) break;
+                    for (int k = 0; k < kn; ++k) {
+                        const int s = (g + k) % C::WSTAGES, x = (u0 + u + k) * I8_UNIT;
+                        if (g + k >= ahead) {
+                            mbar_arrive_expect_tx(&w_full[s], unit_bytes);
+                            tma_load_2d(sW + s * C::WT, &tmW, &w_full[s], x, n0);
+                        }
+                        if (C::DIRECT) tma_load_2d(sW + s * C::WT + I8_ROWS * I8_UNIT, &tmX, &w_full[s], x, 0);
+                    }
+                    g += kn;
                 }
             }
             // leaving early: the copies in flight land first (bounded)
@@ -270,24 +271,27 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         // Eight lanes take a token's 128 codes of a unit, four tokens a pass, and write them as f16 in the
         // 128-byte swizzle.  (Read from global memory here instead, under the weights' stream, a unit's codes
         // took 3000 cycles to come.)
-        const int row0 = (warp - C::W_ACT) * 8 + (lane >> 3), c = lane & 7;
+        const int aw = warp - C::W_ACT, grp = aw / C::ACT_G;
+        const int row0 = aw % C::ACT_G * C::ACT_TOK + (lane >> 3), c = lane & 7;
+        constexpr int PASSES = C::ACT_TOK / 4;
         bool ok = true;
         int g = 0;
         for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
             for (int u = 0; u < nu; ++u, ++g) {
+                if (g % C::GROUPS != grp) continue;
                 const int s = g % C::STAGES, ws = g % C::WSTAGES;
                 if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, kI8WaitNs)))) break;
                 const uint8_t *xt = sW + ws * C::WT + I8_ROWS * I8_UNIT;
-                uint4 v[2];
+                uint4 v[PASSES];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < PASSES; ++i) {
                     const int row = row0 + 4 * i;
                     v[i] = *reinterpret_cast<const uint4 *>(xt + row * I8_UNIT + ((c ^ (row & 7)) << 4));
                 }
                 if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / C::STAGES) & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
                 uint8_t *bt = sB + (2 * s + (c >> 2)) * C::BT;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < PASSES; ++i) {
                     const int row = row0 + 4 * i, pc = 2 * (c & 3);
                     uint4 a, b;
                     i8x4_to_f16(v[i].x, a.x, a.y);
@@ -387,36 +391,38 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         }
     } else if (warp >= C::EPI) {
         // ------------------------------------------------------------ weight converters
-        // A thread converts its row's 128 codes of a unit, half of them at a time.
-        const int q = warp & 3, row = 32 * q + lane;
+        // A thread converts its row's 128 codes of a unit; all eight loads go out before the first conversion.
+        // With eight warps, four take every other unit: a unit's barriers and latencies cost a warp more
+        // than its conversions do.
+        const int q = warp & 3, row = 32 * q + lane, grp = (warp - C::EPI) >> 2;
         const uint32_t ta = tbase + ((uint32_t)(32 * q) << 16) + C::TM_A;
         bool ok = true;
         int g = 0;  // units so far
         for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
             for (int u = 0; u < nu && ok; ++u, ++g) {
-                const int ws = g % C::WSTAGES;
+                if (g % C::GROUPS != grp) continue;
+                const int ws = g % C::WSTAGES, s = g % C::STAGES;
                 if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, kI8WaitNs)))) break;
+                // 16-byte piece p of row `row` sits at piece p ^ (row & 7) (128-byte swizzle); rows past the
+                // tile's hold whatever was there: they end in lanes that nobody reads
                 const uint8_t *wr = sW + ws * C::WT + row * I8_UNIT;
-                const int s = g % C::STAGES;
+                uint4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4 *>(wr + ((i ^ (row & 7)) << 4));
+                if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / C::STAGES) & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
+                tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     uint32_t o[32];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        // 16-byte piece p of row `row` sits at piece p ^ (row & 7) (128-byte swizzle)
-                        const uint4 v = *reinterpret_cast<const uint4 *>(wr + (((4 * j + i) ^ (row & 7)) << 4));
-                        i8x4_to_f16(v.x, o[8 * i], o[8 * i + 1]);
-                        i8x4_to_f16(v.y, o[8 * i + 2], o[8 * i + 3]);
-                        i8x4_to_f16(v.z, o[8 * i + 4], o[8 * i + 5]);
-                        i8x4_to_f16(v.w, o[8 * i + 6], o[8 * i + 7]);
-                    }
-                    if (j == 0) {
-                        if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / C::STAGES) & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
-                        tc_fence_after();
+                        i8x4_to_f16(v[4 * j + i].x, o[8 * i], o[8 * i + 1]);
+                        i8x4_to_f16(v[4 * j + i].y, o[8 * i + 2], o[8 * i + 3]);
+                        i8x4_to_f16(v[4 * j + i].z, o[8 * i + 4], o[8 * i + 5]);
+                        i8x4_to_f16(v[4 * j + i].w, o[8 * i + 6], o[8 * i + 7]);
                     }
                     tmem_st32(ta + s * 64 + j * 32, o);
                 }
-                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -439,12 +445,13 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         grid_dependency_wait();  // scales may be the output of the kernel before this one
         for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
             // this tile's scales, on their way while it is computed: lane l keeps the tokens l, l + 32
-            const int n = (tile % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS + row;
+            const int n = (tile % P.n_tiles) * (P.rows * C::CG) + r * P.rows + row;
             const int m0 = (tile / P.n_tiles) * C::NT + tok0;
             float sx[(C::COLS + 31) / 32];
 #pragma unroll
             for (int j = 0; j < (C::COLS + 31) / 32; ++j) sx[j] = m0 + lane + 32 * j < P.M ? P.sx[m0 + lane + 32 * j] : 0.0f;
-            const float sw = n < P.N ? P.sw[n] : 0.0f, b = P.bias && n < P.N ? P.bias[n] : 0.0f;
+            const bool mine = row < P.rows && n < P.N;
+            const float sw = mine ? P.sw[n] : 0.0f, b = P.bias && mine ? P.bias[n] : 0.0f;
             for (int c0 = 0; c0 < nu; c0 += I8_CHUNK, ++job) {
                 const int buf = C::H == 2 ? h : job % C::NACC;
                 const uint32_t use = C::H == 2 ? job : job / C::NACC;
@@ -472,7 +479,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
             for (int i = 0; i < C::COLS; ++i) {
                 float v = __fmul_rn(__fmul_rn((float)acc[i], __shfl_sync(~0u, sx[i / 32], i % 32)), sw);
                 if (P.bias) v = __fadd_rn(v, b);
-                if (n < P.N && m0 + i < P.M) *y = from_f32<TY>(v);
+                if (mine && m0 + i < P.M) *y = from_f32<TY>(v);
                 // one addition a token: left to itself the compiler multiplies 64 offsets out (3.8 us for 128
                 // tokens against 1.2)
                 y += P.ldy;
@@ -492,7 +499,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
             for (int i = 0; i < C::COLS; ++i) red[(col0 + i) * C::RED_LD + row] = acc[i];
         }
         // four rows a thread, the same in every round, and all splits' loads at once
-        const int n = (tile0 % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS + lane * 4;
+        const int n = (tile0 % P.n_tiles) * (P.rows * C::CG) + r * P.rows + lane * 4;
         float sw[4], bias[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -527,7 +534,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
             for (int j = 0; j < 4; ++j) {
                 float f = __fmul_rn(__fmul_rn((float)sum[j], sx), sw[j]);
                 if (P.bias) f = __fadd_rn(f, bias[j]);
-                if (n + j < P.N) y[j] = from_f32<TY>(f);
+                if (lane * 4 < P.rows && n + j < P.N) y[j] = from_f32<TY>(f);
             }
         }
     }
@@ -541,7 +548,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     else __syncthreads();
     if (warp == C::W_MMA) {
         tc_fence_after();
-        cg_dealloc<C::CG, C::TM_COLS>(*tmem_holder);
+        cg_dealloc<C::CG>(*tmem_holder);
     }
 }
 
@@ -560,57 +567,51 @@ static PFN_cuTensorMapEncodeTiled_v12000 i8_encoder() {
     return fn;
 }
 
-static int i8_sms() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        n <= 0) {
-        cudaGetLastError();
-        n = 152;
-    }
-    return n;
-}
-
-// Tiles (groups of CG CTAs) of this form that the current device holds at once.  Looked up once a device.
+// Clusters of CG x 1 x splits CTAs of this form that the current device holds at once (clusters fill a GPC
+// only in whole multiples of their size).  Looked up once a device and split.
 template <typename C>
-static int i8_resident() {
-    static int cache[64] = {};
+static int i8_resident(int splits) {
+    static int cache[64][4] = {};
+    const int si = splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3;
+    const int fallback = 8 * (19 / (C::CG * splits));
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         cudaGetLastError();
-        return i8_sms() / C::CG;
+        return fallback;
     }
-    if (!cache[dev]) {
+    if (!cache[dev][si]) {
         auto kern = i8_tc_kernel<C, float>;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(C::CG);
+        cfg.gridDim = dim3(C::CG, 1, splits);
         cfg.blockDim = dim3(C::THREADS);
         cfg.dynamicSmemBytes = C::TOTAL;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = C::CG;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = splits;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
             cudaGetLastError();
-            n = i8_sms() / C::CG;
+            n = fallback;
         }
-        cache[dev] = n;
+        cache[dev][si] = n;
     }
-    return cache[dev];
+    return cache[dev][si];
 }
 
 template <typename C, typename TY>
-static kq_status i8_launch(const char *fn, const I8TcArgs &a, int splits, cudaStream_t st) {
+static kq_status i8_launch(const char *fn, const I8TcArgs &a, int rows, int splits, cudaStream_t st) {
     auto encode = i8_encoder();
     if (!encode) return fail(KQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", fn);
     CUtensorMap tmW, tmX;
     const cuuint32_t es[2] = {1, 1};
     {
         const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.N}, strides[1] = {(cuuint64_t)a.ldw};
-        const cuuint32_t box[2] = {I8_UNIT, I8_ROWS};
+        const cuuint32_t box[2] = {I8_UNIT, (cuuint32_t)rows};
         const CUresult e = encode(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(a.w), dims, strides, box, es,
                                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -634,7 +635,8 @@ static kq_status i8_launch(const char *fn, const I8TcArgs &a, int splits, cudaSt
     I8TcParams p{};
     p.sx = a.sx; p.sw = a.sw; p.bias = a.bias; p.y = a.y; p.ldy = a.ldy;
     p.M = (int)a.M; p.N = (int)a.N;
-    p.n_tiles = (int)((a.N + I8_ROWS * C::CG - 1) / (I8_ROWS * C::CG));
+    p.rows = rows;
+    p.n_tiles = (int)((a.N + rows * C::CG - 1) / (rows * C::CG));
     const int64_t tiles = (int64_t)p.n_tiles * ((a.M + C::NT - 1) / C::NT);
     if (tiles > 0x7fffffff / C::CG) return fail(KQ_ERR_INVALID_ARG, "%s: too many tiles", fn);
     p.tiles = (int)tiles;
@@ -646,7 +648,7 @@ static kq_status i8_launch(const char *fn, const I8TcArgs &a, int splits, cudaSt
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
-    const int64_t groups = splits > 1 ? tiles : std::min<int64_t>(tiles, i8_resident<C>());
+    const int64_t groups = splits > 1 ? tiles : std::min<int64_t>(tiles, i8_resident<C>(1));
     cfg.gridDim = dim3((unsigned)(groups * C::CG), 1, (unsigned)splits);
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::TOTAL;
@@ -666,25 +668,54 @@ static kq_status i8_launch(const char *fn, const I8TcArgs &a, int splits, cudaSt
     return KQ_OK;
 }
 
-// Splits of K for `tiles` tiles of CG CTAs, PER_SM of which share an SM: doubled while all CTAs still run
-// at once and every split keeps two units (256 elements).
-template <typename C>
-static int i8_splits(int64_t tiles, int64_t units) {
-    const int64_t room = (int64_t)i8_sms() * C::PER_SM;
+// Splits of K for `tiles` pair tiles: doubled while all CTAs still run at once and every split keeps two
+// units (256 elements).
+static int i8_pair_splits(int64_t tiles, int64_t units) {
     int s = 1;
-    while (s < I8_MAX_SPLIT / C::CG && tiles * C::CG * s * 2 <= room && units >= 2 * s * 2 && (units + 2 * s - 1) / (2 * s) * (2 * s - 1) < units)
+    while (s < I8_MAX_SPLIT / 2 && tiles <= i8_resident<I8Pair>(2 * s) && units >= 2 * s * 2 && (units + 2 * s - 1) / (2 * s) * (2 * s - 1) < units)
         s *= 2;
     return s;
+}
+
+// Up to 128 tokens the weights' bytes bound the product, and an SM reads some 38 GB/s of them when all do;
+// so a tile's rows and the split of K are chosen to give every SM the same share: for each split the rows
+// that spread N over all SMs (an MMA computes 128 rows whether they are there or not), and of the splits
+// the one with the least estimated time.  A unit takes its bytes at that rate but 0.25 us at least (the
+// converters), a split's reduction 3 us.  [14336 x 4096], 64 tokens: 112 tiles of 128 rows took 23.6 us,
+// 150 of 96 rows 16.9; [4096 x 4096], 16 tokens: four splits of 37 tiles 8.0, unsplit 10.4.
+template <typename C>
+static void i8_share(int64_t N, int64_t units, int &rows, int &splits) {
+    double best = 1e30;
+    for (int s = 1; s <= I8_MAX_SPLIT; s *= 2) {
+        const int64_t per = (units + s - 1) / s;
+        if (s > 1 && (per < 2 || per * (s - 1) >= units)) break;
+        const int64_t groups = i8_resident<C>(s);
+        const int64_t r = std::min<int64_t>(I8_ROWS, ((N + groups - 1) / groups + 7) / 8 * 8);
+        const int64_t waves = ((N + r - 1) / r + groups - 1) / groups;
+        const double t = (double)(waves * per) * std::max(0.25, (double)r * I8_UNIT / 38e3) + (s > 1 ? 3.0 : 0.0);
+        if (t < best) {
+            best = t;
+            rows = (int)r;
+            splits = s;
+        }
+    }
 }
 
 kq_status i8_tc_product(const char *fn, const I8TcArgs &a, cudaStream_t st) {
     return with_type(a.yt, [&](auto t) {
         using TY = decltype(t);
-        const int64_t units = (a.K + I8_UNIT - 1) / I8_UNIT, rows = (a.N + 127) / 128;
-        if (a.M <= 32) return i8_launch<I8One32, TY>(fn, a, i8_splits<I8One32>(rows, units), st);
-        if (a.M <= 64) return i8_launch<I8One64, TY>(fn, a, i8_splits<I8One64>(rows, units), st);
-        if (a.M <= 128) return i8_launch<I8One128, TY>(fn, a, i8_splits<I8One128>(rows, units), st);
-        return i8_launch<I8Pair, TY>(fn, a, i8_splits<I8Pair>((rows + 1) / 2 * ((a.M + 255) / 256), units), st);
+        const int64_t units = (a.K + I8_UNIT - 1) / I8_UNIT;
+        if (a.M > 128) {
+            const int64_t tiles = (a.N + 2 * I8_ROWS - 1) / (2 * I8_ROWS) * ((a.M + 255) / 256);
+            return i8_launch<I8Pair, TY>(fn, a, I8_ROWS, i8_pair_splits(tiles, units), st);
+        }
+        int rows = I8_ROWS, splits = 1;
+        auto shared = [&](auto c) {
+            using C = decltype(c);
+            i8_share<C>(a.N, units, rows, splits);
+            return i8_launch<C, TY>(fn, a, rows, splits, st);
+        };
+        return a.M <= 32 ? shared(I8One32{}) : a.M <= 64 ? shared(I8One64{}) : shared(I8One128{});
     });
 }
 

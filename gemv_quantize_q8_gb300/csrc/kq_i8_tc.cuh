@@ -7,6 +7,18 @@ namespace kq {
 // Tokens up to which the kernel takes int8 codes as they are; more come as an f16 panel.
 constexpr int kI8DirectTokens = 64;
 
+// Four codes to four f16.  A byte under a 0x64 high byte is the f16 1024 + byte, so with the sign bit
+// flipped it is 1152 + c, and one subtraction gives c exactly.
+__device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    w ^= 0x80808080u;
+    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
 struct I8TcArgs {
     const int8_t *q;      // M <= kI8DirectTokens: codes [M][ldq], ldq a multiple of 16
     int64_t ldq;
