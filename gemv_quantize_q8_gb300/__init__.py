@@ -88,6 +88,8 @@ _SIGS = {
 def lib():
     """The loaded CUDA library (ctypes handle).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -110,11 +112,20 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = _device = None
+
+
 def _stream(stream) -> int | None:
+    """The stream's handle; None: the current torch stream (read without building a Stream object: 0.3 us for 3)."""
+    global _raw_stream, _device
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        import torch
+        _device = torch.cuda.current_device
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(_device())
 
 
 def _check(status: int) -> None:

@@ -1,4 +1,22 @@
-// kq_logprobs.cu -- log probabilities of given tokens, with the entropy and the top alternatives of a row.
+// kq_logprobs.cu -- log probabilities of given tokens, with the entropy and the top alternatives of a row,
+// in one pass over the logits.
+//
+// Bound by the logits' bytes.  Every thread keeps a running maximum m and, relative to it,
+//   S = sum 2^d,  T = sum 2^d * d,   d = max((x - m) * log2 e, -200)
+// over batches of 16 elements: a batch's own maximum is taken first, and only when it is above m are S and T
+// brought to the new one:  S' = f S,  T' = f (T + delta S),  delta = (m - m') log2 e,  f = 2^delta.  Threads,
+// and the CTAs of a cluster that share a row when there are few rows, are joined the same way.  Then
+//   log Z = m + ln S,   entropy = ln S - (T / S) ln 2.
+// (The bound -200 stands for -inf: 2^-200 is 0 in fp32, and 0 * -200 is, unlike 0 * -inf, 0.)
+//
+// Alternatives: a thread also keeps its largest logit.  The k-th largest of 32 such maxima (eight threads
+// each) is reached by k elements at least, and by few more (31 expected for k = 20, 130 for 32); so when the row has been read, only the threads whose
+// maximum reaches it look through their own elements again, and of those only the batches that reached the
+// same bound of the first round (a bit each).  What they find goes to a buffer in shared memory; should it
+// overflow (a sorted row, a row of equals), its k-th best becomes the bound and they look again.  Order and
+// ties are one 64-bit number: the logit in order-preserving bits, then the inverted id.  Masked tokens (-inf)
+// and NaN are never candidates; a row with fewer than k others takes the first of them at the end.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "kq_value.cuh"
@@ -7,77 +25,368 @@ namespace kq {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpMaxTop = 32;
+constexpr int kLpBatch = 16;                        // elements of a thread's batch
+constexpr int kLpRound = kLpThreads * kLpBatch;     // elements of the block's
+constexpr int kLpCap = 2048;                        // candidates that the buffer holds
+constexpr int kLpFew = 256;                         // candidates that are ranked without a filter
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f, kLowest = -3.4028234663852886e38f;
 
-// The order of the alternatives as one unsigned number: larger logits first, then lower ids.  NaN ranks
-// with -inf, -0 with +0.
+// NaN ranks with -inf, -0 with +0.
 __device__ __forceinline__ uint64_t lp_key(float x, int id) {
     if (isnan(x)) x = -INFINITY;
     uint32_t b = __float_as_uint(x + 0.0f);
     b = (b & 0x80000000u) ? ~b : b | 0x80000000u;
     return ((uint64_t)b << 32) | (uint32_t)~id;
 }
-
-template <typename V, typename F>
-__device__ V lp_block(V v, V *red, F f) {
-#pragma unroll
-    for (int s = 16; s; s >>= 1) v = f(v, __shfl_xor_sync(~0u, v, s));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-    for (int i = 1; i < kLpThreads / 32; ++i) v = f(v, red[i]);
-    return v;
+__device__ __forceinline__ int lp_key_id(uint64_t k) { return (int)~(uint32_t)k; }
+__device__ __forceinline__ float lp_key_value(uint64_t k) {
+    const uint32_t b = (uint32_t)(k >> 32);
+    return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
 }
 
-// One block per row.
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads)
-    lp_kernel(const T *__restrict__ x, int64_t ldx, int V, const int32_t *__restrict__ targets, int n_targets,
-              float *__restrict__ logprob, float *__restrict__ entropy, int top_k, int32_t *__restrict__ top_ids,
-              float *__restrict__ top_logprob) {
-    __shared__ uint64_t red[kLpThreads / 32];
-    const int64_t row = blockIdx.x;
-    const T *xr = x + row * ldx;
-    auto add = [](float a, float b) { return a + b; };
-    auto larger = [](uint64_t a, uint64_t b) { return a > b ? a : b; };
-    float m = -INFINITY, bad = 0.0f;
-    for (int i = threadIdx.x; i < V; i += kLpThreads) {
-        const float v = to_f32(xr[i]);
-        m = fmaxf(m, v);
-        if (isnan(v) || v == INFINITY) bad = 1.0f;
-    }
-    m = lp_block(m, reinterpret_cast<float *>(red), [](float a, float b) { return fmaxf(a, b); });
-    bad = lp_block(bad, reinterpret_cast<float *>(red), add);
-    float S = 0.0f, U = 0.0f;
-    for (int i = threadIdx.x; i < V && m > -INFINITY; i += kLpThreads) {
-        const float d = to_f32(xr[i]) - m, e = expf(d);
-        S += e;
-        if (e > 0.0f) U += e * d;
-    }
-    S = lp_block(S, reinterpret_cast<float *>(red), add);
-    U = lp_block(U, reinterpret_cast<float *>(red), add);
-    const bool empty = m == -INFINITY;
-    const float logS = logf(S);
-    auto lp_of = [&](float v) { return bad > 0.0f ? NAN : empty ? -INFINITY : (v - m) - logS; };
-    if (threadIdx.x == 0 && entropy) entropy[row] = bad > 0.0f ? NAN : empty ? 0.0f : logS - U / S;
-    for (int j = threadIdx.x; j < n_targets; j += kLpThreads) {
-        const int t = targets[row * n_targets + j];
-        logprob[row * n_targets + j] = t < 0 ? 0.0f : t >= V ? NAN : lp_of(to_f32(xr[t]));
-    }
-    uint64_t last = ~0ull;
-    for (int j = 0; j < top_k; ++j) {
-        uint64_t best = 0;
-        for (int i = threadIdx.x; i < V; i += kLpThreads) {
-            const uint64_t key = lp_key(to_f32(xr[i]), i);
-            if (key < last && key > best) best = key;
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
+struct LpStats {
+    float m, S, T, bad;  // bad != 0: a NaN was seen
+};
+__device__ __forceinline__ void lp_raise(LpStats &s, float m) {
+    const float delta = fmaxf((s.m - m) * kLog2e, -200.0f), f = exp2_fast(delta);
+    s.T = f * (s.T + delta * s.S);
+    s.S *= f;
+    s.m = m;
+}
+__device__ __forceinline__ LpStats lp_join(LpStats a, LpStats b) {
+    const float m = fmaxf(a.m, b.m);
+    if (a.m < m) lp_raise(a, m);
+    if (b.m < m) lp_raise(b, m);
+    return {m, a.S + b.S, a.T + b.T, a.bad + b.bad};
+}
+
+struct LpShared {
+    LpStats warp[kLpThreads / 32], row;
+    __align__(16) float part[32];
+    uint64_t best[kLpMaxTop];
+    int count;
+};
+
+// The k best of the buffer's n candidates to sh.best, best first (0 where there are fewer).  All threads.
+__device__ __noinline__ void lp_cut(uint64_t *buf, int n, int k, LpShared &sh) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (n > kLpFew) {
+        // drop those below the k-th largest of 32 maxima over disjoint parts: k of them reach it
+        uint64_t top = 0;
+        for (int i = tid; i < n; i += kLpThreads) top = buf[i] > top ? buf[i] : top;
+#pragma unroll
+        for (int s = 1; s < 8; s *= 2) {
+            const uint64_t o = __shfl_xor_sync(~0u, top, s);
+            top = o > top ? o : top;
         }
-        last = lp_block(best, red, larger);
-        if (threadIdx.x == 0) {
-            const int id = (int)~(uint32_t)last;
-            top_ids[row * top_k + j] = id;
-            top_logprob[row * top_k + j] = lp_of(to_f32(xr[id]));
+        if ((tid & 7) == 0) sh.best[tid >> 3] = top;
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+        const uint64_t mine = sh.best[tid & 31];
+        int rank = 0;
+        for (int i = 0; i < 32; ++i) {
+            const uint64_t o = __shfl_sync(~0u, mine, i);
+            rank += o > mine || (o == mine && i < (tid & 31));
+        }
+        const uint64_t least = __shfl_sync(~0u, mine, __ffs(__ballot_sync(~0u, rank == k - 1)) - 1);
+        // in place: what a piece of the buffer keeps fits where that piece and those before it were
+        for (int i0 = 0; i0 < n; i0 += kLpThreads) {
+            const uint64_t key = i0 + tid < n ? buf[i0 + tid] : 0;
+            const bool stays = key && key >= least;
+            __syncthreads();
+            const unsigned votes = __ballot_sync(~0u, stays);
+            int at = 0;
+            if ((tid & 31) == 0 && votes) at = atomicAdd(&sh.count, __popc(votes));
+            at = __shfl_sync(~0u, at, 0) + __popc(votes & ((1u << (tid & 31)) - 1u));
+            if (stays) buf[at] = key;
+        }
+        __syncthreads();
+        n = sh.count;
+    }
+    if (tid < kLpMaxTop) sh.best[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kLpThreads) {
+        const uint64_t key = buf[i];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) rank += buf[j] > key;
+        if (rank < k) sh.best[rank] = key;
+    }
+    __syncthreads();
+}
+
+struct LpParams {
+    const void *x;
+    int64_t ldx;
+    int V;
+    const int32_t *targets;
+    int n_targets;
+    float *logprob, *entropy;
+    int top_k;
+    int32_t *top_ids;
+    float *top_logprob;
+    int64_t row0;
+};
+
+// The k-th largest of 32 maxima of the block's values, eight threads each.  All threads.
+__device__ __forceinline__ float lp_kth(float v, int k, LpShared &sh) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int s = 1; s < 8; s *= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, s));
+    __syncthreads();
+    if ((threadIdx.x & 7) == 0) sh.part[threadIdx.x >> 3] = v;
+    __syncthreads();
+    v = sh.part[lane];
+    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const float4 o = *reinterpret_cast<const float4 *>(sh.part + i);
+        rank += (o.x > v || (o.x == v && i < lane)) + (o.y > v || (o.y == v && i + 1 < lane)) +
+                (o.z > v || (o.z == v && i + 2 < lane)) + (o.w > v || (o.w == v && i + 3 < lane));
+    }
+    return __shfl_sync(~0u, v, __ffs(__ballot_sync(~0u, rank == k - 1)) - 1);
+}
+
+// One cluster (gridDim.x CTAs, one or more) a row; blockIdx.y the row.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
+    constexpr int VEC = kVec<T>, NV = kLpBatch / VEC;
+    extern __shared__ uint64_t buf[];  // TOP: kLpCap candidates
+    __shared__ LpShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, part = blockIdx.x, parts = gridDim.x;
+    const int64_t row = P.row0 + blockIdx.y;
+    const T *x = static_cast<const T *>(P.x) + row * P.ldx;
+    const int V = P.V, k = P.top_k;
+    const float none = -INFINITY;
+    // vectors from the first 16-byte boundary on; the few elements before and after them go separately
+    const int head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T));
+    const int nvec = (V - head) / VEC, rest = V - nvec * VEC;
+    const int v0 = (int)((int64_t)nvec * part / parts), v1 = (int)((int64_t)nvec * (part + 1) / parts);
+
+    LpStats st = {kLowest, 0.0f, 0.0f, 0.0f};
+    float2 S2 = make_float2(0.0f, 0.0f), T2 = S2;
+    // The statistics of a batch; returns its maximum (-inf for nothing but NaN and -inf).
+    auto count_in = [&](const float (&v)[kLpBatch]) {
+        float top = v[0];
+#pragma unroll
+        for (int i = 1; i < kLpBatch; ++i) top = max_nan(top, v[i]);
+        if (!(top <= st.m)) {
+            if (isnan(top)) {
+                st.bad = 1.0f;
+                top = none;
+#pragma unroll
+                for (int i = 0; i < kLpBatch; ++i) top = fmaxf(top, v[i]);
+            }
+            if (top > st.m) {
+                st.S = S2.x + S2.y;
+                st.T = T2.x + T2.y;
+                lp_raise(st, top);
+                S2 = make_float2(st.S, 0.0f);
+                T2 = make_float2(st.T, 0.0f);
+            }
+        }
+        const float2 minus = make_float2(-st.m, -st.m), l2e = make_float2(kLog2e, kLog2e);
+#pragma unroll
+        for (int i = 0; i < kLpBatch; i += 2) {
+            float2 d = mul2(add2(make_float2(v[i], v[i + 1]), minus), l2e);
+            d.x = fmaxf(d.x, -200.0f);
+            d.y = fmaxf(d.y, -200.0f);
+            const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+            S2 = add2(S2, e);
+            T2 = fma2(e, d, T2);
+        }
+        return top;
+    };
+
+    const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
+    uint4 next[NV];
+    auto fetch = [&](int v) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            if (v + u * kLpThreads < v1) next[u] = TOP ? __ldg(xv + v + u * kLpThreads) : __ldcs(xv + v + u * kLpThreads);
+    };
+    const int rounds = (v1 - v0 + NV * kLpThreads - 1) / (NV * kLpThreads);
+    int shift = 0;  // rounds of one bit of `worth`
+    while ((rounds - 1) >> shift >= 32) ++shift;
+    float largest = none, bound = none;
+    uint32_t worth = 0;  // rounds (in groups) in which this thread's batch reached the bound
+    fetch(v0 + tid);
+    for (int j = 0; j < rounds; ++j) {
+        const int at = v0 + tid + j * NV * kLpThreads;
+        float v[kLpBatch];
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            float f[VEC];
+            unpack16<T>(next[u], f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[u * VEC + i] = at + u * kLpThreads < v1 ? f[i] : none;
+        }
+        fetch(at + NV * kLpThreads);
+        const float top = count_in(v);
+        if (TOP) {
+            largest = fmaxf(largest, top);
+            if (top >= bound) worth |= 1u << (j >> shift);
+            if (j == 0 && rounds > 1) bound = lp_kth(largest, k, sh);
         }
     }
+    const int odd_id = part == 0 && tid < rest ? (tid < head ? tid : nvec * VEC + tid) : -1;
+    float odd = none;  // elements before the first vector and after the last: one a thread
+    if (part == 0 && rest) {
+        float v[kLpBatch];
+#pragma unroll
+        for (int i = 0; i < kLpBatch; ++i) v[i] = none;
+        if (odd_id >= 0) v[0] = odd = to_f32(x[odd_id]);
+        largest = fmaxf(largest, count_in(v));
+    }
+    if (TOP) {
+        float least_value = fmaxf(lp_kth(largest, k, sh), kLowest);  // never -inf
+        uint64_t least = lp_key(least_value, -1);                    // the lowest key of that value
+        for (;;) {
+            if (tid == 0) sh.count = 0;
+            __syncthreads();
+            auto put = [&](float v, int id) {
+                if (!(v >= least_value)) return;
+                const uint64_t key = lp_key(v, id);
+                if (key < least) return;
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kLpCap) buf[at] = key;
+            };
+            // The warp looks through one such thread's batches at a time, lane i through the i-th bit's: their
+            // loads are then under way together (a thread by itself waited for each: 295 us for 157).
+            for (unsigned who = __ballot_sync(~0u, largest >= least_value); who; who &= who - 1) {
+                const int owner = __ffs(who) - 1;
+                const bool mine = __shfl_sync(~0u, worth, owner) >> lane & 1;
+                if (__any_sync(~0u, *reinterpret_cast<volatile int *>(&sh.count) > kLpCap)) break;
+                for (int j = lane << shift; mine && j < min(rounds, (lane + 1) << shift); ++j) {
+                    uint4 w[NV];
+                    const int at = v0 + (tid - lane + owner) + j * NV * kLpThreads;
+#pragma unroll
+                    for (int u = 0; u < NV; ++u) w[u] = __ldg(xv + min(at + u * kLpThreads, v1 - 1));
+#pragma unroll
+                    for (int u = 0; u < NV; ++u) {
+                        if (at + u * kLpThreads >= v1) break;
+                        float f[VEC];
+                        unpack16<T>(w[u], f);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) put(f[i], head + (at + u * kLpThreads) * VEC + i);
+                    }
+                }
+            }
+            if (odd_id >= 0) put(odd, odd_id);
+            __syncthreads();
+            const int n = sh.count;
+            lp_cut(buf, min(n, kLpCap), k, sh);
+            if (n <= kLpCap) break;
+            least = sh.best[k - 1];
+            least_value = lp_key_value(least);
+            __syncthreads();
+        }
+    }
+
+    // the threads' statistics, then (several CTAs a row) the cluster's, and its candidates
+    st.S = S2.x + S2.y;
+    st.T = T2.x + T2.y;
+#pragma unroll
+    for (int s = 16; s; s >>= 1)
+        st = lp_join(st, {__shfl_xor_sync(~0u, st.m, s), __shfl_xor_sync(~0u, st.S, s), __shfl_xor_sync(~0u, st.T, s),
+                          __shfl_xor_sync(~0u, st.bad, s)});
+    if (lane == 0) sh.warp[tid >> 5] = st;
+    __syncthreads();
+    st = sh.warp[lane % (kLpThreads / 32)];
+#pragma unroll
+    for (int s = kLpThreads / 64; s; s >>= 1)
+        st = lp_join(st, {__shfl_xor_sync(~0u, st.m, s), __shfl_xor_sync(~0u, st.S, s), __shfl_xor_sync(~0u, st.T, s),
+                          __shfl_xor_sync(~0u, st.bad, s)});
+    if (parts > 1) {
+        namespace cg = cooperative_groups;
+        cg::cluster_group cluster = cg::this_cluster();
+        if (tid == 0) sh.row = st;
+        cluster.sync();
+        if (part == 0) {
+            for (int i = 1; i < parts; ++i) st = lp_join(st, cluster.map_shared_rank(&sh, i)->row);
+            if (TOP) {
+                const int n = parts * k;  // at most 8 * 32
+                if (tid < n) buf[tid] = cluster.map_shared_rank(&sh, tid / k)->best[tid % k];
+            }
+        }
+        cluster.sync();
+        if (part) return;
+        if (TOP) lp_cut(buf, parts * k, k, sh);
+    }
+
+    const bool bad = st.bad != 0.0f || st.m == INFINITY, empty = st.S == 0.0f;
+    const float logS = logf(st.S);
+    auto lp_of = [&](float v) { return bad ? NAN : empty ? -INFINITY : (v - st.m) - logS; };
+    if (tid == 0 && P.entropy) P.entropy[row] = bad ? NAN : empty ? 0.0f : logS - st.T / st.S * kLn2;
+    for (int j = tid; j < P.n_targets; j += kLpThreads) {
+        const int t = P.targets[row * P.n_targets + j];
+        P.logprob[row * P.n_targets + j] = t < 0 ? 0.0f : t >= V ? NAN : lp_of(to_f32(x[t]));
+    }
+    if (TOP && !sh.best[k - 1]) {
+        // fewer than k tokens are neither masked nor NaN: the first of those fill up, in the order of their ids
+        if (tid < 32) {
+            int n = __popc(__ballot_sync(~0u, sh.best[lane] != 0));
+            for (int i = 0; i < V && n < k; i += 32) {
+                const float v = i + lane < V ? to_f32(x[i + lane]) : 0.0f;
+                const bool low = isnan(v) || v == none;
+                const unsigned votes = __ballot_sync(~0u, low);
+                const int at = n + __popc(votes & ((1u << lane) - 1u));
+                if (low && at < k) sh.best[at] = lp_key(none, i + lane);
+                n += __popc(votes);
+            }
+        }
+        __syncthreads();
+    }
+    if (TOP && tid < k) {
+        const uint64_t key = sh.best[tid];
+        P.top_ids[row * k + tid] = lp_key_id(key);
+        P.top_logprob[row * k + tid] = lp_of(lp_key_value(key));
+    }
+}
+
+template <typename T, bool TOP>
+static kq_status launch_lp(const char *fn, LpParams P, int64_t M, cudaStream_t st) {
+    constexpr int smem = TOP ? kLpCap * 8 : 0;
+    auto kern = lp_kernel<T, TOP>;
+    cudaError_t e = smem ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
+    // CTAs that share a row: doubled while all still run at once (five an SM) and each
+    // has a whole round of its own
+    int parts = 1;
+    while (parts < 8 && M * parts * 2 <= 152 * 5 && P.V >= parts * 2 * kLpRound) parts *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)parts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = parts > 1 ? 1 : 0;
+    for (int64_t r = 0; e == cudaSuccess && r < M; r += 65535) {  // the grid's second dimension ends there
+        P.row0 = r;
+        cfg.gridDim = dim3((unsigned)parts, (unsigned)(M - r < 65535 ? M - r : 65535));
+        e = cudaLaunchKernelEx(&cfg, kern, P);
+        if (e == cudaSuccess) count_launch(R_LOGPROBS);
+    }
+    return e == cudaSuccess ? KQ_OK : fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
 }
 
 }  // namespace kq
@@ -102,13 +411,9 @@ extern "C" kq_status kq_logprobs(kq_dtype xt, const void *logits, int64_t ldx, i
     if (!aligned(logits, value_bytes(xt)) || (n_targets && (!aligned(targets, 4) || !aligned(logprob, 4))) ||
         (entropy && !aligned(entropy, 4)) || (top_k && (!aligned(top_ids, 4) || !aligned(top_logprob, 4))))
         return fail(KQ_ERR_ALIGNMENT, "%s: a pointer is not aligned to its elements", fn);
+    const LpParams P{logits, ldx, (int)V, targets, (int)n_targets, logprob, entropy, (int)top_k, top_ids, top_logprob, 0};
     return with_type(xt, [&](auto t) {
         using T = decltype(t);
-        lp_kernel<T><<<(unsigned)M, kLpThreads, 0, (cudaStream_t)stream>>>(
-            static_cast<const T *>(logits), ldx, (int)V, targets, (int)n_targets, logprob, entropy, (int)top_k, top_ids,
-            top_logprob);
-        kq_status s = check_launch(fn);
-        if (s == KQ_OK) count_launch(R_LOGPROBS);
-        return s;
+        return top_k ? launch_lp<T, true>(fn, P, M, (cudaStream_t)stream) : launch_lp<T, false>(fn, P, M, (cudaStream_t)stream);
     });
 }
