@@ -11,8 +11,8 @@
 //
 // Alternatives: a thread also keeps its largest logit.  The k-th largest of 32 such maxima (eight threads
 // each) is reached by k elements at least, and by few more (31 expected for k = 20, 130 for 32); so when the row has been read, only the threads whose
-// maximum reaches it look through their own elements again, and of those only the batches that reached the
-// same bound of the first round (a bit each).  What they find goes to a buffer in shared memory; should it
+// maximum reaches it name the batches to look through again: those that reached the same bound of the first
+// round (a bit each).  What is found there goes to a buffer in shared memory; should it
 // overflow (a sorted row, a row of equals), its k-th best becomes the bound and they look again.  Order and
 // ties are one 64-bit number: the logit in order-preserving bits, then the inverted id.  Masked tokens (-inf)
 // and NaN are never candidates; a row with fewer than k others takes the first of them at the end.
@@ -25,8 +25,9 @@ namespace kq {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpMaxTop = 32;
-constexpr int kLpBatch = 16;                        // elements of a thread's batch
-constexpr int kLpRound = kLpThreads * kLpBatch;     // elements of the block's
+constexpr int kLpBatch = 16;                        // elements whose maximum a thread takes at once
+constexpr int kLpVecs = 4;                          // 16-byte vectors of a thread in a round: 64 bytes under way
+constexpr int kLpMaxParts = 8;                      // CTAs that share a row (portable cluster size)
 constexpr int kLpCap = 2048;                        // candidates that the buffer holds
 constexpr int kLpFew = 256;                         // candidates that are ranked without a filter
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f, kLowest = -3.4028234663852886e38f;
@@ -80,7 +81,7 @@ struct LpShared {
     LpStats warp[kLpThreads / 32], row;
     __align__(16) float part[32];
     uint64_t best[kLpMaxTop];
-    int count;
+    int count, items;
 };
 
 // The k best of the buffer's n candidates to sh.best, best first (0 where there are fewer).  All threads.
@@ -167,8 +168,9 @@ __device__ __forceinline__ float lp_kth(float v, int k, LpShared &sh) {
 // One cluster (gridDim.x CTAs, one or more) a row; blockIdx.y the row.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
-    constexpr int VEC = kVec<T>, NV = kLpBatch / VEC;
-    extern __shared__ uint64_t buf[];  // TOP: kLpCap candidates
+    constexpr int VEC = kVec<T>, NV = kLpVecs, NB = kLpBatch / VEC;  // NB: vectors of a batch
+    extern __shared__ uint64_t buf[];  // TOP: kLpCap candidates, then the list of batches
+    uint16_t *list = reinterpret_cast<uint16_t *>(buf + kLpCap);
     __shared__ LpShared sh;
     const int tid = threadIdx.x, lane = tid & 31, part = blockIdx.x, parts = gridDim.x;
     const int64_t row = P.row0 + blockIdx.y;
@@ -217,9 +219,9 @@ __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
 
     const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
     uint4 next[NV];
-    auto fetch = [&](int v) {
+    auto fetch = [&](int u0, int v) {  // vectors u0 .. u0 + NB - 1 of the round at v
 #pragma unroll
-        for (int u = 0; u < NV; ++u)
+        for (int u = u0; u < u0 + NB; ++u)
             if (v + u * kLpThreads < v1) next[u] = TOP ? __ldg(xv + v + u * kLpThreads) : __ldcs(xv + v + u * kLpThreads);
     };
     const int rounds = (v1 - v0 + NV * kLpThreads - 1) / (NV * kLpThreads);
@@ -227,19 +229,24 @@ __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
     while ((rounds - 1) >> shift >= 32) ++shift;
     float largest = none, bound = none;
     uint32_t worth = 0;  // rounds (in groups) in which this thread's batch reached the bound
-    fetch(v0 + tid);
+#pragma unroll
+    for (int u0 = 0; u0 < NV; u0 += NB) fetch(u0, v0 + tid);
     for (int j = 0; j < rounds; ++j) {
         const int at = v0 + tid + j * NV * kLpThreads;
-        float v[kLpBatch];
+        float top = none;
 #pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            float f[VEC];
-            unpack16<T>(next[u], f);
+        for (int u0 = 0; u0 < NV; u0 += NB) {
+            float v[kLpBatch];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[u * VEC + i] = at + u * kLpThreads < v1 ? f[i] : none;
+            for (int u = 0; u < NB; ++u) {
+                float f[VEC];
+                unpack16<T>(next[u0 + u], f);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[u * VEC + i] = at + (u0 + u) * kLpThreads < v1 ? f[i] : none;
+            }
+            fetch(u0, at + NV * kLpThreads);
+            top = fmaxf(top, count_in(v));
         }
-        fetch(at + NV * kLpThreads);
-        const float top = count_in(v);
         if (TOP) {
             largest = fmaxf(largest, top);
             if (top >= bound) worth |= 1u << (j >> shift);
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
         float least_value = fmaxf(lp_kth(largest, k, sh), kLowest);  // never -inf
         uint64_t least = lp_key(least_value, -1);                    // the lowest key of that value
         for (;;) {
-            if (tid == 0) sh.count = 0;
+            if (tid == 0) sh.count = sh.items = 0;
             __syncthreads();
             auto put = [&](float v, int id) {
                 if (!(v >= least_value)) return;
@@ -268,25 +275,23 @@ __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
                 const int at = atomicAdd(&sh.count, 1);
                 if (at < kLpCap) buf[at] = key;
             };
-            // The warp looks through one such thread's batches at a time, lane i through the i-th bit's: their
-            // loads are then under way together (a thread by itself waited for each: 295 us for 157).
-            for (unsigned who = __ballot_sync(~0u, largest >= least_value); who; who &= who - 1) {
-                const int owner = __ffs(who) - 1;
-                const bool mine = __shfl_sync(~0u, worth, owner) >> lane & 1;
-                if (__any_sync(~0u, *reinterpret_cast<volatile int *>(&sh.count) > kLpCap)) break;
-                for (int j = lane << shift; mine && j < min(rounds, (lane + 1) << shift); ++j) {
-                    uint4 w[NV];
-                    const int at = v0 + (tid - lane + owner) + j * NV * kLpThreads;
+            // The batches to look through go on a list, so that all threads share their loads (by the thread that
+            // found them, one after the other, they took longer than the row: 295 us for 157 + 42).
+            if (largest >= least_value) {
+                int at = atomicAdd(&sh.items, __popc(worth));
+                for (uint32_t w = worth; w; w &= w - 1) list[at++] = (uint16_t)(tid * 32 + __ffs(w) - 1);
+            }
+            __syncthreads();
+            const int vectors = sh.items * NV;
+            for (int i = tid; i < vectors; i += kLpThreads) {
+                const int item = list[i / NV], bit = item & 31;
+                for (int j = bit << shift; j < min(rounds, (bit + 1) << shift); ++j) {
+                    const int at = v0 + (item >> 5) + (j * NV + i % NV) * kLpThreads;
+                    if (at >= v1 || *reinterpret_cast<volatile int *>(&sh.count) > kLpCap) break;
+                    float f[VEC];
+                    unpack16<T>(__ldg(xv + at), f);
 #pragma unroll
-                    for (int u = 0; u < NV; ++u) w[u] = __ldg(xv + min(at + u * kLpThreads, v1 - 1));
-#pragma unroll
-                    for (int u = 0; u < NV; ++u) {
-                        if (at + u * kLpThreads >= v1) break;
-                        float f[VEC];
-                        unpack16<T>(w[u], f);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) put(f[i], head + (at + u * kLpThreads) * VEC + i);
-                    }
+                    for (int e = 0; e < VEC; ++e) put(f[e], head + at * VEC + e);
                 }
             }
             if (odd_id >= 0) put(odd, odd_id);
@@ -321,14 +326,26 @@ __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
         cluster.sync();
         if (part == 0) {
             for (int i = 1; i < parts; ++i) st = lp_join(st, cluster.map_shared_rank(&sh, i)->row);
-            if (TOP) {
-                const int n = parts * k;  // at most 8 * 32
-                if (tid < n) buf[tid] = cluster.map_shared_rank(&sh, tid / k)->best[tid % k];
-            }
+            if (TOP && tid < parts * k) buf[tid] = cluster.map_shared_rank(&sh, tid / k)->best[tid % k];  // at most 8 * 32
         }
         cluster.sync();
         if (part) return;
-        if (TOP) lp_cut(buf, parts * k, k, sh);
+        if (TOP) {
+            // an element's place in the merged lists: what precedes it in each (their empty ends are zeros)
+            const uint64_t key = tid < parts * k ? buf[tid] : 0;
+            int lo[kLpMaxParts] = {}, place = 0;  // the searches go side by side: their loads overlap
+#pragma unroll
+            for (int step = 32; step; step >>= 1)
+#pragma unroll
+                for (int i = 0; i < kLpMaxParts; ++i)
+                    if (i < parts && lo[i] + step <= k && buf[i * k + lo[i] + step - 1] > key) lo[i] += step;
+#pragma unroll
+            for (int i = 0; i < kLpMaxParts; ++i) place += lo[i];
+            if (tid < kLpMaxTop) sh.best[tid] = 0;
+            __syncthreads();
+            if (key && place < k) sh.best[place] = key;
+            __syncthreads();
+        }
     }
 
     const bool bad = st.bad != 0.0f || st.m == INFINITY, empty = st.S == 0.0f;
@@ -363,13 +380,13 @@ __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
 
 template <typename T, bool TOP>
 static kq_status launch_lp(const char *fn, LpParams P, int64_t M, cudaStream_t st) {
-    constexpr int smem = TOP ? kLpCap * 8 : 0;
+    constexpr int smem = TOP ? kLpCap * 8 + kLpThreads * 32 * 2 : 0;
     auto kern = lp_kernel<T, TOP>;
     cudaError_t e = smem ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
     // CTAs that share a row: doubled while all still run at once (five an SM) and each
     // has a whole round of its own
     int parts = 1;
-    while (parts < 8 && M * parts * 2 <= 152 * 5 && P.V >= parts * 2 * kLpRound) parts *= 2;
+    while (parts < kLpMaxParts && M * parts * 2 <= 152 * 5 && P.V >= parts * 2 * kLpThreads * kLpVecs * kVec<T>) parts *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kLpThreads);
     cfg.dynamicSmemBytes = smem;
