@@ -9,8 +9,9 @@
 //   * activations come as an f16 panel (written once by a prologue), by TMA, as the B operand.
 //   * outputs: weight rows = TMEM lanes, tokens = columns.
 // Large products: a pair of CTAs (cta_group::2) computes 256 rows x 256 tokens; each CTA converts its own
-// 128 rows and loads half of the tokens.  The accumulator's two 128-token halves are filled in turn, two
-// units (of 128 K) each, so that one half's chunk is read out while the other half computes.
+// 128 rows and loads half of the tokens.  The accumulator's two 128-token halves are filled in turn, four
+// units (of 128 K) each, so that one half's chunk is read out (1 us) while the other half computes (1.2 us;
+// with two units each it waited 0.8 us a chunk).
 // Small products: one CTA, up to 128 rows x 32, 64 or 128 tokens, two accumulators taking turns chunk by
 // chunk; up to 64 tokens are converted from int8 by the CTA itself, without a panel.
 // Few tiles split K over a cluster; its CTAs exchange their int32 sums through distributed shared memory,
@@ -352,9 +353,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
                 for (int c0 = 0; c0 < nu && ok; c0 += I8_CHUNK, ++job) {
                     const int un = min(I8_CHUNK, nu - c0);
-                    // two units at a time: the first half's MMAs over both, then the second half's
-                    for (int u = 0; u < un && ok; u += 2) {
-                        const int kn = min(2, un - u);
+                    // all stages at a time: the first half's MMAs over them, then the second half's, which free
+                    // them one by one
+                    for (int u = 0; u < un && ok; u += C::STAGES) {
+                        const int kn = min(C::STAGES, un - u);
                         for (int h = 0; h < C::H && ok; ++h) {
                             const int buf = C::H == 2 ? h : job % C::NACC;
                             const uint32_t use = C::H == 2 ? job : job / C::NACC;
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 }
                                 __syncwarp();
                             }
-                            if (ok && one && u + 2 >= un) cg_commit<C::CG>(&acc_full[buf], mask);
+                            if (ok && one && u + C::STAGES >= un) cg_commit<C::CG>(&acc_full[buf], mask);
                         }
                         s += kn;
                         if (s >= C::STAGES) { s -= C::STAGES; ph ^= 1; }
