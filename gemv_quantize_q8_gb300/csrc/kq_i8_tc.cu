@@ -670,54 +670,52 @@ static kq_status i8_launch(const char *fn, const I8TcArgs &a, int rows, int spli
     return KQ_OK;
 }
 
-// Splits of K for `tiles` pair tiles: doubled while all CTAs still run at once and every split keeps two
-// units (256 elements).
-static int i8_pair_splits(int64_t tiles, int64_t units) {
-    int s = 1;
-    while (s < I8_MAX_SPLIT / 2 && tiles <= i8_resident<I8Pair>(2 * s) && units >= 2 * s * 2 && (units + 2 * s - 1) / (2 * s) * (2 * s - 1) < units)
-        s *= 2;
-    return s;
-}
+// How a product is shared out: weight rows of a CTA's tile, splits of K, and the time that the estimate below
+// gives it (us): the CTAs of a wave walk `per` units at `unit` each, 4 us go to starting and ending, a split
+// adds its reduction.
+struct I8Plan {
+    int rows, splits;
+    double t;
+};
 
-// Up to 128 tokens the weights' bytes bound the product, and an SM reads some 38 GB/s of them when all do;
-// so a tile's rows and the split of K are chosen to give every SM the same share: for each split the rows
-// that spread N over all SMs (an MMA computes 128 rows whether they are there or not), and of the splits
-// the one with the least estimated time.  A unit takes its bytes at that rate but 0.25 us at least (the
-// converters), a split's reduction 3 us.  [14336 x 4096], 64 tokens: 112 tiles of 128 rows took 23.6 us,
-// 150 of 96 rows 16.9; [4096 x 4096], 16 tokens: four splits of 37 tiles 8.0, unsplit 10.4.
+// The best plan of form C.  `unit`: measured time of a 128-row unit.  Up to 128 tokens the weights' bytes bound
+// the product, and an SM reads some 38 GB/s of them when all do; so (`spread`) a tile's rows are chosen to give
+// every SM the same share (an MMA computes 128 rows whether they are there or not).
 template <typename C>
-static void i8_share(int64_t N, int64_t units, int &rows, int &splits) {
-    double best = 1e30;
-    for (int s = 1; s <= I8_MAX_SPLIT; s *= 2) {
+static I8Plan i8_plan(int64_t M, int64_t N, int64_t units, double unit, double reduction, bool spread) {
+    I8Plan best = {I8_ROWS, 1, 1e30};
+    const int64_t m_tiles = (M + C::NT - 1) / C::NT;
+    for (int s = 1; s <= I8_MAX_SPLIT / C::CG; s *= 2) {
         const int64_t per = (units + s - 1) / s;
         if (s > 1 && (per < 2 || per * (s - 1) >= units)) break;
         const int64_t groups = i8_resident<C>(s);
-        const int64_t r = std::min<int64_t>(I8_ROWS, ((N + groups - 1) / groups + 7) / 8 * 8);
-        const int64_t waves = ((N + r - 1) / r + groups - 1) / groups;
-        const double t = (double)(waves * per) * std::max(0.25, (double)r * I8_UNIT / 38e3) + (s > 1 ? 3.0 : 0.0);
-        if (t < best) {
-            best = t;
-            rows = (int)r;
-            splits = s;
-        }
+        int64_t rows = I8_ROWS;
+        if (spread) rows = std::min<int64_t>(I8_ROWS, ((N + groups - 1) / groups + 7) / 8 * 8);
+        const int64_t waves = ((N + rows * C::CG - 1) / (rows * C::CG) * m_tiles + groups - 1) / groups;
+        const double step = spread ? std::max(unit, (double)rows * I8_UNIT / 38e3) : unit;
+        // (unsplit CTAs are persistent: they start and end once; clusters of a split do in every wave)
+        const double t = s == 1 ? 4.0 + (double)(waves * per) * step : (double)waves * (4.0 + (double)per * step + reduction);
+        if (t < best.t) best = {(int)rows, s, t};
     }
+    return best;
 }
 
 kq_status i8_tc_product(const char *fn, const I8TcArgs &a, cudaStream_t st) {
     return with_type(a.yt, [&](auto t) {
         using TY = decltype(t);
         const int64_t units = (a.K + I8_UNIT - 1) / I8_UNIT;
-        if (a.M > 128) {
-            const int64_t tiles = (a.N + 2 * I8_ROWS - 1) / (2 * I8_ROWS) * ((a.M + 255) / 256);
-            return i8_launch<I8Pair, TY>(fn, a, I8_ROWS, i8_pair_splits(tiles, units), st);
-        }
-        int rows = I8_ROWS, splits = 1;
-        auto shared = [&](auto c) {
-            using C = decltype(c);
-            i8_share<C>(a.N, units, rows, splits);
-            return i8_launch<C, TY>(fn, a, rows, splits, st);
-        };
-        return a.M <= 32 ? shared(I8One32{}) : a.M <= 64 ? shared(I8One64{}) : shared(I8One128{});
+        auto go = [&](auto c, I8Plan p) { return i8_launch<decltype(c), TY>(fn, a, p.rows, p.splits, st); };
+        // [14336 x 4096]: 64 tokens on 112 tiles of 128 rows 23.6 us, on 150 of 96 rows 21.0; [4096 x 4096], 16
+        // tokens: four splits 9.0, unsplit 14.6
+        if (a.M <= 32) return go(I8One32{}, i8_plan<I8One32>(a.M, a.N, units, 0.25, 3.0, true));
+        if (a.M <= 64) return go(I8One64{}, i8_plan<I8One64>(a.M, a.N, units, 0.25, 3.0, true));
+        const I8Plan one = i8_plan<I8One128>(a.M, a.N, units, 0.40, 3.5, a.M <= 128);
+        if (a.M <= 128) return go(I8One128{}, one);
+        // A pair does a unit of four times the work in 0.62 us, but its tiles are fewer and its reduction is
+        // dearer.  [4096 x 4096]: 512 tokens 22.7 us by (split) pairs, MEASURED by single CTAs; 2048 tokens of
+        // [14336 x 4096] 138 us by pairs, 214 by single CTAs
+        const I8Plan pair = i8_plan<I8Pair>(a.M, a.N, units, 0.62, 6.0, false);
+        return pair.t + 1.0 <= one.t ? go(I8Pair{}, pair) : go(I8One128{}, one);
     });
 }
 
