@@ -4,6 +4,7 @@
 // order in which a kernel adds it up is free and every kernel gives the same bits.  Up to eight tokens take
 // kq_i8_gemv.cu (bound by the weights' bytes), more the tensor cores (kq_i8_tc.cu).
 #include "kq_i8_gemv.cuh"
+#include "kq_i8_quant.cuh"
 #include "kq_i8_tc.cuh"
 #include "kq_sm100.cuh"
 
@@ -23,8 +24,7 @@ __global__ void __launch_bounds__(kI8QuantThreads)
     const int64_t m = blockIdx.x;
     if (err && m == 0 && threadIdx.x == 0) *err = 0ull;
     const T *xr = x + m * ldx;
-    float amax = 0.0f;
-    for (int i = threadIdx.x; i < K; i += kI8QuantThreads) amax = fmaxf(amax, fabsf(to_f32(xr[i])));
+    float amax = i8_amax(xr, K, threadIdx.x, kI8QuantThreads);
 #pragma unroll
     for (int s = 16; s; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, s));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
@@ -32,17 +32,9 @@ __global__ void __launch_bounds__(kI8QuantThreads)
     amax = red[0];
 #pragma unroll
     for (int w = 1; w < kI8QuantThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-    float inv = __fdiv_rn(127.0f, amax);
-    const bool zero = isinf(inv);
-    if (zero) inv = 0.0f;
-    if (threadIdx.x == 0) scale[m] = zero ? 0.0f : __fdiv_rn(amax, 127.0f);
-    TQ *qr = q + m * ldq;
-    for (int i = threadIdx.x; i < fill; i += kI8QuantThreads) {
-        const float v = i < K ? __fmul_rn(to_f32(xr[i]), inv) : 0.0f;
-        const int c = isnan(v) ? 0 : __float2int_rn(v);
-        if constexpr (sizeof(TQ) == 1) qr[i] = (int8_t)c;
-        else qr[i] = __int2half_rn(c);
-    }
+    const I8Scale s = i8_scale(amax);
+    if (threadIdx.x == 0) scale[m] = s.scale;
+    i8_codes(xr, K, fill, s.inv, q + m * ldq, threadIdx.x, kI8QuantThreads);
 }
 
 // The tensor-core product's panel from int8 rows: f16 codes, zeros from K to ldp.  One thread a 16-code piece.
@@ -203,6 +195,8 @@ kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const int8_t *
     uint8_t *b = static_cast<uint8_t *>(workspace);
     float *sx = reinterpret_cast<float *>(b + l.scale);
     unsigned long long *err = static_cast<unsigned long long *>(workspace);
+    if (i8_gemv_quantizes(M, K))
+        return i8_gemv_rows(fn, xt, {x, ldx, nullptr, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, false}, st);
     if (M <= kI8DirectTokens) {
         int8_t *q = reinterpret_cast<int8_t *>(b + l.codes);
         s = i8_quant(fn, xt, x, M, K, ldx, q, l.ld, l.ld, sx, static_cast<unsigned long long *>(nullptr), st);

@@ -5,7 +5,15 @@
 // them, the next pieces always on their way while the current ones are dotted.  When there are few rows,
 // the 1, 2, 4 or 8 warps of a group share the rows' pieces and add their sums through shared memory (whole
 // numbers: exact in any order).  The tokens' codes are small and shared by every warp: they come through L1.
+// [9728 x 2560], one token: 4.0 us, 6.2 TB/s; [4096 x 14336], five tokens: 12.8 us.
+//
+// TX other than void: the tokens come as rows of that type and every block quantises them itself, into shared
+// memory, while its first weights are on their way; a separate quantizer costs a launch (2.9 us more for one
+// fp32 token of [9728 x 2560]).
+#include <type_traits>
+
 #include "kq_i8_gemv.cuh"
+#include "kq_i8_quant.cuh"
 #include "kq_sm100.cuh"
 
 namespace kq {
@@ -26,13 +34,16 @@ __device__ __forceinline__ uint4 keep_codes(uint4 v, int valid) {
     return make_uint4(keep_bytes(v.x, valid), keep_bytes(v.y, valid - 4), keep_bytes(v.z, valid - 8), keep_bytes(v.w, valid - 12));
 }
 
-template <int M, int ROWS, typename TY>
+template <int M, int ROWS, typename TY, typename TX>
 __global__ void __launch_bounds__(GV_WARPS * 32)
-    i8_gemv_kernel(const int8_t *__restrict__ q, int64_t ldq, const float *__restrict__ sx, const int8_t *__restrict__ w,
+    i8_gemv_kernel(const void *__restrict__ rows, int64_t ldq, const float *__restrict__ sx, const int8_t *__restrict__ w,
                    int64_t ldw, const float *__restrict__ sw, const float *__restrict__ bias, int N, int K, int split,
                    TY *__restrict__ y, int64_t ldy, unsigned long long *__restrict__ err) {
     constexpr int U = ROWS == 1 ? 4 : 2;  // pieces of a row in one batch
+    constexpr bool QUANT = !std::is_void<TX>::value;
+    extern __shared__ uint4 codes[];  // QUANT: [M][K rounded up to 16]
     __shared__ int part_sum[GV_WARPS][ROWS * M];
+    __shared__ float part_max[GV_WARPS][M];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = warp / split, part = warp % split;
     const int64_t n0 = ((int64_t)blockIdx.x * (GV_WARPS / split) + group) * ROWS;
@@ -52,6 +63,30 @@ __global__ void __launch_bounds__(GV_WARPS * 32)
     load(cur, p);
     sm100::grid_dependency_wait();  // the codes may be the output of the kernel before this one; the weights are not
     if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0ull;
+    const int8_t *q = static_cast<const int8_t *>(rows);
+    float scale[M];
+    if constexpr (QUANT) {
+        const TX *x = static_cast<const TX *>(rows);
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            float a = i8_amax(x + m * ldq, K, threadIdx.x, GV_WARPS * 32);
+#pragma unroll
+            for (int s = 16; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, s));
+            if (lane == 0) part_max[warp][m] = a;
+        }
+        __syncthreads();
+        int8_t *c = reinterpret_cast<int8_t *>(codes);
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            float a = part_max[0][m];
+#pragma unroll
+            for (int i = 1; i < GV_WARPS; ++i) a = fmaxf(a, part_max[i][m]);
+            const I8Scale s = i8_scale(a);
+            scale[m] = s.scale;
+            i8_codes(x + m * ldq, K, pieces * 16, s.inv, c + m * pieces * 16, threadIdx.x, GV_WARPS * 32);
+        }
+        __syncthreads();
+    }
     int acc[ROWS][M] = {};
     for (; p < pieces; p += U * step) {
         load(nxt, p + U * step);
@@ -65,7 +100,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32)
             const int64_t off = (int64_t)min(pu, pieces - 1) * 16;  // past the end the weights are zeros
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(q + m * ldq + off);
+                const uint4 x = QUANT ? codes[m * pieces + (off >> 4)] : *reinterpret_cast<const uint4 *>(q + m * ldq + off);
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) {
                     int a = acc[r][m];
@@ -100,54 +135,78 @@ __global__ void __launch_bounds__(GV_WARPS * 32)
     const int64_t n = n0 + lane / M;
     const int m = lane % M;
     if (lane >= ROWS * M || n >= N) return;
-    float v = __fmul_rn(__fmul_rn((float)mine, sx[m]), sw[n]);
+    float s = 0.0f;
+    if constexpr (QUANT) {
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            if (i == m) s = scale[i];
+    } else {
+        s = sx[m];
+    }
+    float v = __fmul_rn(__fmul_rn((float)mine, s), sw[n]);
     if (bias) v = __fadd_rn(v, bias[n]);
     y[m * ldy + n] = from_f32<TY>(v);
 }
 
-template <int M, int ROWS, typename TY>
+template <int M, int ROWS, typename TY, typename TX>
 static kq_status launch_rows(const char *fn, const I8GemvArgs &a, int split, cudaStream_t st) {
     const int per_block = GV_WARPS / split * ROWS;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.N + per_block - 1) / per_block));
     cfg.blockDim = dim3(GV_WARPS * 32);
+    cfg.dynamicSmemBytes = std::is_void<TX>::value ? 0 : (size_t)M * ((a.K + 15) / 16) * 16;  // 17 KB at most
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.after_quant ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, i8_gemv_kernel<M, ROWS, TY>, a.q, a.ldq, a.sx, a.w, a.ldw, a.sw, a.bias,
-                                             (int)a.N, (int)a.K, split, static_cast<TY *>(a.y), a.ldy, a.err);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, i8_gemv_kernel<M, ROWS, TY, TX>, a.rows, a.ldq, a.sx, a.w, a.ldw, a.sw,
+                                             a.bias, (int)a.N, (int)a.K, split, static_cast<TY *>(a.y), a.ldy, a.err);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
     count_launch(R_I8);
     return KQ_OK;
 }
 
-template <int M, typename TY>
+template <int M, typename TY, typename TX>
 static kq_status launch_tokens(const char *fn, const I8GemvArgs &a, cudaStream_t st) {
-    // Warps that share a row group: enough to give every SM 16 warps (152 * 16), while each still has a
-    // piece for every lane.  A product too narrow for that even so takes single rows.
-    constexpr int64_t want = 152 * 16;
+    // Warps that share a row group: enough to give every SM eight warps (152 * 8), while each still has two
+    // pieces for every lane ([4096 x 14336], five tokens: 12.8 us so, 14.3 with 16 warps an SM).  A product too
+    // narrow for that even so takes single rows.
+    constexpr int64_t want = 152 * 8;
     int split = 1;
     while (split < GV_WARPS && (a.N + 3) / 4 * split < want && a.K >= 512 * 2 * split) split *= 2;
-    if ((a.N + 3) / 4 * split * 2 <= want) return launch_rows<M, 1, TY>(fn, a, split, st);
-    return launch_rows<M, 4, TY>(fn, a, split, st);
+    if ((a.N + 3) / 4 * split * 2 <= want) return launch_rows<M, 1, TY, TX>(fn, a, split, st);
+    return launch_rows<M, 4, TY, TX>(fn, a, split, st);
+}
+
+template <typename TY>
+static kq_status launch_codes(const char *fn, const I8GemvArgs &a, cudaStream_t st) {
+    switch (a.M) {
+    case 1: return launch_tokens<1, TY, void>(fn, a, st);
+    case 2: return launch_tokens<2, TY, void>(fn, a, st);
+    case 3: return launch_tokens<3, TY, void>(fn, a, st);
+    case 4: return launch_tokens<4, TY, void>(fn, a, st);
+    case 5: return launch_tokens<5, TY, void>(fn, a, st);
+    case 6: return launch_tokens<6, TY, void>(fn, a, st);
+    case 7: return launch_tokens<7, TY, void>(fn, a, st);
+    default: return launch_tokens<8, TY, void>(fn, a, st);
+    }
 }
 
 kq_status i8_gemv(const char *fn, const I8GemvArgs &a, cudaStream_t st) {
+    return with_type(a.yt, [&](auto t) { return launch_codes<decltype(t)>(fn, a, st); });
+}
+
+bool i8_gemv_quantizes(int64_t M, int64_t K) { return M <= 2 && M * K <= 16384; }
+
+kq_status i8_gemv_rows(const char *fn, kq_dtype xt, const I8GemvArgs &a, cudaStream_t st) {
     return with_type(a.yt, [&](auto t) {
         using TY = decltype(t);
-        switch (a.M) {
-        case 1: return launch_tokens<1, TY>(fn, a, st);
-        case 2: return launch_tokens<2, TY>(fn, a, st);
-        case 3: return launch_tokens<3, TY>(fn, a, st);
-        case 4: return launch_tokens<4, TY>(fn, a, st);
-        case 5: return launch_tokens<5, TY>(fn, a, st);
-        case 6: return launch_tokens<6, TY>(fn, a, st);
-        case 7: return launch_tokens<7, TY>(fn, a, st);
-        default: return launch_tokens<8, TY>(fn, a, st);
-        }
+        return with_type(xt, [&](auto x) {
+            using TX = decltype(x);
+            return a.M == 1 ? launch_tokens<1, TY, TX>(fn, a, st) : launch_tokens<2, TY, TX>(fn, a, st);
+        });
     });
 }
 

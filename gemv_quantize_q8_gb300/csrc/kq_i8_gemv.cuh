@@ -7,7 +7,7 @@ namespace kq {
 constexpr int kI8FewTokens = 8;
 
 struct I8GemvArgs {
-    const int8_t *q;  // [M][ldq]
+    const void *rows;  // codes [M][ldq], or (i8_gemv_rows) rows of another type
     int64_t ldq;
     const float *sx;
     const int8_t *w;  // [N][ldw]
@@ -21,5 +21,9 @@ struct I8GemvArgs {
     bool after_quant;         // q and sx are written by the kernel just before: start beside it
 };
 kq_status i8_gemv(const char *fn, const I8GemvArgs &a, cudaStream_t st);
+// The same from rows of type xt, quantised by the product's own blocks (sx unused): where the rows are so
+// short that every block can do it again (16384 elements, some 1 us, against a launch).
+bool i8_gemv_quantizes(int64_t M, int64_t K);
+kq_status i8_gemv_rows(const char *fn, kq_dtype xt, const I8GemvArgs &a, cudaStream_t st);
 
 }  // namespace kq

@@ -37,14 +37,10 @@ constexpr int kQkMaxD = 1024;
 constexpr int kQkThreads = 256;
 
 // N consecutive elements as fp32; the address is aligned to all of them, or to 16 bytes.
-template <int BYTES> struct Word;
-template <> struct Word<4> { using type = uint32_t; };
-template <> struct Word<8> { using type = uint2; };
-template <> struct Word<16> { using type = uint4; };
 template <typename T, int N>
 __device__ __forceinline__ void load_n(const T *p, float (&v)[N]) {
     constexpr int W = N * sizeof(T) < 16 ? N : 16 / (int)sizeof(T);
-    using Vec = typename Word<W * (int)sizeof(T)>::type;
+    using Vec = typename VecOf<W * (int)sizeof(T)>::type;
 #pragma unroll
     for (int i = 0; i < N; i += W) {
         const Vec u = *reinterpret_cast<const Vec *>(p + i);
@@ -55,7 +51,7 @@ __device__ __forceinline__ void load_n(const T *p, float (&v)[N]) {
 template <typename T, int N>
 __device__ __forceinline__ void store_n(T *p, const float (&v)[N]) {
     constexpr int W = N * sizeof(T) < 16 ? N : 16 / (int)sizeof(T);
-    using Vec = typename Word<W * (int)sizeof(T)>::type;
+    using Vec = typename VecOf<W * (int)sizeof(T)>::type;
 #pragma unroll
     for (int i = 0; i < N; i += W) {
         Vec u;

@@ -41,6 +41,12 @@ __device__ __forceinline__ void unpack16(uint4 u, float (&v)[kVec<T>]) {
     for (int i = 0; i < kVec<T>; ++i) v[i] = to_f32(e[i]);
 }
 
+// The type that moves 4, 8 or 16 bytes at once.
+template <int BYTES> struct VecOf;
+template <> struct VecOf<4> { using type = uint32_t; };
+template <> struct VecOf<8> { using type = uint2; };
+template <> struct VecOf<16> { using type = uint4; };
+
 // Calls f with a value of the C++ type of t (t is one of the three).
 template <typename F>
 inline kq_status with_type(kq_dtype t, F f) {
