@@ -6,7 +6,7 @@
 #include "kq_i8_gemv.cuh"
 #include "kq_i8_quant.cuh"
 #include "kq_i8_tc.cuh"
-#include "kq_sm100.cuh"
+#include "kq_launch.cuh"
 
 namespace kq {
 
@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(kI8QuantThreads)
     i8_quant_kernel(const T *__restrict__ x, int64_t ldx, int K, TQ *__restrict__ q, int64_t ldq, int fill,
                     float *__restrict__ scale, unsigned long long *__restrict__ err) {
     __shared__ float red[kI8QuantThreads / 32];
+    sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
     const int64_t m = blockIdx.x;
     if (err && m == 0 && threadIdx.x == 0) *err = 0ull;
@@ -41,6 +42,7 @@ __global__ void __launch_bounds__(kI8QuantThreads)
 __global__ void __launch_bounds__(256)
     i8_panel_kernel(const int8_t *__restrict__ q, int64_t ldq, int64_t M, int K, __half *__restrict__ panel, int64_t ldp,
                     unsigned long long *__restrict__ err) {
+    sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, pieces = ldp / 16;
     if (i == 0) *err = 0ull;
@@ -84,16 +86,20 @@ static I8Workspace i8_workspace(int64_t M, int64_t K) {
     return l;
 }
 
+static kq_status i8_launched(const char *fn, cudaError_t e) {
+    if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+    count_launch(R_I8);
+    return KQ_OK;
+}
+
 template <typename TQ>
 static kq_status i8_quant(const char *fn, kq_dtype xt, const void *x, int64_t M, int64_t K, int64_t ldx, TQ *q, int64_t ldq,
                           int64_t fill, float *scale, unsigned long long *err, cudaStream_t st) {
     return with_type(xt, [&](auto t) {
         using T = decltype(t);
-        i8_quant_kernel<T, TQ><<<(unsigned)M, kI8QuantThreads, 0, st>>>(static_cast<const T *>(x), ldx, (int)K, q, ldq,
-                                                                        (int)fill, scale, err);
-        kq_status s = check_launch(fn);
-        if (s == KQ_OK) count_launch(R_I8);
-        return s;
+        const cudaError_t e = launch_beside(i8_quant_kernel<T, TQ>, dim3((unsigned)M), dim3(kI8QuantThreads), 0, dim3(1), st,
+                                            static_cast<const T *>(x), ldx, (int)K, q, ldq, (int)fill, scale, err);
+        return i8_launched(fn, e);
     });
 }
 
@@ -176,10 +182,9 @@ kq_status kq_gemm_i8(const int8_t *q, int64_t ldq, const float *sx, const int8_t
     __half *panel = reinterpret_cast<__half *>(static_cast<uint8_t *>(workspace) + l.codes);
     const int64_t blocks = (M * (l.ld / 16) + 255) / 256;
     if (blocks > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: M=%lld is too large", fn, (long long)M);
-    i8_panel_kernel<<<(unsigned)blocks, 256, 0, st>>>(q, ldq, M, (int)K, panel, l.ld, err);
-    s = check_launch(fn);
+    s = i8_launched(fn, launch_beside(i8_panel_kernel, dim3((unsigned)blocks), dim3(256), 0, dim3(1), st, q, ldq, M, (int)K, panel,
+                                      l.ld, err));
     if (s != KQ_OK) return s;
-    count_launch(R_I8);
     return i8_tc_product(fn, {nullptr, 0, panel, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, true}, st);
 }
 

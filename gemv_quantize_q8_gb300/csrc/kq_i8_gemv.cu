@@ -14,7 +14,7 @@
 
 #include "kq_i8_gemv.cuh"
 #include "kq_i8_quant.cuh"
-#include "kq_sm100.cuh"
+#include "kq_launch.cuh"
 
 namespace kq {
 
@@ -38,7 +38,7 @@ template <int M, int ROWS, typename TY, typename TX>
 __global__ void __launch_bounds__(GV_WARPS * 32)
     i8_gemv_kernel(const void *__restrict__ rows, int64_t ldq, const float *__restrict__ sx, const int8_t *__restrict__ w,
                    int64_t ldw, const float *__restrict__ sw, const float *__restrict__ bias, int N, int K, int split,
-                   TY *__restrict__ y, int64_t ldy, unsigned long long *__restrict__ err) {
+                   TY *__restrict__ y, int64_t ldy, unsigned long long *__restrict__ err, bool weights_first) {
     constexpr int U = ROWS == 1 ? 4 : 2;  // pieces of a row in one batch
     constexpr bool QUANT = !std::is_void<TX>::value;
     extern __shared__ uint4 codes[];  // QUANT: [M][K rounded up to 16]
@@ -60,8 +60,11 @@ __global__ void __launch_bounds__(GV_WARPS * 32)
             for (int r = 0; r < ROWS; ++r) v[u][r] = p + u * step < pieces ? load_stream(wr[r] + (int64_t)(p + u * step) * 16) : none;
     };
     int p = part * 32 + lane;
+    // behind the quantizer, which has waited for all that came before it, the weights need no wait
+    if (!weights_first) sm100::grid_dependency_wait();
     load(cur, p);
-    sm100::grid_dependency_wait();  // the codes may be the output of the kernel before this one; the weights are not
+    if (weights_first) sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0ull;
     const int8_t *q = static_cast<const int8_t *>(rows);
     float scale[M];
@@ -151,18 +154,10 @@ __global__ void __launch_bounds__(GV_WARPS * 32)
 template <int M, int ROWS, typename TY, typename TX>
 static kq_status launch_rows(const char *fn, const I8GemvArgs &a, int split, cudaStream_t st) {
     const int per_block = GV_WARPS / split * ROWS;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.N + per_block - 1) / per_block));
-    cfg.blockDim = dim3(GV_WARPS * 32);
-    cfg.dynamicSmemBytes = std::is_void<TX>::value ? 0 : (size_t)M * ((a.K + 15) / 16) * 16;  // 17 KB at most
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.after_quant ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, i8_gemv_kernel<M, ROWS, TY, TX>, a.rows, a.ldq, a.sx, a.w, a.ldw, a.sw,
-                                             a.bias, (int)a.N, (int)a.K, split, static_cast<TY *>(a.y), a.ldy, a.err);
+    const size_t smem = std::is_void<TX>::value ? 0 : (size_t)M * ((a.K + 15) / 16) * 16;  // 17 KB at most
+    const cudaError_t e = launch_beside(i8_gemv_kernel<M, ROWS, TY, TX>, dim3((unsigned)((a.N + per_block - 1) / per_block)),
+                                        dim3(GV_WARPS * 32), smem, dim3(1), st, a.rows, a.ldq, a.sx, a.w, a.ldw, a.sw, a.bias,
+                                        (int)a.N, (int)a.K, split, static_cast<TY *>(a.y), a.ldy, a.err, a.after_quant);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
     count_launch(R_I8);
     return KQ_OK;

@@ -18,7 +18,7 @@ struct I8GemvArgs {
     void *y;
     int64_t ldy;
     unsigned long long *err;  // device flag, cleared here
-    bool after_quant;         // q and sx are written by the kernel just before: start beside it
+    bool after_quant;         // the kernel just before is the quantizer: the weights may be read before its end
 };
 kq_status i8_gemv(const char *fn, const I8GemvArgs &a, cudaStream_t st);
 // The same from rows of type xt, quantised by the product's own blocks (sx unused): where the rows are so

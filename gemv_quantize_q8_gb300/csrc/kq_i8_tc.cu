@@ -26,7 +26,7 @@
 #include <cudaTypedefs.h>
 
 #include "kq_i8_tc.cuh"
-#include "kq_sm100.cuh"
+#include "kq_launch.cuh"
 
 namespace kq {
 
@@ -83,6 +83,7 @@ struct I8TcParams {
     int rows;                            // weight rows of a CTA's tile, a multiple of 8 up to I8_ROWS
     int units, units_per_split, nsplit;  // K in units of 128
     unsigned long long *err;
+    bool after_prologue;  // the weights may be read before the kernel before this one has ended
 };
 
 // ---------------------------------------------------------------- cta_group forms
@@ -211,9 +212,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (warp == C::W_MMA) cg_alloc<C::CG>(tmem_holder);
     if (warp == C::W_PROD && lane == 0) prefetch_tmap(&tmW);
     if (warp == C::W_ACT && lane == 0) prefetch_tmap(&tmX);
-    // the direct form's flag: an error is counted two seconds later at the earliest
-    if (C::DIRECT && tid == 0 && blockIdx.x == 0 && z == 0) *P.err = 0ull;
     tc_fence_before();
+    if (!P.after_prologue) grid_dependency_wait();
     __syncthreads();
     if (C::CG > 1) cooperative_groups::this_cluster().sync();  // the pair's barriers are ready
     tc_fence_after();
@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     tma_load_2d(sW + u * C::WT, &tmW, &w_full[u], (u0 + u) * I8_UNIT, (tile0 % P.n_tiles) * P.rows);
                 }
                 grid_dependency_wait();
+                grid_launch_dependents();
             }
             for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
                 const int n0 = (tile % P.n_tiles) * (P.rows * C::CG) + r * P.rows;
@@ -316,6 +317,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bool ok = true;
             int g = 0;
             grid_dependency_wait();  // the panel is the output of the kernel before this one
+            grid_launch_dependents();
             for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
                 const int m0 = (tile / P.n_tiles) * C::NT + r * (C::NT / C::CG);
                 for (int u = 0; u < nu; ++u, ++g) {
@@ -445,6 +447,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         bool ok = true;
         int job = 0;
         grid_dependency_wait();  // scales may be the output of the kernel before this one
+        // the direct form's flag: an error is counted two seconds later at the earliest
+        if (C::DIRECT && tid == 0 && blockIdx.x == 0 && z == 0) *P.err = 0ull;
         for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
             // this tile's scales, on their way while it is computed: lane l keeps the tokens l, l + 32
             const int n = (tile % P.n_tiles) * (P.rows * C::CG) + r * P.rows + row;
@@ -646,25 +650,13 @@ static kq_status i8_launch(const char *fn, const I8TcArgs &a, int rows, int spli
     p.units_per_split = (p.units + splits - 1) / splits;
     p.nsplit = splits;
     p.err = a.err;
+    p.after_prologue = a.after_prologue;
     auto kern = i8_tc_kernel<C, TY>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-    cudaLaunchConfig_t cfg = {};
     const int64_t groups = splits > 1 ? tiles : std::min<int64_t>(tiles, i8_resident<C>(1));
-    cfg.gridDim = dim3((unsigned)(groups * C::CG), 1, (unsigned)splits);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::TOTAL;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = C::CG;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = (unsigned)splits;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // starts beside the panel's or the quantizer's kernel
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.after_prologue ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kern, tmW, tmX, p);
+    e = launch_beside(kern, dim3((unsigned)(groups * C::CG), 1, (unsigned)splits), dim3(C::THREADS), C::TOTAL,
+                      dim3(C::CG, 1, (unsigned)splits), st, tmW, tmX, p);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
     count_launch(R_I8);
     return KQ_OK;

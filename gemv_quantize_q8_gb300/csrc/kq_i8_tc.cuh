@@ -33,7 +33,7 @@ struct I8TcArgs {
     void *y;
     int64_t ldy;
     unsigned long long *err;  // device flag: cleared here (int8 codes) or by the panel's kernel
-    bool after_prologue;      // the kernel just before is this library's own (quantizer or panel): start beside it
+    bool after_prologue;      // the kernel just before is the quantizer or the panel's: the weights may be read before its end
 };
 kq_status i8_tc_product(const char *fn, const I8TcArgs &a, cudaStream_t st);
 

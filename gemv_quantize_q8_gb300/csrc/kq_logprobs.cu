@@ -19,6 +19,7 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
+#include "kq_launch.cuh"
 #include "kq_value.cuh"
 
 namespace kq {
@@ -172,6 +173,8 @@ __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
     extern __shared__ uint64_t buf[];  // TOP: kLpCap candidates, then the list of batches
     uint16_t *list = reinterpret_cast<uint16_t *>(buf + kLpCap);
     __shared__ LpShared sh;
+    sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, part = blockIdx.x, parts = gridDim.x;
     const int64_t row = P.row0 + blockIdx.y;
     const T *x = static_cast<const T *>(P.x) + row * P.ldx;
@@ -387,20 +390,10 @@ static kq_status launch_lp(const char *fn, LpParams P, int64_t M, cudaStream_t s
     // has a whole round of its own
     int parts = 1;
     while (parts < kLpMaxParts && M * parts * 2 <= 152 * 5 && P.V >= parts * 2 * kLpThreads * kLpVecs * kVec<T>) parts *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kLpThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)parts;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = parts > 1 ? 1 : 0;
     for (int64_t r = 0; e == cudaSuccess && r < M; r += 65535) {  // the grid's second dimension ends there
         P.row0 = r;
-        cfg.gridDim = dim3((unsigned)parts, (unsigned)(M - r < 65535 ? M - r : 65535));
-        e = cudaLaunchKernelEx(&cfg, kern, P);
+        e = launch_beside(kern, dim3((unsigned)parts, (unsigned)(M - r < 65535 ? M - r : 65535)), dim3(kLpThreads), smem,
+                          dim3((unsigned)parts), st, P);
         if (e == cudaSuccess) count_launch(R_LOGPROBS);
     }
     return e == cudaSuccess ? KQ_OK : fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));

@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <math.h>
 
+#include "kq_launch.cuh"
 #include "kq_value.cuh"
 
 namespace kq {
@@ -87,6 +88,8 @@ __device__ __forceinline__ void store4(T *p, Four f) {
 // The lanes take G heads of their token (queries or keys, not both): angles and gamma are read once for them.
 template <typename TX, typename TY, bool PAIRS, int R, int LANES, int G>
 __global__ void __launch_bounds__(kQkThreads) qk_kernel(QkParams P) {
+    sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
     const unsigned gq = (P.heads[0] + G - 1) / G, per_token = gq + (P.heads[1] + G - 1) / G;
     const unsigned unit = blockIdx.x * (kQkThreads / LANES) + threadIdx.x / LANES;  // below 2^31
     const int lane = threadIdx.x % LANES;
@@ -166,6 +169,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(QkParams P) {
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(128) qk_any_kernel(QkParams P, bool pairs) {
     __shared__ float buf[4][kQkMaxD];
+    sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned nh = P.heads[0] + P.heads[1], unit = blockIdx.x * 4 + warp;
     if (unit >= (unsigned)P.M * nh) return;
@@ -204,13 +209,12 @@ __global__ void __launch_bounds__(128) qk_any_kernel(QkParams P, bool pairs) {
 }
 
 template <typename TX, typename TY>
-static void launch_qk(const QkParams &P, bool pairs, bool aligned4, cudaStream_t st) {
+static cudaError_t launch_qk(const QkParams &P, bool pairs, bool aligned4, cudaStream_t st) {
     const int64_t units = P.M * (P.heads[0] + P.heads[1]);
     // vectors of four elements (16 bytes of fp32, 8 of 16-bit types) wherever they tile the halves and the rest
     const bool vec = aligned4 && P.D % 8 == 0 && (P.rot / 2) % 4 == 0 && P.D <= 512;
     if (!vec) {
-        qk_any_kernel<TX, TY><<<(unsigned)((units + 3) / 4), 128, 0, st>>>(P, pairs);
-        return;
+        return launch_beside(qk_any_kernel<TX, TY>, dim3((unsigned)((units + 3) / 4)), dim3(128), 0, dim3(1), st, P, pairs);
     }
     auto go = [&](auto pr, auto rounds, auto lanes, auto heads) {
         constexpr int R = decltype(rounds)::value, L = decltype(lanes)::value, G = decltype(heads)::value;
@@ -224,23 +228,22 @@ static void launch_qk(const QkParams &P, bool pairs, bool aligned4, cudaStream_t
         q.shift = 31 + l;
         q.magic = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
         q.inv_d = 1.0f / (float)P.D;
-        qk_kernel<TX, TY, decltype(pr)::value, R, L, G><<<(unsigned)blocks, kQkThreads, 0, st>>>(q);
+        return launch_beside(qk_kernel<TX, TY, decltype(pr)::value, R, L, G>, dim3((unsigned)blocks), dim3(kQkThreads), 0, dim3(1), st, q);
     };
     auto heads = [&](auto pr, auto rounds, auto lanes) {
         // four heads a lane group once that still fills every SM's threads (152 * 2048): 8192 tokens of 40
         // heads of 128, fp32 to bf16, 37.2 us (6.9 TB/s) against 40.1 with two and 42.8 with eight
-        if (units * decltype(lanes)::value / 4 >= 152 * 2048) go(pr, rounds, lanes, std::integral_constant<int, 4>{});
-        else go(pr, rounds, lanes, std::integral_constant<int, 1>{});
+        if (units * decltype(lanes)::value / 4 >= 152 * 2048) return go(pr, rounds, lanes, std::integral_constant<int, 4>{});
+        return go(pr, rounds, lanes, std::integral_constant<int, 1>{});
     };
     auto form = [&](auto pr) {
         // a lane for each of a head's D/8 vector pairs (two from 256 elements on)
-        if (P.D <= 64) heads(pr, std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
-        else if (P.D <= 128) heads(pr, std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
-        else if (P.D <= 256) heads(pr, std::integral_constant<int, 1>{}, std::integral_constant<int, 32>{});
-        else heads(pr, std::integral_constant<int, 2>{}, std::integral_constant<int, 32>{});
+        if (P.D <= 64) return heads(pr, std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+        if (P.D <= 128) return heads(pr, std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
+        if (P.D <= 256) return heads(pr, std::integral_constant<int, 1>{}, std::integral_constant<int, 32>{});
+        return heads(pr, std::integral_constant<int, 2>{}, std::integral_constant<int, 32>{});
     };
-    if (pairs) form(std::true_type{});
-    else form(std::false_type{});
+    return pairs ? form(std::true_type{}) : form(std::false_type{});
 }
 
 }  // namespace kq
@@ -290,10 +293,10 @@ extern "C" kq_status kq_qk_norm_rope(kq_dtype xt, const void *q, int64_t ldq, co
     if (n_k) al = al && aligned(k, 4 * xb) && ldk % 4 == 0 && aligned(k_out, 4 * yb) && ldko % 4 == 0;
     return with_type(xt, [&](auto tx) {
         return with_type(yt, [&](auto ty) {
-            launch_qk<decltype(tx), decltype(ty)>(P, pairs != 0, al, (cudaStream_t)stream);
-            kq_status s = check_launch(fn);
-            if (s == KQ_OK) count_launch(R_QK);
-            return s;
+            const cudaError_t e = launch_qk<decltype(tx), decltype(ty)>(P, pairs != 0, al, (cudaStream_t)stream);
+            if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+            count_launch(R_QK);
+            return KQ_OK;
         });
     });
 }
