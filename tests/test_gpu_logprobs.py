@@ -146,6 +146,21 @@ def test_large_values():
     check(logits(g, 4, 2000, "f32", 1e37), g.integers(0, 2000, (4, 2)), 10, "f32")
 
 
+def test_rows_of_many_rounds():
+    """More rounds of a block over its row than the 32 bits that remember where the alternatives are."""
+    M, V, k = 400, 270001, 20
+    g = torch.Generator(device=DEV)
+    g.manual_seed(0)
+    x = (torch.randn((M, V), generator=g, device=DEV) * 2.5).to(torch.bfloat16)
+    ent, ids, top = torch.empty(M, device=DEV), torch.empty((M, k), dtype=torch.int32, device=DEV), torch.empty((M, k), device=DEV)
+    kq.kq_logprobs(kq.BF16, x, V, M, V, None, 0, None, ent, k, ids, top)
+    for r in (0, 199, 399):
+        want = reference(x[r : r + 1].double().cpu().numpy(), np.zeros((1, 0), int), k)
+        assert np.array_equal(ids[r].cpu().numpy(), want["ids"][0])
+        assert abs(ent[r].item() - want["ent"][0]) <= 2 * (V / 256 + 160) * U * want["scale"][0]
+        assert np.abs(top[r].cpu().numpy() - want["top"][0]).max() <= (V / 256 + 160) * U * want["scale"][0]
+
+
 def test_offsets_past_32_bits():
     M, V, ld = 3, 1000, 1_100_000_000
     g = np.random.default_rng(2)
