@@ -240,25 +240,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
                 const int n0 = (tile % P.n_tiles) * (P.rows * C::CG) + r * P.rows;
-                // two neighbouring units at a time: 256 consecutive bytes of every row, which device memory
-                // gives faster than 128 (4.7 against 4.1 TB/s, copies alone)
-                for (int u = 0; u < nu && ok; u += 2) {
-                    const int kn = min(2, nu - u);
-                    for (int k = 0; k < kn && ok; ++k) {
-                        const int gk = g + k;
-                        if (gk >= ahead)
-                            ok = mbar_wait_sleep(&w_empty[gk % C::WSTAGES], ((gk / C::WSTAGES) & 1) ^ 1, abort_flag, kI8WaitNs);
+                for (int u = 0; u < nu; ++u, ++g) {
+                    const int s = g % C::WSTAGES, x = (u0 + u) * I8_UNIT;
+                    if (g >= ahead) {
+                        if (!(ok = mbar_wait_sleep(&w_empty[s], ((g / C::WSTAGES) & 1) ^ 1, abort_flag, kI8WaitNs))) break;
+                        mbar_arrive_expect_tx(&w_full[s], unit_bytes);
+                        tma_load_2d(sW + s * C::WT, &tmW, &w_full[s], x, n0);
                     }
-                    if (!ok) break;
-                    for (int k = 0; k < kn; ++k) {
-                        const int s = (g + k) % C::WSTAGES, x = (u0 + u + k) * I8_UNIT;
-                        if (g + k >= ahead) {
-                            mbar_arrive_expect_tx(&w_full[s], unit_bytes);
-                            tma_load_2d(sW + s * C::WT, &tmW, &w_full[s], x, n0);
-                        }
-                        if (C::DIRECT) tma_load_2d(sW + s * C::WT + I8_ROWS * I8_UNIT, &tmX, &w_full[s], x, 0);
-                    }
-                    g += kn;
+                    if (C::DIRECT) tma_load_2d(sW + s * C::WT + I8_ROWS * I8_UNIT, &tmX, &w_full[s], x, 0);
                 }
             }
             // leaving early: the copies in flight land first (bounded)

@@ -386,10 +386,10 @@ static kq_status launch_lp(const char *fn, LpParams P, int64_t M, cudaStream_t s
     constexpr int smem = TOP ? kLpCap * 8 + kLpThreads * 32 * 2 : 0;
     auto kern = lp_kernel<T, TOP>;
     cudaError_t e = smem ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
-    // CTAs that share a row: doubled while all still run at once (five an SM) and each
-    // has a whole round of its own
+    // CTAs that share a row: doubled up to two and a half an SM, while each has a whole round of its own (64 rows
+    // of 131072 bf16, 20 alternatives: four a row 13.5 us, eight 18.3, two 13.8; 167 of 49999: two 15.3, four 17.2)
     int parts = 1;
-    while (parts < kLpMaxParts && M * parts * 2 <= 152 * 5 && P.V >= parts * 2 * kLpThreads * kLpVecs * kVec<T>) parts *= 2;
+    while (parts < kLpMaxParts && M * parts * 2 <= 380 && P.V >= parts * 2 * kLpThreads * kLpVecs * kVec<T>) parts *= 2;
     for (int64_t r = 0; e == cudaSuccess && r < M; r += 65535) {  // the grid's second dimension ends there
         P.row0 = r;
         e = launch_beside(kern, dim3((unsigned)parts, (unsigned)(M - r < 65535 ? M - r : 65535)), dim3(kLpThreads), smem,
