@@ -2,10 +2,11 @@
 // (dp4a, exact int32) against all tokens.
 //
 // Bound by the weights' bytes.  A warp takes ROWS weight rows; its lanes take consecutive 16-byte pieces of
-// them, the next pieces always on their way while the current ones are dotted.  When there are few rows,
-// the 1, 2, 4 or 8 warps of a group share the rows' pieces and add their sums through shared memory (whole
-// numbers: exact in any order).  The tokens' codes are small and shared by every warp: they come through L1.
-// [9728 x 2560], one token: 4.0 us, 6.2 TB/s; [4096 x 14336], five tokens: 12.8 us.
+// them, the next pieces always on their way while the current ones are dotted.  The 1, 2, 4 or 8 warps of a
+// group share the rows' pieces and add their sums through shared memory (whole numbers: exact in any order).
+// Blocks stay and walk the row groups, so that a group's first pieces are on their way while the group before
+// it is summed up and stored.  The tokens' codes are small and shared by every warp: they come through L1.
+// [9728 x 2560], one token: 3.6 us back to back (some of it from L2); [4096 x 14336], five tokens: 12.8 us.
 //
 // TX other than void: the tokens come as rows of that type and every block quantises them itself, into shared
 // memory, while its first weights are on their way; a separate quantizer costs a launch (2.9 us more for one
@@ -34,23 +35,26 @@ __device__ __forceinline__ uint4 keep_codes(uint4 v, int valid) {
     return make_uint4(keep_bytes(v.x, valid), keep_bytes(v.y, valid - 4), keep_bytes(v.z, valid - 8), keep_bytes(v.w, valid - 12));
 }
 
+constexpr int kGemvPerSm = 2;  // blocks of an SM: up to 128 registers a thread, half of them for pieces under way
+
 template <int M, int ROWS, typename TY, typename TX>
-__global__ void __launch_bounds__(GV_WARPS * 32)
+__global__ void __launch_bounds__(GV_WARPS * 32, kGemvPerSm)
     i8_gemv_kernel(const void *__restrict__ rows, int64_t ldq, const float *__restrict__ sx, const int8_t *__restrict__ w,
-                   int64_t ldw, const float *__restrict__ sw, const float *__restrict__ bias, int N, int K, int split,
+                   int64_t ldw, const float *__restrict__ sw, const float *__restrict__ bias, int N, int K, int split, int tasks,
                    TY *__restrict__ y, int64_t ldy, unsigned long long *__restrict__ err, bool weights_first) {
-    constexpr int U = ROWS == 1 ? 4 : 2;  // pieces of a row in one batch
     constexpr bool QUANT = !std::is_void<TX>::value;
-    extern __shared__ uint4 codes[];  // QUANT: [M][K rounded up to 16]
+    constexpr int U = ROWS == 1 ? 4 : 2;  // pieces of a row in one batch
+    extern __shared__ uint4 codes[];      // QUANT: [M][K rounded up to 16]
     __shared__ int part_sum[GV_WARPS][ROWS * M];
     __shared__ float part_max[GV_WARPS][M];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = warp / split, part = warp % split;
-    const int64_t n0 = ((int64_t)blockIdx.x * (GV_WARPS / split) + group) * ROWS;
-    const int pieces = (K + 15) >> 4, step = 32 * split;
+    const int group = warp / split, part = warp % split, groups = GV_WARPS / split;
+    const int pieces = (K + 15) >> 4, step = 32 * split, p0 = part * 32 + lane;
     const int8_t *wr[ROWS];
+    auto rows_of = [&](int task) {
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) wr[r] = w + min(n0 + r, (int64_t)N - 1) * ldw;
+        for (int r = 0; r < ROWS; ++r) wr[r] = w + min(((int64_t)task * groups + group) * ROWS + r, (int64_t)N - 1) * ldw;
+    };
     const uint4 none = make_uint4(0, 0, 0, 0);
     uint4 cur[U][ROWS], nxt[U][ROWS];
     auto load = [&](uint4 (&v)[U][ROWS], int p) {
@@ -59,10 +63,11 @@ __global__ void __launch_bounds__(GV_WARPS * 32)
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) v[u][r] = p + u * step < pieces ? load_stream(wr[r] + (int64_t)(p + u * step) * 16) : none;
     };
-    int p = part * 32 + lane;
+    int task = blockIdx.x;
+    rows_of(task);
     // behind the quantizer, which has waited for all that came before it, the weights need no wait
     if (!weights_first) sm100::grid_dependency_wait();
-    load(cur, p);
+    load(cur, p0);
     if (weights_first) sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0ull;
@@ -90,74 +95,100 @@ __global__ void __launch_bounds__(GV_WARPS * 32)
         }
         __syncthreads();
     }
-    int acc[ROWS][M] = {};
-    for (; p < pieces; p += U * step) {
-        load(nxt, p + U * step);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int pu = p + u * step;
-            if (pu == pieces - 1 && (K & 15)) {
-#pragma unroll
-                for (int r = 0; r < ROWS; ++r) cur[u][r] = keep_codes(cur[u][r], K & 15);
+    for (; task < tasks; task += gridDim.x) {
+        int acc[ROWS][M] = {};
+        for (int b = 0; b < pieces; b += U * step) {  // (b: the same for every lane)
+            const int p = p0 + b;
+            if (b + U * step < pieces) {
+                load(nxt, p + U * step);
+            } else if (task + (int)gridDim.x < tasks) {
+                rows_of(task + gridDim.x);
+                load(nxt, p0);
             }
-            const int64_t off = (int64_t)min(pu, pieces - 1) * 16;  // past the end the weights are zeros
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const uint4 x = QUANT ? codes[m * pieces + (off >> 4)] : *reinterpret_cast<const uint4 *>(q + m * ldq + off);
+            for (int u = 0; u < U; ++u) {
+                const int pu = p + u * step;
+                if (pu == pieces - 1 && (K & 15)) {
 #pragma unroll
-                for (int r = 0; r < ROWS; ++r) {
-                    int a = acc[r][m];
-                    a = dp4a((int)cur[u][r].x, (int)x.x, a);
-                    a = dp4a((int)cur[u][r].y, (int)x.y, a);
-                    a = dp4a((int)cur[u][r].z, (int)x.z, a);
-                    acc[r][m] = dp4a((int)cur[u][r].w, (int)x.w, a);
+                    for (int r = 0; r < ROWS; ++r) cur[u][r] = keep_codes(cur[u][r], K & 15);
+                }
+                const int64_t off = (int64_t)min(pu, pieces - 1) * 16;  // past the end the weights are zeros
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const uint4 x = QUANT ? codes[m * pieces + (off >> 4)] : *reinterpret_cast<const uint4 *>(q + m * ldq + off);
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) {
+                        int a = acc[r][m];
+                        a = dp4a((int)cur[u][r].x, (int)x.x, a);
+                        a = dp4a((int)cur[u][r].y, (int)x.y, a);
+                        a = dp4a((int)cur[u][r].z, (int)x.z, a);
+                        acc[r][m] = dp4a((int)cur[u][r].w, (int)x.w, a);
+                    }
                 }
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) cur[u][r] = nxt[u][r];
         }
+        // lane r*M + m ends with the warp's sum of row r, token m
+        int mine = 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) cur[u][r] = nxt[u][r];
-    }
-    // lane r*M + m ends with the warp's sum of row r, token m
-    int mine = 0;
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            const int s = __reduce_add_sync(~0u, acc[r][m]);
-            if (lane == r * M + m) mine = s;
+            for (int m = 0; m < M; ++m) {
+                const int s = __reduce_add_sync(~0u, acc[r][m]);
+                if (lane == r * M + m) mine = s;
+            }
+        if (split > 1) {
+            if (lane < ROWS * M) part_sum[warp][lane] = mine;
+            __syncthreads();
+            mine = 0;
+            for (int s = 0; s < split && !part && lane < ROWS * M; ++s) mine += part_sum[warp + s][lane];
+            __syncthreads();
         }
-    if (split > 1) {
-        if (lane < ROWS * M) part_sum[warp][lane] = mine;
-        __syncthreads();
-        if (part || lane >= ROWS * M) return;
-        mine = 0;
-        for (int s = 0; s < split; ++s) mine += part_sum[warp + s][lane];
-    }
-    const int64_t n = n0 + lane / M;
-    const int m = lane % M;
-    if (lane >= ROWS * M || n >= N) return;
-    float s = 0.0f;
-    if constexpr (QUANT) {
+        const int64_t n = ((int64_t)task * groups + group) * ROWS + lane / M;
+        const int m = lane % M;
+        if (!part && lane < ROWS * M && n < N) {
+            float s = 0.0f;
+            if constexpr (QUANT) {
 #pragma unroll
-        for (int i = 0; i < M; ++i)
-            if (i == m) s = scale[i];
-    } else {
-        s = sx[m];
+                for (int i = 0; i < M; ++i)
+                    if (i == m) s = scale[i];
+            } else {
+                s = sx[m];
+            }
+            float v = __fmul_rn(__fmul_rn((float)mine, s), sw[n]);
+            if (bias) v = __fadd_rn(v, bias[n]);
+            y[m * ldy + n] = from_f32<TY>(v);
+        }
     }
-    float v = __fmul_rn(__fmul_rn((float)mine, s), sw[n]);
-    if (bias) v = __fadd_rn(v, bias[n]);
-    y[m * ldy + n] = from_f32<TY>(v);
+}
+
+// A launch's split of a group's pieces, its tasks (of 8/split groups) and its time in batches of a warp: every
+// block walks its tasks, each so many batches and, for its sums and stores, about half a batch more.
+struct GemvPlan {
+    int split;
+    int64_t tasks, blocks;
+    double t;
+};
+static GemvPlan gemv_plan(int64_t N, int64_t K, int rows) {
+    const int64_t groups = (N + rows - 1) / rows, pieces = (K + 15) / 16, batch = rows == 1 ? 4 * 32 : 2 * 32;
+    GemvPlan best{};
+    for (int s = 1; s <= GV_WARPS; s *= 2) {
+        const int64_t tasks = (groups + GV_WARPS / s - 1) / (GV_WARPS / s), blocks = tasks < 152 * kGemvPerSm ? tasks : 152 * kGemvPerSm;
+        const double t = (double)((tasks + blocks - 1) / blocks) * ((double)((pieces + batch * s - 1) / (batch * s)) + 0.5);
+        if (s == 1 || t < best.t) best = {s, tasks, blocks, t};
+    }
+    return best;
 }
 
 template <int M, int ROWS, typename TY, typename TX>
-static kq_status launch_rows(const char *fn, const I8GemvArgs &a, int split, cudaStream_t st) {
-    const int per_block = GV_WARPS / split * ROWS;
+static kq_status launch_rows(const char *fn, const I8GemvArgs &a, const GemvPlan &p, cudaStream_t st) {
     const size_t smem = std::is_void<TX>::value ? 0 : (size_t)M * ((a.K + 15) / 16) * 16;  // 17 KB at most
-    const cudaError_t e = launch_beside(i8_gemv_kernel<M, ROWS, TY, TX>, dim3((unsigned)((a.N + per_block - 1) / per_block)),
-                                        dim3(GV_WARPS * 32), smem, dim3(1), st, a.rows, a.ldq, a.sx, a.w, a.ldw, a.sw, a.bias,
-                                        (int)a.N, (int)a.K, split, static_cast<TY *>(a.y), a.ldy, a.err, a.after_quant);
+    const cudaError_t e = launch_beside(i8_gemv_kernel<M, ROWS, TY, TX>, dim3((unsigned)p.blocks), dim3(GV_WARPS * 32), smem,
+                                        dim3(1), st, a.rows, a.ldq, a.sx, a.w, a.ldw, a.sw, a.bias, (int)a.N, (int)a.K, p.split,
+                                        (int)p.tasks, static_cast<TY *>(a.y), a.ldy, a.err, a.after_quant);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
     count_launch(R_I8);
     return KQ_OK;
@@ -165,14 +196,11 @@ static kq_status launch_rows(const char *fn, const I8GemvArgs &a, int split, cud
 
 template <int M, typename TY, typename TX>
 static kq_status launch_tokens(const char *fn, const I8GemvArgs &a, cudaStream_t st) {
-    // Warps that share a row group: enough to give every SM eight warps (152 * 8), while each still has two
-    // pieces for every lane ([4096 x 14336], five tokens: 12.8 us so, 14.3 with 16 warps an SM).  A product too
-    // narrow for that even so takes single rows.
-    constexpr int64_t want = 152 * 8;
-    int split = 1;
-    while (split < GV_WARPS && (a.N + 3) / 4 * split < want && a.K >= 512 * 2 * split) split *= 2;
-    if ((a.N + 3) / 4 * split * 2 <= want) return launch_rows<M, 1, TY, TX>(fn, a, split, st);
-    return launch_rows<M, 4, TY, TX>(fn, a, split, st);
+    // Four rows a warp; single rows where four would leave most blocks without a task (a batch has the same bytes
+    // either way).
+    const GemvPlan four = gemv_plan(a.N, a.K, 4), one = gemv_plan(a.N, a.K, 1);
+    if (four.blocks < 152 && one.blocks > four.blocks) return launch_rows<M, 1, TY, TX>(fn, a, one, st);
+    return launch_rows<M, 4, TY, TX>(fn, a, four, st);
 }
 
 template <typename TY>
