@@ -6,7 +6,7 @@
 // group share the rows' pieces and add their sums through shared memory (whole numbers: exact in any order).
 // Blocks stay and walk the row groups, so that a group's first pieces are on their way while the group before
 // it is summed up and stored.  The tokens' codes are small and shared by every warp: they come through L1.
-// [9728 x 2560], one token: 3.6 us back to back (some of it from L2); [4096 x 14336], five tokens: 12.8 us.
+// One token of [14336 x 4096]: 10.8 us, 5.5 TB/s; [4096 x 14336], five tokens: 13.0 us.
 //
 // TX other than void: the tokens come as rows of that type and every block quantises them itself, into shared
 // memory, while its first weights are on their way; a separate quantizer costs a launch (2.9 us more for one
@@ -35,10 +35,16 @@ __device__ __forceinline__ uint4 keep_codes(uint4 v, int valid) {
     return make_uint4(keep_bytes(v.x, valid), keep_bytes(v.y, valid - 4), keep_bytes(v.z, valid - 8), keep_bytes(v.w, valid - 12));
 }
 
-constexpr int kGemvPerSm = 2;  // blocks of an SM: up to 128 registers a thread, half of them for pieces under way
+// Weight rows of a warp and blocks of an SM, by tokens: what a warp's pieces under way and its ROWS*M sums
+// need in registers against how many warps there are to wait for memory.  [14336 x 4096]: one token 10.8 us with
+// 2 rows and 4 blocks, 10.9 with 4 and 2 ([4096 x 4096]: 3.1 against 4.1); three tokens 11.8 with 4 and 2, 11.9
+// with 2 and 4; eight tokens 14.1 with 2 and 2, 17.1 with 4 and 2, 16.2 with 2 and 3.  Blocks that quantise are
+// better few ([9728 x 2560], one fp32 token: 4.8 us with 4 and 2, 5.4 with 2 and 4).
+template <int M, typename TX> constexpr int kGemvRows = M == 3 || M == 4 || !std::is_void<TX>::value ? 4 : 2;
+template <int M, typename TX> constexpr int kGemvPerSm = M <= 2 && std::is_void<TX>::value ? 4 : 2;
 
 template <int M, int ROWS, typename TY, typename TX>
-__global__ void __launch_bounds__(GV_WARPS * 32, kGemvPerSm)
+__global__ void __launch_bounds__(GV_WARPS * 32, kGemvPerSm<M, TX>)
     i8_gemv_kernel(const void *__restrict__ rows, int64_t ldq, const float *__restrict__ sx, const int8_t *__restrict__ w,
                    int64_t ldw, const float *__restrict__ sw, const float *__restrict__ bias, int N, int K, int split, int tasks,
                    TY *__restrict__ y, int64_t ldy, unsigned long long *__restrict__ err, bool weights_first) {
@@ -172,11 +178,11 @@ struct GemvPlan {
     int64_t tasks, blocks;
     double t;
 };
-static GemvPlan gemv_plan(int64_t N, int64_t K, int rows) {
+static GemvPlan gemv_plan(int64_t N, int64_t K, int rows, int per_sm) {
     const int64_t groups = (N + rows - 1) / rows, pieces = (K + 15) / 16, batch = rows == 1 ? 4 * 32 : 2 * 32;
     GemvPlan best{};
     for (int s = 1; s <= GV_WARPS; s *= 2) {
-        const int64_t tasks = (groups + GV_WARPS / s - 1) / (GV_WARPS / s), blocks = tasks < 152 * kGemvPerSm ? tasks : 152 * kGemvPerSm;
+        const int64_t tasks = (groups + GV_WARPS / s - 1) / (GV_WARPS / s), blocks = tasks < 152 * per_sm ? tasks : 152 * per_sm;
         const double t = (double)((tasks + blocks - 1) / blocks) * ((double)((pieces + batch * s - 1) / (batch * s)) + 0.5);
         if (s == 1 || t < best.t) best = {s, tasks, blocks, t};
     }
@@ -196,11 +202,11 @@ static kq_status launch_rows(const char *fn, const I8GemvArgs &a, const GemvPlan
 
 template <int M, typename TY, typename TX>
 static kq_status launch_tokens(const char *fn, const I8GemvArgs &a, cudaStream_t st) {
-    // Four rows a warp; single rows where four would leave most blocks without a task (a batch has the same bytes
-    // either way).
-    const GemvPlan four = gemv_plan(a.N, a.K, 4), one = gemv_plan(a.N, a.K, 1);
-    if (four.blocks < 152 && one.blocks > four.blocks) return launch_rows<M, 1, TY, TX>(fn, a, one, st);
-    return launch_rows<M, 4, TY, TX>(fn, a, four, st);
+    // Single rows a warp where more would leave most SMs without a task (a batch has the same bytes either way).
+    constexpr int R = kGemvRows<M, TX>, S = kGemvPerSm<M, TX>;
+    const GemvPlan some = gemv_plan(a.N, a.K, R, S), one = gemv_plan(a.N, a.K, 1, S);
+    if (some.blocks < 152 && one.blocks > some.blocks) return launch_rows<M, 1, TY, TX>(fn, a, one, st);
+    return launch_rows<M, R, TY, TX>(fn, a, some, st);
 }
 
 template <typename TY>
