@@ -566,15 +566,14 @@ static PFN_cuTensorMapEncodeTiled_v12000 i8_encoder() {
 // only in whole multiples of their size).  Looked up once a device and split.
 template <typename C>
 static int i8_resident(int splits) {
-    static int cache[64][4] = {};
-    const int si = splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3;
+    static int cache[64][I8_MAX_SPLIT + 1] = {};
     const int fallback = 8 * (19 / (C::CG * splits));
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         cudaGetLastError();
         return fallback;
     }
-    if (!cache[dev][si]) {
+    if (!cache[dev][splits]) {
         auto kern = i8_tc_kernel<C, float>;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(C::CG, 1, splits);
@@ -593,9 +592,9 @@ static int i8_resident(int splits) {
             cudaGetLastError();
             n = fallback;
         }
-        cache[dev][si] = n;
+        cache[dev][splits] = n;
     }
-    return cache[dev][si];
+    return cache[dev][splits];
 }
 
 template <typename C, typename TY>
@@ -666,9 +665,9 @@ template <typename C>
 static I8Plan i8_plan(int64_t M, int64_t N, int64_t units, double unit, double reduction, bool spread) {
     I8Plan best = {I8_ROWS, 1, 1e30};
     const int64_t m_tiles = (M + C::NT - 1) / C::NT;
-    for (int s = 1; s <= I8_MAX_SPLIT / C::CG; s *= 2) {
+    for (int s = 1; s <= I8_MAX_SPLIT / C::CG; ++s) {
         const int64_t per = (units + s - 1) / s;
-        if (s > 1 && (per < 2 || per * (s - 1) >= units)) break;
+        if (s > 1 && (per < 2 || per * (s - 1) >= units)) continue;
         const int64_t groups = i8_resident<C>(s);
         int64_t rows = I8_ROWS;
         if (spread) rows = std::min<int64_t>(I8_ROWS, ((N + groups - 1) / groups + 7) / 8 * 8);
