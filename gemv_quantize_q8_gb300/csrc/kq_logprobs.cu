@@ -166,9 +166,11 @@ __device__ __forceinline__ float lp_kth(float v, int k, LpShared &sh) {
     return __shfl_sync(~0u, v, __ffs(__ballot_sync(~0u, rank == k - 1)) - 1);
 }
 
-// One cluster (gridDim.x CTAs, one or more) a row; blockIdx.y the row.
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
+// One cluster (gridDim.x CTAs, one or more) a row; blockIdx.y the row.  DEPTH rounds of loads are under way: one
+// where five CTAs share an SM, more where there are too few CTAs for that (300 rows of 32000 fp32, five
+// alternatives: 17.9 us with one, 10.9 with three).
+template <typename T, bool TOP, int DEPTH>
+__global__ void __launch_bounds__(kLpThreads, DEPTH == 1 ? 5 : DEPTH == 2 ? 3 : 2) lp_kernel(LpParams P) {
     constexpr int VEC = kVec<T>, NV = kLpVecs, NB = kLpBatch / VEC;  // NB: vectors of a batch
     extern __shared__ uint64_t buf[];  // TOP: kLpCap candidates, then the list of batches
     uint16_t *list = reinterpret_cast<uint16_t *>(buf + kLpCap);
@@ -221,11 +223,11 @@ __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
     };
 
     const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
-    uint4 next[NV];
-    auto fetch = [&](int u0, int v) {  // vectors u0 .. u0 + NB - 1 of the round at v
+    uint4 next[DEPTH][NV];
+    auto fetch = [&](int d, int u0, int v) {  // vectors u0 .. u0 + NB - 1 of the round at v
 #pragma unroll
         for (int u = u0; u < u0 + NB; ++u)
-            if (v + u * kLpThreads < v1) next[u] = TOP ? __ldg(xv + v + u * kLpThreads) : __ldcs(xv + v + u * kLpThreads);
+            if (v + u * kLpThreads < v1) next[d][u] = TOP ? __ldg(xv + v + u * kLpThreads) : __ldcs(xv + v + u * kLpThreads);
     };
     const int rounds = (v1 - v0 + NV * kLpThreads - 1) / (NV * kLpThreads);
     int shift = 0;  // rounds of one bit of `worth`
@@ -233,27 +235,33 @@ __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
     float largest = none, bound = none;
     uint32_t worth = 0;  // rounds (in groups) in which this thread's batch reached the bound
 #pragma unroll
-    for (int u0 = 0; u0 < NV; u0 += NB) fetch(u0, v0 + tid);
-    for (int j = 0; j < rounds; ++j) {
-        const int at = v0 + tid + j * NV * kLpThreads;
-        float top = none;
+    for (int d = 0; d < DEPTH; ++d)
 #pragma unroll
-        for (int u0 = 0; u0 < NV; u0 += NB) {
-            float v[kLpBatch];
+        for (int u0 = 0; u0 < NV; u0 += NB) fetch(d, u0, v0 + tid + d * NV * kLpThreads);
+    for (int j0 = 0; j0 < rounds; j0 += DEPTH) {
 #pragma unroll
-            for (int u = 0; u < NB; ++u) {
-                float f[VEC];
-                unpack16<T>(next[u0 + u], f);
+        for (int d = 0; d < DEPTH; ++d) {
+            const int j = j0 + d, at = v0 + tid + j * NV * kLpThreads;
+            if (j >= rounds) break;
+            float top = none;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) v[u * VEC + i] = at + (u0 + u) * kLpThreads < v1 ? f[i] : none;
+            for (int u0 = 0; u0 < NV; u0 += NB) {
+                float v[kLpBatch];
+#pragma unroll
+                for (int u = 0; u < NB; ++u) {
+                    float f[VEC];
+                    unpack16<T>(next[d][u0 + u], f);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) v[u * VEC + i] = at + (u0 + u) * kLpThreads < v1 ? f[i] : none;
+                }
+                fetch(d, u0, at + DEPTH * NV * kLpThreads);
+                top = fmaxf(top, count_in(v));
             }
-            fetch(u0, at + NV * kLpThreads);
-            top = fmaxf(top, count_in(v));
-        }
-        if (TOP) {
-            largest = fmaxf(largest, top);
-            if (top >= bound) worth |= 1u << (j >> shift);
-            if (j == 0 && rounds > 1) bound = lp_kth(largest, k, sh);
+            if (TOP) {
+                largest = fmaxf(largest, top);
+                if (top >= bound) worth |= 1u << (j >> shift);
+                if (j == 0 && rounds > 1) bound = lp_kth(largest, k, sh);
+            }
         }
     }
     const int odd_id = part == 0 && tid < rest ? (tid < head ? tid : nvec * VEC + tid) : -1;
@@ -381,15 +389,11 @@ __global__ void __launch_bounds__(kLpThreads, 5) lp_kernel(LpParams P) {
     }
 }
 
-template <typename T, bool TOP>
-static kq_status launch_lp(const char *fn, LpParams P, int64_t M, cudaStream_t st) {
+template <typename T, bool TOP, int DEPTH>
+static kq_status launch_lp(const char *fn, LpParams P, int64_t M, int parts, cudaStream_t st) {
     constexpr int smem = TOP ? kLpCap * 8 + kLpThreads * 32 * 2 : 0;
-    auto kern = lp_kernel<T, TOP>;
+    auto kern = lp_kernel<T, TOP, DEPTH>;
     cudaError_t e = smem ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
-    // CTAs that share a row: doubled up to two and a half an SM, while each has a whole round of its own (64 rows
-    // of 131072 bf16, 20 alternatives: four a row 13.5 us, eight 18.3, two 13.8; 167 of 49999: two 15.3, four 17.2)
-    int parts = 1;
-    while (parts < kLpMaxParts && M * parts * 2 <= 380 && P.V >= parts * 2 * kLpThreads * kLpVecs * kVec<T>) parts *= 2;
     for (int64_t r = 0; e == cudaSuccess && r < M; r += 65535) {  // the grid's second dimension ends there
         P.row0 = r;
         e = launch_beside(kern, dim3((unsigned)parts, (unsigned)(M - r < 65535 ? M - r : 65535)), dim3(kLpThreads), smem,
@@ -397,6 +401,19 @@ static kq_status launch_lp(const char *fn, LpParams P, int64_t M, cudaStream_t s
         if (e == cudaSuccess) count_launch(R_LOGPROBS);
     }
     return e == cudaSuccess ? KQ_OK : fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+}
+
+template <typename T, bool TOP>
+static kq_status share_rows(const char *fn, const LpParams &P, int64_t M, cudaStream_t st) {
+    // CTAs that share a row: doubled up to two and a half an SM, while each has a whole round of its own (64 rows
+    // of 131072 bf16, 20 alternatives: four a row 13.5 us, eight 18.3, two 13.8; 167 of 49999: two 15.3, four 17.2)
+    int parts = 1;
+    while (parts < kLpMaxParts && M * parts * 2 <= 380 && P.V >= parts * 2 * kLpThreads * kLpVecs * kVec<T>) parts *= 2;
+    // as many CTAs an SM as it takes to hold them all, not more: they then spread over the SMs (64 rows as above:
+    // 12.1 us with two an SM, 14.8 where a third would fit)
+    if (M * parts <= 152 * 2) return launch_lp<T, TOP, 3>(fn, P, M, parts, st);
+    if (M * parts <= 152 * 3) return launch_lp<T, TOP, 2>(fn, P, M, parts, st);
+    return launch_lp<T, TOP, 1>(fn, P, M, parts, st);
 }
 
 }  // namespace kq
@@ -424,6 +441,6 @@ extern "C" kq_status kq_logprobs(kq_dtype xt, const void *logits, int64_t ldx, i
     const LpParams P{logits, ldx, (int)V, targets, (int)n_targets, logprob, entropy, (int)top_k, top_ids, top_logprob, 0};
     return with_type(xt, [&](auto t) {
         using T = decltype(t);
-        return top_k ? launch_lp<T, true>(fn, P, M, (cudaStream_t)stream) : launch_lp<T, false>(fn, P, M, (cudaStream_t)stream);
+        return top_k ? share_rows<T, true>(fn, P, M, (cudaStream_t)stream) : share_rows<T, false>(fn, P, M, (cudaStream_t)stream);
     });
 }
