@@ -46,9 +46,9 @@ __device__ __forceinline__ float lp_key_value(uint64_t k) {
     return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
     float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -167,10 +167,10 @@ __device__ __forceinline__ float lp_kth(float v, int k, LpShared &sh) {
 }
 
 // One cluster (gridDim.x CTAs, one or more) a row; blockIdx.y the row.  DEPTH rounds of loads are under way: one
-// where five CTAs share an SM, more where there are too few CTAs for that (300 rows of 32000 fp32, five
+// where four or five CTAs share an SM, more where there are too few CTAs for that (300 rows of 32000 fp32, five
 // alternatives: 17.9 us with one, 10.9 with three).
 template <typename T, bool TOP, int DEPTH>
-__global__ void __launch_bounds__(kLpThreads, DEPTH == 1 ? 5 : DEPTH == 2 ? 3 : 2) lp_kernel(LpParams P) {
+__global__ void __launch_bounds__(kLpThreads, DEPTH == 1 ? (TOP ? 4 : 5) : DEPTH == 2 ? 3 : 2) lp_kernel(LpParams P) {
     constexpr int VEC = kVec<T>, NV = kLpVecs, NB = kLpBatch / VEC;  // NB: vectors of a batch
     extern __shared__ uint64_t buf[];  // TOP: kLpCap candidates, then the list of batches
     uint16_t *list = reinterpret_cast<uint16_t *>(buf + kLpCap);
@@ -191,9 +191,9 @@ __global__ void __launch_bounds__(kLpThreads, DEPTH == 1 ? 5 : DEPTH == 2 ? 3 : 
     float2 S2 = make_float2(0.0f, 0.0f), T2 = S2;
     // The statistics of a batch; returns its maximum (-inf for nothing but NaN and -inf).
     auto count_in = [&](const float (&v)[kLpBatch]) {
-        float top = v[0];
+        float top = max_nan(v[0], v[1], v[1]);
 #pragma unroll
-        for (int i = 1; i < kLpBatch; ++i) top = max_nan(top, v[i]);
+        for (int i = 2; i < kLpBatch; i += 2) top = max_nan(top, v[i], v[i + 1]);
         if (!(top <= st.m)) {
             if (isnan(top)) {
                 st.bad = 1.0f;
@@ -252,7 +252,12 @@ __global__ void __launch_bounds__(kLpThreads, DEPTH == 1 ? 5 : DEPTH == 2 ? 3 : 
                     float f[VEC];
                     unpack16<T>(next[d][u0 + u], f);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) v[u * VEC + i] = at + (u0 + u) * kLpThreads < v1 ? f[i] : none;
+                    for (int i = 0; i < VEC; ++i) v[u * VEC + i] = f[i];
+                }
+                if (j + 1 == rounds) {  // the last round may be short
+#pragma unroll
+                    for (int i = 0; i < kLpBatch; ++i)
+                        if (at + (u0 + i / VEC) * kLpThreads >= v1) v[i] = none;
                 }
                 fetch(d, u0, at + DEPTH * NV * kLpThreads);
                 top = fmaxf(top, count_in(v));
