@@ -9,8 +9,8 @@
 // One token of [14336 x 4096]: 10.8 us, 5.5 TB/s; [4096 x 14336], five tokens: 13.0 us.
 //
 // TX other than void: the tokens come as rows of that type and every block quantises them itself, into shared
-// memory, while its first weights are on their way; a separate quantizer costs a launch (2.9 us more for one
-// fp32 token of [9728 x 2560]).
+// memory, while its first weights are on their way: one fp32 token of [9728 x 2560] 4.9 us, 5.6 behind a
+// quantizer of its own; of [2560 x 9728] 6.7 and 8.3.
 #include <type_traits>
 
 #include "kq_i8_gemv.cuh"

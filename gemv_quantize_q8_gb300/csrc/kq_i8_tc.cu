@@ -12,7 +12,7 @@
 // 128 rows and loads half of the tokens.  The accumulator's two 128-token halves are filled in turn, four
 // units (of 128 K) each, so that one half's chunk is read out (1 us) while the other half computes (1.2 us;
 // with two units each it waited 0.8 us a chunk).
-// Small products: one CTA, up to 128 rows x 32, 64 or 128 tokens, two accumulators taking turns chunk by
+// Small products: one CTA, 128 rows x 32, 64 or 128 tokens, two accumulators taking turns chunk by
 // chunk; up to 64 tokens are converted from int8 by the CTA itself, without a panel.
 // Few tiles split K over a cluster; its CTAs exchange their int32 sums through distributed shared memory,
 // which is exact in any order.
@@ -32,7 +32,7 @@ namespace kq {
 
 using namespace sm100;
 
-constexpr int I8_ROWS = 128;      // weight rows of an MMA; a CTA's tile may have fewer
+constexpr int I8_ROWS = 128;      // weight rows of a CTA's tile: TMEM lanes
 constexpr int I8_KS = 64;         // K per activation tile (a 128-byte swizzled row of f16)
 constexpr int I8_UNIT = 128;      // K per unit: a weight tile, two activation tiles, one TMEM stage of A
 constexpr int I8_CHUNK = 8;       // units per chunk: 1024 elements, the longest exact fp32 accumulation
@@ -80,7 +80,6 @@ struct I8TcParams {
     void *y;
     int64_t ldy;
     int M, N, n_tiles, tiles;
-    int rows;                            // weight rows of a CTA's tile, a multiple of 8 up to I8_ROWS
     int units, units_per_split, nsplit;  // K in units of 128
     unsigned long long *err;
     bool after_prologue;  // the weights may be read before the kernel before this one has ended
@@ -226,25 +225,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (lane == 0) {
             bool ok = true;
             int g = 0, ahead = 0;
-            const uint32_t unit_bytes = (P.rows + (C::DIRECT ? C::NT : 0)) * I8_UNIT;
             if (C::DIRECT) {
                 // the weights of the first units start before the codes, which the kernel before this one
                 // may still be writing
                 ahead = min(C::WSTAGES, nu);
                 for (int u = 0; u < ahead; ++u) {
-                    mbar_arrive_expect_tx(&w_full[u], unit_bytes);
-                    tma_load_2d(sW + u * C::WT, &tmW, &w_full[u], (u0 + u) * I8_UNIT, (tile0 % P.n_tiles) * P.rows);
+                    mbar_arrive_expect_tx(&w_full[u], C::WT);
+                    tma_load_2d(sW + u * C::WT, &tmW, &w_full[u], (u0 + u) * I8_UNIT, (tile0 % P.n_tiles) * I8_ROWS);
                 }
                 grid_dependency_wait();
                 grid_launch_dependents();
             }
             for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
-                const int n0 = (tile % P.n_tiles) * (P.rows * C::CG) + r * P.rows;
+                const int n0 = (tile % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS;
                 for (int u = 0; u < nu; ++u, ++g) {
                     const int s = g % C::WSTAGES, x = (u0 + u) * I8_UNIT;
                     if (g >= ahead) {
                         if (!(ok = mbar_wait_sleep(&w_empty[s], ((g / C::WSTAGES) & 1) ^ 1, abort_flag, kI8WaitNs))) break;
-                        mbar_arrive_expect_tx(&w_full[s], unit_bytes);
+                        mbar_arrive_expect_tx(&w_full[s], C::WT);
                         tma_load_2d(sW + s * C::WT, &tmW, &w_full[s], x, n0);
                     }
                     if (C::DIRECT) tma_load_2d(sW + s * C::WT + I8_ROWS * I8_UNIT, &tmX, &w_full[s], x, 0);
@@ -396,8 +394,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (g % C::GROUPS != grp) continue;
                 const int ws = g % C::WSTAGES, s = g % C::STAGES;
                 if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, kI8WaitNs)))) break;
-                // 16-byte piece p of row `row` sits at piece p ^ (row & 7) (128-byte swizzle); rows past the
-                // tile's hold whatever was there: they end in lanes that nobody reads
+                // 16-byte piece p of row `row` sits at piece p ^ (row & 7) (128-byte swizzle)
                 const uint8_t *wr = sW + ws * C::WT + row * I8_UNIT;
                 uint4 v[8];
 #pragma unroll
@@ -440,12 +437,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (C::DIRECT && tid == 0 && blockIdx.x == 0 && z == 0) *P.err = 0ull;
         for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
             // this tile's scales, on their way while it is computed: lane l keeps the tokens l, l + 32
-            const int n = (tile % P.n_tiles) * (P.rows * C::CG) + r * P.rows + row;
+            const int n = (tile % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS + row;
             const int m0 = (tile / P.n_tiles) * C::NT + tok0;
             float sx[(C::COLS + 31) / 32];
 #pragma unroll
             for (int j = 0; j < (C::COLS + 31) / 32; ++j) sx[j] = m0 + lane + 32 * j < P.M ? P.sx[m0 + lane + 32 * j] : 0.0f;
-            const bool mine = row < P.rows && n < P.N;
+            const bool mine = n < P.N;
             const float sw = mine ? P.sw[n] : 0.0f, b = P.bias && mine ? P.bias[n] : 0.0f;
             for (int c0 = 0; c0 < nu; c0 += I8_CHUNK, ++job) {
                 const int buf = C::H == 2 ? h : job % C::NACC;
@@ -494,7 +491,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int i = 0; i < C::COLS; ++i) red[(col0 + i) * C::RED_LD + row] = acc[i];
         }
         // four rows a thread, the same in every round, and all splits' loads at once
-        const int n = (tile0 % P.n_tiles) * (P.rows * C::CG) + r * P.rows + lane * 4;
+        const int n = (tile0 % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS + lane * 4;
         float sw[4], bias[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -529,7 +526,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int j = 0; j < 4; ++j) {
                 float f = __fmul_rn(__fmul_rn((float)sum[j], sx), sw[j]);
                 if (P.bias) f = __fadd_rn(f, bias[j]);
-                if (lane * 4 < P.rows && n + j < P.N) y[j] = from_f32<TY>(f);
+                if (n + j < P.N) y[j] = from_f32<TY>(f);
             }
         }
     }
@@ -598,14 +595,14 @@ static int i8_resident(int splits) {
 }
 
 template <typename C, typename TY>
-static kq_status i8_launch(const char *fn, const I8TcArgs &a, int rows, int splits, cudaStream_t st) {
+static kq_status i8_launch(const char *fn, const I8TcArgs &a, int splits, cudaStream_t st) {
     auto encode = i8_encoder();
     if (!encode) return fail(KQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", fn);
     CUtensorMap tmW, tmX;
     const cuuint32_t es[2] = {1, 1};
     {
         const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.N}, strides[1] = {(cuuint64_t)a.ldw};
-        const cuuint32_t box[2] = {I8_UNIT, (cuuint32_t)rows};
+        const cuuint32_t box[2] = {I8_UNIT, I8_ROWS};
         const CUresult e = encode(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(a.w), dims, strides, box, es,
                                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -629,8 +626,7 @@ static kq_status i8_launch(const char *fn, const I8TcArgs &a, int rows, int spli
     I8TcParams p{};
     p.sx = a.sx; p.sw = a.sw; p.bias = a.bias; p.y = a.y; p.ldy = a.ldy;
     p.M = (int)a.M; p.N = (int)a.N;
-    p.rows = rows;
-    p.n_tiles = (int)((a.N + rows * C::CG - 1) / (rows * C::CG));
+    p.n_tiles = (int)((a.N + I8_ROWS * C::CG - 1) / (I8_ROWS * C::CG));
     const int64_t tiles = (int64_t)p.n_tiles * ((a.M + C::NT - 1) / C::NT);
     if (tiles > 0x7fffffff / C::CG) return fail(KQ_ERR_INVALID_ARG, "%s: too many tiles", fn);
     p.tiles = (int)tiles;
@@ -650,32 +646,24 @@ static kq_status i8_launch(const char *fn, const I8TcArgs &a, int rows, int spli
     return KQ_OK;
 }
 
-// How a product is shared out: weight rows of a CTA's tile, splits of K, and the time that the estimate below
-// gives it (us): the CTAs of a wave walk `per` units at `unit` each, 4 us go to starting and ending, a split
-// adds its reduction.
+// How a product is shared out: splits of K, and the time that the estimate below gives it (us): the CTAs of a
+// wave walk `per` units at `unit` each, 4 us go to starting and ending, a split adds its reduction.
 struct I8Plan {
-    int rows, splits;
+    int splits;
     double t;
 };
 
-// The best plan of form C.  `unit`: measured time of a 128-row unit.  Up to 128 tokens the weights' bytes bound
-// the product, and an SM reads some 38 GB/s of them when all do; so (`spread`) a tile's rows are chosen to give
-// every SM the same share (an MMA computes 128 rows whether they are there or not).
 template <typename C>
-static I8Plan i8_plan(int64_t M, int64_t N, int64_t units, double unit, double reduction, bool spread) {
-    I8Plan best = {I8_ROWS, 1, 1e30};
-    const int64_t m_tiles = (M + C::NT - 1) / C::NT;
+static I8Plan i8_plan(int64_t M, int64_t N, int64_t units, double unit, double reduction) {
+    I8Plan best = {1, 1e30};
+    const int64_t tiles = (N + I8_ROWS * C::CG - 1) / (I8_ROWS * C::CG) * ((M + C::NT - 1) / C::NT);
     for (int s = 1; s <= I8_MAX_SPLIT / C::CG; ++s) {
         const int64_t per = (units + s - 1) / s;
         if (s > 1 && (per < 2 || per * (s - 1) >= units)) continue;
-        const int64_t groups = i8_resident<C>(s);
-        int64_t rows = I8_ROWS;
-        if (spread) rows = std::min<int64_t>(I8_ROWS, ((N + groups - 1) / groups + 7) / 8 * 8);
-        const int64_t waves = ((N + rows * C::CG - 1) / (rows * C::CG) * m_tiles + groups - 1) / groups;
-        const double step = spread ? std::max(unit, (double)rows * I8_UNIT / 38e3) : unit;
+        const int64_t groups = i8_resident<C>(s), waves = (tiles + groups - 1) / groups;
         // (unsplit CTAs are persistent: they start and end once; clusters of a split do in every wave)
-        const double t = s == 1 ? 4.0 + (double)(waves * per) * step : (double)waves * (4.0 + (double)per * step + reduction);
-        if (t < best.t) best = {(int)rows, s, t};
+        const double t = s == 1 ? 4.0 + (double)(waves * per) * unit : (double)waves * (4.0 + (double)per * unit + reduction);
+        if (t < best.t) best = {s, t};
     }
     return best;
 }
@@ -684,18 +672,17 @@ kq_status i8_tc_product(const char *fn, const I8TcArgs &a, cudaStream_t st) {
     return with_type(a.yt, [&](auto t) {
         using TY = decltype(t);
         const int64_t units = (a.K + I8_UNIT - 1) / I8_UNIT;
-        auto go = [&](auto c, I8Plan p) { return i8_launch<decltype(c), TY>(fn, a, p.rows, p.splits, st); };
-        // [14336 x 4096]: 64 tokens on 112 tiles of 128 rows 23.6 us, on 150 of 96 rows 21.0; [4096 x 4096], 16
-        // tokens: four splits 9.0, unsplit 14.6
-        if (a.M <= 32) return go(I8One32{}, i8_plan<I8One32>(a.M, a.N, units, 0.25, 3.0, true));
-        if (a.M <= 64) return go(I8One64{}, i8_plan<I8One64>(a.M, a.N, units, 0.25, 3.0, true));
-        const I8Plan one = i8_plan<I8One128>(a.M, a.N, units, 0.40, 3.5, a.M <= 128);
+        auto go = [&](auto c, I8Plan p) { return i8_launch<decltype(c), TY>(fn, a, p.splits, st); };
+        // (16 tokens, [4096 x 4096]: four splits 8.1 us, unsplit 14.8; [4096 x 14336]: 17.3 and 43.4)
+        if (a.M <= 32) return go(I8One32{}, i8_plan<I8One32>(a.M, a.N, units, 0.43, 3.0));
+        if (a.M <= 64) return go(I8One64{}, i8_plan<I8One64>(a.M, a.N, units, 0.43, 3.0));
+        const I8Plan one = i8_plan<I8One128>(a.M, a.N, units, 0.43, 3.5);
         if (a.M <= 128) return go(I8One128{}, one);
         // A pair does a unit of four times the work in 0.62 us, but its tiles are fewer and its reduction is
-        // dearer.  [4096 x 4096]: 512 tokens 22.7 us by (split) pairs, MEASURED by single CTAs; 2048 tokens of
-        // [14336 x 4096] 138 us by pairs, 214 by single CTAs
-        const I8Plan pair = i8_plan<I8Pair>(a.M, a.N, units, 0.62, 6.0, false);
-        return pair.t + 1.0 <= one.t ? go(I8Pair{}, pair) : go(I8One128{}, one);
+        // dearer.  [4096 x 4096]: 256 tokens 18.6 us by pairs, 15.7 by single CTAs, 512 tokens 23.2 and 20.7;
+        // [14336 x 4096]: 384 tokens 50.4 and 46.7, 2048 tokens 138 and 166
+        const I8Plan pair = i8_plan<I8Pair>(a.M, a.N, units, 0.62, 6.0);
+        return pair.t + 3.0 <= one.t ? go(I8Pair{}, pair) : go(I8One128{}, one);
     });
 }
 
