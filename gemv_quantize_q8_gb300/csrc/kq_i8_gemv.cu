@@ -6,11 +6,11 @@
 // group share the rows' pieces and add their sums through shared memory (whole numbers: exact in any order).
 // Blocks stay and walk the row groups, so that a group's first pieces are on their way while the group before
 // it is summed up and stored.  The tokens' codes are small and shared by every warp: they come through L1.
-// One token of [14336 x 4096]: 10.8 us, 5.5 TB/s; [4096 x 14336], five tokens: 13.0 us.
+// One token of [14336 x 4096]: 10.7 us, 5.5 TB/s; [4096 x 14336], five tokens: 12.9 us.
 //
 // TX other than void: the tokens come as rows of that type and every block quantises them itself, into shared
 // memory, while its first weights are on their way: one fp32 token of [9728 x 2560] 4.9 us, 5.6 behind a
-// quantizer of its own; of [2560 x 9728] 6.7 and 8.3.
+// quantizer of its own; of [2560 x 9728] 6.5 and 8.3.
 #include <type_traits>
 
 #include "kq_i8_gemv.cuh"
@@ -36,10 +36,10 @@ __device__ __forceinline__ uint4 keep_codes(uint4 v, int valid) {
 }
 
 // Weight rows of a warp and blocks of an SM, by tokens: what a warp's pieces under way and its ROWS*M sums
-// need in registers against how many warps there are to wait for memory.  [14336 x 4096]: one token 10.8 us with
+// need in registers against how many warps there are to wait for memory.  [14336 x 4096]: one token 10.7 us with
 // 2 rows and 4 blocks, 10.9 with 4 and 2 ([4096 x 4096]: 3.1 against 4.1); three tokens 11.8 with 4 and 2, 11.9
 // with 2 and 4; eight tokens 14.1 with 2 and 2, 17.1 with 4 and 2, 16.2 with 2 and 3.  Blocks that quantise are
-// better few ([9728 x 2560], one fp32 token: 4.8 us with 4 and 2, 5.4 with 2 and 4).
+// better few ([9728 x 2560], one fp32 token: 4.9 us with 4 and 2, 5.4 with 2 and 4).
 template <int M, typename TX> constexpr int kGemvRows = M == 3 || M == 4 || !std::is_void<TX>::value ? 4 : 2;
 template <int M, typename TX> constexpr int kGemvPerSm = M <= 2 && std::is_void<TX>::value ? 4 : 2;
 

@@ -4,12 +4,14 @@
 // -128..127 are exact in f16, their products in fp32, and a sum of 1024 products stays within
 // 1024 * 2^14 = 2^24, where fp32 still holds every integer.  So an accumulator in tensor memory runs over
 // 1024 elements of K at most (a chunk) and is then added to int32 sums in the epilogue's registers.
-//   * weights (int8 rows) reach shared memory by TMA; converter warps turn 128 rows x 64 codes into f16
+//   * weights (int8 rows) reach shared memory by TMA; converter warps turn 128 rows x 128 codes into f16
 //     and store them into tensor memory, where the MMA reads them as its A operand.
 //   * activations come as an f16 panel (written once by a prologue), by TMA, as the B operand.
 //   * outputs: weight rows = TMEM lanes, tokens = columns.
 // Large products: a pair of CTAs (cta_group::2) computes 256 rows x 256 tokens; each CTA converts its own
-// 128 rows and loads half of the tokens.  The accumulator's two 128-token halves are filled in turn, four
+// 128 rows and loads half of the tokens.  [14336 x 4096], 2048 tokens: 135 us, 1.78 PFLOP/s, the f16 pipe's rate.
+// (Tiles of fewer tokens where they cover a batch with less: an MMA of 96 columns takes nearly as long as one of
+// 128; 768 tokens in three waves of 192s 69 us, of 256s 74, and the 256s' 5% slower for the choice.)  The accumulator's two 128-token halves are filled in turn, four
 // units (of 128 K) each, so that one half's chunk is read out (1 us) while the other half computes (1.2 us;
 // with two units each it waited 0.8 us a chunk).
 // Small products: one CTA, 128 rows x 32, 64 or 128 tokens, two accumulators taking turns chunk by
@@ -679,8 +681,8 @@ kq_status i8_tc_product(const char *fn, const I8TcArgs &a, cudaStream_t st) {
         const I8Plan one = i8_plan<I8One128>(a.M, a.N, units, 0.43, 3.5);
         if (a.M <= 128) return go(I8One128{}, one);
         // A pair does a unit of four times the work in 0.62 us, but its tiles are fewer and its reduction is
-        // dearer.  [4096 x 4096]: 256 tokens 18.6 us by pairs, 15.7 by single CTAs, 512 tokens 23.2 and 20.7;
-        // [14336 x 4096]: 384 tokens 50.4 and 46.7, 2048 tokens 138 and 166
+        // dearer.  [4096 x 4096]: 256 tokens 18.6 us by pairs, 15.7 by single CTAs, 512 tokens 23.2 and 20.5;
+        // [14336 x 4096]: 384 tokens 50.4 and 45.8, 2048 tokens 135 and 166
         const I8Plan pair = i8_plan<I8Pair>(a.M, a.N, units, 0.62, 6.0);
         return pair.t + 3.0 <= one.t ? go(I8Pair{}, pair) : go(I8One128{}, one);
     });

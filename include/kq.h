@@ -320,7 +320,7 @@ KQ_API kq_status kq_moe_weighted_sum(const float *y_slots, const float *w, int64
  * scale an output channel, and both stay plain row-major int8 (no repack).  Rows of codes start on
  * 16-byte boundaries (q and w 16-byte aligned, ldq and ldw multiples of 16); K itself is free (1 to
  * 131071, so that any sum of K products fits 32 bits), and the bytes from K to the end of a row are
- * never used.
+ * never used (those up to K rounded up to 16 may be read, and are part of q's and w's last rows too).
  *
  *   y[m][n] = ((float)(sum_k q[m][k]*w[n][k]) * sx[m]) * sw[n] + bias[n]
  *
@@ -368,8 +368,9 @@ KQ_API kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const i
  * (both may be column ranges of one product's rows); n_q or n_k may be 0 (its pointers are then unused).
  * q_gamma, k_gamma: fp32 [D] or NULL.  cos_tab, sin_tab: fp32 [n_pos][rot/2] (unused when rot = 0).
  * q_out, k_out: of type yt, row strides ldqo and ldko; an output may be its own input (same pointer, type
- * and stride), so a cache row can be written directly.  D is even, 2 .. 1024; rot is even, 0 .. D.  M*(n_q + n_k) is below 2^31.  A
- * position outside [0, n_pos) has no angle: its token's rows are written as NaN. */
+ * and stride), so a cache row can be written directly.  D is even, 2 .. 1024; rot is even,
+ * 0 .. D.  M*(n_q + n_k) is below 2^31.  A position outside [0, n_pos) has no angle: its token's rows are written
+ * as NaN. */
 KQ_API kq_status kq_qk_norm_rope(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, int64_t M,
                                  int64_t n_q, int64_t n_k, int64_t D, const float *q_gamma, const float *k_gamma,
                                  float eps, const int32_t *positions, const float *cos_tab, const float *sin_tab,
