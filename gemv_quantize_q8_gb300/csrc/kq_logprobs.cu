@@ -372,25 +372,24 @@ __global__ void __launch_bounds__(kLpThreads, DEPTH == 1 ? (TOP ? 4 : 5) : DEPTH
         const int t = P.targets[row * P.n_targets + j];
         P.logprob[row * P.n_targets + j] = t < 0 ? 0.0f : t >= V ? NAN : lp_of(to_f32(x[t]));
     }
-    if (TOP && !sh.best[k - 1]) {
+    // from here on the list is warp 0's alone (it has 32 entries at most)
+    if (TOP && tid < 32) {
+        int n = __popc(__ballot_sync(~0u, sh.best[lane] != 0));
         // fewer than k tokens are neither masked nor NaN: the first of those fill up, in the order of their ids
-        if (tid < 32) {
-            int n = __popc(__ballot_sync(~0u, sh.best[lane] != 0));
-            for (int i = 0; i < V && n < k; i += 32) {
-                const float v = i + lane < V ? to_f32(x[i + lane]) : 0.0f;
-                const bool low = isnan(v) || v == none;
-                const unsigned votes = __ballot_sync(~0u, low);
-                const int at = n + __popc(votes & ((1u << lane) - 1u));
-                if (low && at < k) sh.best[at] = lp_key(none, i + lane);
-                n += __popc(votes);
-            }
+        for (int i = 0; i < V && n < k; i += 32) {
+            const float v = i + lane < V ? to_f32(x[i + lane]) : 0.0f;
+            const bool low = isnan(v) || v == none;
+            const unsigned votes = __ballot_sync(~0u, low);
+            const int at = n + __popc(votes & ((1u << lane) - 1u));
+            if (low && at < k) sh.best[at] = lp_key(none, i + lane);
+            n += __popc(votes);
         }
-        __syncthreads();
-    }
-    if (TOP && tid < k) {
-        const uint64_t key = sh.best[tid];
-        P.top_ids[row * k + tid] = lp_key_id(key);
-        P.top_logprob[row * k + tid] = lp_of(lp_key_value(key));
+        __syncwarp();
+        if (lane < k) {
+            const uint64_t key = sh.best[lane];
+            P.top_ids[row * k + lane] = lp_key_id(key);
+            P.top_logprob[row * k + lane] = lp_of(lp_key_value(key));
+        }
     }
 }
 

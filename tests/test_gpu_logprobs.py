@@ -185,3 +185,17 @@ def test_again_gives_the_same_bits():
             outs.append((ent.cpu(), top.cpu()))
         for e, t in outs[1:]:
             assert torch.equal(e, outs[0][0]) and torch.equal(t, outs[0][1])
+
+
+@pytest.mark.parametrize("M", [2, 330])
+@pytest.mark.parametrize("left", [0, 1, 19])
+def test_few_tokens_left_and_many_targets(M, left):
+    """Rows with fewer unmasked tokens than alternatives, whose list is filled up while the block's other warps still look
+    targets up: several rounds of them for some warps, one fewer for others."""
+    V, k, T = 5003, 20, 700
+    g = np.random.default_rng(left)
+    x = torch.full((M, V), float("-inf"))
+    for r in range(M):
+        x[r, torch.from_numpy(g.permutation(V)[:left])] = torch.from_numpy(g.standard_normal(left).astype(np.float32))
+    x[0, 5] = float("nan")
+    check(x, g.integers(0, V, (M, T)), k, "f32")
