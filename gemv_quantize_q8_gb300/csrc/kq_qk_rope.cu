@@ -70,6 +70,11 @@ struct Four {
 __device__ __forceinline__ Four mul(Four a, Four b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
 __device__ __forceinline__ Four fma(Four a, Four b, Four c) { return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)}; }
 __device__ __forceinline__ Four all(float v) { return {make_float2(v, v), make_float2(v, v)}; }
+// v where the mask is all ones, 0 where it is 0.
+__device__ __forceinline__ Four masked(Four v, uint32_t mask) {
+    auto m = [mask](float f) { return __uint_as_float(__float_as_uint(f) & mask); };
+    return {make_float2(m(v.lo.x), m(v.lo.y)), make_float2(m(v.hi.x), m(v.hi.y))};
+}
 template <typename T>
 __device__ __forceinline__ Four load4(const T *p) {
     float v[4];
@@ -86,7 +91,11 @@ __device__ __forceinline__ void store4(T *p, Four f) {
 // [hi, hi + 4).  Pairs 0 .. rot/8 - 1 are rotated: lo = 4j, hi = lo + rot/2 (halves) or lo = 8j, hi = lo + 4
 // (neighbours); the following pairs cover rot .. D.
 // The lanes take G heads of their token (queries or keys, not both): angles and gamma are read once for them.
-template <typename TX, typename TY, bool PAIRS, int R, int LANES, int G>
+// PART: rot < D.  Lanes past the rotated part go through the rotation's arithmetic too, by an angle of 0 (c = 1, s = 0),
+// but with 0 for their partners: an infinity or NaN times s = 0 would be a NaN.  (8192 tokens, 40 heads of 128, half of
+// them rotated, fp32 to bf16: 40.0 us with the masks, 38.5 with a branch a head, 37.1 with neither; bf16: 31.1, 32.3
+// and 30.2; heads of 80 in f16: 13.6, 14.4 and 13.5.  So whole heads have a form without.)
+template <typename TX, typename TY, bool PAIRS, bool PART, int R, int LANES, int G>
 __global__ void __launch_bounds__(kQkThreads) qk_kernel(QkParams P) {
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
@@ -144,21 +153,28 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(QkParams P) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             Four u = mul(mul(a[g][r], rs), ga[r]), w = mul(mul(b[g][r], rs), gb[r]);
+            const uint32_t partners = !PART || lane + LANES * r < rotated ? ~0u : 0u;
+            Four u0, w0;  // the elements' own shares, then their partners'
             if (PAIRS) {  // angles: c.lo for the pairs of u, c.hi for those of w
-                auto turn = [](float2 v, float c, float s) {
-                    return fma2(make_float2(v.y, v.x), make_float2(-s, s), mul2(v, make_float2(c, c)));
-                };
-                u = {turn(u.lo, c[r].lo.x, s[r].lo.x), turn(u.hi, c[r].lo.y, s[r].lo.y)};
-                w = {turn(w.lo, c[r].hi.x, s[r].hi.x), turn(w.hi, c[r].hi.y, s[r].hi.y)};
+                auto twice = [](float2 v) { return Four{make_float2(v.x, v.x), make_float2(v.y, v.y)}; };
+                auto signs = [](float2 v) { return Four{make_float2(-v.x, v.x), make_float2(-v.y, v.y)}; };
+                auto swap = [](Four v) { return Four{make_float2(v.lo.y, v.lo.x), make_float2(v.hi.y, v.hi.x)}; };
+                u0 = mul(u, twice(c[r].lo));
+                w0 = mul(w, twice(c[r].hi));
+                if (PART) u = masked(u, partners), w = masked(w, partners);
+                u0 = fma(swap(u), signs(s[r].lo), u0);
+                w0 = fma(swap(w), signs(s[r].hi), w0);
             } else {
                 const Four minus = {make_float2(-s[r].lo.x, -s[r].lo.y), make_float2(-s[r].hi.x, -s[r].hi.y)};
-                const Four u0 = u;
-                u = fma(w, minus, mul(u0, c[r]));
-                w = fma(u0, s[r], mul(w, c[r]));
+                u0 = mul(u, c[r]);
+                w0 = mul(w, c[r]);
+                if (PART) u = masked(u, partners), w = masked(w, partners);
+                u0 = fma(w, minus, u0);
+                w0 = fma(u, s[r], w0);
             }
             if (g < n && lane + LANES * r < np) {
-                store4(y + g * P.D + lo[r], u);
-                store4(y + g * P.D + hi[r], w);
+                store4(y + g * P.D + lo[r], u0);
+                store4(y + g * P.D + hi[r], w0);
             }
         }
     }
@@ -228,7 +244,8 @@ static cudaError_t launch_qk(const QkParams &P, bool pairs, bool aligned4, cudaS
         q.shift = 31 + l;
         q.magic = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
         q.inv_d = 1.0f / (float)P.D;
-        return launch_beside(qk_kernel<TX, TY, decltype(pr)::value, R, L, G>, dim3((unsigned)blocks), dim3(kQkThreads), 0, dim3(1), st, q);
+        auto kern = P.rot < P.D ? qk_kernel<TX, TY, decltype(pr)::value, true, R, L, G> : qk_kernel<TX, TY, decltype(pr)::value, false, R, L, G>;
+        return launch_beside(kern, dim3((unsigned)blocks), dim3(kQkThreads), 0, dim3(1), st, q);
     };
     auto heads = [&](auto pr, auto rounds, auto lanes) {
         // four heads a lane group once that still fills every SM's threads (152 * 2048): 8192 tokens of 40

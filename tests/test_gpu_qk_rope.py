@@ -138,3 +138,21 @@ def test_offsets_past_32_bits():
     ref, size = reference(x.double().numpy()[:, None], np.ones(128), 0.0, pos, cos, sin, 128, False)
     got = out.view(M, ld)[:, :128].double().cpu().numpy()[:, None]
     assert (np.abs(got - ref) <= 72 * U * size + 2.0 ** -8 * 1.001 * np.abs(ref) + 1e-30).all()
+
+
+@pytest.mark.parametrize("D,rot", [(128, 0), (128, 64), (80, 40), (512, 128), (72, 36)])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("gamma", [False, True])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_infinities_and_nan_past_the_rotated_part(D, rot, pairs, gamma, offset):
+    """Elements from rot on are normed only: an infinity or NaN among them stays where it is (without a norm), or is the
+    only NaN of its head (with one, whose factor is then 0).  offset 1: rows that no vector form takes give the same."""
+    M, Hq, Hk, n = 9, 2, 1, D - rot
+    g = np.random.default_rng(D + rot)
+    x = torch.from_numpy(g.standard_normal((M, 3 * D)).astype(np.float32))
+    for m in range(M):  # (a NaN makes a normed head NaN as a whole)
+        x[m, m % 3 * D + rot + (5 * m) % n] = [float("inf"), float("-inf"), float("inf") if gamma else float("nan")][m % 3]
+    outs = check(M, Hq, Hk, D, rot, pairs, "f32", "f32", gamma=gamma, offset=offset, x=x.clone())
+    if not gamma:
+        got = torch.cat([o.cpu().reshape(M, -1) for o in outs], 1).view(M, 3, D)[:, :, rot:]
+        assert torch.equal(got.nan_to_num(nan=12345.0), x.view(M, 3, D)[:, :, rot:].nan_to_num(nan=12345.0))
