@@ -291,10 +291,13 @@ extern "C" kq_status kq_qk_norm_rope(kq_dtype xt, const void *q, int64_t ldq, co
         return fail(KQ_ERR_INVALID_ARG, "%s: ldk=%lld or ldko=%lld is less than n_k*D", fn, (long long)ldk, (long long)ldko);
     if (rot && (!positions || !cos_tab || !sin_tab || n_pos <= 0))
         return fail(KQ_ERR_INVALID_ARG, "%s: a rotation needs positions, cos_tab, sin_tab and n_pos > 0", fn);
+    // what the call does not use is not looked at
+    if (!n_q) q = q_out = nullptr, q_gamma = nullptr, ldq = ldqo = 0;
+    if (!n_k) k = k_out = nullptr, k_gamma = nullptr, ldk = ldko = 0;
+    if (!rot) positions = nullptr, cos_tab = sin_tab = nullptr;
     const size_t xb = value_bytes(xt), yb = value_bytes(yt);
-    if ((n_q && (!aligned(q, xb) || !aligned(q_out, yb))) || (n_k && (!aligned(k, xb) || !aligned(k_out, yb))) ||
-        (q_gamma && !aligned(q_gamma, 4)) || (k_gamma && !aligned(k_gamma, 4)) ||
-        (rot && (!aligned(positions, 4) || !aligned(cos_tab, 4) || !aligned(sin_tab, 4))))
+    if (!aligned(q, xb) || !aligned(q_out, yb) || !aligned(k, xb) || !aligned(k_out, yb) || !aligned(q_gamma, 4) ||
+        !aligned(k_gamma, 4) || !aligned(positions, 4) || !aligned(cos_tab, 4) || !aligned(sin_tab, 4))
         return fail(KQ_ERR_ALIGNMENT, "%s: a pointer is not aligned to its elements", fn);
     QkParams P{};
     P.x[0] = q; P.x[1] = k; P.y[0] = q_out; P.y[1] = k_out;
@@ -305,9 +308,9 @@ extern "C" kq_status kq_qk_norm_rope(kq_dtype xt, const void *q, int64_t ldq, co
     if (M > 0x7fffffff || M * (n_q + n_k) > 0x7fffffff)
         return fail(KQ_ERR_INVALID_ARG, "%s: M=%lld is too large", fn, (long long)M);
     // every head's first element on a boundary of four elements, and the tables' rows on 16 bytes
-    bool al = aligned(cos_tab, 16) && aligned(sin_tab, 16) && aligned(q_gamma, 16) && aligned(k_gamma, 16);
-    if (n_q) al = al && aligned(q, 4 * xb) && ldq % 4 == 0 && aligned(q_out, 4 * yb) && ldqo % 4 == 0;
-    if (n_k) al = al && aligned(k, 4 * xb) && ldk % 4 == 0 && aligned(k_out, 4 * yb) && ldko % 4 == 0;
+    const bool al = aligned(cos_tab, 16) && aligned(sin_tab, 16) && aligned(q_gamma, 16) && aligned(k_gamma, 16) &&
+                    aligned(q, 4 * xb) && aligned(k, 4 * xb) && aligned(q_out, 4 * yb) && aligned(k_out, 4 * yb) &&
+                    ldq % 4 == 0 && ldk % 4 == 0 && ldqo % 4 == 0 && ldko % 4 == 0;
     return with_type(xt, [&](auto tx) {
         return with_type(yt, [&](auto ty) {
             const cudaError_t e = launch_qk<decltype(tx), decltype(ty)>(P, pairs != 0, al, (cudaStream_t)stream);

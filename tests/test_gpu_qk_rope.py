@@ -156,3 +156,19 @@ def test_infinities_and_nan_past_the_rotated_part(D, rot, pairs, gamma, offset):
     if not gamma:
         got = torch.cat([o.cpu().reshape(M, -1) for o in outs], 1).view(M, 3, D)[:, :, rot:]
         assert torch.equal(got.nan_to_num(nan=12345.0), x.view(M, 3, D)[:, :, rot:].nan_to_num(nan=12345.0))
+
+
+def test_pointers_of_nothing_are_not_looked_at():
+    """With no key heads the keys' gamma is unused, and without a rotation the tables: whatever they are, the call is taken
+    and gives the bits of one without them."""
+    M, D = 5, 128
+    g = torch.Generator(device=DEV)
+    g.manual_seed(0)
+    x, gamma = torch.randn((M, 2 * D), generator=g, device=DEV), torch.rand(D, generator=g, device=DEV)
+    outs = []
+    for odd in (None, torch.zeros(4, device=DEV).data_ptr() + 1):
+        y = torch.empty((M, 2 * D), device=DEV)
+        kq.kq_qk_norm_rope(kq.F32, x, 2 * D, odd, 0, M, 2, 0, D, gamma, odd, 1e-6, odd, odd, odd, 0, 0, 0, kq.F32, y, 2 * D, odd, 0)
+        kq.kq_qk_norm_rope(kq.F32, odd, 0, y, 2 * D, M, 0, 2, D, odd, gamma, 1e-6, odd, odd, odd, 0, 0, 0, kq.F32, odd, 0, y, 2 * D)
+        outs.append(y)
+    assert torch.equal(outs[0], outs[1])
