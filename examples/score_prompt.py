@@ -81,7 +81,8 @@ class Decoder:
         given = tokens[1:].int().contiguous()
         logprob, entropy = torch.empty(M, device=DEV), torch.empty(M, device=DEV)
         ids, best = torch.empty((M, top), dtype=torch.int32, device=DEV), torch.empty((M, top), device=DEV)
-        kq.kq_logprobs(kq.F32, logits, self.vocab, M, self.vocab, given, 1, logprob, entropy, top, ids, best)
+        if M:  # (the only token of a prompt follows nothing)
+            kq.kq_logprobs(kq.F32, logits, self.vocab, M, self.vocab, given, 1, logprob, entropy, top, ids, best)
         return logprob, entropy, ids, best
 
 

@@ -71,3 +71,10 @@ def test_example_runs(capsys):
     _load().main()
     out = capsys.readouterr().out
     assert "perplexity" in out and out.count("position") == 3
+
+
+def test_prompt_of_one_token():
+    """Nothing precedes the only token, so nothing is scored: empty results, not an error."""
+    m = _load().Decoder(vocab=199, hidden=128, heads=2, kv_heads=1, D=64, max_len=16)
+    logprob, entropy, ids, best = m.score(torch.tensor([7], device=DEV), top=4)
+    assert logprob.shape == entropy.shape == (0,) and ids.shape == best.shape == (0, 4)
