@@ -723,15 +723,13 @@ __global__ void __launch_bounds__(32 * kGemv16MaxWarps, (MC == 2 && DT == KQ_Q4_
 
 // Number of SMs of the current device (looked up once per device).
 static int gemv_sm_count() {
-    static int cache[64] = {0};
+    static std::atomic<int> cache[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-    if (!cache[dev]) {
+    return looked_up(cache[dev], [dev] {
         int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-        cache[dev] = n;
-    }
-    return cache[dev];
+        return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0 ? 152 : n;
+    });
 }
 
 template <int DT, bool FUSED, int MC>

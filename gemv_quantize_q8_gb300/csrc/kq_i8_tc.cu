@@ -565,14 +565,14 @@ static PFN_cuTensorMapEncodeTiled_v12000 i8_encoder() {
 // only in whole multiples of their size).  Looked up once a device and split.
 template <typename C>
 static int i8_resident(int splits) {
-    static int cache[64][I8_MAX_SPLIT + 1] = {};
+    static std::atomic<int> cache[64][I8_MAX_SPLIT + 1];
     const int fallback = 8 * (19 / (C::CG * splits));
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         cudaGetLastError();
         return fallback;
     }
-    if (!cache[dev][splits]) {
+    return looked_up(cache[dev][splits], [&] {
         auto kern = i8_tc_kernel<C, float>;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(C::CG, 1, splits);
@@ -591,9 +591,8 @@ static int i8_resident(int splits) {
             cudaGetLastError();
             n = fallback;
         }
-        cache[dev][splits] = n;
-    }
-    return cache[dev][splits];
+        return n;
+    });
 }
 
 template <typename C, typename TY>

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/kq.h"
+#include "kq_lookup.cuh"
 
 namespace kq {
 

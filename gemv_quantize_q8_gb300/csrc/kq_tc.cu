@@ -1560,21 +1560,20 @@ bool tc_eligible(kq_dtype wt, int64_t M, int64_t N, int64_t K) {
 
 // Number of SMs of the current device (looked up once per device).
 static int sm_count() {
-    static int cache[64] = {0};
+    static std::atomic<int> cache[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         cudaGetLastError();
         return 152;
     }
-    if (!cache[dev]) {
+    return looked_up(cache[dev], [dev] {
         int n = 0;
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
             cudaGetLastError();
             n = 152;
         }
-        cache[dev] = n;
-    }
-    return cache[dev];
+        return n;
+    });
 }
 
 // CTAs of the tensor-core kernel that the current device runs at once when they are launched in
@@ -1583,7 +1582,7 @@ static int sm_count() {
 // without a device it falls back to GB300's 8 GPCs of 19 SMs.  Cached per device and S.
 template <int DT>
 static int resident_ctas(int S) {
-    static int cache[64][4] = {};
+    static std::atomic<int> cache[64][4];
     const int si = S == 1 ? 0 : S == 2 ? 1 : S == 4 ? 2 : 3;
     const int fallback = S == 1 ? 152 : 8 * (19 / S) * S;
     int dev = 0;
@@ -1591,11 +1590,8 @@ static int resident_ctas(int S) {
         cudaGetLastError();
         return fallback;
     }
-    if (cache[dev][si]) return cache[dev][si];
-    int n = 0;
-    if (S == 1) {
-        n = sm_count();
-    } else {
+    return looked_up(cache[dev][si], [&] {
+        if (S == 1) return sm_count();
         auto kern = tc_gemm_kernel<DT, false, false>;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(1, 1, (unsigned)S);
@@ -1612,13 +1608,10 @@ static int resident_ctas(int S) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcLayout<DT>::ALLOC) ==
                 cudaSuccess &&
             cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess)
-            n = clusters * S;
-        else
-            cudaGetLastError();  // leave no error behind for the next launch check
-    }
-    if (n <= 0) n = fallback;
-    cache[dev][si] = n;
-    return n;
+            return clusters > 0 ? clusters * S : fallback;
+        cudaGetLastError();  // leave no error behind for the next launch check
+        return fallback;
+    });
 }
 
 static int resident_ctas_dt(kq_dtype wt, int S) {
