@@ -304,7 +304,7 @@ def kq_qk_norm_rope(xt, q, ldq, k, ldk, M, n_q, n_k, D, q_gamma, k_gamma, eps, p
 
 def kq_logprobs(xt, logits, ldx, M, V, targets, n_targets, logprob, entropy, top_k=0, top_ids=None, top_logprob=None,
                 stream=None):
-    """Log probabilities of the given tokens, the entropy and the top alternatives of every row of logits."""
+    """Log probabilities of the given tokens (V a row at most), the entropy and the top alternatives of every row of logits."""
     _check(lib().kq_logprobs(xt, _ptr(logits), ldx, M, V, _ptr(targets), n_targets, _ptr(logprob), _ptr(entropy),
                              top_k, _ptr(top_ids), _ptr(top_logprob), _stream(stream)))
 

@@ -327,7 +327,7 @@ KQ_API kq_status kq_moe_weighted_sum(const float *y_slots, const float *w, int64
  * The sum is exact in 32-bit integers for every int8 input, then rounded once to fp32; the two products
  * and the sum with the bias are each rounded (no fused multiply-add), and an f16 or bf16 output is
  * rounded once more.  So y does not depend on which kernel a size takes, nor on the other rows of the
- * batch. */
+ * batch.  M and N are 1 .. 2^31 - 256. */
 
 /* Quantise rows to int8 with one scale a row: amax = max |x[m][.]| (NaN never wins), scale[m] = amax/127,
  * q = nearest-even(x * (127/amax)) with both divisions IEEE; a NaN product gives code 0.  A row whose
@@ -339,7 +339,8 @@ KQ_API kq_status kq_moe_weighted_sum(const float *y_slots, const float *w, int64
 KQ_API kq_status kq_quantize_i8(kq_dtype xt, const void *x, int64_t M, int64_t K, int64_t ldx, int8_t *q, int64_t ldq,
                                 float *scale, kq_stream_t stream);
 
-/* Workspace bytes of kq_gemm_i8 and kq_gemm_i8_dyn for this shape (never 0). */
+/* Workspace bytes of kq_gemm_i8 and kq_gemm_i8_dyn for this shape; 0 for one that they refuse.  More of M or K never
+ * takes less, so one workspace of the largest serves them all. */
 KQ_API size_t kq_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* The product from quantised rows.  q: int8 [M][ldq], sx: fp32 [M]; w: int8 [N][ldw], sw: fp32 [N]; bias:
@@ -369,7 +370,8 @@ KQ_API kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const i
  * q_gamma, k_gamma: fp32 [D] or NULL.  cos_tab, sin_tab: fp32 [n_pos][rot/2] (unused when rot = 0).
  * q_out, k_out: of type yt, row strides ldqo and ldko; an output may be its own input (same pointer, type
  * and stride), so a cache row can be written directly.  D is even, 2 .. 1024; rot is even,
- * 0 .. D.  M*(n_q + n_k) is below 2^31.  A position outside [0, n_pos) has no angle: its token's rows are written
+ * 0 .. D; n_q and n_k are at most 65536 each, not both 0; eps is finite and not negative.  M*(n_q + n_k) is
+ * below 2^31.  A position outside [0, n_pos) has no angle: its token's rows are written
  * as NaN. */
 KQ_API kq_status kq_qk_norm_rope(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, int64_t M,
                                  int64_t n_q, int64_t n_k, int64_t D, const float *q_gamma, const float *k_gamma,
@@ -384,7 +386,8 @@ KQ_API kq_status kq_qk_norm_rope(kq_dtype xt, const void *q, int64_t ldq, const 
  *   top_logprob their log probabilities.
  * logits: [M][ldx] of type xt; targets: int32 [M][n_targets] (NULL when n_targets = 0); logprob: fp32
  * [M][n_targets]; entropy: fp32 [M] or NULL; top_ids: int32 [M][top_k], top_logprob: fp32 [M][top_k]
- * (unused when top_k = 0).  top_k is 0 .. 32 and at most V; V at most 2^30.
+ * (unused when top_k = 0).  top_k is 0 .. 32 and at most V; n_targets is 0 .. V; V is 1 .. 2^30 and M
+ * 1 .. 2^31 - 1.
  * Logits of -inf (masked tokens) have probability 0, log probability -inf and no share in the entropy.  A
  * row with nothing but -inf gives log probabilities -inf, entropy 0 and the ids 0 .. top_k-1.  A row with
  * a NaN or +inf gives NaN for its log probabilities and entropy; its ids rank +inf first and NaN with
