@@ -81,6 +81,8 @@ _SIGS = {
     "kq_qk_norm_rope": ([_I32, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _P, _I64,
                          _I64, _I32, _I32, _P, _I64, _P, _I64, _P], _I32),
     "kq_logprobs": ([_I32, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P, _P], _I32),
+    "kq_debug_i8_form": ([_I64, _I64, _I64, _P, _P, _P], _I32),
+    "kq_debug_i8_wait_timeout": ([_P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I32, _I64, _P, _SZ, _P], _I32),
     "kq_debug_tc_wait_timeout": ([_I32, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _SZ, _P], _I32),
 }
 
@@ -335,3 +337,16 @@ def kq_debug_tc_wait_timeout(wt, w, xq, M, N, K, y, ldy, wait_limit_ns, workspac
     """The tensor-core kernel with its activation producer idle and every wait limited to wait_limit_ns."""
     _check(lib().kq_debug_tc_wait_timeout(wt, _ptr(w), _ptr(xq), M, N, K, _ptr(y), ldy, wait_limit_ns,
                                           _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def kq_debug_i8_form(M, N, K):
+    """(CTAs that share a tile's rows, tokens of a tile, CTAs that share its K) of kq_gemm_i8; zeros for a few tokens."""
+    out = [ctypes.c_int(0) for _ in range(3)]
+    _check(lib().kq_debug_i8_form(M, N, K, *(ctypes.byref(v) for v in out)))
+    return tuple(v.value for v in out)
+
+
+def kq_debug_i8_wait_timeout(q, ldq, sx, w, ldw, sw, M, N, K, y, ldy, idle, wait_limit_ns, workspace, ws_bytes, stream=None):
+    """kq_gemm_i8's tensor-core kernel with a role idle (1: activations, 2: MMAs) and every wait limited to wait_limit_ns."""
+    _check(lib().kq_debug_i8_wait_timeout(_ptr(q), ldq, _ptr(sx), _ptr(w), ldw, _ptr(sw), M, N, K, _ptr(y), ldy, idle,
+                                          wait_limit_ns, _ptr(workspace), ws_bytes, _stream(stream)))

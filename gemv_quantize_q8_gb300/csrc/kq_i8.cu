@@ -142,6 +142,35 @@ static kq_status i8_check_product(const char *fn, const int8_t *w, int64_t ldw, 
     return KQ_OK;
 }
 
+// kq_gemm_i8, its checks among it; idle: a role of the tensor-core kernel that does nothing, its waits limited to wait_ns.
+static kq_status i8_gemm(const char *fn, const int8_t *q, int64_t ldq, const float *sx, const int8_t *w, int64_t ldw,
+                         const float *sw, const float *bias, int64_t M, int64_t N, int64_t K, kq_dtype yt, void *y,
+                         int64_t ldy, void *workspace, size_t ws_bytes, cudaStream_t st, I8Idle idle = I8_IDLE_NONE,
+                         unsigned long long wait_ns = kI8WaitNs) {
+    kq_status s = i8_check_product(fn, w, ldw, sw, bias, M, N, K, yt, y, ldy, workspace, ws_bytes);
+    if (s == KQ_OK) s = i8_check_codes(fn, "q", q, K, ldq);
+    if (s != KQ_OK) return s;
+    if (!sx) return fail(KQ_ERR_INVALID_ARG, "%s: null sx", fn);
+    if (!aligned(sx, 4)) return fail(KQ_ERR_ALIGNMENT, "%s: sx must be 4-byte aligned", fn);
+    unsigned long long *err = static_cast<unsigned long long *>(workspace);
+    if (idle != I8_IDLE_NONE) {
+        if (M <= kI8FewTokens) return fail(KQ_ERR_INVALID_ARG, "%s: M=%lld does not take the tensor-core path", fn, (long long)M);
+        const cudaError_t e = cudaMemsetAsync(err, 0, sizeof *err, st);
+        if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    }
+    if (M <= kI8FewTokens) return i8_gemv(fn, {q, ldq, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, false}, st);
+    if (M <= kI8DirectTokens)
+        return i8_tc_product(fn, {q, ldq, nullptr, 0, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, false, wait_ns, idle}, st);
+    const I8Workspace l = i8_workspace(M, K);
+    __half *panel = reinterpret_cast<__half *>(static_cast<uint8_t *>(workspace) + l.codes);
+    const int64_t blocks = (M * (l.ld / 16) + 255) / 256;
+    if (blocks > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: M=%lld is too large", fn, (long long)M);
+    s = i8_launched(fn, launch_beside(i8_panel_kernel, dim3((unsigned)blocks), dim3(256), 0, dim3(1), st, q, ldq, M, (int)K, panel,
+                                      l.ld, err));
+    if (s != KQ_OK) return s;
+    return i8_tc_product(fn, {nullptr, 0, panel, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, true, wait_ns, idle}, st);
+}
+
 }  // namespace kq
 
 using namespace kq;
@@ -167,25 +196,30 @@ size_t kq_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 kq_status kq_gemm_i8(const int8_t *q, int64_t ldq, const float *sx, const int8_t *w, int64_t ldw, const float *sw,
                      const float *bias, int64_t M, int64_t N, int64_t K, kq_dtype yt, void *y, int64_t ldy,
                      void *workspace, size_t ws_bytes, kq_stream_t stream) {
-    const char *fn = "kq_gemm_i8";
-    kq_status s = i8_check_product(fn, w, ldw, sw, bias, M, N, K, yt, y, ldy, workspace, ws_bytes);
-    if (s == KQ_OK) s = i8_check_codes(fn, "q", q, K, ldq);
-    if (s != KQ_OK) return s;
-    if (!sx) return fail(KQ_ERR_INVALID_ARG, "%s: null sx", fn);
-    if (!aligned(sx, 4)) return fail(KQ_ERR_ALIGNMENT, "%s: sx must be 4-byte aligned", fn);
-    const cudaStream_t st = (cudaStream_t)stream;
-    unsigned long long *err = static_cast<unsigned long long *>(workspace);
-    if (M <= kI8FewTokens) return i8_gemv(fn, {q, ldq, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, false}, st);
-    if (M <= kI8DirectTokens)
-        return i8_tc_product(fn, {q, ldq, nullptr, 0, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, false}, st);
-    const I8Workspace l = i8_workspace(M, K);
-    __half *panel = reinterpret_cast<__half *>(static_cast<uint8_t *>(workspace) + l.codes);
-    const int64_t blocks = (M * (l.ld / 16) + 255) / 256;
-    if (blocks > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: M=%lld is too large", fn, (long long)M);
-    s = i8_launched(fn, launch_beside(i8_panel_kernel, dim3((unsigned)blocks), dim3(256), 0, dim3(1), st, q, ldq, M, (int)K, panel,
-                                      l.ld, err));
-    if (s != KQ_OK) return s;
-    return i8_tc_product(fn, {nullptr, 0, panel, l.ld, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, err, true}, st);
+    return i8_gemm("kq_gemm_i8", q, ldq, sx, w, ldw, sw, bias, M, N, K, yt, y, ldy, workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+kq_status kq_debug_i8_wait_timeout(const int8_t *q, int64_t ldq, const float *sx, const int8_t *w, int64_t ldw, const float *sw,
+                                   int64_t M, int64_t N, int64_t K, float *y, int64_t ldy, int idle, int64_t wait_limit_ns,
+                                   void *workspace, size_t ws_bytes, kq_stream_t stream) {
+    const char *fn = "kq_debug_i8_wait_timeout";
+    if (idle != I8_IDLE_ACT && idle != I8_IDLE_MMA) return fail(KQ_ERR_INVALID_ARG, "%s: idle=%d is not 1 or 2", fn, idle);
+    if (wait_limit_ns < 1000 || wait_limit_ns > 1000000000)
+        return fail(KQ_ERR_INVALID_ARG, "%s: wait_limit_ns must be in [1e3, 1e9]", fn);
+    return i8_gemm(fn, q, ldq, sx, w, ldw, sw, nullptr, M, N, K, KQ_F32, y, ldy, workspace, ws_bytes, (cudaStream_t)stream,
+                   static_cast<I8Idle>(idle), (unsigned long long)wait_limit_ns);
+}
+
+kq_status kq_debug_i8_form(int64_t M, int64_t N, int64_t K, int *ctas, int *tokens, int *splits) {
+    const char *fn = "kq_debug_i8_form";
+    if (!kq_gemm_i8_workspace_bytes(M, N, K) || !ctas || !tokens || !splits)
+        return fail(KQ_ERR_INVALID_ARG, "%s: a shape that kq_gemm_i8 refuses (M=%lld N=%lld K=%lld) or a null pointer", fn, (long long)M,
+                    (long long)N, (long long)K);
+    const I8Form f = M <= kI8FewTokens ? I8Form{0, 0, 0} : i8_tc_form(M, N, K);
+    *ctas = f.ctas;
+    *tokens = f.tokens;
+    *splits = f.splits;
+    return KQ_OK;
 }
 
 kq_status kq_gemm_i8_dyn(kq_dtype xt, const void *x, int64_t ldx, const int8_t *w, int64_t ldw, const float *sw,

@@ -39,7 +39,6 @@ constexpr int I8_KS = 64;         // K per activation tile (a 128-byte swizzled 
 constexpr int I8_UNIT = 128;      // K per unit: a weight tile, two activation tiles, one TMEM stage of A
 constexpr int I8_CHUNK = 8;       // units per chunk: 1024 elements, the longest exact fp32 accumulation
 constexpr int I8_MAX_SPLIT = 8;  // CTAs that share a tile's K (portable cluster size)
-constexpr unsigned long long kI8WaitNs = 2000000000ull;
 
 template <int CG_, int NT_, int EPI_, int CONV_, int STAGES_, int WSTAGES_>
 struct I8Cfg {
@@ -85,6 +84,9 @@ struct I8TcParams {
     int units, units_per_split, nsplit;  // K in units of 128
     unsigned long long *err;
     bool after_prologue;  // the weights may be read before the kernel before this one has ended
+    bool clear;           // the device flag is cleared here
+    unsigned long long wait_ns;
+    int idle;
 };
 
 // ---------------------------------------------------------------- cta_group forms
@@ -243,18 +245,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 for (int u = 0; u < nu; ++u, ++g) {
                     const int s = g % C::WSTAGES, x = (u0 + u) * I8_UNIT;
                     if (g >= ahead) {
-                        if (!(ok = mbar_wait_sleep(&w_empty[s], ((g / C::WSTAGES) & 1) ^ 1, abort_flag, kI8WaitNs))) break;
+                        if (!(ok = mbar_wait_sleep(&w_empty[s], ((g / C::WSTAGES) & 1) ^ 1, abort_flag, P.wait_ns))) break;
                         mbar_arrive_expect_tx(&w_full[s], C::WT);
                         tma_load_2d(sW + s * C::WT, &tmW, &w_full[s], x, n0);
                     }
                     if (C::DIRECT) tma_load_2d(sW + s * C::WT + I8_ROWS * I8_UNIT, &tmX, &w_full[s], x, 0);
                 }
             }
-            // leaving early: the copies in flight land first (bounded)
-            for (int i = 0; i < C::WSTAGES && !ok; ++i) {
+            // whoever gives up, the copies in flight land before this thread leaves (bounded): shared memory is used
+            // again or left after that
+            for (int i = 0; i < C::WSTAGES; ++i) {
                 const int last = g - 1 - i;
                 volatile int no_abort = 0;
-                if (last >= 0) mbar_wait(&w_full[last % C::WSTAGES], (last / C::WSTAGES) & 1, &no_abort, 100000000ull);
+                if (last >= 0) mbar_wait_sleep(&w_full[last % C::WSTAGES], (last / C::WSTAGES) & 1, &no_abort, 100000000ull);
             }
         }
     } else if (C::DIRECT && warp >= C::W_ACT && warp < C::W_MMA) {
@@ -267,11 +270,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         constexpr int PASSES = C::ACT_TOK / 4;
         bool ok = true;
         int g = 0;
-        for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
+        for (int tile = tile0; tile < P.tiles && ok && P.idle != I8_IDLE_ACT; tile += tstride) {
             for (int u = 0; u < nu; ++u, ++g) {
                 if (g % C::GROUPS != grp) continue;
                 const int s = g % C::STAGES, ws = g % C::WSTAGES;
-                if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, kI8WaitNs)))) break;
+                if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, P.wait_ns)))) break;
                 const uint8_t *xt = sW + ws * C::WT + I8_ROWS * I8_UNIT;
                 uint4 v[PASSES];
 #pragma unroll
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const int row = row0 + 4 * i;
                     v[i] = *reinterpret_cast<const uint4 *>(xt + row * I8_UNIT + ((c ^ (row & 7)) << 4));
                 }
-                if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / C::STAGES) & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
+                if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / C::STAGES) & 1) ^ 1, abort_flag, P.wait_ns)))) break;
                 uint8_t *bt = sB + (2 * s + (c >> 2)) * C::BT;
 #pragma unroll
                 for (int i = 0; i < PASSES; ++i) {
@@ -307,11 +310,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             int g = 0;
             grid_dependency_wait();  // the panel is the output of the kernel before this one
             grid_launch_dependents();
-            for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
+            for (int tile = tile0; tile < P.tiles && ok && P.idle != I8_IDLE_ACT; tile += tstride) {
                 const int m0 = (tile / P.n_tiles) * C::NT + r * (C::NT / C::CG);
                 for (int u = 0; u < nu; ++u, ++g) {
                     const int s = g % C::STAGES, ph = (g / C::STAGES) & 1;
-                    if (!(ok = mbar_wait_sleep(&k_empty[s], ph ^ 1, abort_flag, kI8WaitNs))) break;
+                    if (!(ok = mbar_wait_sleep(&k_empty[s], ph ^ 1, abort_flag, P.wait_ns))) break;
                     const int x = (u0 + u) * I8_UNIT;
                     if (r == 0) mbar_arrive_expect_tx(&k_full[s], C::CG * 2 * C::BT);
 #pragma unroll
@@ -322,9 +325,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                 }
             }
+            // as above: once the MMAs have read them the copies have landed; where somebody gave up, time alone bounds
+            // them (their barrier may be the other CTA's, or wait for converters that have left), far more than they need
+            for (int i = 0; i < C::STAGES && ok; ++i) {
+                const int last = g - 1 - i;
+                if (last >= 0) ok = mbar_wait_sleep(&k_empty[last % C::STAGES], (last / C::STAGES) & 1, abort_flag, P.wait_ns);
+            }
             if (!ok) {
-                // leaving early: give the copies in flight far more time than they need; their barrier may
-                // be the other CTA's or wait for converters that have left, so time alone bounds this
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 10000000ull) {}
             }
@@ -341,7 +348,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bool ok = true;
             int s = 0, job = 0;  // stage, and accumulator fills so far
             uint32_t ph = 0;     // phase of stage s's barriers
-            for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
+            for (int tile = tile0; tile < P.tiles && ok && P.idle != I8_IDLE_MMA; tile += tstride) {
                 for (int c0 = 0; c0 < nu && ok; c0 += I8_CHUNK, ++job) {
                     const int un = min(I8_CHUNK, nu - c0);
                     // all stages at a time: the first half's MMAs over them, then the second half's, which free
@@ -352,14 +359,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             const int buf = C::H == 2 ? h : job % C::NACC;
                             const uint32_t use = C::H == 2 ? job : job / C::NACC;
                             if (u == 0) {
-                                if (!(ok = all_lanes(mbar_wait_sleep(&acc_empty[buf], (use & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
+                                if (!(ok = all_lanes(mbar_wait_sleep(&acc_empty[buf], (use & 1) ^ 1, abort_flag, P.wait_ns)))) break;
                                 tc_fence_after();
                             }
                             for (int k = 0; k < kn; ++k) {
                                 const int sk = (s + k) % C::STAGES;
                                 if (h == 0) {
                                     const uint32_t phk = s + k < C::STAGES ? ph : ph ^ 1;
-                                    if (!(ok = all_lanes(mbar_wait_sleep(&k_full[sk], phk, abort_flag, kI8WaitNs)))) break;
+                                    if (!(ok = all_lanes(mbar_wait_sleep(&k_full[sk], phk, abort_flag, P.wait_ns)))) break;
                                     tc_fence_after();
                                 }
                                 const uint64_t b = dB + (uint64_t)(sk * (2 * C::BT >> 4)) + h * half_rows;
@@ -395,13 +402,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int u = 0; u < nu && ok; ++u, ++g) {
                 if (g % C::GROUPS != grp) continue;
                 const int ws = g % C::WSTAGES, s = g % C::STAGES;
-                if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, kI8WaitNs)))) break;
+                if (!(ok = all_lanes(mbar_wait_sleep(&w_full[ws], (g / C::WSTAGES) & 1, abort_flag, P.wait_ns)))) break;
                 // 16-byte piece p of row `row` sits at piece p ^ (row & 7) (128-byte swizzle)
                 const uint8_t *wr = sW + ws * C::WT + row * I8_UNIT;
                 uint4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4 *>(wr + ((i ^ (row & 7)) << 4));
-                if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / C::STAGES) & 1) ^ 1, abort_flag, kI8WaitNs)))) break;
+                if (!(ok = all_lanes(mbar_wait_sleep(&k_empty[s], ((g / C::STAGES) & 1) ^ 1, abort_flag, P.wait_ns)))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -436,7 +443,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         int job = 0;
         grid_dependency_wait();  // scales may be the output of the kernel before this one
         // the direct form's flag: an error is counted two seconds later at the earliest
-        if (C::DIRECT && tid == 0 && blockIdx.x == 0 && z == 0) *P.err = 0ull;
+        if (P.clear && tid == 0 && blockIdx.x == 0 && z == 0) *P.err = 0ull;
         for (int tile = tile0; tile < P.tiles && ok; tile += tstride) {
             // this tile's scales, on their way while it is computed: lane l keeps the tokens l, l + 32
             const int n = (tile % P.n_tiles) * (I8_ROWS * C::CG) + r * I8_ROWS + row;
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int c0 = 0; c0 < nu; c0 += I8_CHUNK, ++job) {
                 const int buf = C::H == 2 ? h : job % C::NACC;
                 const uint32_t use = C::H == 2 ? job : job / C::NACC;
-                if (!(ok = all_lanes(mbar_wait_sleep(&acc_full[buf], use & 1, abort_flag, kI8WaitNs)))) break;
+                if (!(ok = all_lanes(mbar_wait_sleep(&acc_full[buf], use & 1, abort_flag, P.wait_ns)))) break;
                 tc_fence_after();
                 const uint32_t t = lane_base + (C::H == 2 ? col0 : buf * C::NM + col0);
 #pragma unroll
@@ -636,6 +643,9 @@ static kq_status i8_launch(const char *fn, const I8TcArgs &a, int splits, cudaSt
     p.nsplit = splits;
     p.err = a.err;
     p.after_prologue = a.after_prologue;
+    p.clear = C::DIRECT && a.idle == I8_IDLE_NONE;
+    p.wait_ns = a.wait_ns;
+    p.idle = a.idle;
     auto kern = i8_tc_kernel<C, TY>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
@@ -669,21 +679,31 @@ static I8Plan i8_plan(int64_t M, int64_t N, int64_t units, double unit, double r
     return best;
 }
 
+I8Form i8_tc_form(int64_t M, int64_t N, int64_t K) {
+    const int64_t units = (K + I8_UNIT - 1) / I8_UNIT;
+    // (16 tokens, [4096 x 4096]: four splits 8.1 us, unsplit 14.8; [4096 x 14336]: 17.3 and 43.4)
+    if (M <= 32) return {1, 32, i8_plan<I8One32>(M, N, units, 0.43, 3.0).splits};
+    if (M <= 64) return {1, 64, i8_plan<I8One64>(M, N, units, 0.43, 3.0).splits};
+    const I8Plan one = i8_plan<I8One128>(M, N, units, 0.43, 3.5);
+    if (M <= 128) return {1, 128, one.splits};
+    // A pair does a unit of four times the work in 0.62 us, but its tiles are fewer and its reduction is
+    // dearer.  [4096 x 4096]: 256 tokens 18.6 us by pairs, 15.7 by single CTAs, 512 tokens 23.2 and 20.5;
+    // [14336 x 4096]: 384 tokens 50.4 and 45.8, 2048 tokens 135 and 166
+    const I8Plan pair = i8_plan<I8Pair>(M, N, units, 0.62, 6.0);
+    if (pair.t + 3.0 <= one.t) return {2, 256, pair.splits};
+    return {1, 128, one.splits};
+}
+
 kq_status i8_tc_product(const char *fn, const I8TcArgs &a, cudaStream_t st) {
+    const I8Form f = i8_tc_form(a.M, a.N, a.K);
     return with_type(a.yt, [&](auto t) {
         using TY = decltype(t);
-        const int64_t units = (a.K + I8_UNIT - 1) / I8_UNIT;
-        auto go = [&](auto c, I8Plan p) { return i8_launch<decltype(c), TY>(fn, a, p.splits, st); };
-        // (16 tokens, [4096 x 4096]: four splits 8.1 us, unsplit 14.8; [4096 x 14336]: 17.3 and 43.4)
-        if (a.M <= 32) return go(I8One32{}, i8_plan<I8One32>(a.M, a.N, units, 0.43, 3.0));
-        if (a.M <= 64) return go(I8One64{}, i8_plan<I8One64>(a.M, a.N, units, 0.43, 3.0));
-        const I8Plan one = i8_plan<I8One128>(a.M, a.N, units, 0.43, 3.5);
-        if (a.M <= 128) return go(I8One128{}, one);
-        // A pair does a unit of four times the work in 0.62 us, but its tiles are fewer and its reduction is
-        // dearer.  [4096 x 4096]: 256 tokens 18.6 us by pairs, 15.7 by single CTAs, 512 tokens 23.2 and 20.5;
-        // [14336 x 4096]: 384 tokens 50.4 and 45.8, 2048 tokens 135 and 166
-        const I8Plan pair = i8_plan<I8Pair>(a.M, a.N, units, 0.62, 6.0);
-        return pair.t + 3.0 <= one.t ? go(I8Pair{}, pair) : go(I8One128{}, one);
+        switch (f.tokens) {
+        case 32: return i8_launch<I8One32, TY>(fn, a, f.splits, st);
+        case 64: return i8_launch<I8One64, TY>(fn, a, f.splits, st);
+        case 128: return i8_launch<I8One128, TY>(fn, a, f.splits, st);
+        default: return i8_launch<I8Pair, TY>(fn, a, f.splits, st);
+        }
     });
 }
 

@@ -4,6 +4,12 @@
 
 namespace kq {
 
+// Wall-time limit of every wait of the pipeline: past it the CTA counts an error in the device flag, lets its copies and
+// MMAs in flight end, and leaves.
+constexpr unsigned long long kI8WaitNs = 2000000000ull;
+// Test hook: a role that does nothing, so that what waits for it runs into the limit.
+enum I8Idle { I8_IDLE_NONE = 0, I8_IDLE_ACT = 1, I8_IDLE_MMA = 2 };
+
 // Tokens up to which the kernel takes int8 codes as they are; more come as an f16 panel.
 constexpr int kI8DirectTokens = 64;
 
@@ -34,7 +40,14 @@ struct I8TcArgs {
     int64_t ldy;
     unsigned long long *err;  // device flag: cleared here (int8 codes) or by the panel's kernel
     bool after_prologue;      // the kernel just before is the quantizer or the panel's: the weights may be read before its end
+    unsigned long long wait_ns = kI8WaitNs;
+    I8Idle idle = I8_IDLE_NONE;  // other than none: the flag has been cleared before
 };
+// The form that a product takes: CTAs that share a tile's rows, tokens of a tile, CTAs that share its K.
+struct I8Form {
+    int ctas, tokens, splits;
+};
+I8Form i8_tc_form(int64_t M, int64_t N, int64_t K);
 kq_status i8_tc_product(const char *fn, const I8TcArgs &a, cudaStream_t st);
 
 }  // namespace kq

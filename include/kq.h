@@ -449,6 +449,18 @@ KQ_API kq_status kq_debug_tc_wait_timeout(kq_dtype wt, const void *w, const void
                                           float *y, int64_t ldy, int64_t wait_limit_ns, void *workspace,
                                           size_t ws_bytes, kq_stream_t stream);
 
+/* The form that kq_gemm_i8 takes on the current device: CTAs that share a tile's weight rows (1 or 2), tokens of a tile,
+ * CTAs that share its K; all 0 for the few tokens that need no tensor cores (M <= 8). */
+KQ_API kq_status kq_debug_i8_form(int64_t M, int64_t N, int64_t K, int *ctas, int *tokens, int *splits);
+
+/* Test hook of the int8 product's bounded waits, as kq_debug_tc_wait_timeout: kq_gemm_i8 (fp32 output, no bias, M > 8) with
+ * one role of its tensor-core kernel kept idle (1: what brings the activations, 2: what issues the MMAs) and every wait
+ * limited to wait_limit_ns (1e3 .. 1e9; kq_gemm_i8 uses 2 s).  The waits run out, every CTA counts it in the device flag,
+ * lets its copies and MMAs in flight end, and returns; y is not written or incomplete. */
+KQ_API kq_status kq_debug_i8_wait_timeout(const int8_t *q, int64_t ldq, const float *sx, const int8_t *w, int64_t ldw,
+                                          const float *sw, int64_t M, int64_t N, int64_t K, float *y, int64_t ldy, int idle,
+                                          int64_t wait_limit_ns, void *workspace, size_t ws_bytes, kq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
