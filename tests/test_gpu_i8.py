@@ -225,3 +225,14 @@ def test_on_a_stream_of_its_own_and_again(M):
     want = reference(q.cpu().numpy(), sx.cpu().numpy(), w.cpu().numpy(), sw.cpu().numpy(), None, K, "f32")
     for y in ys:
         same(y.cpu(), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 1000), (3, 129, 2060), (8, 257, 513), (20, 1000, 1025), (60, 300, 4111), (100, 260, 2049),
+                                   (300, 777, 1500), (1100, 4099, 1030)])
+def test_all_codes_at_random(M, N, K):
+    """Codes of -128 to 127, the type's lowest among the others, in random places of both sides."""
+    g = np.random.default_rng(M + N + K)
+    q, w = codes(g, M, K, full=True), codes(g, N, K, full=True)
+    assert (q[:, :K] == -128).any() and (w[:, :K] == -128).any()
+    sx, sw = g.random(M).astype(np.float32), g.random(N).astype(np.float32)
+    same(product(q, sx, w, sw, None, K, "f32"), reference(q, sx, w, sw, None, K, "f32"))

@@ -199,3 +199,18 @@ def test_few_tokens_left_and_many_targets(M, left):
         x[r, torch.from_numpy(g.permutation(V)[:left])] = torch.from_numpy(g.standard_normal(left).astype(np.float32))
     x[0, 5] = float("nan")
     check(x, g.integers(0, V, (M, T)), k, "f32")
+
+
+@pytest.mark.parametrize("k", [0, 3])
+def test_more_rows_than_a_grid_holds(k):
+    """Rows past the grid's 65535 come in a launch of their own, with their own targets and outputs."""
+    M, V = 65541, 40
+    g = np.random.default_rng(6)
+    check(logits(g, M, V, "f32"), g.integers(0, V, (M, 2)), k, "f32")
+
+
+def test_as_many_targets_as_tokens():
+    """Every id of the vocabulary as a target of every row: the most that a call takes."""
+    V = 700
+    g = np.random.default_rng(8)
+    check(logits(g, 3, V, "f32"), np.stack([g.permutation(V) for _ in range(3)]), 5, "f32")
