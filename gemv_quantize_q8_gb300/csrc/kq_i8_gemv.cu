@@ -6,11 +6,12 @@
 // group share the rows' pieces and add their sums through shared memory (whole numbers: exact in any order).
 // Blocks stay and walk the row groups, so that a group's first pieces are on their way while the group before
 // it is summed up and stored.  The tokens' codes are small and shared by every warp: they come through L1.
-// One token of [14336 x 4096]: 10.7 us, 5.5 TB/s; [4096 x 14336], five tokens: 12.9 us.
+// Back to back, from memory (weights rotating over three times the L2; the same weights again, from the L2, in
+// brackets): one token of [14336 x 4096] 10.6 us, 5.6 TB/s (6.5); five tokens of [4096 x 14336] 13.0 us (11.2).
 //
 // TX other than void: the tokens come as rows of that type and every block quantises them itself, into shared
-// memory, while its first weights are on their way: one fp32 token of [9728 x 2560] 4.9 us, 5.6 behind a
-// quantizer of its own; of [2560 x 9728] 6.5 and 8.3.
+// memory, while its first weights are on their way: one fp32 token of [9728 x 2560] 7.0 us (4.5), behind a quantizer
+// of its own 7.2 (5.7); of [2560 x 9728] 8.2 (6.0) and 8.6 (7.9).
 #include <type_traits>
 
 #include "kq_i8_gemv.cuh"
@@ -36,10 +37,12 @@ __device__ __forceinline__ uint4 keep_codes(uint4 v, int valid) {
 }
 
 // Weight rows of a warp and blocks of an SM, by tokens: what a warp's pieces under way and its ROWS*M sums
-// need in registers against how many warps there are to wait for memory.  [14336 x 4096]: one token 10.7 us with
-// 2 rows and 4 blocks, 10.9 with 4 and 2 ([4096 x 4096]: 3.1 against 4.1); three tokens 11.8 with 4 and 2, 11.9
-// with 2 and 4; eight tokens 14.1 with 2 and 2, 17.1 with 4 and 2, 16.2 with 2 and 3.  Blocks that quantise are
-// better few ([9728 x 2560], one fp32 token: 4.9 us with 4 and 2, 5.4 with 2 and 4).
+// need in registers against how many warps there are to wait for memory.  [14336 x 4096], from memory (from the L2 in
+// brackets): one token 10.6 us (6.5) with 2 rows and 4 blocks, 10.8 (6.3) with 4 and 2 ([4096 x 4096]: 4.4 and 4.7);
+// three tokens 11.6 (7.8) with 4 and 2, 11.8 (8.6) with 2 and 4, 10.9 (7.4) with 2 and 3; eight tokens 14.0 (12.5)
+// with 2 and 2, 16.9 (15.0) with 4 and 2, 16.1 (13.4) with 2 and 3.  Blocks that quantise are as good few where the
+// weights come from memory, better from the L2 ([9728 x 2560], one fp32 token: 7.0 (4.5) with 4 and 2, 7.0 (4.9) with
+// 2 and 4).
 template <int M, typename TX> constexpr int kGemvRows = M == 3 || M == 4 || !std::is_void<TX>::value ? 4 : 2;
 template <int M, typename TX> constexpr int kGemvPerSm = M <= 2 && std::is_void<TX>::value ? 4 : 2;
 

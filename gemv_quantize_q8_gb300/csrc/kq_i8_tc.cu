@@ -9,11 +9,12 @@
 //   * activations come as an f16 panel (written once by a prologue), by TMA, as the B operand.
 //   * outputs: weight rows = TMEM lanes, tokens = columns.
 // Large products: a pair of CTAs (cta_group::2) computes 256 rows x 256 tokens; each CTA converts its own
-// 128 rows and loads half of the tokens.  [14336 x 4096], 2048 tokens: 135 us, 1.78 PFLOP/s, the f16 pipe's rate.
-// (Tiles of fewer tokens where they cover a batch with less: an MMA of 96 columns takes nearly as long as one of
-// 128; 768 tokens in three waves of 192s 69 us, of 256s 74, and the 256s' 5% slower for the choice.)  The accumulator's two 128-token halves are filled in turn, four
-// units (of 128 K) each, so that one half's chunk is read out (1 us) while the other half computes (1.2 us;
-// with two units each it waited 0.8 us a chunk).
+// 128 rows and loads half of the tokens.  [14336 x 4096], 2048 tokens, bf16 out: 137 us in short bursts, 1.76
+// PFLOP/s, 0.94 of what a plain bf16 product reaches so.  The accumulator's two 128-token halves are filled in turn,
+// four units (of 128 K) each, so that one half's chunk is read out (1 us) while the other half computes (1.2 us; with
+// two units each it waited 0.8 us a chunk).
+// (Tiles of fewer tokens, to cover a batch with less, are left out: an MMA of 96 columns takes nearly as long as one
+// of 128.  768 tokens took 69 us in three waves of 192s for 74 in 256s, but the choice made the 256s 5% slower.)
 // Small products: one CTA, 128 rows x 32, 64 or 128 tokens, two accumulators taking turns chunk by
 // chunk; up to 64 tokens are converted from int8 by the CTA itself, without a panel.
 // Few tiles split K over a cluster; its CTAs exchange their int32 sums through distributed shared memory,
@@ -681,14 +682,14 @@ static I8Plan i8_plan(int64_t M, int64_t N, int64_t units, double unit, double r
 
 I8Form i8_tc_form(int64_t M, int64_t N, int64_t K) {
     const int64_t units = (K + I8_UNIT - 1) / I8_UNIT;
-    // (16 tokens, [4096 x 4096]: four splits 8.1 us, unsplit 14.8; [4096 x 14336]: 17.3 and 43.4)
+    // (weights from memory, 16 tokens, [4096 x 4096]: split 9.1 us, unsplit 14.6; [4096 x 14336]: 16.9 and 42.7)
     if (M <= 32) return {1, 32, i8_plan<I8One32>(M, N, units, 0.43, 3.0).splits};
     if (M <= 64) return {1, 64, i8_plan<I8One64>(M, N, units, 0.43, 3.0).splits};
     const I8Plan one = i8_plan<I8One128>(M, N, units, 0.43, 3.5);
     if (M <= 128) return {1, 128, one.splits};
     // A pair does a unit of four times the work in 0.62 us, but its tiles are fewer and its reduction is
-    // dearer.  [4096 x 4096]: 256 tokens 18.6 us by pairs, 15.7 by single CTAs, 512 tokens 23.2 and 20.5;
-    // [14336 x 4096]: 384 tokens 50.4 and 45.8, 2048 tokens 135 and 166
+    // dearer.  [4096 x 4096]: 256 tokens 18.9 us by pairs, 16.3 by single CTAs, 512 tokens 23.3 and 20.5;
+    // [14336 x 4096]: 384 tokens 49.5 and 45.8, 2048 tokens 155 and 186 (many in a row, under the power cap)
     const I8Plan pair = i8_plan<I8Pair>(M, N, units, 0.62, 6.0);
     if (pair.t + 3.0 <= one.t) return {2, 256, pair.splits};
     return {1, 128, one.splits};

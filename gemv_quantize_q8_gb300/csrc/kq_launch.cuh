@@ -1,11 +1,15 @@
 // kq_launch.cuh -- launches that may start beside the end of the kernel before them (internal).
 //
-// A kernel launched here calls grid_dependency_wait() before it touches global memory, so it sees all that
-// came before it on its stream; what overlaps is its launch and set-up.  After that wait, not before, it lets
-// the next grid launch (grid_launch_dependents): a grid that starts beside it thus starts after everything
-// earlier has completed, also one that reads its weights before it waits (kq_gemv, and the products here
-// behind their quantizer).
-// (Back to back, [9728 x 2560] with one int8 token: 4.4 us a call without, 3.6 so.)
+// A kernel launched here waits (grid_dependency_wait()) before it touches global memory, so that it sees all that
+// came before it on its stream; what overlaps is its launch and set-up.  After that wait, not before, it lets the
+// next grid launch (grid_launch_dependents).
+// One thing may be read before the wait: weights, their scales and the bias, and only where the launch directly
+// before is the same call's own prologue (quantizer or panel) from here.  That prologue writes none of them and
+// triggers after its own wait, so the product starts when everything before the prologue has completed, a kernel
+// that wrote the weights among it.  (kq_gemv reads its weights before its wait behind any kernel, which must not
+// be the one that wrote them; behind a kernel from here, what came before that one has completed.)
+// Back to back, [9728 x 2560] with one int8 token: 5.4 us a call for 5.5 without, its weights coming from memory;
+// 3.4 for 3.7 where they stay in the L2.  ([14336 x 4096]: 10.6 for 10.2, and 6.5 for 7.2.)
 #pragma once
 #include "kq_internal.cuh"
 #include "kq_sm100.cuh"

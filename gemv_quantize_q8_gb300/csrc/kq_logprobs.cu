@@ -168,7 +168,7 @@ __device__ __forceinline__ float lp_kth(float v, int k, LpShared &sh) {
 
 // One cluster (gridDim.x CTAs, one or more) a row; blockIdx.y the row.  DEPTH rounds of loads are under way: one
 // where four or five CTAs share an SM, more where there are too few CTAs for that (300 rows of 32000 fp32, five
-// alternatives: 17.9 us with one, 10.9 with three).
+// alternatives: 12.1 us with one, 11.1 with three; 167 rows of 49999 f16, eight alternatives: 17.0 and 15.1).
 template <typename T, bool TOP, int DEPTH>
 __global__ void __launch_bounds__(kLpThreads, DEPTH == 1 ? (TOP ? 4 : 5) : DEPTH == 2 ? 3 : 2) lp_kernel(LpParams P) {
     constexpr int VEC = kVec<T>, NV = kLpVecs, NB = kLpBatch / VEC;  // NB: vectors of a batch
@@ -409,12 +409,13 @@ static kq_status launch_lp(const char *fn, LpParams P, int64_t M, int parts, cud
 
 template <typename T, bool TOP>
 static kq_status share_rows(const char *fn, const LpParams &P, int64_t M, cudaStream_t st) {
-    // CTAs that share a row: doubled up to two and a half an SM, while each has a whole round of its own (64 rows
-    // of 131072 bf16, 20 alternatives: four a row 13.5 us, eight 18.3, two 13.8; 167 of 49999: two 15.3, four 17.2)
+    // CTAs that share a row: doubled up to two and a half an SM, while each has a whole round of its own (rows from
+    // memory, 64 of 131072 bf16, 20 alternatives: four a row 13.4 us, eight 16.1, two 13.7; 167 of 49999 f16: two
+    // 15.1, four 19.5, but one 11.8)
     int parts = 1;
     while (parts < kLpMaxParts && M * parts * 2 <= 380 && P.V >= parts * 2 * kLpThreads * kLpVecs * kVec<T>) parts *= 2;
     // as many CTAs an SM as it takes to hold them all, not more: they then spread over the SMs (64 rows as above:
-    // 12.1 us with two an SM, 14.8 where a third would fit)
+    // 13.4 us with two an SM, 15.9 where a third would fit)
     if (M * parts <= 152 * 2) return launch_lp<T, TOP, 3>(fn, P, M, parts, st);
     if (M * parts <= 152 * 3) return launch_lp<T, TOP, 2>(fn, P, M, parts, st);
     return launch_lp<T, TOP, 1>(fn, P, M, parts, st);
