@@ -81,6 +81,15 @@ _SIGS = {
     "kq_qk_norm_rope": ([_I32, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _P, _I64,
                          _I64, _I32, _I32, _P, _I64, _P, _I64, _P], _I32),
     "kq_logprobs": ([_I32, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P, _P], _I32),
+    "kq_kv_append_i8": ([_I32, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _I32, _P, _P, _P, _P,
+                         _I64, _I64, _P, _I64, _P], _I32),
+    "kq_kv_read_i8": ([_P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _P], _I32),
+    "kq_attn_cache_i8_workspace_bytes": ([_I64, _I64, _I64, _I64, _I64], _SZ),
+    "kq_attn_cache_i8": ([_I32, _P, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_float, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P,
+                          _I32, _P, _I64, _P, _SZ, _P], _I32),
+    "kq_attn_prompt_workspace_bytes": ([_I64, _I64, _I64, _I64, _I64], _SZ),
+    "kq_attn_prompt": ([_I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_float, _I32, _P,
+                        _I64, _P, _SZ, _P], _I32),
     "kq_debug_i8_form": ([_I64, _I64, _I64, _P, _P, _P], _I32),
     "kq_debug_i8_wait_timeout": ([_P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I32, _I64, _P, _SZ, _P], _I32),
     "kq_debug_tc_wait_timeout": ([_I32, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _SZ, _P], _I32),
@@ -309,6 +318,44 @@ def kq_logprobs(xt, logits, ldx, M, V, targets, n_targets, logprob, entropy, top
     """Log probabilities of the given tokens (V a row at most), the entropy and the top alternatives of every row of logits."""
     _check(lib().kq_logprobs(xt, _ptr(logits), ldx, M, V, _ptr(targets), n_targets, _ptr(logprob), _ptr(entropy),
                              top_k, _ptr(top_ids), _ptr(top_logprob), _stream(stream)))
+
+
+def kq_kv_append_i8(xt, k, ldk, v, ldv, cu, lens, B, T, n_kv, D, positions, cos_tab, sin_tab, n_pos, rot, pairs, k_cache, v_cache,
+                    k_scale, v_scale, n_pages, page, table, ldt, stream=None):
+    """New tokens' keys (rotated on the way) and values into the paged int8 cache; cu may be None (T / B rows each)."""
+    _check(lib().kq_kv_append_i8(xt, _ptr(k), ldk, _ptr(v), ldv, _ptr(cu), _ptr(lens), B, T, n_kv, D, _ptr(positions),
+                                 _ptr(cos_tab), _ptr(sin_tab), n_pos, rot, pairs, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                 _ptr(v_scale), n_pages, page, _ptr(table), ldt, _stream(stream)))
+
+
+def kq_kv_read_i8(k_cache, v_cache, k_scale, v_scale, n_pages, page, table, ldt, cu, lens, B, T, n_kv, D, yt, k_out, ldk, v_out, ldv,
+                  stream=None):
+    """The last tokens of every sequence in the cache back as rows of type yt."""
+    _check(lib().kq_kv_read_i8(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), n_pages, page, _ptr(table), ldt, _ptr(cu),
+                               _ptr(lens), B, T, n_kv, D, yt, _ptr(k_out), ldk, _ptr(v_out), ldv, _stream(stream)))
+
+
+def kq_attn_cache_i8_workspace_bytes(B, n_new, n_q, n_kv, D) -> int:
+    return int(lib().kq_attn_cache_i8_workspace_bytes(B, n_new, n_q, n_kv, D))
+
+
+def kq_attn_cache_i8(xt, q, ldq, B, n_new, n_q, n_kv, D, scale, k_cache, v_cache, k_scale, v_scale, n_pages, page, table, ldt, lens,
+                     yt, y, ldy, workspace, ws_bytes, stream=None):
+    """Attention of the newest n_new tokens of every sequence over the paged int8 cache."""
+    _check(lib().kq_attn_cache_i8(xt, _ptr(q), ldq, B, n_new, n_q, n_kv, D, float(scale), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                  _ptr(v_scale), n_pages, page, _ptr(table), ldt, _ptr(lens), yt, _ptr(y), ldy, _ptr(workspace),
+                                  ws_bytes, _stream(stream)))
+
+
+def kq_attn_prompt_workspace_bytes(B, Tq, n_q, n_kv, D) -> int:
+    return int(lib().kq_attn_prompt_workspace_bytes(B, Tq, n_q, n_kv, D))
+
+
+def kq_attn_prompt(xt, q, ldq, k, ldk, v, ldv, cu_q, cu_k, B, Tq, Tk, n_q, n_kv, D, scale, causal, y, ldy, workspace, ws_bytes,
+                   stream=None):
+    """Attention over whole packed prompts (F16 or BF16 rows), causal or not."""
+    _check(lib().kq_attn_prompt(xt, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, n_q, n_kv, D,
+                                float(scale), int(causal), _ptr(y), ldy, _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def kq_debug_partials(wt, w, xq, M, N, K, partials, stream=None):

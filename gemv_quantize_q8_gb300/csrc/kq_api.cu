@@ -11,7 +11,7 @@ namespace kq {
 static thread_local char g_last_error[512] = "";
 static std::atomic<int64_t> g_launches[R_COUNT];
 static const char *kRouteNames[R_COUNT] = {"quantize", "repack", "gemv", "mmq_exact", "mmq_tc", "route", "weighted_sum",
-                                              "i8", "qk_norm_rope", "logprobs"};
+                                              "i8", "qk_norm_rope", "logprobs", "kv_cache", "attention"};
 
 void count_launch(Route r, int kernels) { g_launches[r].fetch_add(kernels, std::memory_order_relaxed); }
 

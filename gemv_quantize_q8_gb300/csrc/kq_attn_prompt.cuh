@@ -1,0 +1,59 @@
+// kq_attn_prompt.cuh -- attention over whole prompts: what its kernels share (internal).
+#pragma once
+#include "kq_value.cuh"
+
+namespace kq {
+
+struct PaParams {
+    const void *q, *k, *v;
+    void *y;
+    int64_t ldq, ldk, ldv, ldy;
+    const int32_t *cu_q, *cu_k;  // [B + 1]
+    int64_t B, Tq, Tk;
+    int n_q, G, D;               // query heads, those of a key head, elements
+    float scale;                 // times log2 e
+    bool causal;
+    unsigned long long *err;     // device flag, cleared by the call
+};
+
+// Some tokens of one sequence: `first` on of its n_q, with its n_k keys.
+struct PaTile {
+    int64_t q_row, k_row;
+    int n_q, n_k, first;
+};
+
+__device__ __forceinline__ int64_t pa_row(const int32_t *cu, int64_t b, int64_t T) {
+    const int64_t r = cu[b];
+    return r < 0 ? 0 : r > T ? T : r;
+}
+// Tile `unit` of `size` tokens: sequence b's tiles start at floor(cu_q[b] / size) + b, which leaves room for them all.
+// All threads of the block call it; false where there is no such tile.
+template <int THREADS>
+__device__ __forceinline__ bool pa_tile(const PaParams &P, int64_t unit, int size, PaTile &t) {
+    int64_t b = -1;
+    for (int64_t b0 = 0; b0 < P.B; b0 += THREADS) {
+        const int64_t i = b0 + threadIdx.x;
+        const int n = __syncthreads_count(i < P.B && pa_row(P.cu_q, i, P.Tq) / size + i <= unit);
+        b += n;
+        if (n < THREADS) break;
+    }
+    if (b < 0) return false;
+    t.q_row = pa_row(P.cu_q, b, P.Tq);
+    t.k_row = pa_row(P.cu_k, b, P.Tk);
+    const int64_t first = (unit - t.q_row / size - b) * size;
+    const int64_t n_q = pa_row(P.cu_q, b + 1, P.Tq) - t.q_row, n_k = pa_row(P.cu_k, b + 1, P.Tk) - t.k_row;
+    if (first >= n_q) return false;
+    t.n_q = (int)n_q;
+    t.n_k = n_k > 0 ? (int)n_k : 0;
+    t.first = (int)first;
+    return true;
+}
+// The keys that token i of the sequence sees: those below this (the last token sees them all where causal).
+__device__ __forceinline__ int pa_limit(const PaParams &P, const PaTile &t, int i) {
+    if (i >= t.n_q) return 0;
+    if (!P.causal) return t.n_k;
+    const int n = t.n_k - t.n_q + 1 + i;
+    return n > 0 ? n : 0;
+}
+
+}  // namespace kq

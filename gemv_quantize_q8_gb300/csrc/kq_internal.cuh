@@ -17,7 +17,7 @@ kq_status check_launch(const char *what);
 const char *dtype_name(kq_dtype d);
 
 // Host-side routing witness: counts kernel launches per route.
-enum Route { R_QUANT = 0, R_REPACK, R_GEMV, R_MMQ_EXACT, R_MMQ_TC, R_ROUTE, R_WSUM, R_I8, R_QK, R_LOGPROBS, R_COUNT };
+enum Route { R_QUANT = 0, R_REPACK, R_GEMV, R_MMQ_EXACT, R_MMQ_TC, R_ROUTE, R_WSUM, R_I8, R_QK, R_LOGPROBS, R_KV, R_ATTN, R_COUNT };
 void count_launch(Route r, int kernels = 1);
 
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

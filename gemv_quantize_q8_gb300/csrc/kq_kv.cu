@@ -1,0 +1,343 @@
+// kq_kv.cu -- new keys (rotated on the way) and values into the paged 8-bit cache, and cached rows back.
+//
+// A block of the cache (a page and head) has one scale, so its largest magnitude has to be known before its
+// first code is written, and when a later token raises it the codes that are there follow:
+//   s' = max(s, max |x| / 127),   q' = rint(q * (s / s')) for the old tokens,   q = rint(x * (1 / s')) for the new.
+// One thread block takes one block of the cache that the call touches: it keeps the new rows in registers between
+// the maximum and the codes, so every row is read once and every code written once.  Which blocks those are follows
+// from cu and lens on the device: sequence b's share of the grid starts at floor(cu[b] / page) + 2b, which leaves
+// room for every page that its rows can touch (a run of n tokens touches at most floor(n / page) + 2).
+// The maximum, every product and sum are rounded one by one, so that codes and scales are the same bits whatever
+// the grid or the vector width.
+#include "kq_kv.cuh"
+#include "kq_launch.cuh"
+
+namespace kq {
+
+constexpr int kKvThreads = 256;
+constexpr int kKvHeld = 4;  // vector pairs of a thread that stay in registers: 64 tokens of 128
+
+struct KvRows {
+    void *k, *v;  // [T][ldk], [T][ldv]
+    int64_t ldk, ldv;
+    const int32_t *cu;  // [B + 1] or NULL
+    int64_t T;
+};
+struct KvTurn {
+    const int32_t *pos;
+    const float *cos_tab, *sin_tab;
+    int64_t n_pos;
+    int rot;
+};
+
+// A thread block's part of the cache: tokens [lo, hi) of a page from row `row` on.
+struct KvPart {
+    int64_t page, row;
+    int lo, hi;
+};
+// All threads of the block call it; false where there is nothing to do.
+__device__ __forceinline__ bool kv_part(const KvCache &c, const KvRows &r, int64_t unit, KvPart &p) {
+    // the last sequence whose share starts at or before the unit; shares start in rising order
+    int64_t b = -1;
+    for (int64_t b0 = 0; b0 < c.B; b0 += kKvThreads) {
+        const int64_t i = b0 + threadIdx.x;
+        const int n = __syncthreads_count(i < c.B && (kv_row(r.cu, i, c.B, r.T) >> c.lp) + 2 * i <= unit);
+        b += n;
+        if (n < kKvThreads) break;
+    }
+    if (b < 0) return false;
+    const int64_t r0 = kv_row(r.cu, b, c.B, r.T), r1 = kv_row(r.cu, b + 1, c.B, r.T), len = c.lens[b], n = r1 - r0;
+    const int64_t first = len - n, begin = first > 0 ? first : 0;  // positions of the rows; those before 0 have no place
+    const int64_t i = (begin >> c.lp) + (unit - (r0 >> c.lp) - 2 * b);
+    const int64_t lo = max(begin, i << c.lp), hi = min(len, (i + 1) << c.lp);
+    if (n <= 0 || lo >= hi || i >= c.ldt) return false;
+    p.page = c.table[b * c.ldt + i];
+    if (p.page < 0 || p.page >= c.n_pages) return false;
+    p.row = r0 + (lo - first);
+    p.lo = (int)(lo - (i << c.lp));
+    p.hi = (int)(hi - (i << c.lp));
+    return true;
+}
+
+// W elements as fp32; the address is aligned to all of them.
+template <int W, typename T>
+__device__ __forceinline__ void kv_load(const T *p, float (&v)[W]) {
+    if constexpr (W == 1) {
+        v[0] = to_f32(*p);
+    } else {
+        using Vec = typename VecOf<W * (int)sizeof(T)>::type;
+        const Vec u = *reinterpret_cast<const Vec *>(p);
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = to_f32(reinterpret_cast<const T *>(&u)[i]);
+    }
+}
+
+// Codes of a row's elements: NaN gives 0, and what rounding carries past 127 stays there.
+__device__ __forceinline__ int kv_code(float x, float inv) {
+    const float v = __fmul_rn(x, inv);
+    return isnan(v) ? 0 : __float2int_rn(fminf(fmaxf(v, -127.0f), 127.0f));
+}
+__device__ __forceinline__ uint32_t kv_pack(int a, int b, int c, int d) {
+    return (a & 255) | (b & 255) << 8 | (c & 255) << 16 | (uint32_t)d << 24;
+}
+
+// Vector pair j of a row covers [lo, lo + W) and [hi, hi + W): first the rotated pairs (both partners in one
+// thread), then the rest of the head.  W is 4, or 1 where rows or halves do not lie on four elements.
+template <typename TX, bool PAIRS, int W>
+__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(KvCache c, KvRows r, KvTurn turn) {
+    __shared__ float red[kKvThreads / 32];
+    sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
+    const int tid = threadIdx.x, which = blockIdx.y >= c.n_kv, head = blockIdx.y - (which ? c.n_kv : 0);
+    KvPart p;
+    if (!kv_part(c, r, blockIdx.x, p)) return;
+    const int64_t block = p.page * c.n_kv + head;
+    float *scale = (which ? c.v_scale : c.k_scale) + block;
+    int8_t *codes = (which ? c.v : c.k) + (block << c.lp) * c.D;
+    const int64_t ld = which ? r.ldv : r.ldk;
+    const TX *x = static_cast<const TX *>(which ? r.v : r.k) + p.row * ld + head * c.D;
+    const float was = p.lo ? *scale : 0.0f;  // a page's first token starts it anew
+    const int rot = which ? 0 : turn.rot, half = rot / 2, turned = half / W, np = c.D / (2 * W), items = (p.hi - p.lo) * np;
+
+    auto places = [&](int item, int &t, int &lo, int &hi, int &j) {
+        t = item / np;
+        j = item - t * np;
+        lo = PAIRS || j >= turned ? 2 * W * j : W * j;
+        hi = PAIRS || j >= turned ? lo + W : lo + half;
+    };
+    auto load = [&](int item, float (&u)[W], float (&w)[W]) {
+        int t, lo, hi, j;
+        places(item, t, lo, hi, j);
+        kv_load<W>(x + t * ld + lo, u);
+        kv_load<W>(x + t * ld + hi, w);
+        if (j >= turned) return;
+        const int64_t at = turn.pos[p.row + t];
+        const bool known = at >= 0 && at < turn.n_pos;  // else no angle: NaN, whose code is 0
+        float cs[W], sn[W];
+        if (known) {
+            kv_load<W>(turn.cos_tab + at * half + j * W, cs);
+            kv_load<W>(turn.sin_tab + at * half + j * W, sn);
+        }
+        auto rotate = [&](float &a, float &b, float cv, float sv) {
+            const float a0 = a, b0 = b;
+            a = known ? __fsub_rn(__fmul_rn(a0, cv), __fmul_rn(b0, sv)) : nanf("");
+            b = known ? __fadd_rn(__fmul_rn(b0, cv), __fmul_rn(a0, sv)) : nanf("");
+        };
+        if constexpr (PAIRS && W == 4) {
+            rotate(u[0], u[1], cs[0], sn[0]);
+            rotate(u[2], u[3], cs[1], sn[1]);
+            rotate(w[0], w[1], cs[2], sn[2]);
+            rotate(w[2], w[3], cs[3], sn[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) rotate(u[i], w[i], cs[i], sn[i]);
+        }
+    };
+
+    float u[kKvHeld][W], w[kKvHeld][W], amax = 0.0f;
+    auto widen = [&](const float (&a)[W], const float (&b)[W]) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) amax = fmaxf(amax, fmaxf(fabsf(a[i]), fabsf(b[i])));  // (NaN never wins)
+    };
+#pragma unroll
+    for (int k = 0; k < kKvHeld; ++k)
+        if (tid + k * kKvThreads < items) {
+            load(tid + k * kKvThreads, u[k], w[k]);
+            widen(u[k], w[k]);
+        }
+    for (int i = tid + kKvHeld * kKvThreads; i < items; i += kKvThreads) {
+        float a[W], b[W];
+        load(i, a, b);
+        widen(a, b);
+    }
+#pragma unroll
+    for (int s = 16; s; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, s));
+    if ((tid & 31) == 0) red[tid >> 5] = amax;
+    __syncthreads();
+    amax = red[0];
+#pragma unroll
+    for (int i = 1; i < kKvThreads / 32; ++i) amax = fmaxf(amax, red[i]);
+
+    const float now = fmaxf(was, __fdiv_rn(amax, 127.0f));
+    if (tid == 0) *scale = now;
+    if (now > was && was > 0.0f) {
+        const float f = __fdiv_rn(was, now);
+        uint32_t *old = reinterpret_cast<uint32_t *>(codes);
+        for (int i = tid; i < p.lo * c.D / 4; i += kKvThreads) {
+            const uint32_t q = old[i];
+            auto again = [&](int shift) { return kv_code((float)(int8_t)(q >> shift), f); };
+            old[i] = kv_pack(again(0), again(8), again(16), again(24));
+        }
+    }
+    float inv = __fdiv_rn(1.0f, now);
+    if (isinf(inv)) inv = 0.0f;  // a block of zeros, or below 2^-128
+    auto store = [&](int item, const float (&a)[W], const float (&b)[W]) {
+        int t, lo, hi, j;
+        places(item, t, lo, hi, j);
+        int8_t *row = codes + (p.lo + t) * c.D;
+        if constexpr (W == 4) {
+            *reinterpret_cast<uint32_t *>(row + lo) = kv_pack(kv_code(a[0], inv), kv_code(a[1], inv), kv_code(a[2], inv), kv_code(a[3], inv));
+            *reinterpret_cast<uint32_t *>(row + hi) = kv_pack(kv_code(b[0], inv), kv_code(b[1], inv), kv_code(b[2], inv), kv_code(b[3], inv));
+        } else {
+            row[lo] = (int8_t)kv_code(a[0], inv);
+            row[hi] = (int8_t)kv_code(b[0], inv);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < kKvHeld; ++k)
+        if (tid + k * kKvThreads < items) store(tid + k * kKvThreads, u[k], w[k]);
+    for (int i = tid + kKvHeld * kKvThreads; i < items; i += kKvThreads) {
+        float a[W], b[W];
+        load(i, a, b);
+        store(i, a, b);
+    }
+}
+
+// Sixteen codes a thread at a time.  VEC: rows that 16-byte stores fit.
+template <typename TY, bool VEC>
+__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(KvCache c, KvRows r) {
+    sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
+    const int which = blockIdx.y >= c.n_kv, head = blockIdx.y - (which ? c.n_kv : 0);
+    KvPart p;
+    if (!kv_part(c, r, blockIdx.x, p)) return;
+    const int64_t block = p.page * c.n_kv + head;
+    const float scale = (which ? c.v_scale : c.k_scale)[block];
+    const int8_t *codes = (which ? c.v : c.k) + ((block << c.lp) + p.lo) * c.D;
+    const int64_t ld = which ? r.ldv : r.ldk;
+    TY *y = static_cast<TY *>(which ? r.v : r.k) + p.row * ld + head * c.D;
+    const int pieces = c.D / 16, items = (p.hi - p.lo) * pieces;
+    for (int i = threadIdx.x; i < items; i += kKvThreads) {
+        const int t = i / pieces, d = (i - t * pieces) * 16;
+        const uint4 q = *reinterpret_cast<const uint4 *>(codes + (int64_t)i * 16);
+        TY v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = from_f32<TY>(__fmul_rn((float)reinterpret_cast<const int8_t *>(&q)[j], scale));
+        TY *dst = y + t * ld + d;
+        if (VEC) {
+#pragma unroll
+            for (int j = 0; j < 16; j += kVec<TY>) *reinterpret_cast<uint4 *>(dst + j) = *reinterpret_cast<const uint4 *>(v + j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) dst[j] = v[j];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+kq_status kv_check(const char *fn, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale, const float *v_scale,
+                   int64_t n_pages, int64_t page, const int32_t *table, int64_t ldt, const int32_t *lens, int64_t B,
+                   int64_t n_kv, int64_t D, KvCache &c) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale) return fail(KQ_ERR_INVALID_ARG, "%s: null cache or scales", fn);
+    if (!table || !lens) return fail(KQ_ERR_INVALID_ARG, "%s: null %s", fn, table ? "lens" : "table");
+    if (B <= 0 || B > (1 << 24) || n_kv <= 0 || n_kv > kKvMaxHeads || D <= 0 || D > kKvMaxD || D % 16)
+        return fail(KQ_ERR_INVALID_ARG, "%s: need 1 to 2^24 sequences, 1 to %d key heads and D a multiple of 16 up to %d (B=%lld n_kv=%lld D=%lld)",
+                    fn, kKvMaxHeads, kKvMaxD, (long long)B, (long long)n_kv, (long long)D);
+    if (page < 16 || page > kKvMaxPage || (page & (page - 1)))
+        return fail(KQ_ERR_INVALID_ARG, "%s: page=%lld is not a power of two in 16..%d", fn, (long long)page, kKvMaxPage);
+    if (n_pages <= 0 || n_pages > 0x7fffffff || ldt <= 0 || ldt > 0x7fffffff)
+        return fail(KQ_ERR_INVALID_ARG, "%s: need n_pages and ldt in 1..2^31-1 (n_pages=%lld ldt=%lld)", fn, (long long)n_pages, (long long)ldt);
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(table, 4) || !aligned(lens, 4))
+        return fail(KQ_ERR_ALIGNMENT, "%s: the caches must be 16-byte aligned, scales, table and lens to their elements", fn);
+    c.k = const_cast<int8_t *>(k_cache);
+    c.v = const_cast<int8_t *>(v_cache);
+    c.k_scale = const_cast<float *>(k_scale);
+    c.v_scale = const_cast<float *>(v_scale);
+    c.table = table;
+    c.lens = lens;
+    c.n_pages = n_pages;
+    c.ldt = ldt;
+    c.B = B;
+    c.n_kv = (int)n_kv;
+    c.D = (int)D;
+    for (c.lp = 4; (1 << c.lp) < page; ++c.lp) {}
+    return KQ_OK;
+}
+
+// The packed rows of a call, and the grid over the blocks of the cache that they can touch.
+static kq_status kv_check_rows(const char *fn, kq_dtype t, const void *k, int64_t ldk, const void *v, int64_t ldv, const int32_t *cu,
+                               int64_t T, const KvCache &c, KvRows &r, dim3 &grid) {
+    if (!is_value_type(t)) return fail(KQ_ERR_UNSUPPORTED_DTYPE, "%s: row type %s is not F32, F16 or BF16", fn, dtype_name(t));
+    if (!k || !v) return fail(KQ_ERR_INVALID_ARG, "%s: null rows", fn);
+    const int64_t width = (int64_t)c.n_kv * c.D;
+    if (T <= 0 || T > 0x7fffffff || (!cu && T % c.B))
+        return fail(KQ_ERR_INVALID_ARG, "%s: need T > 0, and a multiple of B where cu is NULL (T=%lld)", fn, (long long)T);
+    if (ldk < width || ldv < width)
+        return fail(KQ_ERR_INVALID_ARG, "%s: ldk=%lld or ldv=%lld is less than n_kv*D", fn, (long long)ldk, (long long)ldv);
+    const size_t e = value_bytes(t);
+    if (!aligned(k, e) || !aligned(v, e) || !aligned(cu, 4))
+        return fail(KQ_ERR_ALIGNMENT, "%s: a pointer is not aligned to its elements", fn);
+    const int64_t units = (T >> c.lp) + 2 * c.B;
+    if (units > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: T=%lld is too large", fn, (long long)T);
+    r = {const_cast<void *>(k), const_cast<void *>(v), ldk, ldv, cu, T};
+    grid = dim3((unsigned)units, 2 * c.n_kv);
+    return KQ_OK;
+}
+
+template <typename TX>
+static cudaError_t launch_append(const KvCache &c, const KvRows &r, const KvTurn &t, bool pairs, bool vec, dim3 grid, cudaStream_t st) {
+    auto kern = vec ? (pairs ? kv_append_kernel<TX, true, 4> : kv_append_kernel<TX, false, 4>)
+                    : (pairs ? kv_append_kernel<TX, true, 1> : kv_append_kernel<TX, false, 1>);
+    return launch_beside(kern, grid, dim3(kKvThreads), 0, dim3(1), st, c, r, t);
+}
+
+}  // namespace kq
+
+using namespace kq;
+
+extern "C" {
+
+kq_status kq_kv_append_i8(kq_dtype xt, const void *k, int64_t ldk, const void *v, int64_t ldv, const int32_t *cu,
+                          const int32_t *lens, int64_t B, int64_t T, int64_t n_kv, int64_t D, const int32_t *positions,
+                          const float *cos_tab, const float *sin_tab, int64_t n_pos, int64_t rot, int pairs, int8_t *k_cache,
+                          int8_t *v_cache, float *k_scale, float *v_scale, int64_t n_pages, int64_t page, const int32_t *table,
+                          int64_t ldt, kq_stream_t stream) {
+    const char *fn = "kq_kv_append_i8";
+    KvCache c;
+    KvRows r;
+    dim3 grid;
+    kq_status s = kv_check(fn, k_cache, v_cache, k_scale, v_scale, n_pages, page, table, ldt, lens, B, n_kv, D, c);
+    if (s == KQ_OK) s = kv_check_rows(fn, xt, k, ldk, v, ldv, cu, T, c, r, grid);
+    if (s != KQ_OK) return s;
+    if (rot < 0 || rot > D || rot % 2) return fail(KQ_ERR_INVALID_ARG, "%s: rot=%lld is not even in 0..D", fn, (long long)rot);
+    if (pairs != 0 && pairs != 1) return fail(KQ_ERR_INVALID_ARG, "%s: pairs=%d is not 0 or 1", fn, pairs);
+    if (rot && (!positions || !cos_tab || !sin_tab || n_pos <= 0))
+        return fail(KQ_ERR_INVALID_ARG, "%s: a rotation needs positions, cos_tab, sin_tab and n_pos > 0", fn);
+    if (!rot) positions = nullptr, cos_tab = sin_tab = nullptr;
+    if (!aligned(positions, 4) || !aligned(cos_tab, 4) || !aligned(sin_tab, 4))
+        return fail(KQ_ERR_ALIGNMENT, "%s: a pointer is not aligned to its elements", fn);
+    // four elements at once: rows, halves and the tables' rows on boundaries of four
+    const size_t four = 4 * value_bytes(xt);
+    const bool vec = aligned(k, four) && aligned(v, four) && ldk % 4 == 0 && ldv % 4 == 0 && (rot / 2) % 4 == 0 && aligned(cos_tab, 16) &&
+                     aligned(sin_tab, 16);
+    return with_type(xt, [&](auto t) {
+        const cudaError_t e = launch_append<decltype(t)>(c, r, {positions, cos_tab, sin_tab, n_pos, (int)rot}, pairs != 0, vec, grid,
+                                                         (cudaStream_t)stream);
+        if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+        count_launch(R_KV);
+        return KQ_OK;
+    });
+}
+
+kq_status kq_kv_read_i8(const int8_t *k_cache, const int8_t *v_cache, const float *k_scale, const float *v_scale, int64_t n_pages,
+                        int64_t page, const int32_t *table, int64_t ldt, const int32_t *cu, const int32_t *lens, int64_t B, int64_t T,
+                        int64_t n_kv, int64_t D, kq_dtype yt, void *k_out, int64_t ldk, void *v_out, int64_t ldv, kq_stream_t stream) {
+    const char *fn = "kq_kv_read_i8";
+    KvCache c;
+    KvRows r;
+    dim3 grid;
+    kq_status s = kv_check(fn, k_cache, v_cache, k_scale, v_scale, n_pages, page, table, ldt, lens, B, n_kv, D, c);
+    if (s == KQ_OK) s = kv_check_rows(fn, yt, k_out, ldk, v_out, ldv, cu, T, c, r, grid);
+    if (s != KQ_OK) return s;
+    const int64_t e16 = 16 / (int64_t)value_bytes(yt);
+    const bool vec = aligned(k_out, 16) && aligned(v_out, 16) && ldk % e16 == 0 && ldv % e16 == 0;
+    return with_type(yt, [&](auto t) {
+        auto kern = vec ? kv_read_kernel<decltype(t), true> : kv_read_kernel<decltype(t), false>;
+        const cudaError_t e = launch_beside(kern, grid, dim3(kKvThreads), 0, dim3(1), (cudaStream_t)stream, c, r);
+        if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+        count_launch(R_KV);
+        return KQ_OK;
+    });
+}
+
+}  // extern "C"

@@ -396,10 +396,86 @@ KQ_API kq_status kq_logprobs(kq_dtype xt, const void *logits, int64_t ldx, int64
                              int64_t n_targets, float *logprob, float *entropy, int64_t top_k, int32_t *top_ids,
                              float *top_logprob, kq_stream_t stream);
 
+/* ---- attention and its cache ----
+ *
+ * The cache of keys and values is paged and held in 8 bits.  A page holds `page` consecutive tokens of one
+ * sequence (a power of two, 16 .. 256); k_cache and v_cache are int8 [n_pages][n_kv][page][D] (16-byte aligned, D
+ * a multiple of 16 up to 256, n_kv up to 1024), k_scale and v_scale fp32 [n_pages][n_kv]: one scale for each
+ * page and head.  A cached element stands for code * scale.  table: int32 [B][ldt], table[b][i] the page with the
+ * tokens i*page .. i*page + page - 1 of sequence b; lens: int32 [B], the tokens in each sequence's cache, those that
+ * the call brings among them.  B is up to 2^24, n_pages and ldt up to 2^31 - 1.  Entries of the table behind
+ * a sequence's last page are not read.  Several sequences may share a page that is only read.
+ *
+ * Packed rows: sequence b has the rows cu[b] .. cu[b+1] - 1 of a call's T rows (cu: int32 [B + 1], not
+ * falling); they are its last tokens, so the last row is token lens[b] - 1.  cu = NULL: T / B rows each (T
+ * a multiple of B).  Rows that no sequence has (behind cu[B]) are neither read nor written. */
+
+/* Append keys and values of new tokens, the keys rotated on the way.
+ * k: [T][ldk] of type xt (KQ_F32, KQ_F16 or KQ_BF16, element-aligned), n_kv heads of D elements side by side; v likewise
+ * (both may be column ranges of one product's rows).  The rotation is kq_qk_norm_rope's: positions int32
+ * [T], cos_tab and sin_tab fp32 [n_pos][rot/2], rot even in 0 .. D, pairs 0 (halves) or 1 (neighbours), each product and sum
+ * rounded once; a position outside [0, n_pos) makes NaN of the rotated part.  rot = 0: keys as they come (the tables unused).
+ * For each page, head, and keys and values apart, with x the new tokens' elements of the page:
+ *   s' = max(s, max |x| / 127), where s is the block's scale, or 0 if the call writes the page's first token,
+ *   codes of the page's earlier tokens: nearest-even(code * (s / s')) where s' > s > 0,
+ *   codes of the new tokens: nearest-even(x * (1 / s')) within -127 .. 127,
+ * in fp32, divisions IEEE.  NaN never wins the maximum and gives code 0; where 1/s' is not finite (s' below 2.94e-39)
+ * the codes are 0; an infinity makes the block's scale infinite (what reads it gives NaN) until its page is begun
+ * anew.  Writing a token again, or fewer tokens than before (lens taken back), is fine: the scale keeps
+ * its size.  No page may get tokens of two sequences in one call.  Tokens without a place
+ * (a row before token 0, or a page that is outside [0, n_pages) or past the table's ldt) are left out. */
+KQ_API kq_status kq_kv_append_i8(kq_dtype xt, const void *k, int64_t ldk, const void *v, int64_t ldv, const int32_t *cu,
+                                 const int32_t *lens, int64_t B, int64_t T, int64_t n_kv, int64_t D, const int32_t *positions,
+                                 const float *cos_tab, const float *sin_tab, int64_t n_pos, int64_t rot, int pairs, int8_t *k_cache,
+                                 int8_t *v_cache, float *k_scale, float *v_scale, int64_t n_pages, int64_t page,
+                                 const int32_t *table, int64_t ldt, kq_stream_t stream);
+
+/* Cached rows back: the last tokens of every sequence, as many as cu gives it, to k_out [T][ldk] and v_out [T][ldv] of
+ * type yt (element-aligned), each element code * scale rounded once to fp32 and once more to yt.  With it a prompt goes
+ * on behind a cached part through kq_attn_prompt.  Rows of tokens without a place are left as they were. */
+KQ_API kq_status kq_kv_read_i8(const int8_t *k_cache, const int8_t *v_cache, const float *k_scale, const float *v_scale,
+                               int64_t n_pages, int64_t page, const int32_t *table, int64_t ldt, const int32_t *cu,
+                               const int32_t *lens, int64_t B, int64_t T, int64_t n_kv, int64_t D, kq_dtype yt, void *k_out,
+                               int64_t ldk, void *v_out, int64_t ldv, kq_stream_t stream);
+
+/* Attention of the newest tokens over the cache, as decoding does: sequence b has the n_new query rows b*n_new ..
+ * b*n_new + n_new - 1, its tokens lens[b] - n_new .. lens[b] - 1 (in the cache already: append first), each of which sees the
+ * tokens up to itself:
+ *   y = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * (q . k_j) - max)
+ * q: [B*n_new][ldq] of type xt, n_q heads of D elements; query head h reads key head h / (n_q / n_kv), n_q a multiple of
+ * n_kv.  y: [B*n_new][ldy] of type yt.  q and y are element-aligned; y may be q itself (same type and stride).  n_new*n_q is
+ * at most 65536; scale is finite.  Queries and weights are carried in 22 bits, sums in fp32, so fp32 rows come out
+ * with about fp32's accuracy.  A token that sees nothing (lens[b] = 0, or a row before token 0) gives 0.  A page
+ * outside [0, n_pages), or a length past ldt pages, gives NaN.
+ * workspace: kq_attn_cache_i8_workspace_bytes(...) bytes (0: a shape that the call refuses), 256-byte aligned; its content
+ * does not matter before the call, and calls that share it must not overlap. */
+KQ_API size_t kq_attn_cache_i8_workspace_bytes(int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv, int64_t D);
+KQ_API kq_status kq_attn_cache_i8(kq_dtype xt, const void *q, int64_t ldq, int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv,
+                                  int64_t D, float scale, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale,
+                                  const float *v_scale, int64_t n_pages, int64_t page, const int32_t *table, int64_t ldt,
+                                  const int32_t *lens, kq_dtype yt, void *y, int64_t ldy, void *workspace, size_t ws_bytes,
+                                  kq_stream_t stream);
+
+/* Attention over whole prompts, packed: sequence b has the query rows cu_q[b] .. cu_q[b+1] - 1 and the key and value
+ * rows cu_k[b] .. cu_k[b+1] - 1 (int32 [B + 1] each, not falling; one array may serve both).  causal = 1: its query tokens are the
+ * last of its keys (token i of n_q sees the first n_k - n_q + 1 + i keys); causal = 0: every token sees every key.
+ * The formula is kq_attn_cache_i8's.  q: [Tq][ldq], k: [Tk][ldk], v: [Tk][ldv], y: [Tq][ldy], all of
+ * type xt (KQ_F16 or KQ_BF16), element-aligned; n_q heads of D elements over n_kv, a multiple; D a multiple of 8 up
+ * to 256; Tq and Tk up to 2^31 - 256, B up to 2^24, n_q up to 65535; scale is finite.  y may be q itself (same stride).
+ * Scores and sums are fp32; the weights are rounded to xt for the second product.  A token that sees no key gives 0; what a
+ * token does not see has no influence on it, infinities and NaN included.  Rows behind cu_q[B] are left as they were.
+ * workspace: kq_attn_prompt_workspace_bytes(...) bytes (0: a shape that the call refuses), 256-byte aligned;
+ * kq_read_device_flag applies to it (a tensor-core pipeline wait that timed out). */
+KQ_API size_t kq_attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv, int64_t D);
+KQ_API kq_status kq_attn_prompt(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                const int32_t *cu_q, const int32_t *cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t n_q,
+                                int64_t n_kv, int64_t D, float scale, int causal, void *y, int64_t ldy, void *workspace,
+                                size_t ws_bytes, kq_stream_t stream);
+
 /* Routing witness (host-side dispatch counters): number of kernel launches made by this library
  * since load, in total (route = NULL) or for one route: "quantize", "repack", "gemv", "mmq_exact",
- * "mmq_tc", "route", "weighted_sum", "i8" (the int8 products), "qk_norm_rope", "logprobs".  Unknown
- * route names return -1.  Thread-safe. */
+ * "mmq_tc", "route", "weighted_sum", "i8" (the int8 products), "qk_norm_rope", "logprobs", "kv_cache",
+ * "attention".  Unknown route names return -1.  Thread-safe. */
 KQ_API int64_t kq_launch_count(const char *route);
 
 /* Debug: the integer sub-block dots of kq_gemm, partials[m][n][j] (int32)
