@@ -223,6 +223,7 @@ kq_status kq_attn_prompt(kq_dtype xt, const void *q, int64_t ldq, const void *k,
     const PaParams P{q, k, v, y, ldq, ldk, ldv, ldy, cu_q, cu_k, B, Tq, Tk, (int)n_q, (int)(n_q / n_kv), (int)D,
                      scale * 1.44269504f, causal != 0, static_cast<unsigned long long *>(workspace)};
     const cudaStream_t st = (cudaStream_t)stream;
+    if (pa_takes_tc(P)) return pa_tc(fn, xt, P, kPtWaitNs, 0, st);
     auto go = [&](auto t) {
         using T = decltype(t);
         return D <= 64 ? launch_pa<T, 64>(fn, P, st) : D <= 128 ? launch_pa<T, 128>(fn, P, st) : launch_pa<T, 256>(fn, P, st);
