@@ -3,21 +3,24 @@
 // For a query row q (one token and head) over the tokens j that it sees, with s_j = scale * ks * (q . K_j) for codes
 // K, V and their blocks' scales ks, vs:
 //   m = max s_j,  l = sum 2^(s_j - m),  y = (sum 2^(s_j - m) vs V_j) / l       (s in units of log 2)
-// Bound by the cache's bytes: each is read once, by the warp that needs it, straight into the registers that
-// feed its matrix instructions; nothing is staged.
+// Bound by the cache's bytes: each is read once, by TMA, into a ring of the warp that needs it (2 or 4 KB a copy,
+// several units under way; a warp waits for nobody else).  (By 16-byte copies of every lane the loads alone took
+// 136 us for two sequences of 131072, 537 MB.)
 //
 // The products run on m16n8k16 instructions.  Codes are exact in f16; a query row is brought to |q| < 2 by a power
 // of two and split into two f16 (22 bits), as the weights 2^(s - m) vs are.  With up to eight rows (the query heads of
 // one key head) the second parts fill the tile's other eight rows, so they cost nothing; 9 to 16 rows take twice
 // the instructions.  Which of its elements a lane holds is free where both operands agree, so it follows the loads:
-//   keys:   lane 4n + c of an eight-token tile loads 16-byte pieces c, c + 4, .. of token n; 4 bytes make the two
+//   keys:   lane 4n + c of an eight-token tile takes the 16-byte pieces 2c and 2c + 1 of token n; 4 bytes make the two
 //           registers of one step.
-//   values: lane 4n + c loads 16 bytes at n * 16 of tokens 2c, 2c + 1, 2c + 8, 2c + 9: the tokens whose weights it
-//           holds, the bytes of two tokens paired by permutes.
-// A unit is 16 tokens (a page holds whole units).  All units of all sequences and heads form one line, cut into equal shares, one a
+//   values: lane 4n + c takes piece n of tokens 2c, 2c + 1, 2c + 8, 2c + 9: the tokens whose weights it holds, the
+//           bytes of two tokens paired by permutes.
+// With the copies' 128-byte swizzle neither has bank conflicts.
+// A unit is 32 tokens, two halves of 16 with scales of their own (a page holds whole halves).  All units of all sequences and heads form one line, cut into equal shares, one a
 // warp: lengths may differ as they like.  A row whose units are shared by warps is put together in shared memory,
 // one that is shared by thread blocks through the workspace and a second kernel, in a fixed order.
-#include <algorithm>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <math.h>
 
 #include "kq_i8_tc.cuh"
@@ -26,7 +29,9 @@
 
 namespace kq {
 
-constexpr int kAcUnit = 16;           // tokens
+constexpr int kAcUnit = 32;           // tokens
+constexpr int kAcLeast = 2;           // units of a warp
+constexpr int kAcMaxBlocks = 152;     // one an SM
 constexpr float kAcLift = 128.0f;     // weights are held times this: f16 keeps their low bits, with room for kAcSlack
 constexpr float kAcSlack = 8.0f;      // a weight may grow to 2^8 before the sums are brought to a new maximum
 constexpr float kAcNone = -3.0e38f;   // the maximum of no token
@@ -37,12 +42,13 @@ struct AcParams {
     void *y;
     int64_t ldq, ldy;
     kq_dtype xt, yt;
-    bool qvec;            // query rows on boundaries of four elements
+    bool qvec, yvec;      // query rows on boundaries of four elements, output rows on 16 bytes
     int n_new, n_q, G;    // query tokens of a sequence, query heads, and those of a key head
     int rows, tiles;      // rows of a key head (n_new * G), and the row tiles that they take
     float scale;          // times log2 e
-    float *parts;         // [blocks][2] partial results
-    int blocks;           // of the first kernel's grid
+    unsigned long long *err;  // device flag, cleared by the call
+    float *parts;             // [blocks][2] partial results
+    int blocks, warps;    // of the first kernel's grid
 };
 
 // What a warp (or a block) hands over: rows of m, l and D sums, relative to 2^m.
@@ -76,8 +82,18 @@ __device__ __forceinline__ int64_t ac_total(const AcParams &P, int64_t *red) {
     for (int i = 0; i < THREADS / 32; ++i) n += red[i];
     return n * P.c.n_kv * P.tiles;
 }
-// The share that worker w of n begins with.  (n is at most a few thousand, the line below 2^50.)
-__device__ __forceinline__ int64_t ac_share(int64_t total, int w, int n) { return total / n * w + total % n * w / n; }
+// The line of units cut into n shares (n is at most a few hundred): where share w begins.
+struct AcShares {
+    int64_t each;
+    int rest, n;
+    __device__ __forceinline__ AcShares(int64_t total, int n_) : each(total / n_), rest((int)(total - each * n_)), n(n_) {}
+    __device__ __forceinline__ int64_t operator()(int w) const { return each * w + rest * w / n; }
+};
+// The blocks that share the line: each warp has kAcLeast units at least, if there are so many.
+__device__ __forceinline__ int ac_blocks(const AcParams &P, int64_t total, int warps) {
+    const int64_t n = total / (kAcLeast * warps);
+    return n < 1 ? 1 : n < P.blocks ? (int)n : P.blocks;
+}
 
 // The warp finds the item that unit u lies in, and its place in it.
 __device__ __forceinline__ AcItem ac_find(const AcParams &P, int64_t u, int &at) {
@@ -145,8 +161,13 @@ __device__ __forceinline__ void ac_store(void *p, kq_dtype t, int64_t i, float v
     else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
 }
 
+__device__ __forceinline__ float ac_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ void ac_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -181,6 +202,44 @@ __device__ __forceinline__ int ac_element(int j, int n) {
     return DP == 64 ? n * 8 + j : (j / 16) * 128 + n * 16 + j % 16;
 }
 
+__device__ __forceinline__ void ac_copy(uint8_t *dst, const CUtensorMap *tm, uint64_t *bar, int d, int row, int page) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            sm100::smem_u32(dst)),
+        "l"(tm), "r"(sm100::smem_u32(bar)), "r"(d), "r"(row), "r"(page)
+        : "memory");
+}
+
+// A unit in a warp's ring: 32 rows of keys, then of values, in boxes of W bytes of a row as the copies write them
+// (16-byte pieces swizzled: by row % 8 in rows of 128 bytes, by row / 2 % 4 in rows of 64).
+template <int DP>
+struct AcRing {
+    static constexpr int W = DP < 128 ? DP : 128, BOXES = DP / W, BOX = kAcUnit * W, BYTES = 2 * BOXES * BOX;
+    static constexpr int KP = DP / 64;               // 16-byte pieces of a key that a lane takes
+    static constexpr int VWORDS = DP == 64 ? 2 : 4;  // 4-byte words of a value that a lane takes at once
+    // Piece i of a lane's key (of eight-token tile t) begins at this element of the head.
+    static __device__ __forceinline__ int key_element(int i) {
+        const int c = threadIdx.x & 3;
+        return DP == 64 ? c * 16 : (i >> 1) * 128 + (2 * c + (i & 1)) * 16;
+    }
+    // (volatile: the loads stay where they are written, well ahead of their use)
+    static __device__ __forceinline__ void get_key(uint32_t stage, int t, int i, uint32_t (&v)[4]) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+        const uint32_t at = stage + (i >> 1) * BOX + (t * 8 + g) * W + ((DP == 64 ? c ^ (g >> 1) : (2 * c + (i & 1)) ^ g) << 4);
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at));
+    }
+    // Words 4i on of a lane's value of token 16h + 2c + (t & 1) + 8 (t >> 1).
+    static __device__ __forceinline__ void get_value(uint32_t stage, int h, int t, int i, uint32_t (&v)[VWORDS]) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, low = 2 * c + (t & 1), row = 16 * h + low + 8 * (t >> 1);
+        const uint32_t at = stage + (BOXES + i) * BOX + row * W;
+        if constexpr (DP == 64)
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at + (((g >> 1) ^ c) << 4) + (g & 1) * 8));
+        else
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(at + ((g ^ low) << 4)));
+    }
+};
+
 // A warp's state for one item: DP is D rounded up to 64, 128 or 256; MT is 8 rows (parts of the split in the other
 // eight) or 16.
 template <int DP, int MT>
@@ -193,11 +252,11 @@ struct AcWarp {
     float o[NT][4];
     static constexpr int R = MT / 8;     // rows of a lane: g and, with 16, g + 8
     float m[R], l[R], factor[R];
-    int limit[R];                        // tokens that a row sees
-    float vref;                          // a power of two above the value scales so far
+    int limit[R], sure;                  // tokens that a row sees, and that all rows see
+    float vref, lift;                    // a power of two above the value scales so far; kAcLift over it
 
     __device__ __forceinline__ void begin(const AcParams &P, const AcItem &it) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+        const int g = (threadIdx.x & 31) >> 2;
         const int64_t len = ac_len(P, it.b);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -210,7 +269,7 @@ struct AcWarp {
             float v[KS][4], amax = 0.0f;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const int d = (s / 4) * 64 + c * 16 + (s % 4) * 4;
+                const int d = AcRing<DP>::key_element(s / 4) + (s % 4) * 4;
                 v[s][0] = v[s][1] = v[s][2] = v[s][3] = 0.0f;
                 if (live && d < P.c.D) ac_load4(P.q, P.xt, at + d, P.qvec, v[s]);
 #pragma unroll
@@ -233,52 +292,31 @@ struct AcWarp {
             l[r] = 0.0f;
         }
         vref = 0.0f;
+        lift = 0.0f;
+        sure = (int)max(len - P.n_new + 1, (int64_t)0);  // (rows past the tile's end are not kept)
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     }
 
-    __device__ __forceinline__ void load(const int8_t *kb, const int8_t *vb, int D, uint4 (&k)[2][KP], uint32_t (&v)[4][VW]) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < KP; ++i) {
-                const int d = i * 64 + c * 16;
-                k[t][i] = make_uint4(0, 0, 0, 0);
-                if (d < D) k[t][i] = __ldg(reinterpret_cast<const uint4 *>(kb + (t * 8 + g) * D + d));
-            }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int8_t *p = vb + (2 * c + (t & 1) + (t >> 1) * 8) * D;
-            if constexpr (DP == 64) {
-                uint2 u = make_uint2(0, 0);
-                if (g * 8 < D) u = __ldg(reinterpret_cast<const uint2 *>(p + g * 8));
-                v[t][0] = u.x; v[t][1] = u.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < VW / 4; ++i) {
-                    const int d = i * 128 + g * 16;
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (d < D) u = __ldg(reinterpret_cast<const uint4 *>(p + d));
-                    v[t][4 * i] = u.x; v[t][4 * i + 1] = u.y; v[t][4 * i + 2] = u.z; v[t][4 * i + 3] = u.w;
-                }
-            }
-        }
-    }
-
-    // A unit: tokens t0 .. t0 + 15, of which a row sees those below its limit.
-    __device__ __forceinline__ void unit(const uint4 (&k)[2][KP], const uint32_t (&v)[4][VW], float ks, float vs, int t0) {
+    // A unit: tokens t0 .. t0 + 31, of which a row sees those below its limit.
+    // scales: of keys and values, of its first and second half.
+    __device__ __forceinline__ void unit(uint32_t stage, float4 scales, int t0) {
+        using Ring = AcRing<DP>;
         const int c = threadIdx.x & 3;
-        float s[2][4] = {};
+        uint32_t k[KP][4][4];
 #pragma unroll
         for (int i = 0; i < KP; ++i)
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
+            for (int t = 0; t < 4; ++t) Ring::get_key(stage, t, i, k[i][t]);
+        float s[4][4] = {};
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+        for (int i = 0; i < KP; ++i)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
                     uint32_t b0, b1;
-                    const uint4 q = k[t][i];
-                    i8x4_to_f16(w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w, b0, b1);
+                    i8x4_to_f16(k[i][t][w], b0, b1);
                     const int st = i * 4 + w;
                     if constexpr (MT == 8) {
                         ac_mma(s[t], qh[st][0], ql[st][0], qh[st][1], ql[st][1], b0, b1);
@@ -287,38 +325,59 @@ struct AcWarp {
                         ac_mma(s[t], ql[st][0], ql[st][2], ql[st][1], ql[st][3], b0, b1);
                     }
                 }
-        // x[r][0..3]: a row's logits for tokens 2c, 2c + 1, 2c + 8, 2c + 9
-        float x[R][4];
+            }
+        uint32_t v[VW / Ring::VWORDS][2][4][Ring::VWORDS];
+        auto values = [&](int i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) Ring::get_value(stage, h, t, i, v[i][h][t]);
+        };
+        values(0);
+        // x[r][2t + e]: a row's logits for tokens 8t + 2c + e, in units of log 2
+        float x[R][8], top[R];
         bool grows = false;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r) {
+            const float f[2] = {factor[r] * scales.x, factor[r] * scales.z};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float raw = MT == 8 ? s[i >> 1][i & 1] + s[i >> 1][2 + (i & 1)] : s[i >> 1][2 * r + (i & 1)];
-                const int token = t0 + 2 * c + (i & 1) + (i >> 1) * 8;
-                x[r][i] = token < limit[r] ? raw * (factor[r] * ks) : -INFINITY;
-                grows |= x[r][i] > m[r] + kAcSlack;
+            for (int i = 0; i < 8; ++i) {
+                const int t = i >> 1, e = i & 1;
+                x[r][i] = (MT == 8 ? s[t][e] + s[t][2 + e] : s[t][2 * r + e]) * f[t >> 1];
             }
-        const bool wider = vs > vref && vs < INFINITY;
-        if (__any_sync(~0u, grows || wider)) {
+        }
+        if (t0 + kAcUnit > sure) {  // not every row sees all of the unit
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (t0 + (i >> 1) * 8 + 2 * c + (i & 1) >= limit[r]) x[r][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            top[r] = fmaxf(fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3])), fmaxf(fmaxf(x[r][4], x[r][5]), fmaxf(x[r][6], x[r][7])));
+            grows |= top[r] > m[r] + kAcSlack;
+        }
+        const float vtop = fmaxf(scales.y < INFINITY ? scales.y : 0.0f, scales.w < INFINITY ? scales.w : 0.0f);
+        if (__any_sync(~0u, grows || vtop > vref)) {
             // bring the sums to a new maximum and a new reference of the value scales
             float ref = vref;
-            if (wider) {
-                const uint32_t e = __float_as_uint(vs) & 0x7f800000u;
-                ref = e < 0x00800000u ? 2.3509887e-38f : e >= 0x7f000000u ? vs : __uint_as_float(e + 0x00800000u);
+            if (vtop > vref) {
+                const uint32_t e = __float_as_uint(vtop) & 0x7f800000u;
+                ref = e < 0x00800000u ? 2.3509887e-38f : e >= 0x7f000000u ? vtop : __uint_as_float(e + 0x00800000u);
             }
             const float fv = vref > 0.0f ? vref / ref : 0.0f;
             vref = ref;
+            lift = ref > 0.0f ? kAcLift / ref : 0.0f;
             float f[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float top = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                top = fmaxf(top, m[r]);
-                f[r] = exp2f(m[r] - top);
+                float mx = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+                mx = fmaxf(mx, m[r]);
+                f[r] = ac_exp2(m[r] - mx);
                 l[r] *= f[r];
-                m[r] = top;
+                m[r] = mx;
                 f[r] *= fv;
             }
 #pragma unroll
@@ -329,36 +388,54 @@ struct AcWarp {
                 o[j][3] *= f[R - 1];
             }
         }
-        float lift = vref > 0.0f ? vs / vref * kAcLift : 0.0f * vs;
-        const bool poison = !(lift <= kAcLift);  // a block with an infinity: NaN for the rows that see it, for them alone
-        if (poison) lift = 0.0f;
-        uint32_t ph[R][2], pl[R][2];
+        float by[2] = {scales.y * lift, scales.w * lift};
+        const bool poison = !(by[0] <= kAcLift && by[1] <= kAcLift);
+        if (poison) poisoned(x, by);
+        uint32_t ph[R][4], pl[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float p[4];
+            float p[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[i] = exp2f(x[r][i] - m[r]);
-                l[r] += poison && x[r][i] > -INFINITY ? NAN : p[i];
-            }
-            ac_split(p[0] * lift, p[1] * lift, ph[r][0], pl[r][0]);
-            ac_split(p[2] * lift, p[3] * lift, ph[r][1], pl[r][1]);
+            for (int i = 0; i < 8; ++i) p[i] = ac_exp2(x[r][i] - m[r]);
+            l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) ac_split(p[2 * t] * by[t >> 1], p[2 * t + 1] * by[t >> 1], ph[r][t], pl[r][t]);
         }
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-            uint32_t a[4], b[4];
-            ac_pair(v[0][w], v[1][w], a);
-            ac_pair(v[2][w], v[3][w], b);
+        for (int n = 0; n < VW / Ring::VWORDS; ++n) {
+            if (n) values(n);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (MT == 8) {
-                    ac_mma(o[4 * w + i], ph[0][0], pl[0][0], ph[0][1], pl[0][1], a[i], b[i]);
-                } else {
-                    ac_mma(o[4 * w + i], ph[0][0], ph[1][0], ph[0][1], ph[1][1], a[i], b[i]);
-                    ac_mma(o[4 * w + i], pl[0][0], pl[1][0], pl[0][1], pl[1][1], a[i], b[i]);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int w = 0; w < Ring::VWORDS; ++w) {
+                    uint32_t a[4], b[4];
+                    ac_pair(v[n][h][0][w], v[n][h][1][w], a);
+                    ac_pair(v[n][h][2][w], v[n][h][3][w], b);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float (&acc)[4] = o[4 * (n * Ring::VWORDS + w) + i];
+                        if constexpr (MT == 8) {
+                            ac_mma(acc, ph[0][2 * h], pl[0][2 * h], ph[0][2 * h + 1], pl[0][2 * h + 1], a[i], b[i]);
+                        } else {
+                            ac_mma(acc, ph[0][2 * h], ph[1][2 * h], ph[0][2 * h + 1], ph[1][2 * h + 1], a[i], b[i]);
+                            ac_mma(acc, pl[0][2 * h], pl[1][2 * h], pl[0][2 * h + 1], pl[1][2 * h + 1], a[i], b[i]);
+                        }
+                    }
                 }
-            }
         }
+    }
+    // A block of values with an infinity: NaN for the rows that see it, for them alone.
+    __device__ __forceinline__ void poisoned(const float (&x)[R][8], float (&by)[2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (!(by[h] <= kAcLift)) {
+                by[h] = 0.0f;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (x[r][4 * h + i] > -INFINITY) l[r] = NAN;
+            }
     }
 
     // The item's sums so far: m, l, and D values a row that stand relative to 2^m.
@@ -379,45 +456,168 @@ struct AcWarp {
             for (int i = 0; i < 4; ++i) o[j][i] = o[j][i] * back;
         }
     }
+    // What a lane holds of a row lies in runs: f(r, d0, run) for the RUN elements from d0 on of its row r.
+    static constexpr int RUN = DP == 64 ? 8 : 16;
+    template <typename F>
+    __device__ __forceinline__ void runs(int D, F f) {
+        const int c = threadIdx.x & 3;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < NT; j += RUN)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int d0 = ac_element<DP>(j, 2 * c + e);
+                    float v[RUN];
+#pragma unroll
+                    for (int i = 0; i < RUN; ++i) v[i] = o[j + i][2 * r + e];
+                    if (d0 < D) f(r, d0, v);
+                }
+    }
     __device__ __forceinline__ void put(float *part, int D) {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int row = g + 8 * r;
-            if (c == 0) part[row] = m[r], part[MT + row] = l[r];
-            float *dst = part + 2 * MT + row * D;
+        for (int r = 0; r < R; ++r)
+            if (c == 0) part[g + 8 * r] = m[r], part[MT + g + 8 * r] = l[r];
+        runs(D, [&](int r, int d0, const float (&v)[RUN]) {
+            float4 *dst = reinterpret_cast<float4 *>(part + 2 * MT + (g + 8 * r) * D + d0);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int d = ac_element<DP>(j, 2 * c + e);
-                    if (d < D) dst[d] = o[j][2 * r + e];
-                }
-        }
+            for (int i = 0; i < RUN; i += 4) dst[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        });
     }
 };
 
-// Row `row` (of the item's tile) of the output, element d; a token that sees nothing gives 0.
-__device__ __forceinline__ void ac_write(const AcParams &P, const AcItem &it, int MT, int row, int d, float o, float l) {
+// A run of row `row` (of the item's tile) of the output; a token that sees nothing gives 0.
+template <int N>
+__device__ __forceinline__ void ac_write_run(const AcParams &P, const AcItem &it, int MT, int row, int d0, const float (&v)[N], float l) {
     const int i = it.tile * MT + row;
     if (i >= P.rows) return;
     const int token = i / P.G, head = it.h * P.G + i - token * P.G;
     const bool sees = ac_len(P, it.b) - P.n_new + token >= 0;
-    ac_store(P.y, P.yt, (it.b * P.n_new + token) * P.ldy + (int64_t)head * P.c.D + d, sees ? o / l : 0.0f);
+    const int64_t at = (it.b * P.n_new + token) * P.ldy + (int64_t)head * P.c.D + d0;
+    float x[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = sees ? v[j] / l : 0.0f;
+    if (!P.yvec) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) ac_store(P.y, P.yt, at + j, x[j]);
+    } else if (P.yt == KQ_F32) {
+        float4 *y = reinterpret_cast<float4 *>(static_cast<float *>(P.y) + at);
+#pragma unroll
+        for (int j = 0; j < N; j += 4) y[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    } else {
+        uint2 *y = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.y) + at);
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            const __half2 h = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+            w[k] = P.yt == KQ_F16 ? *reinterpret_cast<const uint32_t *>(&h) : *reinterpret_cast<const uint32_t *>(&b);
+        }
+        if constexpr (N % 8 == 0) {
+#pragma unroll
+            for (int k = 0; k < N / 2; k += 4) reinterpret_cast<uint4 *>(y)[k / 4] = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+        } else {
+            y[0] = make_uint2(w[0], w[1]);
+        }
+    }
+}
+__device__ __forceinline__ void ac_write4(const AcParams &P, const AcItem &it, int MT, int row, int d0, float4 v, float l) {
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    ac_write_run(P, it, MT, row, d0, x, l);
 }
 
-template <int DP, int MT, int NW>
-__global__ void __launch_bounds__(NW * 32, 1) ac_kernel(AcParams P) {
-    extern __shared__ float parts[];  // [NW][2] parts of items that warps share
+// The units of a warp's share, fetched ahead of their use.
+template <int DP>
+struct AcFetch {
+    AcItem it;
+    int at, pages, base;  // next unit of the item; the sequence's pages; lanes hold what follows of the 32 pages from base on
+    int64_t left;         // units to fetch
+    int page;
+    float ks, vs;
+    __device__ __forceinline__ void start(const AcParams &P) {
+        pages = (int)((ac_len(P, it.b) + (1 << P.c.lp) - 1) >> P.c.lp);
+        base = -64;
+    }
+    __device__ __forceinline__ void next(const AcParams &P, const CUtensorMap *tmK, const CUtensorMap *tmV, uint8_t *stage, float4 *scales,
+                                         uint64_t *bar) {
+        using Ring = AcRing<DP>;
+        if (left <= 0) return;
+        const int lane = threadIdx.x & 31;
+        if (at == it.units) {
+            ac_next(P, it);
+            at = 0;
+            start(P);
+        }
+        const int halves = P.c.lp == 4 ? 2 : 1;  // a page of 16 holds half a unit
+        float k[2], v[2];
+        int first[2];
+        for (int h = 0; h < halves; ++h) {
+            const int pi = (at * kAcUnit + h * 16) >> P.c.lp;
+            if (pi >= base + 32 || base < 0) {
+                base = pi;
+                const bool in = base + lane < pages;
+                page = in ? P.c.table[it.b * P.c.ldt + base + lane] : -1;
+                const bool ok = page >= 0 && page < P.c.n_pages && !ac_bad(P, it.b);
+                if (!ok) page = in ? 0 : -1;
+                const int64_t block = (int64_t)page * P.c.n_kv + it.h;
+                // (a unit's second half may lie past the last page: weight 0, whatever is there)
+                ks = !in ? 0.0f : ok ? P.c.k_scale[block] : NAN;
+                vs = in && ok ? P.c.v_scale[block] : 0.0f;
+            }
+            first[h] = __shfl_sync(~0u, page, pi - base);
+            k[h] = __shfl_sync(~0u, ks, pi - base);
+            v[h] = __shfl_sync(~0u, vs, pi - base);
+        }
+        if (lane == 0) {
+            const int row = (it.h << P.c.lp) + (at * kAcUnit & ((1 << P.c.lp) - 1)), parts = halves == 1 ? 1 : first[1] < 0 ? 1 : 2;
+            *scales = make_float4(k[0], v[0], halves == 1 ? k[0] : k[1], halves == 1 ? v[0] : v[1]);
+            sm100::mbar_arrive_expect_tx(bar, halves == parts ? Ring::BYTES : Ring::BYTES / 2);
+            for (int h = 0; h < parts; ++h)
+#pragma unroll
+                for (int i = 0; i < Ring::BOXES; ++i) {
+                    ac_copy(stage + i * Ring::BOX + h * 16 * Ring::W, tmK, bar, i * 128, row, first[h]);
+                    ac_copy(stage + (Ring::BOXES + i) * Ring::BOX + h * 16 * Ring::W, tmV, bar, i * 128, row, first[h]);
+                }
+        }
+        ++at;
+        --left;
+    }
+};
+
+template <int DP, int MT, int NW, int NS>
+__global__ void __launch_bounds__(NW * 32, 1)
+    ac_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, AcParams P) {
+    using Ring = AcRing<DP>;
+    extern __shared__ __align__(1024) uint8_t rings[];
+    // the warps' rings, then a part each.  A warp shares at most its first and its last item with others: what it has of
+    // the first goes to that part, what it has of the last into its ring, which is idle by then.
     __shared__ int64_t red[NW];
     __shared__ int64_t owner[NW][2];  // the item (its first unit on the line) of each, or -1
     __shared__ AcItem items[NW][2];
+    __shared__ float4 scales[NW][NS];
+    __shared__ uint64_t full[NW][NS];
+    __shared__ float weight[2 * NW][MT], sum[MT];
+    __shared__ int aborted;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = P.c.D, size = ac_part_floats<MT>(D);
+    uint8_t *ring = rings + warp * NS * Ring::BYTES;
+    auto part = [&](int s) {
+        return reinterpret_cast<float *>(rings + (s & 1 ? (s >> 1) * NS * Ring::BYTES : NW * NS * Ring::BYTES + (s >> 1) * size * 4));
+    };
+    static_assert(ac_part_floats<MT>(DP) * 4 <= NS * Ring::BYTES, "a part fits a ring");
+    if (lane < NS) sm100::mbar_init(&full[warp][lane], 1);
+    if (lane < 2) owner[warp][lane] = -1;
+    if (tid == 0) {
+        aborted = 0;
+        sm100::fence_mbar_init();
+        sm100::prefetch_tmap(&tmK);
+        sm100::prefetch_tmap(&tmV);
+    }
+    sm100::fence_proxy_async_smem();  // (each warp's barriers are its own: ready for its copies)
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = P.c.D;
-    const int size = ac_part_floats<MT>(D);
+    if (blockIdx.x == 0 && tid == 0) *P.err = 0ull;  // (an error is counted two seconds later at the earliest)
     const int64_t total = ac_total<NW * 32>(P, red);
-    if (lane < 2) owner[warp][lane] = -1;
     // rows of sequences without tokens
     for (int64_t b = blockIdx.x; b < P.c.B; b += gridDim.x)
         if (P.c.lens[b] <= 0)
@@ -425,47 +625,45 @@ __global__ void __launch_bounds__(NW * 32, 1) ac_kernel(AcParams P) {
                 const int t = i / (P.n_q * D);
                 ac_store(P.y, P.yt, (b * P.n_new + t) * P.ldy + i - t * (P.n_q * D), 0.0f);
             }
-    const int64_t first = ac_share(total, blockIdx.x, P.blocks), last = ac_share(total, blockIdx.x + 1, P.blocks);
+    const int blocks = ac_blocks(P, total, NW);
+    if ((int)blockIdx.x >= blocks) return;
+    const AcShares shares(total, blocks);
+    const int64_t first = shares(blockIdx.x), last = shares(blockIdx.x + 1);
     if (first >= last) return;
-    const int64_t u0 = first + ac_share(last - first, warp, NW), u1 = first + ac_share(last - first, warp + 1, NW);
+    const AcShares mine(last - first, NW);
+    const int64_t u0 = first + mine(warp), u1 = first + mine(warp + 1);
     if (u0 < u1) {
-        int at;
-        AcItem it = ac_find(P, u0, at);
+        AcFetch<DP> ahead;
+        ahead.it = ac_find(P, u0, ahead.at);
+        ahead.left = u1 - u0;
+        AcItem it = ahead.it;
+        int at = ahead.at;
+        ahead.start(P);
+        for (int i = 0; i < NS - 1; ++i) ahead.next(P, &tmK, &tmV, ring + i * Ring::BYTES, &scales[warp][i], &full[warp][i]);
         AcWarp<DP, MT> w;
-        uint4 k[2][AcWarp<DP, MT>::KP];
-        uint32_t v[4][AcWarp<DP, MT>::VW];
+        int stage = 0;
+        uint32_t phase = 0;
         for (int64_t u = u0; u < u1;) {
             const int n = (int)min((int64_t)(it.units - at), u1 - u);
             const int64_t start = u - at;  // the item's first unit on the line
             w.begin(P, it);
-            const bool bad = ac_bad(P, it.b);
-            const int32_t *table = P.c.table + it.b * P.c.ldt;
             for (int i = 0; i < n; ++i) {
-                const int t0 = (at + i) * kAcUnit;
-                int64_t page = table[t0 >> P.c.lp];
-                const bool ok = page >= 0 && page < P.c.n_pages && !bad;
-                if (!ok) page = 0;
-                const int64_t block = page * P.c.n_kv + it.h;
-                const int64_t off = ((block << P.c.lp) + (t0 & ((1 << P.c.lp) - 1))) * D;
-                w.load(P.c.k + off, P.c.v + off, D, k, v);
-                const float ks = ok ? P.c.k_scale[block] : NAN, vs = P.c.v_scale[block];
-                w.unit(k, v, ks, vs, t0);
+                // the stage before this one is free: every lane is through with it
+                __syncwarp();
+                const int free = stage == 0 ? NS - 1 : stage - 1;
+                ahead.next(P, &tmK, &tmV, ring + free * Ring::BYTES, &scales[warp][free], &full[warp][free]);
+                // (a wait that runs out spoils the result, which the device flag tells)
+                if (!sm100::mbar_wait(&full[warp][stage], phase, &aborted)) aborted = 1;
+                w.unit(sm100::smem_u32(ring + stage * Ring::BYTES), scales[warp][stage], (at + i) * kAcUnit);
+                if (++stage == NS) stage = 0, phase ^= 1;
             }
             w.end();
             if (at == 0 && n == it.units) {
-                const int g = lane >> 2, c = lane & 3;
-#pragma unroll
-                for (int r = 0; r < MT / 8; ++r)
-#pragma unroll
-                    for (int j = 0; j < DP / 8; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int d = ac_element<DP>(j, 2 * c + e);
-                            if (d < D) ac_write(P, it, MT, g + 8 * r, d, w.o[j][2 * r + e], w.l[r]);
-                        }
+                w.runs(D, [&](int r, int d0, const auto &v) { ac_write_run(P, it, MT, (lane >> 2) + 8 * r, d0, v, w.l[r]); });
             } else {
                 const int slot = u == u0 ? 0 : 1;
-                w.put(parts + (warp * 2 + slot) * size, D);
+                __syncwarp();
+                w.put(part(warp * 2 + slot), D);
                 if (lane == 0) owner[warp][slot] = start, items[warp][slot] = it;
             }
             u += n;
@@ -474,6 +672,12 @@ __global__ void __launch_bounds__(NW * 32, 1) ac_kernel(AcParams P) {
         }
     }
     __syncthreads();
+    if (aborted) {
+        // copies may be under way still: far more time than they need
+        const uint64_t t0 = sm100::globaltimer_ns();
+        while (sm100::globaltimer_ns() - t0 < 10000000ull) {}
+        if (tid == 0) atomicAdd(P.err, 1ull);
+    }
     // items that several warps share, in the order of the line
     for (int i = 0; i < 2 * NW;) {
         const int64_t start = owner[i >> 1][i & 1];
@@ -483,22 +687,37 @@ __global__ void __launch_bounds__(NW * 32, 1) ac_kernel(AcParams P) {
         const AcItem it = items[i >> 1][i & 1];
         const bool whole = start >= first && start + it.units <= last;
         float *out = P.parts + ((int64_t)blockIdx.x * 2 + (start < first ? 0 : 1)) * size;
-        for (int e = tid; e < MT * D; e += NW * 32) {
-            const int row = e / D, d = e - row * D;
-            float m = kAcNone, l = 0.0f, o = 0.0f;
+        __syncthreads();
+        if (tid < MT) {
+            float m = kAcNone, l = 0.0f;
             for (int s = i; s < j; ++s)
-                if (owner[s >> 1][s & 1] >= 0) m = fmaxf(m, parts[s * size + row]);
+                if (owner[s >> 1][s & 1] >= 0) m = fmaxf(m, part(s)[tid]);
+            for (int s = i; s < j; ++s) {
+                const bool has = owner[s >> 1][s & 1] >= 0;
+                const float f = has ? ac_exp2(part(s)[tid] - m) : 0.0f;
+                weight[s][tid] = f;
+                if (has) l += part(s)[MT + tid] * f;
+            }
+            sum[tid] = l;
+            if (!whole) out[tid] = m, out[MT + tid] = l;
+        }
+        __syncthreads();
+        for (int e = tid * 4; e < MT * D; e += NW * 32 * 4) {
+            const int row = e / D, d = e - row * D;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int s = i; s < j; ++s)
                 if (owner[s >> 1][s & 1] >= 0) {
-                    const float f = exp2f(parts[s * size + row] - m);
-                    l += parts[s * size + MT + row] * f;
-                    o += parts[s * size + 2 * MT + e] * f;
+                    const float4 v = *reinterpret_cast<const float4 *>(part(s) + 2 * MT + e);
+                    const float f = weight[s][row];
+                    o.x += v.x * f;
+                    o.y += v.y * f;
+                    o.z += v.z * f;
+                    o.w += v.w * f;
                 }
             if (whole) {
-                ac_write(P, it, MT, row, d, o, l);
+                ac_write4(P, it, MT, row, d, o, sum[row]);
             } else {
-                out[2 * MT + e] = o;
-                if (d == 0) out[row] = m, out[MT + row] = l;
+                *reinterpret_cast<float4 *>(out + 2 * MT + e) = o;
             }
         }
         i = j;
@@ -506,57 +725,115 @@ __global__ void __launch_bounds__(NW * 32, 1) ac_kernel(AcParams P) {
 }
 
 // Items that thread blocks share.  Block c takes the item that the c-th border between shares cuts, if no earlier
-// border does: its parts are those of the shares that it reaches into, in their order.
+// border does: its parts are those of the shares that it reaches into, in their order.  Which those are follows from
+// the lengths alone, which were there before the first kernel: it is found out while that one still runs.
 template <int MT>
 __global__ void __launch_bounds__(256) ac_join_kernel(AcParams P) {
     __shared__ int64_t red[8];
-    sm100::grid_dependency_wait();
-    sm100::grid_launch_dependents();
+    __shared__ float weight[kAcMaxBlocks][MT], ls[kAcMaxBlocks][MT], sum[MT];
     const int c = blockIdx.x + 1, D = P.c.D;
     const int size = ac_part_floats<MT>(D);
     const int64_t total = ac_total<256>(P, red);
-    const int64_t border = ac_share(total, c, P.blocks), before = ac_share(total, c - 1, P.blocks);
-    if (border >= total || border == 0 || before == border) return;
-    int at;
-    const AcItem it = ac_find(P, border, at);
-    const int64_t start = border - at, end = start + it.units;
-    if (at == 0 || before > start) return;  // the border cuts nothing, or an earlier one cuts the item
-    // the shares up to the one that the item ends in (empty shares, between equal borders, have no part)
-    int last = c;
-    while (last + 1 < P.blocks && ac_share(total, last + 1, P.blocks) < end) ++last;
-    for (int e = threadIdx.x; e < MT * D; e += 256) {
+    const int blocks = ac_blocks(P, total, P.warps);
+    bool cut = c < blocks;
+    const AcShares shares(total, blocks);
+    const int64_t border = cut ? shares(c) : 0, before = cut ? shares(c - 1) : 0;
+    cut = cut && border < total && border > before;
+    AcItem it;
+    int parts = 0;
+    if (cut) {
+        int at;
+        it = ac_find(P, border, at);
+        const int64_t start = border - at, end = start + it.units;
+        cut = at > 0 && before <= start;  // (else the border cuts nothing, or an earlier one cuts the item)
+        // the shares up to the one that the item ends in; with kAcLeast units a warp none of them is empty
+        for (parts = 2; c - 1 + parts < blocks && shares(c - 1 + parts) < end;) ++parts;
+    }
+    sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
+    if (!cut) return;
+    auto part = [&](int s) { return P.parts + ((int64_t)(c - 1 + s) * 2 + (s == 0 ? 1 : 0)) * size; };
+    const int row0 = threadIdx.x % MT, s0 = threadIdx.x / MT;
+    for (int s = s0; s < parts; s += 256 / MT) {
+        weight[s][row0] = part(s)[row0];
+        ls[s][row0] = part(s)[MT + row0];
+    }
+    __syncthreads();
+    if (threadIdx.x < MT) {
+        float m = kAcNone, l = 0.0f;
+        for (int s = 0; s < parts; ++s) m = fmaxf(m, weight[s][row0]);
+        for (int s = 0; s < parts; ++s) {
+            const float f = ac_exp2(weight[s][row0] - m);
+            l += ls[s][row0] * f;
+            weight[s][row0] = f;
+        }
+        sum[row0] = l;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x * 4; e < MT * D; e += 256 * 4) {
         const int row = e / D, d = e - row * D;
-        float m = kAcNone, l = 0.0f, o = 0.0f;
-        auto part = [&](int s) { return P.parts + ((int64_t)s * 2 + (s == c - 1 ? 1 : 0)) * size; };
-        for (int s = c - 1; s <= last; ++s)
-            if (ac_share(total, s, P.blocks) < ac_share(total, s + 1, P.blocks)) m = fmaxf(m, part(s)[row]);
-        for (int s = c - 1; s <= last; ++s)
-            if (ac_share(total, s, P.blocks) < ac_share(total, s + 1, P.blocks)) {
-                const float f = exp2f(part(s)[row] - m);
-                l += part(s)[MT + row] * f;
-                o += part(s)[2 * MT + e] * f;
-            }
-        ac_write(P, it, MT, row, d, o, l);
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int s = 0; s < parts; ++s) {
+            const float4 v = *reinterpret_cast<const float4 *>(part(s) + 2 * MT + e);
+            const float f = weight[s][row];
+            o.x += v.x * f;
+            o.y += v.y * f;
+            o.z += v.z * f;
+            o.w += v.w * f;
+        }
+        ac_write4(P, it, MT, row, d, o, sum[row]);
     }
 }
 
 // ---------------------------------------------------------------- host
-constexpr int kAcMaxBlocks = 152;
 static int ac_row_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
 static size_t ac_workspace(int64_t rows, int64_t D) {
     const int mt = ac_row_tile(rows);
-    return (size_t)kAcMaxBlocks * 2 * mt * (D + 2) * 4;
+    return 256 + (size_t)kAcMaxBlocks * 2 * mt * (D + 2) * 4;
+}
+
+static PFN_cuTensorMapEncodeTiled_v12000 ac_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *p = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
 }
 
 template <int DP, int MT>
-static kq_status launch_ac(const char *fn, const AcParams &P, cudaStream_t st) {
-    constexpr int NW = DP * MT >= 4096 ? 4 : 8;  // a part is up to 16 KB, two a warp
-    const int smem = NW * 2 * ac_part_floats<MT>(P.c.D) * 4;
-    auto kern = ac_kernel<DP, MT, NW>;
+static kq_status launch_ac(const char *fn, AcParams P, cudaStream_t st) {
+    // 8 KB a unit of 128 elements, up to 16 KB a part
+    constexpr int NW = DP == 256 ? 4 : 8, NS = DP == 64 ? 4 : DP == 128 && MT == 8 ? 3 : 2;
+    using Ring = AcRing<DP>;
+    const int smem = NW * (NS * Ring::BYTES + ac_part_floats<MT>(P.c.D) * 4);
+    static_assert(NW * (NS * Ring::BYTES + ac_part_floats<MT>(DP) * 4) <= 224 * 1024 + 512, "shared memory");
+    auto encode = ac_encoder();
+    if (!encode) return fail(KQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", fn);
+    CUtensorMap tm[2];
+    for (int i = 0; i < 2; ++i) {
+        // a page's heads and tokens are the rows of one plane
+        const int64_t D = P.c.D, rows = (int64_t)P.c.n_kv << P.c.lp;
+        const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)P.c.n_pages};
+        const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)(D * rows)};
+        const cuuint32_t box[3] = {Ring::W, (cuuint32_t)(P.c.lp == 4 ? 16 : kAcUnit), 1}, es[3] = {1, 1, 1};
+        const CUresult e = encode(&tm[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, i ? P.c.v : P.c.k, dims, strides, box, es,
+                                  CU_TENSOR_MAP_INTERLEAVE_NONE, DP == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (e != CUDA_SUCCESS) return fail(KQ_ERR_CUDA, "%s: tensor map of the cache failed (%d)", fn, (int)e);
+    }
+    auto kern = ac_kernel<DP, MT, NW, NS>;
+    P.warps = NW;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = launch_beside(kern, dim3(P.blocks), dim3(NW * 32), smem, dim3(1), st, P);
+    if (e == cudaSuccess) e = launch_beside(kern, dim3(P.blocks), dim3(NW * 32), smem, dim3(1), st, tm[0], tm[1], P);
     if (e == cudaSuccess) count_launch(R_ATTN);
-    if (e == cudaSuccess && P.blocks > 1) {
+    if (e == cudaSuccess) {
         e = launch_beside(ac_join_kernel<MT>, dim3(P.blocks - 1), dim3(256), 0, dim3(1), st, P);
         if (e == cudaSuccess) count_launch(R_ATTN);
     }
@@ -604,12 +881,14 @@ kq_status kq_attn_cache_i8(kq_dtype xt, const void *q, int64_t ldq, int64_t B, i
     if (!aligned(workspace, 256)) return fail(KQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", fn);
     P.q = q; P.y = y; P.ldq = ldq; P.ldy = ldy; P.xt = xt; P.yt = yt;
     P.qvec = aligned(q, 4 * value_bytes(xt)) && ldq % 4 == 0;
+    P.yvec = aligned(y, 16) && ldy * (int64_t)value_bytes(yt) % 16 == 0;
     P.n_new = (int)n_new; P.n_q = (int)n_q; P.G = (int)(n_q / n_kv);
     P.rows = P.n_new * P.G;
     const int mt = ac_row_tile(P.rows);
     P.tiles = (P.rows + mt - 1) / mt;
     P.scale = scale * 1.44269504f;
-    P.parts = static_cast<float *>(workspace);
+    P.err = static_cast<unsigned long long *>(workspace);
+    P.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + 256);
     P.blocks = kAcMaxBlocks;
     const cudaStream_t st = (cudaStream_t)stream;
     if (mt == 8) return D <= 64 ? launch_ac<64, 8>(fn, P, st) : D <= 128 ? launch_ac<128, 8>(fn, P, st) : launch_ac<256, 8>(fn, P, st);

@@ -26,10 +26,12 @@ def call(c, q, n_new, n_q, scale, xt="f32", yt="f32", out=None, ws=None, stream=
     return y
 
 
-def check(y, c, q, lens, n_new, n_q, scale, yt):
+def check(y, c, q, lens, n_new, n_q, scale, yt, only=None):
     q = q.double().cpu().numpy().reshape(c.B, n_new, n_q, c.D)
     y = y.double().cpu().numpy().reshape(c.B, n_new, n_q, c.D)
     for b, t in enumerate(lens):
+        if only is not None and b not in only:
+            continue
         limits = [max(t - n_new + 1 + i, 0) for i in range(n_new)]
         ref, V, S = attention(q[b], c.rows(b, t, 0), c.rows(b, t, 1), float(np.float32(scale)), limits)
         tol = (2 * (c.D + 16) * U * S + (t / 4 + 64) * U) * V
@@ -161,7 +163,8 @@ def test_bad_pages_and_lengths():
     c.lens = ints([50, 20, 16 * c.ldt + 1, 33])
     again = call(c, q.to(DEV), 1, 2, 32 ** -0.5)
     torch.cuda.synchronize()
-    assert bool(again[[0, 2, 3]].isnan().all()) and torch.equal(again[1], y[1])
+    assert bool(again[[0, 2, 3]].isnan().all())
+    check(again, c, q, lens, 1, 2, 32 ** -0.5, "f32", only=[1])  # (its sums may be cut elsewhere: another length is another line)
 
 
 def test_shared_pages():
