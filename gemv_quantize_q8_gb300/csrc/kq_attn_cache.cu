@@ -22,6 +22,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
+#include <type_traits>
 
 #include "kq_i8_tc.cuh"
 #include "kq_kv.cuh"
@@ -135,24 +136,16 @@ __device__ __forceinline__ void ac_next(const AcParams &P, AcItem &it) {
     it.units = ac_units(P, it.b);
 }
 
-__device__ __forceinline__ float ac_load(const void *p, kq_dtype t, int64_t i) {
-    return t == KQ_F32 ? static_cast<const float *>(p)[i] : t == KQ_F16 ? __half2float(static_cast<const __half *>(p)[i])
-                                                                        : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-}
-__device__ __forceinline__ void ac_load4(const void *p, kq_dtype t, int64_t i, bool vec, float (&v)[4]) {
-    if (!vec) {
+// Four consecutive elements.
+template <typename T, bool VEC>
+__device__ __forceinline__ void ac_load4(const T *p, float (&v)[4]) {
+    if constexpr (VEC) {
+        const auto u = *reinterpret_cast<const typename VecOf<4 * (int)sizeof(T)>::type *>(p);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = ac_load(p, t, i + j);
-    } else if (t == KQ_F32) {
-        const float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        for (int j = 0; j < 4; ++j) v[j] = to_f32(reinterpret_cast<const T *>(&u)[j]);
     } else {
-        const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint16_t e = (uint16_t)((j < 2 ? u.x : u.y) >> (16 * (j & 1)));
-            v[j] = t == KQ_F16 ? __half2float(__ushort_as_half(e)) : __uint_as_float((uint32_t)e << 16);
-        }
+        for (int j = 0; j < 4; ++j) v[j] = to_f32(p[j]);
     }
 }
 __device__ __forceinline__ void ac_store(void *p, kq_dtype t, int64_t i, float v) {
@@ -267,14 +260,24 @@ struct AcWarp {
             const int64_t sees = len - P.n_new + 1 + token;
             limit[r] = live && sees > 0 ? (int)sees : 0;
             float v[KS][4], amax = 0.0f;
+            // (one branch a type around all loads: they are under way together)
+            auto fill = [&](auto type, auto vec) {
+                using T = decltype(type);
+                const T *x = static_cast<const T *>(P.q) + at;
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const int d = AcRing<DP>::key_element(s / 4) + (s % 4) * 4;
-                v[s][0] = v[s][1] = v[s][2] = v[s][3] = 0.0f;
-                if (live && d < P.c.D) ac_load4(P.q, P.xt, at + d, P.qvec, v[s]);
+                for (int s = 0; s < KS; ++s) {
+                    const int d = AcRing<DP>::key_element(s / 4) + (s % 4) * 4;
+                    v[s][0] = v[s][1] = v[s][2] = v[s][3] = 0.0f;
+                    if (live && d < P.c.D) ac_load4<T, decltype(vec)::value>(x + d, v[s]);
+                }
+            };
+            auto typed = [&](auto vec) { P.xt == KQ_F32 ? fill(float{}, vec) : P.xt == KQ_F16 ? fill(__half{}, vec) : fill(__nv_bfloat16{}, vec); };
+            if (P.qvec) typed(std::true_type{});
+            else typed(std::false_type{});
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fabsf(v[s][i]));
-            }
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
             // the power of two at or below the largest (1 for rows of zeros and of infinities)
@@ -678,35 +681,37 @@ __global__ void __launch_bounds__(NW * 32, 1)
         while (sm100::globaltimer_ns() - t0 < 10000000ull) {}
         if (tid == 0) atomicAdd(P.err, 1ull);
     }
-    // items that several warps share, in the order of the line
-    for (int i = 0; i < 2 * NW;) {
-        const int64_t start = owner[i >> 1][i & 1];
-        if (start < 0) { ++i; continue; }
-        int j = i + 1;
-        while (j < 2 * NW && (owner[j >> 1][j & 1] == start || owner[j >> 1][j & 1] < 0)) ++j;
-        const AcItem it = items[i >> 1][i & 1];
-        const bool whole = start >= first && start + it.units <= last;
+    // Items that several warps share, in the order of the line: a lane for each part finds its weight, a row at a time.
+    const int64_t mine_of = lane < 2 * NW ? owner[lane >> 1][lane & 1] : -1;
+    for (unsigned left = __ballot_sync(~0u, mine_of >= 0); left;) {
+        const int lead = __ffs(left) - 1;
+        const int64_t start = __shfl_sync(~0u, mine_of, lead);
+        const unsigned group = __ballot_sync(~0u, mine_of == start);
+        left &= ~group;
+        const AcItem it = items[lead >> 1][lead & 1];
+        const bool whole = start >= first && start + it.units <= last, in = group >> lane & 1;
         float *out = P.parts + ((int64_t)blockIdx.x * 2 + (start < first ? 0 : 1)) * size;
-        __syncthreads();
-        if (tid < MT) {
-            float m = kAcNone, l = 0.0f;
-            for (int s = i; s < j; ++s)
-                if (owner[s >> 1][s & 1] >= 0) m = fmaxf(m, part(s)[tid]);
-            for (int s = i; s < j; ++s) {
-                const bool has = owner[s >> 1][s & 1] >= 0;
-                const float f = has ? ac_exp2(part(s)[tid] - m) : 0.0f;
-                weight[s][tid] = f;
-                if (has) l += part(s)[MT + tid] * f;
+        for (int row = warp; row < MT; row += NW) {
+            float m = in ? part(lane)[row] : kAcNone, l = in ? part(lane)[MT + row] : 0.0f, top = m;
+#pragma unroll
+            for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, s));
+            const float f = ac_exp2(m - top);
+            l *= in ? f : 0.0f;
+#pragma unroll
+            for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(~0u, l, s);
+            if (lane < 2 * NW) weight[lane][row] = f;
+            if (lane == 0) {
+                sum[row] = l;
+                if (!whole) out[row] = top, out[MT + row] = l;
             }
-            sum[tid] = l;
-            if (!whole) out[tid] = m, out[MT + tid] = l;
         }
         __syncthreads();
         for (int e = tid * 4; e < MT * D; e += NW * 32 * 4) {
             const int row = e / D, d = e - row * D;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int s = i; s < j; ++s)
-                if (owner[s >> 1][s & 1] >= 0) {
+#pragma unroll
+            for (int s = 0; s < 2 * NW; ++s)
+                if (group >> s & 1) {
                     const float4 v = *reinterpret_cast<const float4 *>(part(s) + 2 * MT + e);
                     const float f = weight[s][row];
                     o.x += v.x * f;
@@ -720,7 +725,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 *reinterpret_cast<float4 *>(out + 2 * MT + e) = o;
             }
         }
-        i = j;
+        __syncthreads();
     }
 }
 
@@ -730,7 +735,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
 template <int MT>
 __global__ void __launch_bounds__(256) ac_join_kernel(AcParams P) {
     __shared__ int64_t red[8];
-    __shared__ float weight[kAcMaxBlocks][MT], ls[kAcMaxBlocks][MT], sum[MT];
+    __shared__ float weight[kAcMaxBlocks][MT], sum[MT];
     const int c = blockIdx.x + 1, D = P.c.D;
     const int size = ac_part_floats<MT>(D);
     const int64_t total = ac_total<256>(P, red);
@@ -753,21 +758,20 @@ __global__ void __launch_bounds__(256) ac_join_kernel(AcParams P) {
     sm100::grid_launch_dependents();
     if (!cut) return;
     auto part = [&](int s) { return P.parts + ((int64_t)(c - 1 + s) * 2 + (s == 0 ? 1 : 0)) * size; };
-    const int row0 = threadIdx.x % MT, s0 = threadIdx.x / MT;
-    for (int s = s0; s < parts; s += 256 / MT) {
-        weight[s][row0] = part(s)[row0];
-        ls[s][row0] = part(s)[MT + row0];
-    }
-    __syncthreads();
-    if (threadIdx.x < MT) {
-        float m = kAcNone, l = 0.0f;
-        for (int s = 0; s < parts; ++s) m = fmaxf(m, weight[s][row0]);
-        for (int s = 0; s < parts; ++s) {
-            const float f = ac_exp2(weight[s][row0] - m);
-            l += ls[s][row0] * f;
-            weight[s][row0] = f;
+    const int lane = threadIdx.x & 31;
+    for (int row = threadIdx.x >> 5; row < MT; row += 8) {
+        float top = kAcNone, l = 0.0f;
+        for (int s = lane; s < parts; s += 32) top = fmaxf(top, weight[s][row] = part(s)[row]);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+        for (int s = lane; s < parts; s += 32) {
+            const float f = ac_exp2(weight[s][row] - top);
+            weight[s][row] = f;
+            l += part(s)[MT + row] * f;
         }
-        sum[row0] = l;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(~0u, l, x);
+        if (lane == 0) sum[row] = l;
     }
     __syncthreads();
     for (int e = threadIdx.x * 4; e < MT * D; e += 256 * 4) {
