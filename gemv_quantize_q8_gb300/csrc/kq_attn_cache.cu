@@ -498,9 +498,10 @@ __device__ __forceinline__ void ac_write_run(const AcParams &P, const AcItem &it
     const int token = i / P.G, head = it.h * P.G + i - token * P.G;
     const bool sees = ac_len(P, it.b) - P.n_new + token >= 0;
     const int64_t at = (it.b * P.n_new + token) * P.ldy + (int64_t)head * P.c.D + d0;
+    const float inv = 1.0f / l;
     float x[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = sees ? v[j] / l : 0.0f;
+    for (int j = 0; j < N; ++j) x[j] = sees ? v[j] * inv : 0.0f;
     if (!P.yvec) {
 #pragma unroll
         for (int j = 0; j < N; ++j) ac_store(P.y, P.yt, at + j, x[j]);
@@ -530,76 +531,95 @@ __device__ __forceinline__ void ac_write4(const AcParams &P, const AcItem &it, i
     ac_write_run(P, it, MT, row, d0, x, l);
 }
 
-// The units of a warp's share, fetched ahead of their use.
+__device__ __forceinline__ void ac_copy4(float *dst, const float *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sm100::smem_u32(dst)), "l"(src) : "memory");
+}
+
+// The units of one consumer's share, brought by one lane of the fetching warp: codes by TMA, scales by small copies
+// that arrive at the same barrier.  The numbers of the next unit's pages are asked for when a unit has been sent off.
 template <int DP>
 struct AcFetch {
     AcItem it;
-    int at, pages, base;  // next unit of the item; the sequence's pages; lanes hold what follows of the 32 pages from base on
-    int64_t left;         // units to fetch
-    int page;
-    float ks, vs;
+    int at;        // next unit of the item
+    int64_t left;  // units to fetch
+    int page[2];   // the next unit's
+    int64_t len;   // of the item's sequence
+    bool bad;
+    const int32_t *table;
     __device__ __forceinline__ void start(const AcParams &P) {
-        pages = (int)((ac_len(P, it.b) + (1 << P.c.lp) - 1) >> P.c.lp);
-        base = -64;
+        len = ac_len(P, it.b);
+        bad = ac_bad(P, it.b);
+        table = P.c.table + it.b * P.c.ldt;
     }
-    __device__ __forceinline__ void next(const AcParams &P, const CUtensorMap *tmK, const CUtensorMap *tmV, uint8_t *stage, float4 *scales,
-                                         uint64_t *bar) {
+    __device__ __forceinline__ void look(const AcParams &P) {
+        const int t0 = at * kAcUnit;
+        page[0] = table[t0 >> P.c.lp];
+        if (P.c.lp == 4) page[1] = t0 + 16 < len ? table[(t0 + 16) >> P.c.lp] : 0;  // (a page of 16 holds half a unit)
+    }
+    // The item's query rows, soon to be read, into the first-level cache.
+    __device__ __forceinline__ void announce(const AcParams &P, int MT) {
+        const int size = P.xt == KQ_F32 ? 4 : 2;
+        for (int row = it.tile * MT; row < min(P.rows, it.tile * MT + MT); ++row) {
+            const int token = row / P.G, head = it.h * P.G + row - token * P.G;
+            const char *x = static_cast<const char *>(P.q) + ((it.b * P.n_new + token) * P.ldq + (int64_t)head * P.c.D) * size;
+            for (int i = 0; i < P.c.D * size; i += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(x + i));
+        }
+    }
+    __device__ __forceinline__ void send(const AcParams &P, const CUtensorMap *tmK, const CUtensorMap *tmV, uint8_t *stage, float4 *scales,
+                                         uint64_t *bar, int MT) {
         using Ring = AcRing<DP>;
-        if (left <= 0) return;
-        const int lane = threadIdx.x & 31;
-        if (at == it.units) {
-            ac_next(P, it);
-            at = 0;
-            start(P);
-        }
-        const int halves = P.c.lp == 4 ? 2 : 1;  // a page of 16 holds half a unit
-        float k[2], v[2];
-        int first[2];
-        for (int h = 0; h < halves; ++h) {
-            const int pi = (at * kAcUnit + h * 16) >> P.c.lp;
-            if (pi >= base + 32 || base < 0) {
-                base = pi;
-                const bool in = base + lane < pages;
-                page = in ? P.c.table[it.b * P.c.ldt + base + lane] : -1;
-                const bool ok = page >= 0 && page < P.c.n_pages && !ac_bad(P, it.b);
-                if (!ok) page = in ? 0 : -1;
-                const int64_t block = (int64_t)page * P.c.n_kv + it.h;
-                // (a unit's second half may lie past the last page: weight 0, whatever is there)
-                ks = !in ? 0.0f : ok ? P.c.k_scale[block] : NAN;
-                vs = in && ok ? P.c.v_scale[block] : 0.0f;
-            }
-            first[h] = __shfl_sync(~0u, page, pi - base);
-            k[h] = __shfl_sync(~0u, ks, pi - base);
-            v[h] = __shfl_sync(~0u, vs, pi - base);
-        }
-        if (lane == 0) {
-            const int row = (it.h << P.c.lp) + (at * kAcUnit & ((1 << P.c.lp) - 1)), parts = halves == 1 ? 1 : first[1] < 0 ? 1 : 2;
-            *scales = make_float4(k[0], v[0], halves == 1 ? k[0] : k[1], halves == 1 ? v[0] : v[1]);
-            sm100::mbar_arrive_expect_tx(bar, halves == parts ? Ring::BYTES : Ring::BYTES / 2);
-            for (int h = 0; h < parts; ++h)
+        const int t0 = at * kAcUnit, row = (it.h << P.c.lp) + (t0 & ((1 << P.c.lp) - 1));
+        const bool small = P.c.lp == 4;
+        // a unit's second half may lie past the last page: weight 0, whatever is there
+        const int parts = small && t0 + 16 < len ? 2 : 1;
+        sm100::mbar_arrive_expect_tx(bar, small && parts == 1 ? Ring::BYTES / 2 : Ring::BYTES);
+        float *sc = reinterpret_cast<float *>(scales);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int number = h && small ? page[1] : page[0];
+            const bool ok = number >= 0 && number < P.c.n_pages && !bad;
+            if (h < parts) {
 #pragma unroll
                 for (int i = 0; i < Ring::BOXES; ++i) {
-                    ac_copy(stage + i * Ring::BOX + h * 16 * Ring::W, tmK, bar, i * 128, row, first[h]);
-                    ac_copy(stage + (Ring::BOXES + i) * Ring::BOX + h * 16 * Ring::W, tmV, bar, i * 128, row, first[h]);
+                    ac_copy(stage + i * Ring::BOX + h * 16 * Ring::W, tmK, bar, i * 128, row, ok ? number : 0);
+                    ac_copy(stage + (Ring::BOXES + i) * Ring::BOX + h * 16 * Ring::W, tmV, bar, i * 128, row, ok ? number : 0);
                 }
+            }
+            const bool there = h < parts || !small;
+            if (there && ok) {
+                const int64_t block = (int64_t)number * P.c.n_kv + it.h;
+                ac_copy4(sc + 2 * h, P.c.k_scale + block);
+                ac_copy4(sc + 2 * h + 1, P.c.v_scale + block);
+            } else {
+                sc[2 * h] = there ? NAN : 0.0f;
+                sc[2 * h + 1] = 0.0f;
+            }
         }
-        ++at;
-        --left;
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(bar)) : "memory");
+        if (--left == 0) return;
+        if (++at == it.units) {
+            const int64_t b = it.b;
+            ac_next(P, it);
+            at = 0;
+            if (it.b != b) start(P);
+            announce(P, MT);
+        }
+        look(P);
     }
 };
 
 template <int DP, int MT, int NW, int NS>
-__global__ void __launch_bounds__(NW * 32, 1)
+__global__ void __launch_bounds__(NW * 64, 1)
     ac_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, AcParams P) {
     using Ring = AcRing<DP>;
     extern __shared__ __align__(1024) uint8_t rings[];
     // the warps' rings, then a part each.  A warp shares at most its first and its last item with others: what it has of
     // the first goes to that part, what it has of the last into its ring, which is idle by then.
-    __shared__ int64_t red[NW];
+    __shared__ int64_t red[NW * 2];
     __shared__ int64_t owner[NW][2];  // the item (its first unit on the line) of each, or -1
     __shared__ AcItem items[NW][2];
     __shared__ float4 scales[NW][NS];
-    __shared__ uint64_t full[NW][NS];
+    __shared__ uint64_t full[NW][NS], empty[NW][NS];
     __shared__ float weight[2 * NW][MT], sum[MT];
     __shared__ int aborted;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = P.c.D, size = ac_part_floats<MT>(D);
@@ -608,23 +628,24 @@ __global__ void __launch_bounds__(NW * 32, 1)
         return reinterpret_cast<float *>(rings + (s & 1 ? (s >> 1) * NS * Ring::BYTES : NW * NS * Ring::BYTES + (s >> 1) * size * 4));
     };
     static_assert(ac_part_floats<MT>(DP) * 4 <= NS * Ring::BYTES, "a part fits a ring");
-    if (lane < NS) sm100::mbar_init(&full[warp][lane], 1);
-    if (lane < 2) owner[warp][lane] = -1;
-    if (tid == 0) {
+    AcFetch<DP> *begin_at = reinterpret_cast<AcFetch<DP> *>(part(0));  // [NW], before the parts have anything
+    if (warp < NW) {
+        if (lane < NS) sm100::mbar_init(&full[warp][lane], 2), sm100::mbar_init(&empty[warp][lane], 1);
+        if (lane < 2) owner[warp][lane] = -1;
+    } else if (tid == NW * 32) {
         aborted = 0;
-        sm100::fence_mbar_init();
         sm100::prefetch_tmap(&tmK);
         sm100::prefetch_tmap(&tmV);
     }
-    sm100::fence_proxy_async_smem();  // (each warp's barriers are its own: ready for its copies)
+    sm100::fence_mbar_init();
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
     if (blockIdx.x == 0 && tid == 0) *P.err = 0ull;  // (an error is counted two seconds later at the earliest)
-    const int64_t total = ac_total<NW * 32>(P, red);
+    const int64_t total = ac_total<NW * 64>(P, red);
     // rows of sequences without tokens
     for (int64_t b = blockIdx.x; b < P.c.B; b += gridDim.x)
         if (P.c.lens[b] <= 0)
-            for (int i = tid; i < P.n_new * P.n_q * D; i += NW * 32) {
+            for (int i = tid; i < P.n_new * P.n_q * D; i += NW * 64) {
                 const int t = i / (P.n_q * D);
                 ac_store(P.y, P.yt, (b * P.n_new + t) * P.ldy + i - t * (P.n_q * D), 0.0f);
             }
@@ -634,15 +655,45 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const int64_t first = shares(blockIdx.x), last = shares(blockIdx.x + 1);
     if (first >= last) return;
     const AcShares mine(last - first, NW);
-    const int64_t u0 = first + mine(warp), u1 = first + mine(warp + 1);
-    if (u0 < u1) {
-        AcFetch<DP> ahead;
-        ahead.it = ac_find(P, u0, ahead.at);
-        ahead.left = u1 - u0;
-        AcItem it = ahead.it;
-        int at = ahead.at;
-        ahead.start(P);
-        for (int i = 0; i < NS - 1; ++i) ahead.next(P, &tmK, &tmV, ring + i * Ring::BYTES, &scales[warp][i], &full[warp][i]);
+    const int64_t u0 = first + mine(min(warp, NW - 1)), u1 = first + mine(min(warp, NW - 1) + 1);
+    AcItem it;
+    int at = 0;
+    if (warp < NW) {
+        if (u0 < u1) it = ac_find(P, u0, at);
+        if (lane == 0) begin_at[warp] = AcFetch<DP>{it, at, u1 - u0};
+    }
+    __syncthreads();
+    if (warp >= NW) {
+        // ------------------------------------------------------------ one lane brings the units of one of the first warps
+        // (one warp for all, its lanes in turns, could not keep up, nor could two lanes a warp)
+        if (NW == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        const int mate = warp - NW;
+        if (lane == 0) {
+            AcFetch<DP> f = begin_at[mate];
+            if (f.left > 0) f.start(P), f.look(P);
+            int stage = 0;
+            uint32_t phase = 1;
+            while (f.left > 0) {
+                bool free = sm100::mbar_test_wait(&empty[mate][stage], phase);
+                if (!free) {  // (bounded: whoever waits too long tells the others)
+                    const uint64_t since = sm100::globaltimer_ns();
+                    for (int i = 0; !free; ++i) {
+                        free = sm100::mbar_test_wait(&empty[mate][stage], phase);
+                        if (!free && (i & 255) == 255 && (*(volatile int *)&aborted || sm100::globaltimer_ns() - since > 2000000000ull)) break;
+                    }
+                }
+                if (!free) {
+                    *(volatile int *)&aborted = 1;
+                    break;
+                }
+                f.send(P, &tmK, &tmV, rings + (mate * NS + stage) * Ring::BYTES, &scales[mate][stage], &full[mate][stage], MT);
+                if (++stage == NS) stage = 0, phase ^= 1;
+            }
+        }
+        __syncwarp();
+    } else {
+        if (NW == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (u0 < u1) {
         AcWarp<DP, MT> w;
         int stage = 0;
         uint32_t phase = 0;
@@ -651,13 +702,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
             const int64_t start = u - at;  // the item's first unit on the line
             w.begin(P, it);
             for (int i = 0; i < n; ++i) {
-                // the stage before this one is free: every lane is through with it
-                __syncwarp();
-                const int free = stage == 0 ? NS - 1 : stage - 1;
-                ahead.next(P, &tmK, &tmV, ring + free * Ring::BYTES, &scales[warp][free], &full[warp][free]);
                 // (a wait that runs out spoils the result, which the device flag tells)
                 if (!sm100::mbar_wait(&full[warp][stage], phase, &aborted)) aborted = 1;
                 w.unit(sm100::smem_u32(ring + stage * Ring::BYTES), scales[warp][stage], (at + i) * kAcUnit);
+                __syncwarp();
+                if (lane == 0) sm100::mbar_arrive(&empty[warp][stage]);
                 if (++stage == NS) stage = 0, phase ^= 1;
             }
             w.end();
@@ -672,6 +721,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             u += n;
             at = 0;
             if (u < u1) ac_next(P, it);
+        }
         }
     }
     __syncthreads();
@@ -691,7 +741,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         const AcItem it = items[lead >> 1][lead & 1];
         const bool whole = start >= first && start + it.units <= last, in = group >> lane & 1;
         float *out = P.parts + ((int64_t)blockIdx.x * 2 + (start < first ? 0 : 1)) * size;
-        for (int row = warp; row < MT; row += NW) {
+        for (int row = warp; row < MT && warp < NW; row += NW) {
             float m = in ? part(lane)[row] : kAcNone, l = in ? part(lane)[MT + row] : 0.0f, top = m;
 #pragma unroll
             for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, s));
@@ -706,7 +756,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             }
         }
         __syncthreads();
-        for (int e = tid * 4; e < MT * D; e += NW * 32 * 4) {
+        for (int e = tid * 4; e < MT * D && warp < NW; e += NW * 32 * 4) {
             const int row = e / D, d = e - row * D;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -835,7 +885,7 @@ static kq_status launch_ac(const char *fn, AcParams P, cudaStream_t st) {
     auto kern = ac_kernel<DP, MT, NW, NS>;
     P.warps = NW;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = launch_beside(kern, dim3(P.blocks), dim3(NW * 32), smem, dim3(1), st, tm[0], tm[1], P);
+    if (e == cudaSuccess) e = launch_beside(kern, dim3(P.blocks), dim3(NW * 64), smem, dim3(1), st, tm[0], tm[1], P);
     if (e == cudaSuccess) count_launch(R_ATTN);
     if (e == cudaSuccess) {
         e = launch_beside(ac_join_kernel<MT>, dim3(P.blocks - 1), dim3(256), 0, dim3(1), st, P);
