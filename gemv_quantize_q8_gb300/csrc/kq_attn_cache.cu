@@ -31,7 +31,7 @@
 namespace kq {
 
 constexpr int kAcUnit = 32;           // tokens
-constexpr int kAcLeast = 2;           // units of a warp
+constexpr int kAcLeast = 1;           // units of a warp
 constexpr int kAcMaxBlocks = 152;     // one an SM
 constexpr float kAcLift = 128.0f;     // weights are held times this: f16 keeps their low bits, with room for kAcSlack
 constexpr float kAcSlack = 8.0f;      // a weight may grow to 2^8 before the sums are brought to a new maximum
@@ -52,8 +52,9 @@ struct AcParams {
     int blocks, warps;    // of the first kernel's grid
 };
 
-// What a warp (or a block) hands over: rows of m, l and D sums, relative to 2^m.
-template <int MT> __host__ __device__ constexpr int ac_part_floats(int D) { return MT * (D + 2); }
+// What a warp (or a block) hands over: m and l of its rows, then their sums relative to 2^m, in the order in which a
+// warp's lanes hold them (32 lanes side by side, 16 bytes each: no bank conflicts).
+template <int DP, int MT> constexpr int kAcPart = MT * (DP + 2);
 
 // A place on the line of units.
 struct AcItem {
@@ -69,61 +70,75 @@ __device__ __forceinline__ int64_t ac_len(const AcParams &P, int64_t b) {
 __device__ __forceinline__ bool ac_bad(const AcParams &P, int64_t b) { return P.c.lens[b] > P.c.ldt << P.c.lp; }
 __device__ __forceinline__ int ac_units(const AcParams &P, int64_t b) { return (int)((ac_len(P, b) + kAcUnit - 1) / kAcUnit); }
 
-// All threads of the block: the units of all sequences together (times heads and row tiles).
-template <int THREADS>
-__device__ __forceinline__ int64_t ac_total(const AcParams &P, int64_t *red) {
-    int64_t n = 0;
-    for (int64_t b = threadIdx.x; b < P.c.B; b += THREADS) n += ac_units(P, b);
-#pragma unroll
-    for (int s = 16; s; s >>= 1) n += __shfl_xor_sync(~0u, n, s);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = n;
-    __syncthreads();
-    n = 0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) n += red[i];
-    return n * P.c.n_kv * P.tiles;
+// Quotients: 32 bits wherever they do.
+__device__ __forceinline__ int64_t ac_div(int64_t a, int64_t b) {
+    return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 // The line of units cut into n shares (n is at most a few hundred): where share w begins.
 struct AcShares {
     int64_t each;
     int rest, n;
-    __device__ __forceinline__ AcShares(int64_t total, int n_) : each(total / n_), rest((int)(total - each * n_)), n(n_) {}
-    __device__ __forceinline__ int64_t operator()(int w) const { return each * w + rest * w / n; }
+    __device__ __forceinline__ AcShares(int64_t total, int n_) : each(ac_div(total, n_)), rest((int)(total - each * n_)), n(n_) {}
+    __device__ __forceinline__ int64_t operator()(int w) const { return each * w + (unsigned)(rest * w) / (unsigned)n; }
 };
 // The blocks that share the line: each warp has kAcLeast units at least, if there are so many.
 __device__ __forceinline__ int ac_blocks(const AcParams &P, int64_t total, int warps) {
-    const int64_t n = total / (kAcLeast * warps);
+    const int64_t n = ac_div(total, kAcLeast * warps);
     return n < 1 ? 1 : n < P.blocks ? (int)n : P.blocks;
 }
 
-// The warp finds the item that unit u lies in, and its place in it.
-__device__ __forceinline__ AcItem ac_find(const AcParams &P, int64_t u, int &at) {
-    const int lane = threadIdx.x & 31;
-    const int64_t per = (int64_t)P.c.n_kv * P.tiles;
-    AcItem it;
-    for (int64_t b0 = 0;; b0 += 32) {
-        const int64_t b = b0 + lane;
-        const int64_t mine = b < P.c.B ? ac_units(P, b) * per : 0;
-        int64_t sum = mine;
+// Where the sequences lie on the line: thread t of the block sums up `per` of them, and end[t] is where they end.
+template <int THREADS>
+struct AcLine {
+    int64_t end[THREADS], warps[THREADS / 32];
+};
+// All threads of the block; the line's length, in units of all heads and row tiles.
+template <int THREADS>
+__device__ __forceinline__ int64_t ac_line(const AcParams &P, AcLine<THREADS> &line) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t per = (P.c.B + THREADS - 1) / THREADS, b0 = threadIdx.x * per;
+    int64_t n = 0;
+    for (int64_t b = b0; b < b0 + per && b < P.c.B; ++b) n += ac_units(P, b);
+    n *= P.c.n_kv * P.tiles;
 #pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const int64_t o = __shfl_up_sync(~0u, sum, s);
-            if (lane >= s) sum += o;
-        }
-        const unsigned past = __ballot_sync(~0u, sum > u);
-        if (past || b0 + 32 >= P.c.B) {
-            const int l = past ? __ffs(past) - 1 : 31;
-            const int64_t rest = u - __shfl_sync(~0u, sum - mine, l);
-            it.b = b0 + l;
-            it.units = (int)(__shfl_sync(~0u, mine, l) / per);
-            const int64_t i = rest / it.units;
-            at = (int)(rest - i * it.units);
-            it.h = (int)(i / P.tiles);
-            it.tile = (int)(i - it.h * P.tiles);
-            return it;
-        }
-        u -= __shfl_sync(~0u, sum, 31);
+    for (int s = 1; s < 32; s <<= 1) {
+        const int64_t o = __shfl_up_sync(~0u, n, s);
+        if (lane >= s) n += o;
     }
+    if (lane == 31) line.warps[warp] = n;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w == warp) n += total;
+        total += line.warps[w];
+    }
+    line.end[threadIdx.x] = n;
+    __syncthreads();
+    return total;
+}
+// The item that unit u (below the line's length) lies in, and its place in it.
+template <int THREADS>
+__device__ __forceinline__ AcItem ac_find(const AcParams &P, const AcLine<THREADS> &line, int64_t u, int &at) {
+    int lo = 0;  // threads whose sequences end at or before u
+#pragma unroll
+    for (int s = THREADS / 2; s; s >>= 1)
+        if (line.end[lo + s - 1] <= u) lo += s;
+    u -= lo ? line.end[lo - 1] : 0;
+    const int64_t per = (P.c.B + THREADS - 1) / THREADS;
+    AcItem it;
+    it.b = lo * per;
+    for (;; ++it.b) {
+        it.units = ac_units(P, it.b);
+        const int64_t mine = (int64_t)it.units * P.c.n_kv * P.tiles;
+        if (u < mine) break;
+        u -= mine;
+    }
+    const int64_t i = ac_div(u, it.units);
+    at = (int)(u - i * it.units);
+    it.h = (int)((uint32_t)i / (uint32_t)P.tiles);
+    it.tile = (int)i - it.h * P.tiles;
+    return it;
 }
 // The next item that has units (there is one).
 __device__ __forceinline__ void ac_next(const AcParams &P, AcItem &it) {
@@ -477,18 +492,28 @@ struct AcWarp {
                     if (d0 < D) f(r, d0, v);
                 }
     }
-    __device__ __forceinline__ void put(float *part, int D) {
+    __device__ __forceinline__ void put(float *part) {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
         for (int r = 0; r < R; ++r)
             if (c == 0) part[g + 8 * r] = m[r], part[MT + g + 8 * r] = l[r];
-        runs(D, [&](int r, int d0, const float (&v)[RUN]) {
-            float4 *dst = reinterpret_cast<float4 *>(part + 2 * MT + (g + 8 * r) * D + d0);
+        float4 *dst = reinterpret_cast<float4 *>(part + 2 * MT) + lane;
 #pragma unroll
-            for (int i = 0; i < RUN; i += 4) dst[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        });
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < NT; j += 4)
+#pragma unroll
+                for (int e = 0; e < 2; ++e, dst += 32)
+                    *dst = make_float4(o[j][2 * r + e], o[j + 1][2 * r + e], o[j + 2][2 * r + e], o[j + 3][2 * r + e]);
     }
 };
+// Row and first element of the four at place x of a part.
+template <int DP>
+__device__ __forceinline__ void ac_place(int x, int &row, int &d) {
+    const int lane = x & 31, e = x >> 5 & 1, j = (x >> 6) % (DP / 32) * 4;
+    row = (lane >> 2) + 8 * ((x >> 6) / (DP / 32));
+    d = ac_element<DP>(j, 2 * (lane & 3) + e);
+}
 
 // A run of row `row` (of the item's tile) of the output; a token that sees nothing gives 0.
 template <int N>
@@ -615,20 +640,23 @@ __global__ void __launch_bounds__(NW * 64, 1)
     extern __shared__ __align__(1024) uint8_t rings[];
     // the warps' rings, then a part each.  A warp shares at most its first and its last item with others: what it has of
     // the first goes to that part, what it has of the last into its ring, which is idle by then.
-    __shared__ int64_t red[NW * 2];
     __shared__ int64_t owner[NW][2];  // the item (its first unit on the line) of each, or -1
     __shared__ AcItem items[NW][2];
     __shared__ float4 scales[NW][NS];
     __shared__ uint64_t full[NW][NS], empty[NW][NS];
     __shared__ float weight[2 * NW][MT], sum[MT];
     __shared__ int aborted;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = P.c.D, size = ac_part_floats<MT>(D);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = P.c.D;
+    constexpr int size = kAcPart<DP, MT>;
     uint8_t *ring = rings + warp * NS * Ring::BYTES;
     auto part = [&](int s) {
         return reinterpret_cast<float *>(rings + (s & 1 ? (s >> 1) * NS * Ring::BYTES : NW * NS * Ring::BYTES + (s >> 1) * size * 4));
     };
-    static_assert(ac_part_floats<MT>(DP) * 4 <= NS * Ring::BYTES, "a part fits a ring");
-    AcFetch<DP> *begin_at = reinterpret_cast<AcFetch<DP> *>(part(0));  // [NW], before the parts have anything
+    static_assert(kAcPart<DP, MT> * 4 <= NS * Ring::BYTES, "a part fits a ring");
+    // before the parts have anything: the line; before the rings' last stages do: where each warp begins
+    AcLine<NW * 64> &line = *reinterpret_cast<AcLine<NW * 64> *>(part(0));
+    static_assert(sizeof(AcLine<NW * 64>) <= NW * size * 4, "shared memory");
+    auto begin_at = [&](int w) -> AcFetch<DP> & { return *reinterpret_cast<AcFetch<DP> *>(rings + ((w + 1) * NS - 1) * Ring::BYTES); };
     if (warp < NW) {
         if (lane < NS) sm100::mbar_init(&full[warp][lane], 2), sm100::mbar_init(&empty[warp][lane], 1);
         if (lane < 2) owner[warp][lane] = -1;
@@ -641,7 +669,7 @@ __global__ void __launch_bounds__(NW * 64, 1)
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
     if (blockIdx.x == 0 && tid == 0) *P.err = 0ull;  // (an error is counted two seconds later at the earliest)
-    const int64_t total = ac_total<NW * 64>(P, red);
+    const int64_t total = ac_line(P, line);
     // rows of sequences without tokens
     for (int64_t b = blockIdx.x; b < P.c.B; b += gridDim.x)
         if (P.c.lens[b] <= 0)
@@ -659,8 +687,8 @@ __global__ void __launch_bounds__(NW * 64, 1)
     AcItem it;
     int at = 0;
     if (warp < NW) {
-        if (u0 < u1) it = ac_find(P, u0, at);
-        if (lane == 0) begin_at[warp] = AcFetch<DP>{it, at, u1 - u0};
+        if (u0 < u1) it = ac_find(P, line, u0, at);
+        if (lane == 0) begin_at(warp) = AcFetch<DP>{it, at, u1 - u0};
     }
     __syncthreads();
     if (warp >= NW) {
@@ -669,7 +697,7 @@ __global__ void __launch_bounds__(NW * 64, 1)
         if (NW == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         const int mate = warp - NW;
         if (lane == 0) {
-            AcFetch<DP> f = begin_at[mate];
+            AcFetch<DP> f = begin_at(mate);
             if (f.left > 0) f.start(P), f.look(P);
             int stage = 0;
             uint32_t phase = 1;
@@ -715,7 +743,7 @@ __global__ void __launch_bounds__(NW * 64, 1)
             } else {
                 const int slot = u == u0 ? 0 : 1;
                 __syncwarp();
-                w.put(part(warp * 2 + slot), D);
+                w.put(part(warp * 2 + slot));
                 if (lane == 0) owner[warp][slot] = start, items[warp][slot] = it;
             }
             u += n;
@@ -756,24 +784,22 @@ __global__ void __launch_bounds__(NW * 64, 1)
             }
         }
         __syncthreads();
-        for (int e = tid * 4; e < MT * D && warp < NW; e += NW * 32 * 4) {
-            const int row = e / D, d = e - row * D;
+        for (int x = tid; x < MT * DP / 4; x += NW * 64) {
+            int row, d;
+            ac_place<DP>(x, row, d);
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int s = 0; s < 2 * NW; ++s)
                 if (group >> s & 1) {
-                    const float4 v = *reinterpret_cast<const float4 *>(part(s) + 2 * MT + e);
+                    const float4 v = reinterpret_cast<const float4 *>(part(s) + 2 * MT)[x];
                     const float f = weight[s][row];
                     o.x += v.x * f;
                     o.y += v.y * f;
                     o.z += v.z * f;
                     o.w += v.w * f;
                 }
-            if (whole) {
-                ac_write4(P, it, MT, row, d, o, sum[row]);
-            } else {
-                *reinterpret_cast<float4 *>(out + 2 * MT + e) = o;
-            }
+            if (!whole) reinterpret_cast<float4 *>(out + 2 * MT)[x] = o;
+            else if (d < D) ac_write4(P, it, MT, row, d, o, sum[row]);
         }
         __syncthreads();
     }
@@ -782,32 +808,37 @@ __global__ void __launch_bounds__(NW * 64, 1)
 // Items that thread blocks share.  Block c takes the item that the c-th border between shares cuts, if no earlier
 // border does: its parts are those of the shares that it reaches into, in their order.  Which those are follows from
 // the lengths alone, which were there before the first kernel: it is found out while that one still runs.
-template <int MT>
+template <int DP, int MT>
 __global__ void __launch_bounds__(256) ac_join_kernel(AcParams P) {
-    __shared__ int64_t red[8];
+    __shared__ AcLine<256> line;
     __shared__ float weight[kAcMaxBlocks][MT], sum[MT];
     const int c = blockIdx.x + 1, D = P.c.D;
-    const int size = ac_part_floats<MT>(D);
-    const int64_t total = ac_total<256>(P, red);
+    constexpr int size = kAcPart<DP, MT>;
+    const int64_t total = ac_line(P, line);
     const int blocks = ac_blocks(P, total, P.warps);
     bool cut = c < blocks;
     const AcShares shares(total, blocks);
     const int64_t border = cut ? shares(c) : 0, before = cut ? shares(c - 1) : 0;
-    cut = cut && border < total && border > before;
     AcItem it;
     int parts = 0;
     if (cut) {
         int at;
-        it = ac_find(P, border, at);
+        it = ac_find(P, line, border, at);
         const int64_t start = border - at, end = start + it.units;
         cut = at > 0 && before <= start;  // (else the border cuts nothing, or an earlier one cuts the item)
-        // the shares up to the one that the item ends in; with kAcLeast units a warp none of them is empty
+        // the shares up to the one that the item ends in; none of them is empty
         for (parts = 2; c - 1 + parts < blocks && shares(c - 1 + parts) < end;) ++parts;
     }
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
     if (!cut) return;
     auto part = [&](int s) { return P.parts + ((int64_t)(c - 1 + s) * 2 + (s == 0 ? 1 : 0)) * size; };
+    // the first parts' sums are on their way while the weights are found
+    constexpr int AHEAD = 8, PER = (MT * DP / 4 + 255) / 256;
+    float4 ahead[AHEAD];
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s)
+        if (s < parts) ahead[s] = __ldcg(reinterpret_cast<const float4 *>(part(s) + 2 * MT) + threadIdx.x % (MT * DP / 4));
     const int lane = threadIdx.x & 31;
     for (int row = threadIdx.x >> 5; row < MT; row += 8) {
         float top = kAcNone, l = 0.0f;
@@ -824,27 +855,34 @@ __global__ void __launch_bounds__(256) ac_join_kernel(AcParams P) {
         if (lane == 0) sum[row] = l;
     }
     __syncthreads();
-    for (int e = threadIdx.x * 4; e < MT * D; e += 256 * 4) {
-        const int row = e / D, d = e - row * D;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int x = threadIdx.x + k * 256;
+        if (x >= MT * DP / 4) break;
+        int row, d;
+        ac_place<DP>(x, row, d);
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int s = 0; s < parts; ++s) {
-            const float4 v = *reinterpret_cast<const float4 *>(part(s) + 2 * MT + e);
+        auto add = [&](float4 v, int s) {
             const float f = weight[s][row];
             o.x += v.x * f;
             o.y += v.y * f;
             o.z += v.z * f;
             o.w += v.w * f;
-        }
-        ac_write4(P, it, MT, row, d, o, sum[row]);
+        };
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s)
+            if (s < parts) add(k == 0 ? ahead[s] : __ldcg(reinterpret_cast<const float4 *>(part(s) + 2 * MT) + x), s);
+#pragma unroll 4
+        for (int s = AHEAD; s < parts; ++s) add(__ldcg(reinterpret_cast<const float4 *>(part(s) + 2 * MT) + x), s);
+        if (d < D) ac_write4(P, it, MT, row, d, o, sum[row]);
     }
 }
 
 // ---------------------------------------------------------------- host
 static int ac_row_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
+static int ac_width(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 static size_t ac_workspace(int64_t rows, int64_t D) {
-    const int mt = ac_row_tile(rows);
-    return 256 + (size_t)kAcMaxBlocks * 2 * mt * (D + 2) * 4;
+    return 256 + (size_t)kAcMaxBlocks * 2 * ac_row_tile(rows) * (ac_width(D) + 2) * 4;
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 ac_encoder() {
@@ -866,8 +904,8 @@ static kq_status launch_ac(const char *fn, AcParams P, cudaStream_t st) {
     // 8 KB a unit of 128 elements, up to 16 KB a part
     constexpr int NW = DP == 256 ? 4 : 8, NS = DP == 64 ? 4 : DP == 128 && MT == 8 ? 3 : 2;
     using Ring = AcRing<DP>;
-    const int smem = NW * (NS * Ring::BYTES + ac_part_floats<MT>(P.c.D) * 4);
-    static_assert(NW * (NS * Ring::BYTES + ac_part_floats<MT>(DP) * 4) <= 224 * 1024 + 512, "shared memory");
+    const int smem = NW * (NS * Ring::BYTES + kAcPart<DP, MT> * 4);
+    static_assert(NW * (NS * Ring::BYTES + kAcPart<DP, MT> * 4) <= 224 * 1024 + 512, "shared memory");
     auto encode = ac_encoder();
     if (!encode) return fail(KQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", fn);
     CUtensorMap tm[2];
@@ -888,7 +926,7 @@ static kq_status launch_ac(const char *fn, AcParams P, cudaStream_t st) {
     if (e == cudaSuccess) e = launch_beside(kern, dim3(P.blocks), dim3(NW * 64), smem, dim3(1), st, tm[0], tm[1], P);
     if (e == cudaSuccess) count_launch(R_ATTN);
     if (e == cudaSuccess) {
-        e = launch_beside(ac_join_kernel<MT>, dim3(P.blocks - 1), dim3(256), 0, dim3(1), st, P);
+        e = launch_beside(ac_join_kernel<DP, MT>, dim3(P.blocks - 1), dim3(256), 0, dim3(1), st, P);
         if (e == cudaSuccess) count_launch(R_ATTN);
     }
     return e == cudaSuccess ? KQ_OK : fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
