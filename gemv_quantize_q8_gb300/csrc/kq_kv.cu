@@ -3,12 +3,15 @@
 // A block of the cache (a page and head) has one scale, so its largest magnitude has to be known before its
 // first code is written, and when a later token raises it the codes that are there follow:
 //   s' = max(s, max |x| / 127),   q' = rint(q * (s / s')) for the old tokens,   q = rint(x * (1 / s')) for the new.
-// One thread block takes one block of the cache that the call touches: it keeps the new rows in registers between
-// the maximum and the codes, so every row is read once and every code written once.  Which blocks those are follows
-// from cu and lens on the device: sequence b's share of the grid starts at floor(cu[b] / page) + 2b, which leaves
-// room for every page that its rows can touch (a run of n tokens touches at most floor(n / page) + 2).
+// A group of threads takes one block of the cache that the call touches (all 256 of a thread block, or a warp where the
+// sequences have few rows): it keeps the new rows in registers between the maximum and the codes, so every row is
+// read once and every code written once.  Which blocks those are follows from cu and lens on the device: a run of n
+// tokens touches at most floor(n / page) + 2 pages, and at most n; so sequence b's share of the grid starts at
+// floor(cu[b] / page) + 2b, or at cu[b], whichever makes the smaller grid.
 // The maximum, every product and sum are rounded one by one, so that codes and scales are the same bits whatever
 // the grid or the vector width.
+#include <type_traits>
+
 #include "kq_kv.cuh"
 #include "kq_launch.cuh"
 
@@ -22,6 +25,7 @@ struct KvRows {
     int64_t ldk, ldv;
     const int32_t *cu;  // [B + 1] or NULL
     int64_t T;
+    bool by_row;        // sequence b's share of the grid starts at cu[b]
 };
 struct KvTurn {
     const int32_t *pos;
@@ -38,17 +42,18 @@ struct KvPart {
 // All threads of the block call it; false where there is nothing to do.
 __device__ __forceinline__ bool kv_part(const KvCache &c, const KvRows &r, int64_t unit, KvPart &p) {
     // the last sequence whose share starts at or before the unit; shares start in rising order
+    auto start = [&](int64_t row, int64_t i) { return r.by_row ? row : (row >> c.lp) + 2 * i; };
     int64_t b = -1;
     for (int64_t b0 = 0; b0 < c.B; b0 += kKvThreads) {
         const int64_t i = b0 + threadIdx.x;
-        const int n = __syncthreads_count(i < c.B && (kv_row(r.cu, i, c.B, r.T) >> c.lp) + 2 * i <= unit);
+        const int n = __syncthreads_count(i < c.B && start(kv_row(r.cu, i, c.B, r.T), i) <= unit);
         b += n;
         if (n < kKvThreads) break;
     }
     if (b < 0) return false;
     const int64_t r0 = kv_row(r.cu, b, c.B, r.T), r1 = kv_row(r.cu, b + 1, c.B, r.T), len = c.lens[b], n = r1 - r0;
     const int64_t first = len - n, begin = first > 0 ? first : 0;  // positions of the rows; those before 0 have no place
-    const int64_t i = (begin >> c.lp) + (unit - (r0 >> c.lp) - 2 * b);
+    const int64_t i = (begin >> c.lp) + (unit - start(r0, b));
     const int64_t lo = max(begin, i << c.lp), hi = min(len, (i + 1) << c.lp);
     if (n <= 0 || lo >= hi || i >= c.ldt) return false;
     p.page = c.table[b * c.ldt + i];
@@ -83,14 +88,16 @@ __device__ __forceinline__ uint32_t kv_pack(int a, int b, int c, int d) {
 
 // Vector pair j of a row covers [lo, lo + W) and [hi, hi + W): first the rotated pairs (both partners in one
 // thread), then the rest of the head.  W is 4, or 1 where rows or halves do not lie on four elements.
-template <typename TX, bool PAIRS, int W>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(KvCache c, KvRows r, KvTurn turn) {
+// G: threads of a group.
+template <typename TX, bool PAIRS, int W, int G>
+__global__ void __launch_bounds__(kKvThreads, 3) kv_append_kernel(KvCache c, KvRows r, KvTurn turn) {
     __shared__ float red[kKvThreads / 32];
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
-    const int tid = threadIdx.x, which = blockIdx.y >= c.n_kv, head = blockIdx.y - (which ? c.n_kv : 0);
+    const int tid = threadIdx.x % G, which_head = blockIdx.y * (kKvThreads / G) + threadIdx.x / G;
     KvPart p;
-    if (!kv_part(c, r, blockIdx.x, p)) return;
+    if (!kv_part(c, r, blockIdx.x, p) || which_head >= 2 * c.n_kv) return;
+    const int which = which_head >= c.n_kv, head = which_head - (which ? c.n_kv : 0);
     const int64_t block = p.page * c.n_kv + head;
     float *scale = (which ? c.v_scale : c.k_scale) + block;
     int8_t *codes = (which ? c.v : c.k) + (block << c.lp) * c.D;
@@ -100,37 +107,46 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(KvCache c, KvRows
     const int rot = which ? 0 : turn.rot, half = rot / 2, turned = half / W, np = c.D / (2 * W), items = (p.hi - p.lo) * np;
 
     auto places = [&](int item, int &t, int &lo, int &hi, int &j) {
-        t = item / np;
+        t = (unsigned)item / (unsigned)np;
         j = item - t * np;
         lo = PAIRS || j >= turned ? 2 * W * j : W * j;
         hi = PAIRS || j >= turned ? lo + W : lo + half;
+    };
+    // where an item's angles are; -1: it is not rotated; -2: its position has none (NaN, whose code is 0)
+    auto angles = [&](int item) -> int64_t {
+        int t, lo, hi, j;
+        places(item, t, lo, hi, j);
+        if (j >= turned) return -1;
+        const int64_t at = turn.pos[p.row + t];
+        return at >= 0 && at < turn.n_pos ? at * half + j * W : -2;
     };
     auto load = [&](int item, float (&u)[W], float (&w)[W]) {
         int t, lo, hi, j;
         places(item, t, lo, hi, j);
         kv_load<W>(x + t * ld + lo, u);
         kv_load<W>(x + t * ld + hi, w);
-        if (j >= turned) return;
-        const int64_t at = turn.pos[p.row + t];
-        const bool known = at >= 0 && at < turn.n_pos;  // else no angle: NaN, whose code is 0
+    };
+    auto rotate = [&](int64_t at, float (&u)[W], float (&w)[W]) {
+        if (at == -1) return;
+        const bool known = at >= 0;
         float cs[W], sn[W];
         if (known) {
-            kv_load<W>(turn.cos_tab + at * half + j * W, cs);
-            kv_load<W>(turn.sin_tab + at * half + j * W, sn);
+            kv_load<W>(turn.cos_tab + at, cs);
+            kv_load<W>(turn.sin_tab + at, sn);
         }
-        auto rotate = [&](float &a, float &b, float cv, float sv) {
+        auto pair = [&](float &a, float &b, float cv, float sv) {
             const float a0 = a, b0 = b;
             a = known ? __fsub_rn(__fmul_rn(a0, cv), __fmul_rn(b0, sv)) : nanf("");
             b = known ? __fadd_rn(__fmul_rn(b0, cv), __fmul_rn(a0, sv)) : nanf("");
         };
         if constexpr (PAIRS && W == 4) {
-            rotate(u[0], u[1], cs[0], sn[0]);
-            rotate(u[2], u[3], cs[1], sn[1]);
-            rotate(w[0], w[1], cs[2], sn[2]);
-            rotate(w[2], w[3], cs[3], sn[3]);
+            pair(u[0], u[1], cs[0], sn[0]);
+            pair(u[2], u[3], cs[1], sn[1]);
+            pair(w[0], w[1], cs[2], sn[2]);
+            pair(w[2], w[3], cs[3], sn[3]);
         } else {
 #pragma unroll
-            for (int i = 0; i < W; ++i) rotate(u[i], w[i], cs[i], sn[i]);
+            for (int i = 0; i < W; ++i) pair(u[i], w[i], cs[i], sn[i]);
         }
     };
 
@@ -139,31 +155,43 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(KvCache c, KvRows
 #pragma unroll
         for (int i = 0; i < W; ++i) amax = fmaxf(amax, fmaxf(fabsf(a[i]), fabsf(b[i])));  // (NaN never wins)
     };
+    // positions, rows and angles of all items that are kept are under way together
+    int64_t at[kKvHeld];
 #pragma unroll
     for (int k = 0; k < kKvHeld; ++k)
-        if (tid + k * kKvThreads < items) {
-            load(tid + k * kKvThreads, u[k], w[k]);
+        if (tid + k * G < items) at[k] = angles(tid + k * G);
+#pragma unroll
+    for (int k = 0; k < kKvHeld; ++k)
+        if (tid + k * G < items) load(tid + k * G, u[k], w[k]);
+#pragma unroll
+    for (int k = 0; k < kKvHeld; ++k)
+        if (tid + k * G < items) {
+            rotate(at[k], u[k], w[k]);
             widen(u[k], w[k]);
         }
-    for (int i = tid + kKvHeld * kKvThreads; i < items; i += kKvThreads) {
+    for (int i = tid + kKvHeld * G; i < items; i += G) {
         float a[W], b[W];
         load(i, a, b);
+        rotate(angles(i), a, b);
         widen(a, b);
     }
 #pragma unroll
     for (int s = 16; s; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, s));
-    if ((tid & 31) == 0) red[tid >> 5] = amax;
-    __syncthreads();
-    amax = red[0];
+    if (G > 32) {
+        if ((tid & 31) == 0) red[tid >> 5] = amax;
+        __syncthreads();
+        amax = red[0];
 #pragma unroll
-    for (int i = 1; i < kKvThreads / 32; ++i) amax = fmaxf(amax, red[i]);
+        for (int i = 1; i < kKvThreads / 32; ++i) amax = fmaxf(amax, red[i]);
+    }
 
     const float now = fmaxf(was, __fdiv_rn(amax, 127.0f));
     if (tid == 0) *scale = now;
     if (now > was && was > 0.0f) {
         const float f = __fdiv_rn(was, now);
         uint32_t *old = reinterpret_cast<uint32_t *>(codes);
-        for (int i = tid; i < p.lo * c.D / 4; i += kKvThreads) {
+#pragma unroll 4
+        for (int i = tid; i < p.lo * c.D / 4; i += G) {
             const uint32_t q = old[i];
             auto again = [&](int shift) { return kv_code((float)(int8_t)(q >> shift), f); };
             old[i] = kv_pack(again(0), again(8), again(16), again(24));
@@ -185,41 +213,46 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(KvCache c, KvRows
     };
 #pragma unroll
     for (int k = 0; k < kKvHeld; ++k)
-        if (tid + k * kKvThreads < items) store(tid + k * kKvThreads, u[k], w[k]);
-    for (int i = tid + kKvHeld * kKvThreads; i < items; i += kKvThreads) {
+        if (tid + k * G < items) store(tid + k * G, u[k], w[k]);
+    for (int i = tid + kKvHeld * G; i < items; i += G) {
         float a[W], b[W];
         load(i, a, b);
+        rotate(angles(i), a, b);
         store(i, a, b);
     }
 }
 
-// Sixteen codes a thread at a time.  VEC: rows that 16-byte stores fit.
-template <typename TY, bool VEC>
+// As many codes at a time as make 16 bytes of the rows' type.  VEC: rows that 16-byte stores fit.
+template <typename TY, bool VEC, int G>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(KvCache c, KvRows r) {
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
-    const int which = blockIdx.y >= c.n_kv, head = blockIdx.y - (which ? c.n_kv : 0);
+    const int tid = threadIdx.x % G, which_head = blockIdx.y * (kKvThreads / G) + threadIdx.x / G;
     KvPart p;
-    if (!kv_part(c, r, blockIdx.x, p)) return;
+    if (!kv_part(c, r, blockIdx.x, p) || which_head >= 2 * c.n_kv) return;
+    const int which = which_head >= c.n_kv, head = which_head - (which ? c.n_kv : 0);
     const int64_t block = p.page * c.n_kv + head;
     const float scale = (which ? c.v_scale : c.k_scale)[block];
     const int8_t *codes = (which ? c.v : c.k) + ((block << c.lp) + p.lo) * c.D;
     const int64_t ld = which ? r.ldv : r.ldk;
     TY *y = static_cast<TY *>(which ? r.v : r.k) + p.row * ld + head * c.D;
-    const int pieces = c.D / 16, items = (p.hi - p.lo) * pieces;
-    for (int i = threadIdx.x; i < items; i += kKvThreads) {
-        const int t = i / pieces, d = (i - t * pieces) * 16;
-        const uint4 q = *reinterpret_cast<const uint4 *>(codes + (int64_t)i * 16);
-        TY v[16];
+    constexpr int N = kVec<TY>;
+    using Codes = typename VecOf<N>::type;
+    const int pieces = c.D / N, items = (p.hi - p.lo) * pieces;
+#pragma unroll 4
+    for (int i = tid; i < items; i += G) {
+        const int t = (unsigned)i / (unsigned)pieces, d = (i - t * pieces) * N;
+        const Codes q = *reinterpret_cast<const Codes *>(codes + i * N);
+        uint4 u;
+        TY *v = reinterpret_cast<TY *>(&u);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = from_f32<TY>(__fmul_rn((float)reinterpret_cast<const int8_t *>(&q)[j], scale));
+        for (int j = 0; j < N; ++j) v[j] = from_f32<TY>(__fmul_rn((float)reinterpret_cast<const int8_t *>(&q)[j], scale));
         TY *dst = y + t * ld + d;
         if (VEC) {
-#pragma unroll
-            for (int j = 0; j < 16; j += kVec<TY>) *reinterpret_cast<uint4 *>(dst + j) = *reinterpret_cast<const uint4 *>(v + j);
+            *reinterpret_cast<uint4 *>(dst) = u;
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) dst[j] = v[j];
+            for (int j = 0; j < N; ++j) dst[j] = v[j];
         }
     }
 }
@@ -254,6 +287,9 @@ kq_status kv_check(const char *fn, const int8_t *k_cache, const int8_t *v_cache,
     return KQ_OK;
 }
 
+// Threads of a group: a warp for sequences of four rows or fewer on average.
+static int kv_group(const KvCache &c, int64_t T) { return T <= 4 * c.B ? 32 : kKvThreads; }
+
 // The packed rows of a call, and the grid over the blocks of the cache that they can touch.
 static kq_status kv_check_rows(const char *fn, kq_dtype t, const void *k, int64_t ldk, const void *v, int64_t ldv, const int32_t *cu,
                                int64_t T, const KvCache &c, KvRows &r, dim3 &grid) {
@@ -267,18 +303,31 @@ static kq_status kv_check_rows(const char *fn, kq_dtype t, const void *k, int64_
     const size_t e = value_bytes(t);
     if (!aligned(k, e) || !aligned(v, e) || !aligned(cu, 4))
         return fail(KQ_ERR_ALIGNMENT, "%s: a pointer is not aligned to its elements", fn);
-    const int64_t units = (T >> c.lp) + 2 * c.B;
+    const bool by_row = T <= (T >> c.lp) + 2 * c.B;
+    const int64_t units = by_row ? T : (T >> c.lp) + 2 * c.B;
     if (units > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: T=%lld is too large", fn, (long long)T);
-    r = {const_cast<void *>(k), const_cast<void *>(v), ldk, ldv, cu, T};
-    grid = dim3((unsigned)units, 2 * c.n_kv);
+    r = {const_cast<void *>(k), const_cast<void *>(v), ldk, ldv, cu, T, by_row};
+    grid = dim3((unsigned)units, (unsigned)((2 * c.n_kv * kv_group(c, T) + kKvThreads - 1) / kKvThreads));
     return KQ_OK;
 }
 
 template <typename TX>
 static cudaError_t launch_append(const KvCache &c, const KvRows &r, const KvTurn &t, bool pairs, bool vec, dim3 grid, cudaStream_t st) {
-    auto kern = vec ? (pairs ? kv_append_kernel<TX, true, 4> : kv_append_kernel<TX, false, 4>)
-                    : (pairs ? kv_append_kernel<TX, true, 1> : kv_append_kernel<TX, false, 1>);
-    return launch_beside(kern, grid, dim3(kKvThreads), 0, dim3(1), st, c, r, t);
+    auto go = [&](auto group) {
+        constexpr int G = decltype(group)::value;
+        auto kern = vec ? (pairs ? kv_append_kernel<TX, true, 4, G> : kv_append_kernel<TX, false, 4, G>)
+                        : (pairs ? kv_append_kernel<TX, true, 1, G> : kv_append_kernel<TX, false, 1, G>);
+        return launch_beside(kern, grid, dim3(kKvThreads), 0, dim3(1), st, c, r, t);
+    };
+    return kv_group(c, r.T) == 32 ? go(std::integral_constant<int, 32>{}) : go(std::integral_constant<int, kKvThreads>{});
+}
+template <typename TY>
+static cudaError_t launch_read(const KvCache &c, const KvRows &r, bool vec, dim3 grid, cudaStream_t st) {
+    auto go = [&](auto group) {
+        constexpr int G = decltype(group)::value;
+        return launch_beside(vec ? kv_read_kernel<TY, true, G> : kv_read_kernel<TY, false, G>, grid, dim3(kKvThreads), 0, dim3(1), st, c, r);
+    };
+    return kv_group(c, r.T) == 32 ? go(std::integral_constant<int, 32>{}) : go(std::integral_constant<int, kKvThreads>{});
 }
 
 }  // namespace kq
@@ -332,8 +381,7 @@ kq_status kq_kv_read_i8(const int8_t *k_cache, const int8_t *v_cache, const floa
     const int64_t e16 = 16 / (int64_t)value_bytes(yt);
     const bool vec = aligned(k_out, 16) && aligned(v_out, 16) && ldk % e16 == 0 && ldv % e16 == 0;
     return with_type(yt, [&](auto t) {
-        auto kern = vec ? kv_read_kernel<decltype(t), true> : kv_read_kernel<decltype(t), false>;
-        const cudaError_t e = launch_beside(kern, grid, dim3(kKvThreads), 0, dim3(1), (cudaStream_t)stream, c, r);
+        const cudaError_t e = launch_read<decltype(t)>(c, r, vec, grid, (cudaStream_t)stream);
         if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
         count_launch(R_KV);
         return KQ_OK;
