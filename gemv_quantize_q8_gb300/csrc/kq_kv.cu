@@ -3,8 +3,7 @@
 // A block of the cache (a page and head) has one scale, so its largest magnitude has to be known before its
 // first code is written, and when a later token raises it the codes that are there follow:
 //   s' = max(s, max |x| / 127),   q' = rint(q * (s / s')) for the old tokens,   q = rint(x * (1 / s')) for the new.
-// A group of threads takes one block of the cache that the call touches (all 256 of a thread block, or a warp where the
-// sequences have few rows): it keeps the new rows in registers between the maximum and the codes, so every row is
+// A group of threads takes one block of the cache that the call touches (four warps, or one where the sequences have few rows): it keeps the new rows in registers between the maximum and the codes, so every row is
 // read once and every code written once.  Which blocks those are follows from cu and lens on the device: a run of n
 // tokens touches at most floor(n / page) + 2 pages, and at most n; so sequence b's share of the grid starts at
 // floor(cu[b] / page) + 2b, or at cu[b], whichever makes the smaller grid.
@@ -18,6 +17,7 @@
 namespace kq {
 
 constexpr int kKvThreads = 256;
+constexpr int kKvGroup = 256;  // threads of a block of the cache (8192 tokens, 8 heads of 128: 34.0 us with the read, 43 with 128 that hold twice as much)
 constexpr int kKvHeld = 4;  // vector pairs of a thread that stay in registers: 64 tokens of 128
 
 struct KvRows {
@@ -34,34 +34,52 @@ struct KvTurn {
     int rot;
 };
 
+__device__ __forceinline__ int64_t kv_start(const KvRows &r, const KvCache &c, int64_t row, int64_t b) {
+    return r.by_row ? row : (row >> c.lp) + 2 * b;
+}
+
 // A thread block's part of the cache: tokens [lo, hi) of a page from row `row` on.
 struct KvPart {
     int64_t page, row;
-    int lo, hi;
+    int lo, hi;  // none: lo = hi
 };
-// All threads of the block call it; false where there is nothing to do.
+// All threads of the block call it; false where there is nothing to do.  (One warp finds it out for all: the block's
+// instructions count.)
+__device__ __forceinline__ KvPart kv_find(const KvCache &c, const KvRows &r, int64_t unit, int64_t b);
 __device__ __forceinline__ bool kv_part(const KvCache &c, const KvRows &r, int64_t unit, KvPart &p) {
+    __shared__ KvPart shared;
     // the last sequence whose share starts at or before the unit; shares start in rising order
-    auto start = [&](int64_t row, int64_t i) { return r.by_row ? row : (row >> c.lp) + 2 * i; };
     int64_t b = -1;
     for (int64_t b0 = 0; b0 < c.B; b0 += kKvThreads) {
         const int64_t i = b0 + threadIdx.x;
-        const int n = __syncthreads_count(i < c.B && start(kv_row(r.cu, i, c.B, r.T), i) <= unit);
+        const int n = __syncthreads_count(i < c.B && kv_start(r, c, kv_row(r.cu, i, c.B, r.T), i) <= unit);
         b += n;
         if (n < kKvThreads) break;
     }
-    if (b < 0) return false;
+    if (threadIdx.x == 0) shared = kv_find(c, r, unit, b);
+    __syncthreads();
+    p = shared;
+    return p.lo < p.hi;
+}
+__device__ __forceinline__ KvPart kv_find(const KvCache &c, const KvRows &r, int64_t unit, int64_t b) {
+    KvPart p = {0, 0, 0, 0};
+    if (b < 0) return p;
     const int64_t r0 = kv_row(r.cu, b, c.B, r.T), r1 = kv_row(r.cu, b + 1, c.B, r.T), len = c.lens[b], n = r1 - r0;
     const int64_t first = len - n, begin = first > 0 ? first : 0;  // positions of the rows; those before 0 have no place
-    const int64_t i = (begin >> c.lp) + (unit - start(r0, b));
+    const int64_t i = (begin >> c.lp) + (unit - kv_start(r, c, r0, b));
     const int64_t lo = max(begin, i << c.lp), hi = min(len, (i + 1) << c.lp);
-    if (n <= 0 || lo >= hi || i >= c.ldt) return false;
+    if (n <= 0 || lo >= hi || i >= c.ldt) return p;
     p.page = c.table[b * c.ldt + i];
-    if (p.page < 0 || p.page >= c.n_pages) return false;
+    if (p.page < 0 || p.page >= c.n_pages) return p;
     p.row = r0 + (lo - first);
     p.lo = (int)(lo - (i << c.lp));
     p.hi = (int)(hi - (i << c.lp));
-    return true;
+    return p;
+}
+// The threads of a group meet.
+template <int G>
+__device__ __forceinline__ void kv_sync() {
+    if (G > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / G), "n"(G) : "memory");
 }
 
 // W elements as fp32; the address is aligned to all of them.
@@ -71,16 +89,27 @@ __device__ __forceinline__ void kv_load(const T *p, float (&v)[W]) {
         v[0] = to_f32(*p);
     } else {
         using Vec = typename VecOf<W * (int)sizeof(T)>::type;
-        const Vec u = *reinterpret_cast<const Vec *>(p);
+        const Vec u = __ldcs(reinterpret_cast<const Vec *>(p));
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] = to_f32(reinterpret_cast<const T *>(&u)[i]);
     }
 }
 
-// Codes of a row's elements: NaN gives 0, and what rounding carries past 127 stays there.
+// A code (|x * inv| is at most 127 and a few units of rounding, or NaN, which gives 0).
 __device__ __forceinline__ int kv_code(float x, float inv) {
     const float v = __fmul_rn(x, inv);
-    return isnan(v) ? 0 : __float2int_rn(fminf(fmaxf(v, -127.0f), 127.0f));
+    return isnan(v) ? 0 : __float2int_rn(v);
+}
+// The same without NaN, in the lowest byte: 1.5 * 2^23 leaves the nearest even whole number in the last bits.  (Conversions
+// go at a quarter of this rate.)
+__device__ __forceinline__ uint32_t kv_byte(float x, float inv) { return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.0f)); }
+__device__ __forceinline__ uint32_t kv_join(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+__device__ __forceinline__ float kv_max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
 }
 __device__ __forceinline__ uint32_t kv_pack(int a, int b, int c, int d) {
     return (a & 255) | (b & 255) << 8 | (c & 255) << 16 | (uint32_t)d << 24;
@@ -106,84 +135,129 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv_append_kernel(KvCache c, KvR
     const float was = p.lo ? *scale : 0.0f;  // a page's first token starts it anew
     const int rot = which ? 0 : turn.rot, half = rot / 2, turned = half / W, np = c.D / (2 * W), items = (p.hi - p.lo) * np;
 
-    auto places = [&](int item, int &t, int &lo, int &hi, int &j) {
-        t = (unsigned)item / (unsigned)np;
-        j = item - t * np;
-        lo = PAIRS || j >= turned ? 2 * W * j : W * j;
-        hi = PAIRS || j >= turned ? lo + W : lo + half;
+    // this thread's items are tid, tid + G, ..: token t and pair j of it, stepped without divisions
+    const int t0 = (unsigned)tid / (unsigned)np, j0 = tid - t0 * np, dt = G / np, dj = G - dt * np;
+    struct Place {
+        int t, j, left;
     };
-    // where an item's angles are; -1: it is not rotated; -2: its position has none (NaN, whose code is 0)
-    auto angles = [&](int item) -> int64_t {
-        int t, lo, hi, j;
-        places(item, t, lo, hi, j);
-        if (j >= turned) return -1;
-        const int64_t at = turn.pos[p.row + t];
-        return at >= 0 && at < turn.n_pos ? at * half + j * W : -2;
+    auto first = [&](int skip) {
+        const int i = tid + skip * G;
+        if (!skip) return Place{t0, j0, items - i};
+        if (items <= skip * G) return Place{0, 0, 0};
+        const int t = (unsigned)i / (unsigned)np;
+        return Place{t, i - t * np, items - i};
     };
-    auto load = [&](int item, float (&u)[W], float (&w)[W]) {
-        int t, lo, hi, j;
-        places(item, t, lo, hi, j);
-        kv_load<W>(x + t * ld + lo, u);
-        kv_load<W>(x + t * ld + hi, w);
+    auto next = [&](Place &a) {
+        a.t += dt;
+        a.j += dj;
+        if (a.j >= np) a.j -= np, ++a.t;
+        a.left -= G;
     };
-    auto rotate = [&](int64_t at, float (&u)[W], float (&w)[W]) {
-        if (at == -1) return;
-        const bool known = at >= 0;
-        float cs[W], sn[W];
-        if (known) {
-            kv_load<W>(turn.cos_tab + at, cs);
-            kv_load<W>(turn.sin_tab + at, sn);
+    auto low = [&](const Place &a) { return PAIRS || a.j >= turned ? 2 * W * a.j : W * a.j; };
+    auto high = [&](const Place &a, int lo) { return PAIRS || a.j >= turned ? lo + W : lo + half; };
+    // an item's position; -1: it has no angle (NaN, whose code is 0).  Items that are not rotated need none.
+    auto position = [&](const Place &a) {
+        const int at = a.j < turned ? turn.pos[p.row + a.t] : 0;
+        return at < turn.n_pos ? at : -1;
+    };
+    auto load = [&](const Place &a, float (&u)[W], float (&w)[W]) {
+        const TX *row = x + a.t * ld;
+        const int lo = low(a);
+        kv_load<W>(row + lo, u);
+        kv_load<W>(row + high(a, lo), w);
+    };
+    struct Angle {
+        float c[W], s[W];
+    };
+    auto angle = [&](const Place &a, int at, Angle &g) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) g.c[i] = g.s[i] = nanf("");
+        if (a.j < turned && at >= 0) {
+            const int64_t i = (int64_t)at * half + a.j * W;
+            kv_load<W>(turn.cos_tab + i, g.c);
+            kv_load<W>(turn.sin_tab + i, g.s);
         }
+    };
+    auto rotate = [&](const Place &place, const Angle &g, float (&u)[W], float (&w)[W]) {
+        if (place.j >= turned) return;
         auto pair = [&](float &a, float &b, float cv, float sv) {
             const float a0 = a, b0 = b;
-            a = known ? __fsub_rn(__fmul_rn(a0, cv), __fmul_rn(b0, sv)) : nanf("");
-            b = known ? __fadd_rn(__fmul_rn(b0, cv), __fmul_rn(a0, sv)) : nanf("");
+            a = __fsub_rn(__fmul_rn(a0, cv), __fmul_rn(b0, sv));
+            b = __fadd_rn(__fmul_rn(b0, cv), __fmul_rn(a0, sv));
         };
         if constexpr (PAIRS && W == 4) {
-            pair(u[0], u[1], cs[0], sn[0]);
-            pair(u[2], u[3], cs[1], sn[1]);
-            pair(w[0], w[1], cs[2], sn[2]);
-            pair(w[2], w[3], cs[3], sn[3]);
+            pair(u[0], u[1], g.c[0], g.s[0]);
+            pair(u[2], u[3], g.c[1], g.s[1]);
+            pair(w[0], w[1], g.c[2], g.s[2]);
+            pair(w[2], w[3], g.c[3], g.s[3]);
         } else {
 #pragma unroll
-            for (int i = 0; i < W; ++i) pair(u[i], w[i], cs[i], sn[i]);
+            for (int i = 0; i < W; ++i) pair(u[i], w[i], g.c[i], g.s[i]);
         }
     };
-
-    float u[kKvHeld][W], w[kKvHeld][W], amax = 0.0f;
-    auto widen = [&](const float (&a)[W], const float (&b)[W]) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) amax = fmaxf(amax, fmaxf(fabsf(a[i]), fabsf(b[i])));  // (NaN never wins)
+    auto turned_item = [&](const Place &a, float (&v)[W], float (&z)[W]) {
+        Angle g;
+        load(a, v, z);
+        angle(a, position(a), g);
+        rotate(a, g, v, z);
     };
-    // positions, rows and angles of all items that are kept are under way together
-    int64_t at[kKvHeld];
+    // all positions, then rows and angles of four items at once: one by one the angles' loads took as long as all the rest
+    float u[kKvHeld][W], w[kKvHeld][W];
+    {
+        int at[kKvHeld];
+        Place a = first(0);
 #pragma unroll
-    for (int k = 0; k < kKvHeld; ++k)
-        if (tid + k * G < items) at[k] = angles(tid + k * G);
+        for (int k = 0; k < kKvHeld; ++k, next(a))
+            if (a.left > 0) at[k] = position(a);
+        a = first(0);
 #pragma unroll
-    for (int k = 0; k < kKvHeld; ++k)
-        if (tid + k * G < items) load(tid + k * G, u[k], w[k]);
+        for (int k0 = 0; k0 < kKvHeld; k0 += 4) {
+            Angle g[4];
+            Place four = a;
 #pragma unroll
-    for (int k = 0; k < kKvHeld; ++k)
-        if (tid + k * G < items) {
-            rotate(at[k], u[k], w[k]);
-            widen(u[k], w[k]);
+            for (int k = k0; k < k0 + 4; ++k, next(a)) {
+                if (a.left > 0) {
+                    load(a, u[k], w[k]);
+                    angle(a, at[k], g[k - k0]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < W; ++i) u[k][i] = w[k][i] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int k = k0; k < k0 + 4; ++k, next(four))
+                if (four.left > 0) rotate(four, g[k - k0], u[k], w[k]);
         }
-    for (int i = tid + kKvHeld * G; i < items; i += G) {
-        float a[W], b[W];
-        load(i, a, b);
-        rotate(angles(i), a, b);
-        widen(a, b);
     }
+    // the largest magnitude; NaN wins here (one instruction an element either way), and is looked after when it did
+    auto largest = [&](auto max2) {
+        float amax = 0.0f;
 #pragma unroll
-    for (int s = 16; s; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, s));
-    if (G > 32) {
-        if ((tid & 31) == 0) red[tid >> 5] = amax;
-        __syncthreads();
-        amax = red[0];
+        for (int k = 0; k < kKvHeld; ++k)
 #pragma unroll
-        for (int i = 1; i < kKvThreads / 32; ++i) amax = fmaxf(amax, red[i]);
-    }
+            for (int i = 0; i < W; ++i) amax = max2(max2(amax, fabsf(u[k][i])), fabsf(w[k][i]));
+        for (Place a = first(kKvHeld); a.left > 0; next(a)) {
+            float v[W], z[W];
+            turned_item(a, v, z);
+#pragma unroll
+            for (int i = 0; i < W; ++i) amax = max2(max2(amax, fabsf(v[i])), fabsf(z[i]));
+        }
+#pragma unroll
+        for (int s = 16; s; s >>= 1) amax = max2(amax, __shfl_xor_sync(~0u, amax, s));
+        if (G > 32) {
+            const int w0 = threadIdx.x / G * (G / 32);
+            kv_sync<G>();
+            if ((tid & 31) == 0) red[w0 + (tid >> 5)] = amax;
+            kv_sync<G>();
+            amax = red[w0];
+#pragma unroll
+            for (int i = 1; i < G / 32; ++i) amax = max2(amax, red[w0 + i]);
+        }
+        return amax;
+    };
+    float amax = largest([](float a, float b) { return kv_max_nan(a, b); });
+    const bool nans = isnan(amax);
+    if (nans) amax = largest([](float a, float b) { return fmaxf(a, b); });
 
     const float now = fmaxf(was, __fdiv_rn(amax, 127.0f));
     if (tid == 0) *scale = now;
@@ -193,33 +267,40 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv_append_kernel(KvCache c, KvR
 #pragma unroll 4
         for (int i = tid; i < p.lo * c.D / 4; i += G) {
             const uint32_t q = old[i];
-            auto again = [&](int shift) { return kv_code((float)(int8_t)(q >> shift), f); };
-            old[i] = kv_pack(again(0), again(8), again(16), again(24));
+            auto again = [&](int shift) { return kv_byte((float)(int8_t)(q >> shift), f); };
+            old[i] = kv_join(again(0), again(8), again(16), again(24));
         }
     }
     float inv = __fdiv_rn(1.0f, now);
     if (isinf(inv)) inv = 0.0f;  // a block of zeros, or below 2^-128
-    auto store = [&](int item, const float (&a)[W], const float (&b)[W]) {
-        int t, lo, hi, j;
-        places(item, t, lo, hi, j);
-        int8_t *row = codes + (p.lo + t) * c.D;
+    auto store = [&](const Place &a, const float (&v)[W], const float (&z)[W], bool careful) {
+        const int lo = low(a);
+        int8_t *row = codes + (p.lo + a.t) * c.D;
         if constexpr (W == 4) {
-            *reinterpret_cast<uint32_t *>(row + lo) = kv_pack(kv_code(a[0], inv), kv_code(a[1], inv), kv_code(a[2], inv), kv_code(a[3], inv));
-            *reinterpret_cast<uint32_t *>(row + hi) = kv_pack(kv_code(b[0], inv), kv_code(b[1], inv), kv_code(b[2], inv), kv_code(b[3], inv));
+            auto word = [&](const float (&f)[W]) {
+                return careful ? kv_pack(kv_code(f[0], inv), kv_code(f[1], inv), kv_code(f[2], inv), kv_code(f[3], inv))
+                               : kv_join(kv_byte(f[0], inv), kv_byte(f[1], inv), kv_byte(f[2], inv), kv_byte(f[3], inv));
+            };
+            *reinterpret_cast<uint32_t *>(row + lo) = word(v);
+            *reinterpret_cast<uint32_t *>(row + high(a, lo)) = word(z);
         } else {
-            row[lo] = (int8_t)kv_code(a[0], inv);
-            row[hi] = (int8_t)kv_code(b[0], inv);
+            row[lo] = (int8_t)kv_code(v[0], inv);
+            row[high(a, lo)] = (int8_t)kv_code(z[0], inv);
         }
     };
+    auto finish = [&](bool careful) {
+        Place a = first(0);
 #pragma unroll
-    for (int k = 0; k < kKvHeld; ++k)
-        if (tid + k * G < items) store(tid + k * G, u[k], w[k]);
-    for (int i = tid + kKvHeld * G; i < items; i += G) {
-        float a[W], b[W];
-        load(i, a, b);
-        rotate(angles(i), a, b);
-        store(i, a, b);
-    }
+        for (int k = 0; k < kKvHeld; ++k, next(a))
+            if (a.left > 0) store(a, u[k], w[k], careful);
+        for (a = first(kKvHeld); a.left > 0; next(a)) {
+            float v[W], z[W];
+            turned_item(a, v, z);
+            store(a, v, z, careful);
+        }
+    };
+    if (nans || isinf(now)) finish(true);  // (an infinity times 1/infinity is NaN, too)
+    else finish(false);
 }
 
 // As many codes at a time as make 16 bytes of the rows' type.  VEC: rows that 16-byte stores fit.
@@ -238,21 +319,29 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(KvCache c, KvRows r
     TY *y = static_cast<TY *>(which ? r.v : r.k) + p.row * ld + head * c.D;
     constexpr int N = kVec<TY>;
     using Codes = typename VecOf<N>::type;
-    const int pieces = c.D / N, items = (p.hi - p.lo) * pieces;
+    const int pieces = c.D / N, items = (p.hi - p.lo) * pieces, dt = G / pieces, dj = G - dt * pieces;
+    int t = (unsigned)tid / (unsigned)pieces, j = tid - t * pieces;
 #pragma unroll 4
     for (int i = tid; i < items; i += G) {
-        const int t = (unsigned)i / (unsigned)pieces, d = (i - t * pieces) * N;
         const Codes q = *reinterpret_cast<const Codes *>(codes + i * N);
+        TY *dst = y + t * ld + j * N;
+        t += dt;
+        j += dj;
+        if (j >= pieces) j -= pieces, ++t;
         uint4 u;
         TY *v = reinterpret_cast<TY *>(&u);
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = from_f32<TY>(__fmul_rn((float)reinterpret_cast<const int8_t *>(&q)[j], scale));
-        TY *dst = y + t * ld + d;
+        for (int x = 0; x < N; ++x) {
+            // the byte with its sign bit turned under the exponent of 2^23 is 2^23 + 128 + code
+            const uint32_t word = reinterpret_cast<const uint32_t *>(&q)[x / 4] ^ 0x80808080u;
+            const float code = __uint_as_float(__byte_perm(word, 0x4b000000u, 0x7440 | x % 4)) - 8388736.0f;
+            v[x] = from_f32<TY>(__fmul_rn(code, scale));
+        }
         if (VEC) {
             *reinterpret_cast<uint4 *>(dst) = u;
         } else {
 #pragma unroll
-            for (int j = 0; j < N; ++j) dst[j] = v[j];
+            for (int x = 0; x < N; ++x) dst[x] = v[x];
         }
     }
 }
@@ -288,7 +377,7 @@ kq_status kv_check(const char *fn, const int8_t *k_cache, const int8_t *v_cache,
 }
 
 // Threads of a group: a warp for sequences of four rows or fewer on average.
-static int kv_group(const KvCache &c, int64_t T) { return T <= 4 * c.B ? 32 : kKvThreads; }
+static int kv_group(const KvCache &c, int64_t T) { return T <= 4 * c.B ? 32 : kKvGroup; }
 
 // The packed rows of a call, and the grid over the blocks of the cache that they can touch.
 static kq_status kv_check_rows(const char *fn, kq_dtype t, const void *k, int64_t ldk, const void *v, int64_t ldv, const int32_t *cu,
@@ -319,7 +408,7 @@ static cudaError_t launch_append(const KvCache &c, const KvRows &r, const KvTurn
                         : (pairs ? kv_append_kernel<TX, true, 1, G> : kv_append_kernel<TX, false, 1, G>);
         return launch_beside(kern, grid, dim3(kKvThreads), 0, dim3(1), st, c, r, t);
     };
-    return kv_group(c, r.T) == 32 ? go(std::integral_constant<int, 32>{}) : go(std::integral_constant<int, kKvThreads>{});
+    return kv_group(c, r.T) == 32 ? go(std::integral_constant<int, 32>{}) : go(std::integral_constant<int, kKvGroup>{});
 }
 template <typename TY>
 static cudaError_t launch_read(const KvCache &c, const KvRows &r, bool vec, dim3 grid, cudaStream_t st) {
@@ -327,7 +416,7 @@ static cudaError_t launch_read(const KvCache &c, const KvRows &r, bool vec, dim3
         constexpr int G = decltype(group)::value;
         return launch_beside(vec ? kv_read_kernel<TY, true, G> : kv_read_kernel<TY, false, G>, grid, dim3(kKvThreads), 0, dim3(1), st, c, r);
     };
-    return kv_group(c, r.T) == 32 ? go(std::integral_constant<int, 32>{}) : go(std::integral_constant<int, kKvThreads>{});
+    return kv_group(c, r.T) == 32 ? go(std::integral_constant<int, 32>{}) : go(std::integral_constant<int, kKvGroup>{});
 }
 
 }  // namespace kq
