@@ -127,11 +127,11 @@ __device__ __forceinline__ bool pt_work(const PaParams &P, int64_t pair, PtWork 
     int lowest = 0x7fffffff;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int64_t tt = (r + i) / P.G;
-        w.head[i] = (int)(r + i - tt * P.G);
+        const unsigned tt = (unsigned)(r + i) / (unsigned)P.G;  // (row tiles of a call are below 2^31)
+        w.head[i] = (int)(r + i - (int64_t)tt * P.G);
         w.first[i] = (int)(tt * PT);
         w.tiles[i] = w.lowest[i] = 0;
-        if (tt * PT >= n_q) continue;
+        if ((int64_t)tt * PT >= n_q) continue;
         w.lowest[i] = pa_limit(P, t, w.first[i]);
         w.tiles[i] = (pa_limit(P, t, min(w.first[i] + PT, t.n_q) - 1) + PT - 1) / PT;
         w.n = max(w.n, w.tiles[i]);
@@ -170,20 +170,26 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         fence_mbar_init();
     }
     if (warp == 9 && lane == 0) { prefetch_tmap(&tmQ); prefetch_tmap(&tmK); prefetch_tmap(&tmV); }
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (blockIdx.x == 0 && tid == 0) *P.err = 0ull;  // (an error is counted two seconds later at the earliest)
-    // the longest first: later tokens see more keys
-    const int kv_head = blockIdx.x % X.n_kv;
-    PtWork w;
-    if (!pt_work(P, X.pairs - 1 - blockIdx.x / X.n_kv, w)) return;
+    // (tensor memory while the block finds its work: no other block that holds some fits beside this one)
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_holder)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (blockIdx.x == 0 && tid == 0) *P.err = 0ull;  // (an error is counted two seconds later at the earliest)
+    // the longest first: later tokens see more keys
+    const unsigned turn = blockIdx.x / (unsigned)X.n_kv;
+    const int kv_head = blockIdx.x - turn * X.n_kv;
+    PtWork w;
+    const bool found = pt_work(P, X.pairs - 1 - turn, w);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (!found) {
+        if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*tmem_holder) : "memory");
+        return;
+    }
     // all 512 columns are this kernel's, so the allocation starts at column 0 of lane 0
 
     if (warp >= 8) {
@@ -207,6 +213,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 if (one) {
 #pragma unroll
                     for (int k = 0; k < C::DP / 16; ++k) {
+                        if (k * 16 >= P.D) break;
                         const uint64_t off = (uint64_t)((k / 4) * (C::BOX >> 4) + (k % 4) * 2);
                         mma_f16(q * 128, dQ + q * (C::TILE >> 4) + off, dK + s * (C::TILE >> 4) + off, id_s, k > 0);
                     }
@@ -437,9 +444,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     }
                 }
             }
-            const bool live = of(w.first, q) < w.t.n_q && token < w.t.n_q;
+            // the rows through shared memory (the row tile's queries are through), so that the warp's stores are whole rows:
+            // a row a thread they took 2 us
             const float inv = 1.0f / l;
-            T *y = static_cast<T *>(P.y) + (w.t.q_row + token) * P.ldy + (int64_t)(kv_head * P.G + of(w.head, q)) * P.D;
+            uint8_t *rows = sm + q * C::TILE + (warp & 3) * 32 * (C::DP * 2);
+            constexpr int PIECES = C::DP / 8;  // of 16 bytes; piece p of row r at p ^ (r % 8)
 #pragma unroll
             for (int c = 0; c < C::DP; c += 32) {
                 float o[32];
@@ -460,9 +469,18 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     uint32_t *e = reinterpret_cast<uint32_t *>(&u);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) e[x] = limit ? pt_pack<T>(o[k + 2 * x] * inv, o[k + 2 * x + 1] * inv) : 0u;
-                    if (live && c + k < P.D) *reinterpret_cast<uint4 *>(y + c + k) = u;
+                    *reinterpret_cast<uint4 *>(rows + lane * (C::DP * 2) + (((c + k) / 8 ^ (lane & 7)) << 4)) = u;
                 }
             }
+            __syncwarp();
+            const int left = w.t.n_q - of(w.first, q) - (warp & 3) * 32, pieces = P.D / 8;  // rows of this warp
+            T *y = static_cast<T *>(P.y) + (w.t.q_row + of(w.first, q) + (warp & 3) * 32) * P.ldy + (int64_t)(kv_head * P.G + of(w.head, q)) * P.D;
+            const int piece = lane % PIECES;
+#pragma unroll 4
+            for (int r = lane / PIECES; r < 32; r += 32 / PIECES)
+                if (r < left && piece < pieces)
+                    *reinterpret_cast<uint4 *>(y + r * P.ldy + piece * 8) =
+                        *reinterpret_cast<const uint4 *>(rows + r * (C::DP * 2) + ((piece ^ (r & 7)) << 4));
         }
     }
     if (tid == 0 && *abort_flag) atomicAdd(P.err, 1ull);
