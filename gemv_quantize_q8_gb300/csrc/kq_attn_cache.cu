@@ -581,17 +581,8 @@ struct AcFetch {
         page[0] = table[t0 >> P.c.lp];
         if (P.c.lp == 4) page[1] = t0 + 16 < len ? table[(t0 + 16) >> P.c.lp] : 0;  // (a page of 16 holds half a unit)
     }
-    // The item's query rows, soon to be read, into the first-level cache.
-    __device__ __forceinline__ void announce(const AcParams &P, int MT) {
-        const int size = P.xt == KQ_F32 ? 4 : 2;
-        for (int row = it.tile * MT; row < min(P.rows, it.tile * MT + MT); ++row) {
-            const int token = row / P.G, head = it.h * P.G + row - token * P.G;
-            const char *x = static_cast<const char *>(P.q) + ((it.b * P.n_new + token) * P.ldq + (int64_t)head * P.c.D) * size;
-            for (int i = 0; i < P.c.D * size; i += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(x + i));
-        }
-    }
     __device__ __forceinline__ void send(const AcParams &P, const CUtensorMap *tmK, const CUtensorMap *tmV, uint8_t *stage, float4 *scales,
-                                         uint64_t *bar, int MT) {
+                                         uint64_t *bar) {
         using Ring = AcRing<DP>;
         const int t0 = at * kAcUnit, row = (it.h << P.c.lp) + (t0 & ((1 << P.c.lp) - 1));
         const bool small = P.c.lp == 4;
@@ -627,7 +618,6 @@ struct AcFetch {
             ac_next(P, it);
             at = 0;
             if (it.b != b) start(P);
-            announce(P, MT);
         }
         look(P);
     }
@@ -644,7 +634,6 @@ __global__ void __launch_bounds__(NW * 64, 1)
     __shared__ AcItem items[NW][2];
     __shared__ float4 scales[NW][NS];
     __shared__ uint64_t full[NW][NS], empty[NW][NS];
-    __shared__ float weight[2 * NW][MT], sum[MT];
     __shared__ int aborted;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = P.c.D;
     constexpr int size = kAcPart<DP, MT>;
@@ -714,7 +703,7 @@ __global__ void __launch_bounds__(NW * 64, 1)
                     *(volatile int *)&aborted = 1;
                     break;
                 }
-                f.send(P, &tmK, &tmV, rings + (mate * NS + stage) * Ring::BYTES, &scales[mate][stage], &full[mate][stage], MT);
+                f.send(P, &tmK, &tmV, rings + (mate * NS + stage) * Ring::BYTES, &scales[mate][stage], &full[mate][stage]);
                 if (++stage == NS) stage = 0, phase ^= 1;
             }
         }
@@ -751,57 +740,60 @@ __global__ void __launch_bounds__(NW * 64, 1)
             if (u < u1) ac_next(P, it);
         }
         }
-    }
-    __syncthreads();
-    if (aborted) {
-        // copies may be under way still: far more time than they need
-        const uint64_t t0 = sm100::globaltimer_ns();
-        while (sm100::globaltimer_ns() - t0 < 10000000ull) {}
-        if (tid == 0) atomicAdd(P.err, 1ull);
-    }
-    // Items that several warps share, in the order of the line: a lane for each part finds its weight, a row at a time.
-    const int64_t mine_of = lane < 2 * NW ? owner[lane >> 1][lane & 1] : -1;
-    for (unsigned left = __ballot_sync(~0u, mine_of >= 0); left;) {
-        const int lead = __ffs(left) - 1;
-        const int64_t start = __shfl_sync(~0u, mine_of, lead);
-        const unsigned group = __ballot_sync(~0u, mine_of == start);
-        left &= ~group;
-        const AcItem it = items[lead >> 1][lead & 1];
-        const bool whole = start >= first && start + it.units <= last, in = group >> lane & 1;
-        float *out = P.parts + ((int64_t)blockIdx.x * 2 + (start < first ? 0 : 1)) * size;
-        for (int row = warp; row < MT && warp < NW; row += NW) {
-            float m = in ? part(lane)[row] : kAcNone, l = in ? part(lane)[MT + row] : 0.0f, top = m;
+        // the first warps meet: what they share is in place
+        asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
+        if (aborted) {
+            // copies may be under way still: far more time than they need
+            const uint64_t t0 = sm100::globaltimer_ns();
+            while (sm100::globaltimer_ns() - t0 < 10000000ull) {}
+            if (tid == 0) atomicAdd(P.err, 1ull);
+        }
+        // Items that several warps share, in the order of the line, a warp for each: a lane goes over the parts for what it
+        // holds of its rows.
+        const int64_t mine_of = lane < 2 * NW ? owner[lane >> 1][lane & 1] : -1;
+        int turn = 0;
+        for (unsigned left = __ballot_sync(~0u, mine_of >= 0); left; ++turn) {
+            const int lead = __ffs(left) - 1;
+            const int64_t start = __shfl_sync(~0u, mine_of, lead);
+            const unsigned group = __ballot_sync(~0u, mine_of == start);
+            left &= ~group;
+            if (turn % NW != warp) continue;
+            const AcItem item = items[lead >> 1][lead & 1];
+            const bool whole = start >= first && start + item.units <= last;
+            float *out = P.parts + ((int64_t)blockIdx.x * 2 + (start < first ? 0 : 1)) * size;
+#pragma unroll 1
+            for (int r = 0; r < MT / 8; ++r) {
+                const int row = (lane >> 2) + 8 * r;
+                float m = kAcNone, l = 0.0f;
+                for (unsigned g = group; g; g &= g - 1) m = fmaxf(m, part(__ffs(g) - 1)[row]);
+                constexpr int N = DP / 16;  // of the lane's four-element pieces in a row
+                float4 o[N];
 #pragma unroll
-            for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, s));
-            const float f = ac_exp2(m - top);
-            l *= in ? f : 0.0f;
+                for (int k = 0; k < N; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (unsigned g = group; g; g &= g - 1) {
+                    const float *p = part(__ffs(g) - 1);
+                    const float f = ac_exp2(p[row] - m);
+                    l += p[MT + row] * f;
 #pragma unroll
-            for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(~0u, l, s);
-            if (lane < 2 * NW) weight[lane][row] = f;
-            if (lane == 0) {
-                sum[row] = l;
-                if (!whole) out[row] = top, out[MT + row] = l;
+                    for (int k = 0; k < N; ++k) {
+                        const float4 v = reinterpret_cast<const float4 *>(p + 2 * MT)[(r * N + k) * 32 + lane];
+                        o[k].x += v.x * f;
+                        o[k].y += v.y * f;
+                        o[k].z += v.z * f;
+                        o[k].w += v.w * f;
+                    }
+                }
+                if (!whole && (lane & 3) == 0) out[row] = m, out[MT + row] = l;
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int x = (r * N + k) * 32 + lane;
+                    int at_row, d;
+                    ac_place<DP>(x, at_row, d);
+                    if (!whole) reinterpret_cast<float4 *>(out + 2 * MT)[x] = o[k];
+                    else if (d < D) ac_write4(P, item, MT, row, d, o[k], l);
+                }
             }
         }
-        __syncthreads();
-        for (int x = tid; x < MT * DP / 4; x += NW * 64) {
-            int row, d;
-            ac_place<DP>(x, row, d);
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int s = 0; s < 2 * NW; ++s)
-                if (group >> s & 1) {
-                    const float4 v = reinterpret_cast<const float4 *>(part(s) + 2 * MT)[x];
-                    const float f = weight[s][row];
-                    o.x += v.x * f;
-                    o.y += v.y * f;
-                    o.z += v.z * f;
-                    o.w += v.w * f;
-                }
-            if (!whole) reinterpret_cast<float4 *>(out + 2 * MT)[x] = o;
-            else if (d < D) ac_write4(P, it, MT, row, d, o, sum[row]);
-        }
-        __syncthreads();
     }
 }
 
@@ -901,8 +893,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 ac_encoder() {
 
 template <int DP, int MT>
 static kq_status launch_ac(const char *fn, AcParams P, cudaStream_t st) {
-    // 8 KB a unit of 128 elements, up to 16 KB a part
-    constexpr int NW = DP == 256 ? 4 : 8, NS = DP == 64 ? 4 : DP == 128 && MT == 8 ? 3 : 2;
+    // 8 KB a unit of 128 elements, two a warp: more under way only makes everything queue longer (64 users of up to
+    // 8192 tokens: three 106 us, two 102)
+    constexpr int NW = DP == 256 ? 4 : 8, NS = 2;
     using Ring = AcRing<DP>;
     const int smem = NW * (NS * Ring::BYTES + kAcPart<DP, MT> * 4);
     static_assert(NW * (NS * Ring::BYTES + kAcPart<DP, MT> * 4) <= 224 * 1024 + 512, "shared memory");
