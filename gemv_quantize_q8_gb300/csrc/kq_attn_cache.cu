@@ -642,10 +642,7 @@ __global__ void __launch_bounds__(NW * 64, 1)
         return reinterpret_cast<float *>(rings + (s & 1 ? (s >> 1) * NS * Ring::BYTES : NW * NS * Ring::BYTES + (s >> 1) * size * 4));
     };
     static_assert(kAcPart<DP, MT> * 4 <= NS * Ring::BYTES, "a part fits a ring");
-    // before the parts have anything: the line; before the rings' last stages do: where each warp begins
-    AcLine<NW * 64> &line = *reinterpret_cast<AcLine<NW * 64> *>(part(0));
-    static_assert(sizeof(AcLine<NW * 64>) <= NW * size * 4, "shared memory");
-    auto begin_at = [&](int w) -> AcFetch<DP> & { return *reinterpret_cast<AcFetch<DP> *>(rings + ((w + 1) * NS - 1) * Ring::BYTES); };
+    __shared__ AcLine<NW * 64> line;
     if (warp < NW) {
         if (lane < NS) sm100::mbar_init(&full[warp][lane], 2), sm100::mbar_init(&empty[warp][lane], 1);
         if (lane < 2) owner[warp][lane] = -1;
@@ -672,21 +669,17 @@ __global__ void __launch_bounds__(NW * 64, 1)
     const int64_t first = shares(blockIdx.x), last = shares(blockIdx.x + 1);
     if (first >= last) return;
     const AcShares mine(last - first, NW);
-    const int64_t u0 = first + mine(min(warp, NW - 1)), u1 = first + mine(min(warp, NW - 1) + 1);
+    const int mate = warp % NW;  // the first warps work on what the others bring
+    const int64_t u0 = first + mine(mate), u1 = first + mine(mate + 1);
     AcItem it;
     int at = 0;
-    if (warp < NW) {
-        if (u0 < u1) it = ac_find(P, line, u0, at);
-        if (lane == 0) begin_at(warp) = AcFetch<DP>{it, at, u1 - u0};
-    }
-    __syncthreads();
+    if (u0 < u1) it = ac_find(P, line, u0, at);
     if (warp >= NW) {
         // ------------------------------------------------------------ one lane brings the units of one of the first warps
         // (one warp for all, its lanes in turns, could not keep up, nor could two lanes a warp)
         if (NW == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        const int mate = warp - NW;
         if (lane == 0) {
-            AcFetch<DP> f = begin_at(mate);
+            AcFetch<DP> f{it, at, u1 - u0};
             if (f.left > 0) f.start(P), f.look(P);
             int stage = 0;
             uint32_t phase = 1;
