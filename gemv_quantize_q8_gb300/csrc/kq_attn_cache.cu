@@ -741,45 +741,47 @@ __global__ void __launch_bounds__(NW * 64, 1)
             while (sm100::globaltimer_ns() - t0 < 10000000ull) {}
             if (tid == 0) atomicAdd(P.err, 1ull);
         }
-        // Items that several warps share, in the order of the line, a warp for each: a lane goes over the parts for what it
-        // holds of its rows.
+        // Items that several warps share, in the order of the line.  A lane goes over the parts for what it holds of its rows;
+        // every two pieces of 16 bytes of it are a job, and the warps take jobs in turn.
         const int64_t mine_of = lane < 2 * NW ? owner[lane >> 1][lane & 1] : -1;
-        int turn = 0;
-        for (unsigned left = __ballot_sync(~0u, mine_of >= 0); left; ++turn) {
+        constexpr int N = DP / 16, JOBS = N / 2 * (MT / 8);  // a lane's pieces in a row, an item's jobs
+        int job = -warp;
+        for (unsigned left = __ballot_sync(~0u, mine_of >= 0); left;) {
             const int lead = __ffs(left) - 1;
             const int64_t start = __shfl_sync(~0u, mine_of, lead);
             const unsigned group = __ballot_sync(~0u, mine_of == start);
             left &= ~group;
-            if (turn % NW != warp) continue;
             const AcItem item = items[lead >> 1][lead & 1];
             const bool whole = start >= first && start + item.units <= last;
             float *out = P.parts + ((int64_t)blockIdx.x * 2 + (start < first ? 0 : 1)) * size;
 #pragma unroll 1
-            for (int r = 0; r < MT / 8; ++r) {
-                const int row = (lane >> 2) + 8 * r;
-                float m = kAcNone, l = 0.0f;
-                for (unsigned g = group; g; g &= g - 1) m = fmaxf(m, part(__ffs(g) - 1)[row]);
-                constexpr int N = DP / 16;  // of the lane's four-element pieces in a row
-                float4 o[N];
+            for (int n = 0; n < JOBS; ++n, ++job) {
+                if (job % NW) continue;
+                const int row = (lane >> 2) + n / (N / 2) * 8;
+                float pm[2 * NW], m = kAcNone, l = 0.0f;
 #pragma unroll
-                for (int k = 0; k < N; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (unsigned g = group; g; g &= g - 1) {
-                    const float *p = part(__ffs(g) - 1);
-                    const float f = ac_exp2(p[row] - m);
-                    l += p[MT + row] * f;
+                for (int s = 0; s < 2 * NW; ++s) pm[s] = group >> s & 1 ? part(s)[row] : kAcNone;
 #pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        const float4 v = reinterpret_cast<const float4 *>(p + 2 * MT)[(r * N + k) * 32 + lane];
-                        o[k].x += v.x * f;
-                        o[k].y += v.y * f;
-                        o[k].z += v.z * f;
-                        o[k].w += v.w * f;
+                for (int s = 0; s < 2 * NW; ++s) m = fmaxf(m, pm[s]);
+                float4 o[2] = {};
+#pragma unroll
+                for (int s = 0; s < 2 * NW; ++s)
+                    if (group >> s & 1) {
+                        const float f = ac_exp2(pm[s] - m);
+                        l += part(s)[MT + row] * f;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float4 v = reinterpret_cast<const float4 *>(part(s) + 2 * MT)[(2 * n + k) * 32 + lane];
+                            o[k].x += v.x * f;
+                            o[k].y += v.y * f;
+                            o[k].z += v.z * f;
+                            o[k].w += v.w * f;
+                        }
                     }
-                }
-                if (!whole && (lane & 3) == 0) out[row] = m, out[MT + row] = l;
+                if (!whole && n % (N / 2) == 0 && (lane & 3) == 0) out[row] = m, out[MT + row] = l;
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const int x = (r * N + k) * 32 + lane;
+                for (int k = 0; k < 2; ++k) {
+                    const int x = (2 * n + k) * 32 + lane;
                     int at_row, d;
                     ac_place<DP>(x, at_row, d);
                     if (!whole) reinterpret_cast<float4 *>(out + 2 * MT)[x] = o[k];
