@@ -13,9 +13,12 @@
 // Roles: warps 0-3 and 4-7 a row tile each, warp 8 issues the products, warp 9 brings tiles by TMA, warps 10 and 11 look through
 // the values of masked tiles: a masked weight is 0, but 0 times an infinity is not, so values that are not finite
 // are taken out of the tile, remembered bit by bit, and given back at the end to the rows that see them.
+// The blocks, one an SM, take the pairs of row tiles from a line as they get through with them; the next pair's tiles come and
+// its first products run while this one's results leave.  (A block a pair lost 6 us each to starting and ending.)
 // Every wait is bounded; on expiry the block counts an error in the device flag and leaves in order.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <algorithm>
 #include <math.h>
 
 #include "kq_attn_prompt.cuh"
@@ -41,20 +44,22 @@ struct PtCfg {
     static constexpr int KV_OFF = 2 * TILE;
     static constexpr int FIX_OFF = KV_OFF + STAGES * TILE;
     static constexpr int FIX_ROW = 2 * DP / 8;  // a key's bits: +infinities (and NaN), then -infinities (and NaN)
-    static constexpr int BAR_OFF = FIX_OFF + PT_MASKED * PT * FIX_ROW;
-    static constexpr int BARS = 2 + 2 * STAGES + 6 + PT_MASKED + 1;
-    static constexpr int TOTAL = BAR_OFF + BARS * 8 + 32 + 1024;
+    static constexpr int BAR_OFF = FIX_OFF + 2 * PT_MASKED * PT * FIX_ROW;  // of two pairs in turn
+    static constexpr int BARS = 4 + 2 * STAGES + 6 + 4 * PT_MASKED + 2 + 4 + 1;
+    static constexpr int TOTAL = BAR_OFF + BARS * 8 + 24 + 2 * PT_MASKED * 2 * 4 + 1024;
     static_assert(TOTAL <= 227 * 1024, "shared memory");
     static constexpr uint32_t O_COL = 256;     // tensor memory: S (and P) of both tiles, then O of both
 };
 
 struct PtParams {
     PaParams p;
-    int64_t pairs;        // of the grid, for one key head
+    int64_t pairs;        // for one key head
     int n_kv;
     bool negate;          // the scale is negative: -Q K^T and |scale|
     unsigned long long wait_ns;
     int idle;
+    bool wide;            // output rows on 32 bytes, and whole heads of them
+    unsigned *next;       // pairs handed out beyond the blocks' first ones; NULL: there are no more
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
@@ -106,16 +111,19 @@ struct PtWork {
     int n, masked;            // key tiles of the block, and how many of them (the last ones) are masked for some row
 };
 __device__ __forceinline__ int of(const int (&v)[2], int q) { return q ? v[1] : v[0]; }  // (an index would put them in local memory)
+// A warp finds it out (every role on its own).
 __device__ __forceinline__ bool pt_work(const PaParams &P, int64_t pair, PtWork &w) {
     auto start = [&](int64_t b) { return ((pa_row(P.cu_q, b, P.Tq) / PT + b) * P.G >> 1) + b; };
-    int64_t b = -1;
-    for (int64_t b0 = 0; b0 < P.B; b0 += PT_THREADS) {
-        const int64_t i = b0 + threadIdx.x;
-        const int n = __syncthreads_count(i < P.B && start(i) <= pair);
-        b += n;
-        if (n < PT_THREADS) break;
+    const int lane = threadIdx.x & 31;
+    int64_t b = 0;
+    for (int64_t n = P.B; n > 1;) {  // the last of n sequences from b on that starts at or before the pair
+        const int64_t step = (n + 31) / 32, at = lane * step;
+        const int k = __popc(__ballot_sync(~0u, at < n && start(b + at) <= pair)) - 1;
+        if (k < 0) return false;
+        b += k * step;
+        n = min(step, n - k * step);
     }
-    if (b < 0) return false;
+    if (start(b) > pair) return false;
     PaTile &t = w.t;
     t.q_row = pa_row(P.cu_q, b, P.Tq);
     t.k_row = pa_row(P.cu_k, b, P.Tk);
@@ -148,52 +156,93 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     extern __shared__ uint8_t pt_smem[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(pt_smem) + 1023) & ~(uintptr_t)1023);
     uint8_t *sKV = sm + C::KV_OFF, *fix = sm + C::FIX_OFF;
-    uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + C::BAR_OFF), *kv_full = q_full + 2, *kv_empty = kv_full + C::STAGES;
-    uint64_t *s_full = kv_empty + C::STAGES, *p_full = s_full + 2, *o_full = p_full + 2, *v_ok = o_full + 2, *mma_done = v_ok + PT_MASKED;
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + C::BAR_OFF), *q_empty = q_full + 2, *kv_full = q_empty + 2, *kv_empty = kv_full + C::STAGES;
+    uint64_t *s_full = kv_empty + C::STAGES, *p_full = s_full + 2, *o_full = p_full + 2;
+    // masked tiles, [pair % 2][place]: its copies have been asked for; its values have been looked through; and of a pair: done with
+    uint64_t *v_sent = o_full + 2, *v_ok = v_sent + 2 * PT_MASKED, *fix_free = v_ok + 2 * PT_MASKED, *turn_full = fix_free + 2,
+             *turn_empty = turn_full + 2, *mma_done = turn_empty + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    volatile int *fixed = abort_flag + 1;  // [PT_MASKED]: the tile had values that are not finite
+    volatile unsigned *turns = reinterpret_cast<volatile unsigned *>(abort_flag + 1);  // [turn % 2]: a place on the line
+    volatile int *fixed = abort_flag + 3;  // [pair % 2][place][half]: values that are not finite were taken out
 
     const PaParams &P = X.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
+            mbar_init(&fix_free[i], 8);
+            mbar_init(&turn_full[i], 1);
+            mbar_init(&turn_empty[i], PT_THREADS / 32 - 1);
         }
         for (int i = 0; i < C::STAGES; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
-        for (int i = 0; i < PT_MASKED; ++i) { mbar_init(&v_ok[i], 2); fixed[i] = 0; }
+        for (int i = 0; i < 2 * PT_MASKED; ++i) { mbar_init(&v_sent[i], 1); mbar_init(&v_ok[i], 2); }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 9 && lane == 0) { prefetch_tmap(&tmQ); prefetch_tmap(&tmK); prefetch_tmap(&tmV); }
-    // (tensor memory while the block finds its work: no other block that holds some fits beside this one)
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_holder)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (blockIdx.x == 0 && tid == 0) *P.err = 0ull;  // (an error is counted two seconds later at the earliest)
-    // the longest first: later tokens see more keys
-    const unsigned turn = blockIdx.x / (unsigned)X.n_kv;
-    const int kv_head = blockIdx.x - turn * X.n_kv;
-    PtWork w;
-    const bool found = pt_work(P, X.pairs - 1 - turn, w);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (!found) {
-        if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*tmem_holder) : "memory");
-        return;
-    }
     // all 512 columns are this kernel's, so the allocation starts at column 0 of lane 0
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (!X.next && blockIdx.x == 0 && tid == 0) *P.err = 0ull;  // (an error is counted two seconds later at the earliest)
+
+    // Every role walks the same pairs: f(w, key head), false to stop.  The warp that brings tiles asks for the next place on the
+    // line and passes it on.
+    auto walk = [&](auto f) {
+        const unsigned items = (unsigned)(X.pairs * X.n_kv);
+        unsigned ahead = blockIdx.x;
+        for (unsigned r = 0;; ++r) {
+            const int s = r & 1;
+            unsigned i = 0;
+            if (warp == 9) {
+                bool ok = true;
+                if (lane == 0) {
+                    i = ahead;
+                    ok = mbar_wait_sleep(&turn_empty[s], (r >> 1 & 1) ^ 1, abort_flag, X.wait_ns);
+                    turns[s] = i;
+                    mbar_arrive(&turn_full[s]);
+                }
+                i = __shfl_sync(~0u, i, 0);
+                if (!__shfl_sync(~0u, (int)ok, 0)) return;
+            } else {
+                if (!__all_sync(~0u, mbar_wait_sleep(&turn_full[s], r >> 1 & 1, abort_flag, X.wait_ns))) return;
+                i = turns[s];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&turn_empty[s]);
+            }
+            if (i >= items) return;
+            // the longest first: later tokens see more keys
+            const unsigned turn = i / (unsigned)X.n_kv;
+            PtWork w;
+            if (pt_work(P, X.pairs - 1 - turn, w) && !f(w, (int)(i - turn * X.n_kv))) return;
+            // (asked for when the pair's last tiles have been sent for, not before: a place taken early waits behind a long pair)
+            if (warp == 9 && lane == 0) ahead = X.next ? gridDim.x + atomicAdd(X.next, 1u) : items;
+        }
+    };
+    // The pairs with masked tiles so far; which barriers of theirs are this pair's, and their phase.
+    int pairs_masked = 0;
+    auto place = [&](int i) { return (pairs_masked & 1) * PT_MASKED + i; };
+    uint32_t uses = 0;  // bit `place`: the phase of its barriers
+    auto phase = [&](int i) { return uses >> place(i) & 1; };
+    auto masked_done = [&](const PtWork &w) {
+        for (int i = 0; i < w.masked; ++i) uses ^= 1u << place(i);
+        if (w.masked) ++pairs_masked;
+    };
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
             // ------------------------------------------------------------ products
             const bool one = pt_elect();
@@ -204,226 +253,269 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             // 64 elements of d a box, boxes BOX apart; eight tokens 1024 bytes apart
             const uint64_t dV = (dK & ~((uint64_t)0x3FFF << 16)) | (uint64_t)(C::BOX >> 4) << 16;
             bool ok = X.idle != 2;
+            unsigned g = 0;                    // key and value tiles so far
+            uint32_t q_phase[2] = {}, p_phase[2] = {};
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 ok = ok && __all_sync(~0u, mbar_wait(bar, parity, abort_flag, X.wait_ns));
                 return ok;
             };
-            auto qk = [&](int q, int i) {  // the block's i-th key tile
-                const int s = 2 * i % C::STAGES;
-                if (one) {
-#pragma unroll
-                    for (int k = 0; k < C::DP / 16; ++k) {
-                        if (k * 16 >= P.D) break;
-                        const uint64_t off = (uint64_t)((k / 4) * (C::BOX >> 4) + (k % 4) * 2);
-                        mma_f16(q * 128, dQ + q * (C::TILE >> 4) + off, dK + s * (C::TILE >> 4) + off, id_s, k > 0);
-                    }
-                    mma_commit(&s_full[q]);
-                }
-                __syncwarp();
-            };
+            auto kv_wait = [&](unsigned t) { return wait(&kv_full[t % C::STAGES], t / C::STAGES & 1); };
             auto commit = [&](uint64_t *bar) {
                 if (one) mma_commit(bar);
                 __syncwarp();
             };
-            if (w.n && wait(&kv_full[0], 0)) {
-                for (int q = 0; q < 2 && ok; ++q)
-                    if (of(w.tiles, q) == w.n && wait(&q_full[q], 0)) {
-                        tc_fence_after();
-                        qk(q, 0);
-                    }
-                if (ok) commit(&kv_empty[0]);
-            }
-            for (int i = 0; i < w.n && ok; ++i) {
-                const int sv = (2 * i + 1) % C::STAGES;
-                if (!wait(&kv_full[sv], (2 * i + 1) / C::STAGES & 1)) break;
-                if (i < w.masked && !wait(&v_ok[i], 0)) break;
-                for (int q = 0; q < 2 && ok; ++q) {
-                    const int at = i - (w.n - of(w.tiles, q));  // the row tile's own count
-                    if (at >= 0) {
-                        if (!wait(&p_full[q], at & 1)) break;
-                        tc_fence_after();
-                        if (one) {
+            walk([&](const PtWork &w, int) {
+                // row tile q's scores of the pair's i-th key tile; after its last the queries may be overwritten
+                auto qk = [&](int q, int i) {
+                    const int s = (g + 2 * i) % C::STAGES;
+                    if (one) {
 #pragma unroll
-                            for (int k = 0; k < PT / 16; ++k)
-                                mma_f16_ts(C::O_COL + q * C::DP, q * 128 + k * 8, dV + (uint64_t)(sv * (C::TILE >> 4) + k * (2048 >> 4)), id_o,
-                                           at > 0 || k > 0);
-                            mma_commit(&o_full[q]);
+                        for (int k = 0; k < C::DP / 16; ++k) {
+                            if (k * 16 >= P.D) break;
+                            const uint64_t off = (uint64_t)((k / 4) * (C::BOX >> 4) + (k % 4) * 2);
+                            mma_f16(q * 128, dQ + q * (C::TILE >> 4) + off, dK + s * (C::TILE >> 4) + off, id_s, k > 0);
                         }
-                        __syncwarp();
+                        mma_commit(&s_full[q]);
+                        if (i + 1 == w.n) mma_commit(&q_empty[q]);
                     }
-                    if (i + 1 < w.n && at + 1 >= 0) {
-                        if (!wait(&kv_full[(2 * i + 2) % C::STAGES], (2 * i + 2) / C::STAGES & 1)) break;
-                        if (at + 1 == 0 && !wait(&q_full[q], 0)) break;
-                        tc_fence_after();
-                        qk(q, i + 1);
-                    }
+                    __syncwarp();
+                };
+                auto queries = [&](int q) {
+                    const uint32_t parity = q ? q_phase[1] : q_phase[0];
+                    (q ? q_phase[1] : q_phase[0]) ^= 1;
+                    return wait(&q_full[q], parity);
+                };
+                if (w.n && kv_wait(g)) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (ok && w.tiles[q] == w.n && queries(q)) {
+                            tc_fence_after();
+                            qk(q, 0);
+                        }
+                    if (ok) commit(&kv_empty[g % C::STAGES]);
                 }
-                if (!ok) break;
-                commit(&kv_empty[sv]);
-                if (i + 1 < w.n) commit(&kv_empty[(2 * i + 2) % C::STAGES]);
-            }
+                for (int i = 0; i < w.n && ok; ++i) {
+                    const unsigned tv = g + 2 * i + 1;
+                    const int sv = tv % C::STAGES;
+                    if (!kv_wait(tv)) break;
+                    if (i < w.masked && !wait(&v_ok[place(i)], phase(i))) break;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int at = i - (w.n - w.tiles[q]);  // the row tile's own count
+                        if (ok && at >= 0 && wait(&p_full[q], p_phase[q])) {
+                            p_phase[q] ^= 1;
+                            tc_fence_after();
+                            if (one) {
+#pragma unroll
+                                for (int k = 0; k < PT / 16; ++k)
+                                    mma_f16_ts(C::O_COL + q * C::DP, q * 128 + k * 8, dV + (uint64_t)(sv * (C::TILE >> 4) + k * (2048 >> 4)),
+                                               id_o, at > 0 || k > 0);
+                                mma_commit(&o_full[q]);
+                            }
+                            __syncwarp();
+                        }
+                        if (ok && i + 1 < w.n && at + 1 >= 0 && kv_wait(tv + 1) && (at + 1 > 0 || queries(q))) {
+                            tc_fence_after();
+                            qk(q, i + 1);
+                        }
+                    }
+                    if (!ok) break;
+                    commit(&kv_empty[sv]);
+                    if (i + 1 < w.n) commit(&kv_empty[(tv + 1) % C::STAGES]);
+                }
+                g += 2 * w.n;
+                masked_done(w);
+                return ok;
+            });
             // every product issued has finished before tensor memory is freed
             commit(mma_done);
             volatile int no_abort = 0;
             mbar_wait(mma_done, 0, &no_abort, 100000000ull);
         } else if (warp == 9) {
             // ------------------------------------------------------------ tiles
-            if (lane == 0 && w.n && X.idle != 1) {
-                bool ok = true;
-                auto tile = [&](uint8_t *dst, const CUtensorMap *tm, uint64_t *bar, int head, int64_t row) {
-                    mbar_arrive_expect_tx(bar, C::TILE);
+            bool ok = true;
+            unsigned g = 0, rows_sent[2] = {};
+            if (X.idle != 1) walk([&](const PtWork &w, int kv_head) {
+                if (lane == 0 && w.n) {
+                    auto tile = [&](uint8_t *dst, const CUtensorMap *tm, uint64_t *bar, int head, int64_t row) {
+                        mbar_arrive_expect_tx(bar, C::TILE);
 #pragma unroll
-                    for (int c = 0; c < C::CH; ++c) tma_load_3d(dst + c * C::BOX, tm, bar, c * 64, head, (int)row);
-                };
-                int g = 0;
-                auto kv = [&](const CUtensorMap *tm, int j) {
-                    const int s = g % C::STAGES;
-                    if (!(ok = mbar_wait_sleep(&kv_empty[s], (g / C::STAGES & 1) ^ 1, abort_flag, X.wait_ns))) return;
-                    tile(sKV + s * C::TILE, tm, &kv_full[s], kv_head, w.t.k_row + (int64_t)j * PT);
-                    ++g;
-                };
-                auto rows = [&](int q) {
-                    if (of(w.tiles, q)) tile(sm + q * C::TILE, &tmQ, &q_full[q], kv_head * P.G + of(w.head, q), w.t.q_row + of(w.first, q));
-                };
-                rows(0);
-                kv(&tmK, w.n - 1);
-                rows(1);
-                if (ok) kv(&tmV, w.n - 1);
-                for (int j = w.n - 2; j >= 0 && ok; --j) {
-                    kv(&tmK, j);
-                    if (ok) kv(&tmV, j);
+                        for (int c = 0; c < C::CH; ++c) tma_load_3d(dst + c * C::BOX, tm, bar, c * 64, head, (int)row);
+                    };
+                    auto kv = [&](const CUtensorMap *tm, int j) {
+                        const int s = g % C::STAGES;
+                        if (!ok || !(ok = mbar_wait_sleep(&kv_empty[s], (g / C::STAGES & 1) ^ 1, abort_flag, X.wait_ns))) return;
+                        tile(sKV + s * C::TILE, tm, &kv_full[s], kv_head, w.t.k_row + (int64_t)j * PT);
+                        ++g;
+                    };
+                    auto rows = [&](int q) {
+                        if (!ok || !of(w.tiles, q)) return;
+                        unsigned &sent = q ? rows_sent[1] : rows_sent[0];
+                        if (!(ok = mbar_wait_sleep(&q_empty[q], (sent & 1) ^ 1, abort_flag, X.wait_ns))) return;
+                        tile(sm + q * C::TILE, &tmQ, &q_full[q], kv_head * P.G + of(w.head, q), w.t.q_row + of(w.first, q));
+                        ++sent;
+                    };
+                    rows(0);
+                    kv(&tmK, w.n - 1);
+                    rows(1);
+                    for (int i = 0; i < w.n; ++i) {
+                        if (i) kv(&tmK, w.n - 1 - i);
+                        kv(&tmV, w.n - 1 - i);
+                        if (ok && i < w.masked) mbar_arrive(&v_sent[place(i)]);
+                    }
                 }
-                // the copies in flight land before this thread leaves (bounded)
+                masked_done(w);
+                return (bool)__shfl_sync(~0u, ok, 0);
+            });
+            // the copies in flight land before this thread leaves (bounded)
+            if (lane == 0) {
                 volatile int no_abort = 0;
+#pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    if (of(w.tiles, q)) mbar_wait_sleep(&q_full[q], 0, &no_abort, 100000000ull);
-                for (int i = 1; i <= C::STAGES; ++i)
+                    if (rows_sent[q]) mbar_wait_sleep(&q_full[q], (rows_sent[q] - 1) & 1, &no_abort, 100000000ull);
+                for (unsigned i = 1; i <= C::STAGES; ++i)
                     if (g >= i) mbar_wait_sleep(&kv_full[(g - i) % C::STAGES], (g - i) / C::STAGES & 1, &no_abort, 100000000ull);
             }
         } else {
             // ------------------------------------------------------------ values of masked tiles
             constexpr uint32_t EXP = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
             const int half = warp - 10;  // tokens 64 * half on
-            for (int i = 0; i < w.masked; ++i) {
-                const int s = (2 * i + 1) % C::STAGES;
-                if (!__all_sync(~0u, mbar_wait_sleep(&kv_full[s], (2 * i + 1) / C::STAGES & 1, abort_flag, X.wait_ns))) break;
-                uint8_t *v = sKV + s * C::TILE + half * (C::BOX / 2);
-                uint32_t top = 0;
+            unsigned g = 0;
+            walk([&](const PtWork &w, int) {
+                bool ok = true;
+                auto wait = [&](uint64_t *bar, uint32_t parity) {
+                    return ok = ok && __all_sync(~0u, mbar_wait_sleep(bar, parity, abort_flag, X.wait_ns));
+                };
+                if (w.masked) wait(&fix_free[pairs_masked & 1], (pairs_masked >> 1 & 1) ^ 1);
+                for (int i = 0; i < w.masked && ok; ++i) {
+                    const unsigned tv = g + 2 * i + 1;
+                    const int s = tv % C::STAGES;
+                    // (only a tile that has been asked for has the phase that is waited for)
+                    if (!wait(&v_sent[place(i)], phase(i)) || !wait(&kv_full[s], tv / C::STAGES & 1)) break;
+                    uint8_t *v = sKV + s * C::TILE + half * (C::BOX / 2);
+                    uint32_t top = 0;
 #pragma unroll 8
-                for (int k = 0; k < C::CH * 16; ++k) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(v + (k / 16) * C::BOX + (k % 16) * 512 + lane * 16);
-                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
-                }
-                if (__any_sync(~0u, (top & 0xffffu) >= EXP || (top >> 16) >= EXP)) {
-                    // a lane takes eight elements of a token: out of the tile, into the bits
-                    uint8_t *bits = fix + (i * PT + half * 64) * C::FIX_ROW;
-                    for (int k = lane; k < 64 * C::DP / 8; k += 32) {
-                        const int r = k / (C::DP / 8), c = k % (C::DP / 8);
-                        uint4 *at = reinterpret_cast<uint4 *>(v + (c / 8) * C::BOX + r * 128 + ((c % 8 ^ (r & 7)) << 4));
-                        uint4 u = *at;
-                        uint32_t plus = 0, minus = 0;
-                        uint16_t *e = reinterpret_cast<uint16_t *>(&u);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t x = e[j];
-                            if ((x & 0x7fffu) < EXP) continue;
-                            const bool nan = (x & 0x7fffu) > EXP;
-                            if (nan || !(x >> 15)) plus |= 1u << j;
-                            if (nan || x >> 15) minus |= 1u << j;
-                            e[j] = 0;
-                        }
-                        *at = u;
-                        bits[r * C::FIX_ROW + c] = (uint8_t)plus;
-                        bits[r * C::FIX_ROW + C::DP / 8 + c] = (uint8_t)minus;
+                    for (int k = 0; k < C::CH * 16; ++k) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(v + (k / 16) * C::BOX + (k % 16) * 512 + lane * 16);
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
                     }
-                    if (lane == 0) atomicOr((int *)&fixed[i], 1 << half);
-                    fence_proxy_async_smem();
+                    const bool found = __any_sync(~0u, (top & 0xffffu) >= EXP || (top >> 16) >= EXP);
+                    if (found) {
+                        // a lane takes eight elements of a token: out of the tile, into the bits
+                        uint8_t *bits = fix + (place(i) * PT + half * 64) * C::FIX_ROW;
+                        for (int k = lane; k < 64 * C::DP / 8; k += 32) {
+                            const int r = k / (C::DP / 8), c = k % (C::DP / 8);
+                            uint4 *at = reinterpret_cast<uint4 *>(v + (c / 8) * C::BOX + r * 128 + ((c % 8 ^ (r & 7)) << 4));
+                            uint4 u = *at;
+                            uint32_t plus = 0, minus = 0;
+                            uint16_t *e = reinterpret_cast<uint16_t *>(&u);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint32_t x = e[j];
+                                if ((x & 0x7fffu) < EXP) continue;
+                                const bool nan = (x & 0x7fffu) > EXP;
+                                if (nan || !(x >> 15)) plus |= 1u << j;
+                                if (nan || x >> 15) minus |= 1u << j;
+                                e[j] = 0;
+                            }
+                            *at = u;
+                            bits[r * C::FIX_ROW + c] = (uint8_t)plus;
+                            bits[r * C::FIX_ROW + C::DP / 8 + c] = (uint8_t)minus;
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    if (lane == 0) fixed[place(i) * 2 + half] = found;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&v_ok[place(i)]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&v_ok[i]);
-            }
+                g += 2 * w.n;
+                masked_done(w);
+                return ok;
+            });
         }
     } else {
         // ------------------------------------------------------------ weights and results, one row a thread
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int q = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16, ts = lane_base + q * 128, to = lane_base + C::O_COL + q * C::DP;
-        const int token = of(w.first, q) + row, limit = of(w.first, q) < w.t.n_q ? pa_limit(P, w.t, token) : 0, n = of(w.tiles, q);
-        float mc = kPtNone, l = 0.0f;  // the maximum times the scale; this row's sum
-        bool ok = true;
-        auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = __all_sync(~0u, mbar_wait(bar, parity, abort_flag, X.wait_ns));
-            tc_fence_after();
-            return ok;
-        };
-        for (int i = 0; i < n; ++i) {
-            const int j = n - 1 - i;
-            if (!wait(&s_full[q], i & 1)) break;
-            float s[PT];
+        unsigned t = 0;  // this row tile's key tiles so far
+        walk([&](const PtWork &w, int kv_head) {
+            const int first = of(w.first, q), token = first + row, limit = first < w.t.n_q ? pa_limit(P, w.t, token) : 0, n = of(w.tiles, q);
+            float mc = kPtNone, l = 0.0f;  // the maximum times the scale; this row's sum
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                ok = __all_sync(~0u, mbar_wait(bar, parity, abort_flag, X.wait_ns));
+                tc_fence_after();
+                return ok;
+            };
+            for (int i = 0; i < n; ++i, ++t) {
+                const int j = n - 1 - i;
+                if (!wait(&s_full[q], t & 1)) break;
+                float s[PT];
 #pragma unroll
-            for (int c = 0; c < PT; c += 32) tmem_ld32(ts + c, s + c);
-            tmem_wait_ld();
-            if ((j + 1) * PT > of(w.lowest, q)) {
-                const int seen = limit - j * PT;
+                for (int c = 0; c < PT; c += 32) tmem_ld32(ts + c, s + c);
+                tmem_wait_ld();
+                if ((j + 1) * PT > of(w.lowest, q)) {
+                    const int seen = limit - j * PT;
 #pragma unroll
-                for (int c = 0; c < PT; ++c) s[c] = c < seen ? s[c] : -INFINITY;
-            }
-            float top[4] = {s[0], s[1], s[2], s[3]};
+                    for (int c = 0; c < PT; ++c) s[c] = c < seen ? s[c] : -INFINITY;
+                }
+                float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int c = 4; c < PT; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
-            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.scale;
-            if (__any_sync(~0u, mx > mc + kPtSlack)) {
-                const float m2 = fmaxf(mc, mx), f = pt_exp2(mc - m2);
-                mc = m2;
-                l *= f;
-                if (i > 0) {
-                    if (!wait(&o_full[q], (i - 1) & 1)) break;
+                for (int c = 4; c < PT; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.scale;
+                if (__any_sync(~0u, mx > mc + kPtSlack)) {
+                    const float m2 = fmaxf(mc, mx), f = pt_exp2(mc - m2);
+                    mc = m2;
+                    l *= f;
+                    if (i > 0) {
+                        if (!wait(&o_full[q], (t - 1) & 1)) break;
 #pragma unroll 1
-                    for (int c = 0; c < C::DP; c += 32) {
-                        float o[32];
-                        uint32_t r[32];
-                        tmem_ld32(to + c, o);
-                        tmem_wait_ld();
+                        for (int c = 0; c < C::DP; c += 32) {
+                            float o[32];
+                            uint32_t r[32];
+                            tmem_ld32(to + c, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(o[k] * f);
-                        tmem_st32(to + c, r);
+                            for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(o[k] * f);
+                            tmem_st32(to + c, r);
+                        }
                     }
                 }
-            }
-            const float2 sc = make_float2(P.scale, P.scale), off = make_float2(-mc, -mc);
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                const float2 sc = make_float2(P.scale, P.scale), off = make_float2(-mc, -mc);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int c = 0; c < PT; c += 64) {
-                uint32_t r[32];
+                for (int c = 0; c < PT; c += 64) {
+                    uint32_t r[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    float2 x = fma2(make_float2(s[c + 2 * k], s[c + 2 * k + 1]), sc, off);
-                    x.x = pt_exp2(x.x);
-                    x.y = pt_exp2(x.y);
-                    sum[k & 1] = fma2(x, make_float2(1.0f, 1.0f), sum[k & 1]);
-                    r[k] = pt_pack<T>(x.x, x.y);
+                    for (int k = 0; k < 32; ++k) {
+                        float2 x = fma2(make_float2(s[c + 2 * k], s[c + 2 * k + 1]), sc, off);
+                        x.x = pt_exp2(x.x);
+                        x.y = pt_exp2(x.y);
+                        sum[k & 1] = fma2(x, make_float2(1.0f, 1.0f), sum[k & 1]);
+                        r[k] = pt_pack<T>(x.x, x.y);
+                    }
+                    tmem_st32(ts + c / 2, r);
                 }
-                tmem_st32(ts + c / 2, r);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[q]);
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[q]);
-        }
-        if (ok && n) wait(&o_full[q], (n - 1) & 1);
-        if (ok && n && w.masked) {  // (the flags of masked tiles are set before this)
-            for (int i = 0; i < w.masked; ++i) wait(&v_ok[i], 0);
-        }
-        if (ok) {
+            if (ok && n) wait(&o_full[q], (t - 1) & 1);
+            for (int i = 0; i < w.masked && ok; ++i) wait(&v_ok[place(i)], phase(i));  // (the flags are in place)
+            if (!ok) return false;
             uint32_t bits[C::FIX_ROW / 4] = {};
             bool any = false;
-            for (int i = 0; i < w.masked; ++i) {
-                if (!fixed[i]) continue;
+#pragma unroll 1
+            for (int i = 0; i < w.masked * 2; ++i) {
+                if (!fixed[place(0) * 2 + i]) continue;
                 any = true;
-                for (int r = 0; r < PT && (w.n - 1 - i) * PT + r < limit; ++r) {
-                    if (!(fixed[i] >> (r / 64) & 1)) continue;
-                    const uint32_t *b = reinterpret_cast<const uint32_t *>(fix + (i * PT + r) * C::FIX_ROW);
+                const int r0 = (i & 1) * 64, key0 = (w.n - 1 - (i >> 1)) * PT + r0;
+#pragma unroll 1
+                for (int r = 0; r < 64 && key0 + r < limit; ++r) {
+                    const uint32_t *b = reinterpret_cast<const uint32_t *>(fix + (place(i >> 1) * PT + r0 + r) * C::FIX_ROW);
                     uint32_t one_sign = 0;
 #pragma unroll
                     for (int k = 0; k < C::DP / 32; ++k) one_sign |= b[k] ^ b[C::DP / 32 + k];
@@ -431,7 +523,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     bool none = false;
                     if (one_sign) {
                         const T *x = static_cast<const T *>(P.q) + (w.t.q_row + token) * P.ldq + (int64_t)(kv_head * P.G + of(w.head, q)) * P.D;
-                        const T *k = static_cast<const T *>(P.k) + (w.t.k_row + (w.n - 1 - i) * PT + r) * P.ldk + (int64_t)kv_head * P.D;
+                        const T *k = static_cast<const T *>(P.k) + (w.t.k_row + key0 + r) * P.ldk + (int64_t)kv_head * P.D;
                         float dot = 0.0f;
                         for (int d = 0; d < P.D; ++d) dot += to_f32(x[d]) * to_f32(k[d]);
                         none = (X.negate ? -dot : dot) == -INFINITY;
@@ -444,12 +536,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     }
                 }
             }
-            // the rows through shared memory (the row tile's queries are through), so that the warp's stores are whole rows:
-            // a row a thread they took 2 us
+            __syncwarp();
+            if (w.masked && lane == 0) mbar_arrive(&fix_free[pairs_masked & 1]);
+            const bool live = first < w.t.n_q && token < w.t.n_q;
             const float inv = 1.0f / l;
-            uint8_t *rows = sm + q * C::TILE + (warp & 3) * 32 * (C::DP * 2);
-            constexpr int PIECES = C::DP / 8;  // of 16 bytes; piece p of row r at p ^ (r % 8)
-#pragma unroll
+            T *y = static_cast<T *>(P.y) + (w.t.q_row + token) * P.ldy + (int64_t)(kv_head * P.G + of(w.head, q)) * P.D;
+            // (not unrolled: code that runs once a pair comes from memory)
+#pragma unroll 1
             for (int c = 0; c < C::DP; c += 32) {
                 float o[32];
                 if (n) {
@@ -457,31 +550,35 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     tmem_wait_ld();
                 }
                 if (any) {
+                    uint32_t plus = bits[0], minus = bits[C::DP / 32];
+#pragma unroll
+                    for (int k = 1; k < C::DP / 32; ++k)
+                        if (c == 32 * k) plus = bits[k], minus = bits[C::DP / 32 + k];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        if (bits[c / 32] >> k & 1) o[k] += INFINITY;
-                        if (bits[C::DP / 32 + c / 32] >> k & 1) o[k] -= INFINITY;
+                        if (plus >> k & 1) o[k] += INFINITY;
+                        if (minus >> k & 1) o[k] -= INFINITY;
                     }
                 }
+                uint32_t r[16];
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    uint4 u;
-                    uint32_t *e = reinterpret_cast<uint32_t *>(&u);
+                for (int k = 0; k < 16; ++k) r[k] = limit ? pt_pack<T>(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
+                if (X.wide) {  // whole sectors
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) e[x] = limit ? pt_pack<T>(o[k + 2 * x] * inv, o[k + 2 * x + 1] * inv) : 0u;
-                    *reinterpret_cast<uint4 *>(rows + lane * (C::DP * 2) + (((c + k) / 8 ^ (lane & 7)) << 4)) = u;
+                    for (int k = 0; k < 16; k += 8)
+                        if (live && c + 2 * k < P.D)
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y + c + 2 * k), "r"(r[k]), "r"(r[k + 1]),
+                                         "r"(r[k + 2]), "r"(r[k + 3]), "r"(r[k + 4]), "r"(r[k + 5]), "r"(r[k + 6]), "r"(r[k + 7])
+                                         : "memory");
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4)
+                        if (live && c + 2 * k < P.D) *reinterpret_cast<uint4 *>(y + c + 2 * k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
                 }
             }
-            __syncwarp();
-            const int left = w.t.n_q - of(w.first, q) - (warp & 3) * 32, pieces = P.D / 8;  // rows of this warp
-            T *y = static_cast<T *>(P.y) + (w.t.q_row + of(w.first, q) + (warp & 3) * 32) * P.ldy + (int64_t)(kv_head * P.G + of(w.head, q)) * P.D;
-            const int piece = lane % PIECES;
-#pragma unroll 4
-            for (int r = lane / PIECES; r < 32; r += 32 / PIECES)
-                if (r < left && piece < pieces)
-                    *reinterpret_cast<uint4 *>(y + r * P.ldy + piece * 8) =
-                        *reinterpret_cast<const uint4 *>(rows + r * (C::DP * 2) + ((piece ^ (r & 7)) << 4));
-        }
+            masked_done(w);
+            return true;
+        });
     }
     if (tid == 0 && *abort_flag) atomicAdd(P.err, 1ull);
     tc_fence_before();
@@ -490,6 +587,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*tmem_holder) : "memory");
     }
+}
+
+// Clears the device flag and the line's counter.
+__global__ void pt_reset_kernel(unsigned long long *err, unsigned *next) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    *err = 0ull;
+    *next = 0u;
 }
 
 // ---------------------------------------------------------------- host
@@ -533,15 +638,22 @@ static kq_status pt_launch(const char *fn, PtParams X, cudaStream_t st) {
     if (X.pairs * X.n_kv > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: too many row tiles", fn);
     auto kern = pt_kernel<T, C>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
+    const int64_t items = X.pairs * X.n_kv;
+    constexpr int SMS = 152;
+    X.next = items > SMS ? reinterpret_cast<unsigned *>(P.err + 1) : nullptr;
+    if (e == cudaSuccess && X.next) {
+        e = launch_beside(pt_reset_kernel, dim3(1), dim3(1), 0, dim3(1), st, P.err, X.next);
+        if (e == cudaSuccess) count_launch(R_ATTN);
+    }
     if (e == cudaSuccess)
-        e = launch_beside(kern, dim3((unsigned)(X.pairs * X.n_kv)), dim3(PT_THREADS), C::TOTAL, dim3(1), st, tm[0], tm[1], tm[2], X);
+        e = launch_beside(kern, dim3((unsigned)std::min<int64_t>(items, SMS)), dim3(PT_THREADS), C::TOTAL, dim3(1), st, tm[0], tm[1], tm[2], X);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
     count_launch(R_ATTN);
     return KQ_OK;
 }
 
 kq_status pa_tc(const char *fn, kq_dtype xt, const PaParams &P, unsigned long long wait_ns, int idle, cudaStream_t st) {
-    PtParams X{P, 0, P.n_q / P.G, P.scale < 0.0f, wait_ns, idle};
+    PtParams X{P, 0, P.n_q / P.G, P.scale < 0.0f, wait_ns, idle, aligned(P.y, 32) && P.ldy % 16 == 0 && P.D % 16 == 0, nullptr};
     // (a scale of 0 weighs all keys alike, as any tiny one does, which keeps -inf times it -inf)
     X.p.scale = P.scale == 0.0f ? 1e-35f : fabsf(P.scale);
     auto go = [&](auto t) {
