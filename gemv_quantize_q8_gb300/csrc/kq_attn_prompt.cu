@@ -193,7 +193,7 @@ using namespace kq;
 extern "C" {
 
 size_t kq_attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv, int64_t D) {
-    return pa_shape(B, Tq, n_q, n_kv, D) ? 256 : 0;
+    return pa_shape(B, Tq, n_q, n_kv, D) ? pa_tc_workspace(B, Tq, n_q / n_kv) : 0;
 }
 
 kq_status kq_attn_prompt(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,

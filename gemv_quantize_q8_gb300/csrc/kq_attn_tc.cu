@@ -60,6 +60,7 @@ struct PtParams {
     int idle;
     bool wide;            // output rows on 32 bytes, and whole heads of them
     unsigned *next;       // pairs handed out beyond the blocks' first ones; NULL: there are no more
+    const int *order;     // the pairs by their places on the line, or NULL: the last first
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
@@ -111,23 +112,13 @@ struct PtWork {
     int n, masked;            // key tiles of the block, and how many of them (the last ones) are masked for some row
 };
 __device__ __forceinline__ int of(const int (&v)[2], int q) { return q ? v[1] : v[0]; }  // (an index would put them in local memory)
-// A warp finds it out (every role on its own).
-__device__ __forceinline__ bool pt_work(const PaParams &P, int64_t pair, PtWork &w) {
-    auto start = [&](int64_t b) { return ((pa_row(P.cu_q, b, P.Tq) / PT + b) * P.G >> 1) + b; };
-    const int lane = threadIdx.x & 31;
-    int64_t b = 0;
-    for (int64_t n = P.B; n > 1;) {  // the last of n sequences from b on that starts at or before the pair
-        const int64_t step = (n + 31) / 32, at = lane * step;
-        const int k = __popc(__ballot_sync(~0u, at < n && start(b + at) <= pair)) - 1;
-        if (k < 0) return false;
-        b += k * step;
-        n = min(step, n - k * step);
-    }
-    if (start(b) > pair) return false;
+__device__ __forceinline__ int64_t pt_start(const PaParams &P, int64_t b) { return ((pa_row(P.cu_q, b, P.Tq) / PT + b) * P.G >> 1) + b; }
+// The pair's work, if there is such a pair; sequence b is the last that starts at or before it.
+__device__ __forceinline__ bool pt_fill(const PaParams &P, int64_t b, int64_t pair, PtWork &w) {
     PaTile &t = w.t;
     t.q_row = pa_row(P.cu_q, b, P.Tq);
     t.k_row = pa_row(P.cu_k, b, P.Tk);
-    const int64_t n_q = pa_row(P.cu_q, b + 1, P.Tq) - t.q_row, n_k = pa_row(P.cu_k, b + 1, P.Tk) - t.k_row, r = (pair - start(b)) * 2;
+    const int64_t n_q = pa_row(P.cu_q, b + 1, P.Tq) - t.q_row, n_k = pa_row(P.cu_k, b + 1, P.Tk) - t.k_row, r = (pair - pt_start(P, b)) * 2;
     if (r >= (n_q + PT - 1) / PT * P.G) return false;
     t.n_q = (int)n_q;
     t.n_k = n_k > 0 ? (int)n_k : 0;
@@ -147,6 +138,19 @@ __device__ __forceinline__ bool pt_work(const PaParams &P, int64_t pair, PtWork 
     }
     w.masked = min(w.n - min(w.n, lowest / PT), PT_MASKED);
     return true;
+}
+// A warp finds it out (every role on its own).
+__device__ __forceinline__ bool pt_work(const PaParams &P, int64_t pair, PtWork &w) {
+    const int lane = threadIdx.x & 31;
+    int64_t b = 0;
+    for (int64_t n = P.B; n > 1;) {  // the sequence is one of n from b on
+        const int64_t step = (n + 31) / 32, at = lane * step;
+        const int k = __popc(__ballot_sync(~0u, at < n && pt_start(P, b + at) <= pair)) - 1;
+        if (k < 0) return false;
+        b += k * step;
+        n = min(step, n - k * step);
+    }
+    return pt_start(P, b) <= pair && pt_fill(P, b, pair, w);
 }
 
 template <typename T, typename C>
@@ -223,10 +227,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 if (lane == 0) mbar_arrive(&turn_empty[s]);
             }
             if (i >= items) return;
-            // the longest first: later tokens see more keys
+            // the longest first: later tokens of a sequence see more keys
             const unsigned turn = i / (unsigned)X.n_kv;
             PtWork w;
-            if (pt_work(P, X.pairs - 1 - turn, w) && !f(w, (int)(i - turn * X.n_kv))) return;
+            if (pt_work(P, X.order ? X.order[turn] : X.pairs - 1 - turn, w) && !f(w, (int)(i - turn * X.n_kv))) return;
             // (asked for when the pair's last tiles have been sent for, not before: a place taken early waits behind a long pair)
             if (warp == 9 && lane == 0) ahead = X.next ? gridDim.x + atomicAdd(X.next, 1u) : items;
         }
@@ -589,12 +593,47 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     }
 }
 
-// Clears the device flag and the line's counter.
-__global__ void pt_reset_kernel(unsigned long long *err, unsigned *next) {
+// Clears the device flag and the line's counter and, for several sequences, puts the pairs in order of their key tiles, most
+// first (pairs of the same number in any order, which no result depends on): a long one that starts last is what all wait
+// for (nine sequences, heads of 80: 40.3 us without).
+constexpr int PT_BINS = 256;
+__global__ void __launch_bounds__(1024) pt_order_kernel(PaParams P, int64_t pairs, unsigned *next, int *order) {
+    __shared__ int bins[PT_BINS];
     grid_dependency_wait();
     grid_launch_dependents();
-    *err = 0ull;
-    *next = 0u;
+    if (threadIdx.x == 0) *P.err = 0ull, *next = 0u;
+    if (!order) return;
+    auto bin = [&](int64_t pair) {
+        int64_t b = 0;
+        for (int64_t n = P.B; n > 1;) {
+            const int64_t half = n / 2;
+            if (pt_start(P, b + half) <= pair) b += half, n -= half;
+            else n = half;
+        }
+        PtWork w;
+        return pt_start(P, b) <= pair && pt_fill(P, b, pair, w) ? PT_BINS - 1 - min(w.n, PT_BINS - 2) : PT_BINS - 1;
+    };
+    for (int i = threadIdx.x; i < PT_BINS; i += blockDim.x) bins[i] = 0;
+    __syncthreads();
+    for (int64_t i = threadIdx.x; i < pairs; i += blockDim.x) atomicAdd(&bins[bin(i)], 1);
+    __syncthreads();
+    if (threadIdx.x < 32) {  // where each bin begins
+        constexpr int PER = PT_BINS / 32;
+        int n[PER], sum = 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) n[k] = bins[threadIdx.x * PER + k], sum += n[k];
+        int upto = sum;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int o = __shfl_up_sync(~0u, upto, s);
+            if ((int)threadIdx.x >= s) upto += o;
+        }
+        int at = upto - sum;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) bins[threadIdx.x * PER + k] = at, at += n[k];
+    }
+    __syncthreads();
+    for (int64_t i = threadIdx.x; i < pairs; i += blockDim.x) order[atomicAdd(&bins[bin(i)], 1)] = (int)i;
 }
 
 // ---------------------------------------------------------------- host
@@ -611,6 +650,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 pt_encoder() {
     }();
     return fn;
 }
+
+static int64_t pt_pairs(int64_t B, int64_t Tq, int64_t G) { return ((Tq / PT + B) * G >> 1) + B; }
+size_t pa_tc_workspace(int64_t B, int64_t Tq, int64_t G) { return 256 + (size_t)(pt_pairs(B, Tq, G) * 4 + 255) / 256 * 256; }
 
 bool pa_takes_tc(const PaParams &P) {
     return P.D <= 128 && P.D % 8 == 0 && aligned(P.q, 16) && aligned(P.k, 16) && aligned(P.v, 16) && aligned(P.y, 16) && P.ldq % 8 == 0 &&
@@ -634,15 +676,17 @@ static kq_status pt_launch(const char *fn, PtParams X, cudaStream_t st) {
                                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (e != CUDA_SUCCESS) return fail(KQ_ERR_CUDA, "%s: tensor map %d failed (%d)", fn, i, (int)e);
     }
-    X.pairs = ((P.Tq / PT + P.B) * P.G >> 1) + P.B;
+    X.pairs = pt_pairs(P.B, P.Tq, P.G);
     if (X.pairs * X.n_kv > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: too many row tiles", fn);
     auto kern = pt_kernel<T, C>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
     const int64_t items = X.pairs * X.n_kv;
     constexpr int SMS = 152;
     X.next = items > SMS ? reinterpret_cast<unsigned *>(P.err + 1) : nullptr;
+    int *order = X.next && P.B > 1 ? reinterpret_cast<int *>(P.err + 32) : nullptr;
+    X.order = order;
     if (e == cudaSuccess && X.next) {
-        e = launch_beside(pt_reset_kernel, dim3(1), dim3(1), 0, dim3(1), st, P.err, X.next);
+        e = launch_beside(pt_order_kernel, dim3(1), dim3(order ? 1024 : 32), 0, dim3(1), st, P, X.pairs, X.next, order);
         if (e == cudaSuccess) count_launch(R_ATTN);
     }
     if (e == cudaSuccess)
@@ -653,7 +697,7 @@ static kq_status pt_launch(const char *fn, PtParams X, cudaStream_t st) {
 }
 
 kq_status pa_tc(const char *fn, kq_dtype xt, const PaParams &P, unsigned long long wait_ns, int idle, cudaStream_t st) {
-    PtParams X{P, 0, P.n_q / P.G, P.scale < 0.0f, wait_ns, idle, aligned(P.y, 32) && P.ldy % 16 == 0 && P.D % 16 == 0, nullptr};
+    PtParams X{P, 0, P.n_q / P.G, P.scale < 0.0f, wait_ns, idle, aligned(P.y, 32) && P.ldy % 16 == 0 && P.D % 16 == 0, nullptr, nullptr};
     // (a scale of 0 weighs all keys alike, as any tiny one does, which keeps -inf times it -inf)
     X.p.scale = P.scale == 0.0f ? 1e-35f : fabsf(P.scale);
     auto go = [&](auto t) {

@@ -52,7 +52,7 @@ CASES = [
         (dict(D=12), BAD, "D=12"), (dict(D=264), BAD, "D=264"), (dict(ldq=511), BAD, "ldq=511"), (dict(ldk=255), BAD, "ldk=255"),
         (dict(ldv=255), BAD, "ldv=255"), (dict(ldy=8), BAD, "ldy=8"), (dict(causal=2), BAD, "causal=2"),
         (dict(scale=float("nan")), BAD, "scale"), (dict(k=P + 1), ALIGN, "aligned"), (dict(cu_k=P + 2), ALIGN, "aligned"),
-        (dict(ws=None), SPACE, "workspace"), (dict(n=255), SPACE, "255 bytes"), (dict(ws=P + 64), ALIGN, "256-byte")]),
+        (dict(ws=None), SPACE, "workspace"), (dict(n=511), SPACE, "511 bytes"), (dict(ws=P + 64), ALIGN, "256-byte")]),
 ]
 
 
