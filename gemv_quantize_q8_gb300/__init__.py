@@ -90,6 +90,10 @@ _SIGS = {
     "kq_attn_prompt_workspace_bytes": ([_I64, _I64, _I64, _I64, _I64], _SZ),
     "kq_attn_prompt": ([_I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_float, _I32, _P,
                         _I64, _P, _SZ, _P], _I32),
+    "kq_debug_attn_prompt_wait_timeout": ([_I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
+                                           ctypes.c_float, _I32, _P, _I64, _I32, _I64, _P, _SZ, _P], _I32),
+    "kq_debug_attn_cache_wait_timeout": ([_I32, _P, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_float, _P, _P, _P, _P, _I64, _I64, _P,
+                                          _I64, _P, _I32, _P, _I64, _I64, _P, _SZ, _P], _I32),
     "kq_debug_i8_form": ([_I64, _I64, _I64, _P, _P, _P], _I32),
     "kq_debug_i8_wait_timeout": ([_P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I32, _I64, _P, _SZ, _P], _I32),
     "kq_debug_tc_wait_timeout": ([_I32, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _SZ, _P], _I32),
@@ -397,3 +401,19 @@ def kq_debug_i8_wait_timeout(q, ldq, sx, w, ldw, sw, M, N, K, y, ldy, idle, wait
     """kq_gemm_i8's tensor-core kernel with a role idle (1: activations, 2: MMAs) and every wait limited to wait_limit_ns."""
     _check(lib().kq_debug_i8_wait_timeout(_ptr(q), ldq, _ptr(sx), _ptr(w), ldw, _ptr(sw), M, N, K, _ptr(y), ldy, idle,
                                           wait_limit_ns, _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def kq_debug_attn_prompt_wait_timeout(xt, q, ldq, k, ldk, v, ldv, cu_q, cu_k, B, Tq, Tk, n_q, n_kv, D, scale, causal, y, ldy, idle,
+                                      wait_limit_ns, workspace, ws_bytes, stream=None):
+    """kq_attn_prompt's tensor-core kernel with a role idle (1: tiles, 2: products) and every wait limited to wait_limit_ns."""
+    _check(lib().kq_debug_attn_prompt_wait_timeout(xt, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, n_q,
+                                                   n_kv, D, float(scale), int(causal), _ptr(y), ldy, idle, wait_limit_ns,
+                                                   _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def kq_debug_attn_cache_wait_timeout(xt, q, ldq, B, n_new, n_q, n_kv, D, scale, k_cache, v_cache, k_scale, v_scale, n_pages, page, table,
+                                     ldt, lens, yt, y, ldy, wait_limit_ns, workspace, ws_bytes, stream=None):
+    """kq_attn_cache_i8 with nothing fetched and every wait limited to wait_limit_ns."""
+    _check(lib().kq_debug_attn_cache_wait_timeout(xt, _ptr(q), ldq, B, n_new, n_q, n_kv, D, float(scale), _ptr(k_cache), _ptr(v_cache),
+                                                  _ptr(k_scale), _ptr(v_scale), n_pages, page, _ptr(table), ldt, _ptr(lens), yt, _ptr(y),
+                                                  ldy, wait_limit_ns, _ptr(workspace), ws_bytes, _stream(stream)))

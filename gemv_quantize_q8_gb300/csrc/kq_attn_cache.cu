@@ -33,6 +33,7 @@ namespace kq {
 constexpr int kAcUnit = 32;           // tokens
 constexpr int kAcLeast = 1;           // units of a warp
 constexpr int kAcMaxBlocks = 152;     // one an SM
+constexpr unsigned long long kAcWaitNs = 2000000000ull;  // limit of every wait
 constexpr float kAcLift = 128.0f;     // weights are held times this: f16 keeps their low bits, with room for kAcSlack
 constexpr float kAcSlack = 8.0f;      // a weight may grow to 2^8 before the sums are brought to a new maximum
 constexpr float kAcNone = -3.0e38f;   // the maximum of no token
@@ -50,6 +51,8 @@ struct AcParams {
     unsigned long long *err;  // device flag, cleared by the call
     float *parts;             // [blocks][2] partial results
     int blocks, warps;    // of the first kernel's grid
+    unsigned long long wait_ns;  // limit of every wait
+    bool idle;            // test hook: nothing is fetched
 };
 
 // What a warp (or a block) hands over: m and l of its rows, then their sums relative to 2^m, in the order in which a
@@ -683,13 +686,13 @@ __global__ void __launch_bounds__(NW * 64, 1)
             if (f.left > 0) f.start(P), f.look(P);
             int stage = 0;
             uint32_t phase = 1;
-            while (f.left > 0) {
+            while (f.left > 0 && !P.idle) {
                 bool free = sm100::mbar_test_wait(&empty[mate][stage], phase);
                 if (!free) {  // (bounded: whoever waits too long tells the others)
                     const uint64_t since = sm100::globaltimer_ns();
                     for (int i = 0; !free; ++i) {
                         free = sm100::mbar_test_wait(&empty[mate][stage], phase);
-                        if (!free && (i & 255) == 255 && (*(volatile int *)&aborted || sm100::globaltimer_ns() - since > 2000000000ull)) break;
+                        if (!free && (i & 255) == 255 && (*(volatile int *)&aborted || sm100::globaltimer_ns() - since > P.wait_ns)) break;
                     }
                 }
                 if (!free) {
@@ -713,7 +716,7 @@ __global__ void __launch_bounds__(NW * 64, 1)
             w.begin(P, it);
             for (int i = 0; i < n; ++i) {
                 // (a wait that runs out spoils the result, which the device flag tells)
-                if (!sm100::mbar_wait(&full[warp][stage], phase, &aborted)) aborted = 1;
+                if (!sm100::mbar_wait(&full[warp][stage], phase, &aborted, P.wait_ns)) aborted = 1;
                 w.unit(sm100::smem_u32(ring + stage * Ring::BYTES), scales[warp][stage], (at + i) * kAcUnit);
                 __syncwarp();
                 if (lane == 0) sm100::mbar_arrive(&empty[warp][stage]);
@@ -925,21 +928,10 @@ static bool ac_shape(int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv, int64_
            n_new * n_q <= 65536 && n_q % n_kv == 0 && D > 0 && D <= kKvMaxD && D % 16 == 0;
 }
 
-}  // namespace kq
-
-using namespace kq;
-
-extern "C" {
-
-size_t kq_attn_cache_i8_workspace_bytes(int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv, int64_t D) {
-    return ac_shape(B, n_new, n_q, n_kv, D) ? ac_workspace(n_new * (n_q / n_kv), D) : 0;
-}
-
-kq_status kq_attn_cache_i8(kq_dtype xt, const void *q, int64_t ldq, int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv, int64_t D,
-                           float scale, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale, const float *v_scale,
-                           int64_t n_pages, int64_t page, const int32_t *table, int64_t ldt, const int32_t *lens, kq_dtype yt, void *y,
-                           int64_t ldy, void *workspace, size_t ws_bytes, kq_stream_t stream) {
-    const char *fn = "kq_attn_cache_i8";
+static kq_status ac_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq, int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv,
+                         int64_t D, float scale, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale, const float *v_scale,
+                         int64_t n_pages, int64_t page, const int32_t *table, int64_t ldt, const int32_t *lens, kq_dtype yt, void *y,
+                         int64_t ldy, void *workspace, size_t ws_bytes, kq_stream_t stream, unsigned long long wait_ns, bool idle) {
     if (!is_value_type(xt) || !is_value_type(yt))
         return fail(KQ_ERR_UNSUPPORTED_DTYPE, "%s: %s type %s is not F32, F16 or BF16", fn, is_value_type(xt) ? "output" : "query",
                     dtype_name(is_value_type(xt) ? yt : xt));
@@ -970,9 +962,41 @@ kq_status kq_attn_cache_i8(kq_dtype xt, const void *q, int64_t ldq, int64_t B, i
     P.err = static_cast<unsigned long long *>(workspace);
     P.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + 256);
     P.blocks = kAcMaxBlocks;
+    P.wait_ns = wait_ns;
+    P.idle = idle;
     const cudaStream_t st = (cudaStream_t)stream;
     if (mt == 8) return D <= 64 ? launch_ac<64, 8>(fn, P, st) : D <= 128 ? launch_ac<128, 8>(fn, P, st) : launch_ac<256, 8>(fn, P, st);
     return D <= 64 ? launch_ac<64, 16>(fn, P, st) : D <= 128 ? launch_ac<128, 16>(fn, P, st) : launch_ac<256, 16>(fn, P, st);
+}
+
+}  // namespace kq
+
+using namespace kq;
+
+extern "C" {
+
+size_t kq_attn_cache_i8_workspace_bytes(int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv, int64_t D) {
+    return ac_shape(B, n_new, n_q, n_kv, D) ? ac_workspace(n_new * (n_q / n_kv), D) : 0;
+}
+
+kq_status kq_attn_cache_i8(kq_dtype xt, const void *q, int64_t ldq, int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv, int64_t D,
+                           float scale, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale, const float *v_scale,
+                           int64_t n_pages, int64_t page, const int32_t *table, int64_t ldt, const int32_t *lens, kq_dtype yt, void *y,
+                           int64_t ldy, void *workspace, size_t ws_bytes, kq_stream_t stream) {
+    return ac_call("kq_attn_cache_i8", xt, q, ldq, B, n_new, n_q, n_kv, D, scale, k_cache, v_cache, k_scale, v_scale, n_pages, page, table,
+                   ldt, lens, yt, y, ldy, workspace, ws_bytes, stream, kAcWaitNs, false);
+}
+
+kq_status kq_debug_attn_cache_wait_timeout(kq_dtype xt, const void *q, int64_t ldq, int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv,
+                                           int64_t D, float scale, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale,
+                                           const float *v_scale, int64_t n_pages, int64_t page, const int32_t *table, int64_t ldt,
+                                           const int32_t *lens, kq_dtype yt, void *y, int64_t ldy, int64_t wait_limit_ns, void *workspace,
+                                           size_t ws_bytes, kq_stream_t stream) {
+    const char *fn = "kq_debug_attn_cache_wait_timeout";
+    if (wait_limit_ns < 1000 || wait_limit_ns > 1000000000)
+        return fail(KQ_ERR_INVALID_ARG, "%s: wait_limit_ns must be in [1e3, 1e9]", fn);
+    return ac_call(fn, xt, q, ldq, B, n_new, n_q, n_kv, D, scale, k_cache, v_cache, k_scale, v_scale, n_pages, page, table, ldt, lens, yt, y,
+                   ldy, workspace, ws_bytes, stream, (unsigned long long)wait_limit_ns, true);
 }
 
 }  // extern "C"

@@ -186,21 +186,10 @@ static bool pa_shape(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv, int64_t D
            n_q % n_kv == 0 && D > 0 && D <= 256 && D % 8 == 0;
 }
 
-}  // namespace kq
-
-using namespace kq;
-
-extern "C" {
-
-size_t kq_attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv, int64_t D) {
-    return pa_shape(B, Tq, n_q, n_kv, D) ? pa_tc_workspace(B, Tq, n_q / n_kv) : 0;
-}
-
-kq_status kq_attn_prompt(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+static kq_status pa_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                          const int32_t *cu_q, const int32_t *cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t n_q, int64_t n_kv,
-                         int64_t D, float scale, int causal, void *y, int64_t ldy, void *workspace, size_t ws_bytes,
-                         kq_stream_t stream) {
-    const char *fn = "kq_attn_prompt";
+                         int64_t D, float scale, int causal, void *y, int64_t ldy, void *workspace, size_t ws_bytes, kq_stream_t stream,
+                         int idle = 0, unsigned long long wait_ns = kPtWaitNs) {
     if (xt != KQ_F16 && xt != KQ_BF16) return fail(KQ_ERR_UNSUPPORTED_DTYPE, "%s: row type %s is not F16 or BF16", fn, dtype_name(xt));
     if (!q || !k || !v || !y) return fail(KQ_ERR_INVALID_ARG, "%s: null rows", fn);
     if (!cu_q || !cu_k) return fail(KQ_ERR_INVALID_ARG, "%s: null %s", fn, cu_q ? "cu_k" : "cu_q");
@@ -216,19 +205,50 @@ kq_status kq_attn_prompt(kq_dtype xt, const void *q, int64_t ldq, const void *k,
     if (!(fabsf(scale) <= 3.0e38f)) return fail(KQ_ERR_INVALID_ARG, "%s: scale must be finite", fn);
     if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(y, 2) || !aligned(cu_q, 4) || !aligned(cu_k, 4))
         return fail(KQ_ERR_ALIGNMENT, "%s: a pointer is not aligned to its elements", fn);
-    const size_t need = kq_attn_prompt_workspace_bytes(B, Tq, n_q, n_kv, D);
+    const size_t need = pa_tc_workspace(B, Tq, n_q / n_kv);
     if (!workspace || ws_bytes < need)
         return fail(KQ_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace ? ws_bytes : (size_t)0, need);
     if (!aligned(workspace, 256)) return fail(KQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", fn);
     const PaParams P{q, k, v, y, ldq, ldk, ldv, ldy, cu_q, cu_k, B, Tq, Tk, (int)n_q, (int)(n_q / n_kv), (int)D,
                      scale * 1.44269504f, causal != 0, static_cast<unsigned long long *>(workspace)};
     const cudaStream_t st = (cudaStream_t)stream;
-    if (pa_takes_tc(P)) return pa_tc(fn, xt, P, kPtWaitNs, 0, st);
+    if (pa_takes_tc(P)) return pa_tc(fn, xt, P, wait_ns, idle, st);
+    if (idle) return fail(KQ_ERR_INVALID_ARG, "%s: these rows do not take the tensor-core path", fn);
     auto go = [&](auto t) {
         using T = decltype(t);
         return D <= 64 ? launch_pa<T, 64>(fn, P, st) : D <= 128 ? launch_pa<T, 128>(fn, P, st) : launch_pa<T, 256>(fn, P, st);
     };
     return xt == KQ_F16 ? go(__half{}) : go(__nv_bfloat16{});
+}
+
+}  // namespace kq
+
+using namespace kq;
+
+extern "C" {
+
+size_t kq_attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv, int64_t D) {
+    return pa_shape(B, Tq, n_q, n_kv, D) ? pa_tc_workspace(B, Tq, n_q / n_kv) : 0;
+}
+
+kq_status kq_attn_prompt(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                         const int32_t *cu_q, const int32_t *cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t n_q, int64_t n_kv,
+                         int64_t D, float scale, int causal, void *y, int64_t ldy, void *workspace, size_t ws_bytes,
+                         kq_stream_t stream) {
+    return pa_call("kq_attn_prompt", xt, q, ldq, k, ldk, v, ldv, cu_q, cu_k, B, Tq, Tk, n_q, n_kv, D, scale, causal, y, ldy, workspace,
+                   ws_bytes, stream);
+}
+
+kq_status kq_debug_attn_prompt_wait_timeout(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                            const int32_t *cu_q, const int32_t *cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t n_q,
+                                            int64_t n_kv, int64_t D, float scale, int causal, void *y, int64_t ldy, int idle,
+                                            int64_t wait_limit_ns, void *workspace, size_t ws_bytes, kq_stream_t stream) {
+    const char *fn = "kq_debug_attn_prompt_wait_timeout";
+    if (idle != 1 && idle != 2) return fail(KQ_ERR_INVALID_ARG, "%s: idle=%d is not 1 or 2", fn, idle);
+    if (wait_limit_ns < 1000 || wait_limit_ns > 1000000000)
+        return fail(KQ_ERR_INVALID_ARG, "%s: wait_limit_ns must be in [1e3, 1e9]", fn);
+    return pa_call(fn, xt, q, ldq, k, ldk, v, ldv, cu_q, cu_k, B, Tq, Tk, n_q, n_kv, D, scale, causal, y, ldy, workspace, ws_bytes, stream,
+                   idle, (unsigned long long)wait_limit_ns);
 }
 
 }  // extern "C"

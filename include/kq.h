@@ -449,7 +449,8 @@ KQ_API kq_status kq_kv_read_i8(const int8_t *k_cache, const int8_t *v_cache, con
  * same bits, but a row's last bits may change with its neighbours' lengths.  A token that sees nothing (lens[b] = 0, or a row before token 0) gives 0.  A page
  * outside [0, n_pages), or a length past ldt pages, gives NaN.
  * workspace: kq_attn_cache_i8_workspace_bytes(...) bytes (0: a shape that the call refuses), 256-byte aligned; its content
- * does not matter before the call, and calls that share it must not overlap. */
+ * does not matter before the call, and calls that share it must not overlap; kq_read_device_flag applies to it (a wait for
+ * the cache that timed out). */
 KQ_API size_t kq_attn_cache_i8_workspace_bytes(int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv, int64_t D);
 KQ_API kq_status kq_attn_cache_i8(kq_dtype xt, const void *q, int64_t ldq, int64_t B, int64_t n_new, int64_t n_q, int64_t n_kv,
                                   int64_t D, float scale, const int8_t *k_cache, const int8_t *v_cache, const float *k_scale,
@@ -465,8 +466,8 @@ KQ_API kq_status kq_attn_cache_i8(kq_dtype xt, const void *q, int64_t ldq, int64
  * to 256; Tq and Tk up to 2^31 - 256, B up to 2^24, n_q up to 65535; scale is finite.  y may be q itself (same stride).
  * Scores and sums are fp32; the weights are rounded to xt for the second product.  A token that sees no key gives 0; what a
  * token does not see has no influence on it, infinities and NaN included.  Rows behind cu_q[B] are left as they were.
- * workspace: kq_attn_prompt_workspace_bytes(...) bytes (0: a shape that the call refuses), 256-byte aligned;
- * kq_read_device_flag applies to it (a tensor-core pipeline wait that timed out). */
+ * workspace: kq_attn_prompt_workspace_bytes(...) bytes (0: a shape that the call refuses), 256-byte aligned; its content does
+ * not matter before the call, and calls that share it must not overlap; kq_read_device_flag applies to it (a tensor-core pipeline wait that timed out). */
 KQ_API size_t kq_attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv, int64_t D);
 KQ_API kq_status kq_attn_prompt(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                                 const int32_t *cu_q, const int32_t *cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t n_q,
@@ -537,6 +538,23 @@ KQ_API kq_status kq_debug_i8_form(int64_t M, int64_t N, int64_t K, int *ctas, in
 KQ_API kq_status kq_debug_i8_wait_timeout(const int8_t *q, int64_t ldq, const float *sx, const int8_t *w, int64_t ldw,
                                           const float *sw, int64_t M, int64_t N, int64_t K, float *y, int64_t ldy, int idle,
                                           int64_t wait_limit_ns, void *workspace, size_t ws_bytes, kq_stream_t stream);
+
+/* Test hooks of the attention kernels' bounded waits: the calls of the same names with one role kept idle and every wait limited
+ * to wait_limit_ns (1e3 .. 1e9; the calls use 2 s).  Prompts: idle = 1 what brings the tiles, 2 what issues the products
+ * (rows that take the tensor-core path); cache: nothing is fetched.  The waits run out, the thread blocks count it in
+ * the device flag (kq_read_device_flag), let their copies and MMAs in flight end, and return; y is not written or
+ * incomplete. */
+KQ_API kq_status kq_debug_attn_prompt_wait_timeout(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
+                                                   int64_t ldv, const int32_t *cu_q, const int32_t *cu_k, int64_t B, int64_t Tq,
+                                                   int64_t Tk, int64_t n_q, int64_t n_kv, int64_t D, float scale, int causal, void *y,
+                                                   int64_t ldy, int idle, int64_t wait_limit_ns, void *workspace, size_t ws_bytes,
+                                                   kq_stream_t stream);
+KQ_API kq_status kq_debug_attn_cache_wait_timeout(kq_dtype xt, const void *q, int64_t ldq, int64_t B, int64_t n_new, int64_t n_q,
+                                                  int64_t n_kv, int64_t D, float scale, const int8_t *k_cache, const int8_t *v_cache,
+                                                  const float *k_scale, const float *v_scale, int64_t n_pages, int64_t page,
+                                                  const int32_t *table, int64_t ldt, const int32_t *lens, kq_dtype yt, void *y,
+                                                  int64_t ldy, int64_t wait_limit_ns, void *workspace, size_t ws_bytes,
+                                                  kq_stream_t stream);
 
 #ifdef __cplusplus
 }
