@@ -3,9 +3,10 @@
 // For a query row q (one token and head) over the tokens j that it sees, with s_j = scale * ks * (q . K_j) for codes
 // K, V and their blocks' scales ks, vs:
 //   m = max s_j,  l = sum 2^(s_j - m),  y = (sum 2^(s_j - m) vs V_j) / l       (s in units of log 2)
-// Bound by the cache's bytes: each is read once, by TMA, into a ring of the warp that needs it (2 or 4 KB a copy,
-// several units under way; a warp waits for nobody else).  (By 16-byte copies of every lane the loads alone took
-// 136 us for two sequences of 131072, 537 MB.)
+// Bound by the cache's bytes: each is read once, by TMA, into a ring of the warp that needs it (2 or 4 KB a copy, two
+// units under way; a warp waits for nobody else).  Two sequences of 131072 tokens, 32 heads over 8 of 128, 537 MB: 89.6
+// us, 6.0 TB/s, of which the start, the parts and their join take 10; 64 users of up to 8192 tokens, 516 MB, 100.8; one user of
+// 900 tokens 9.7, all of it latency.  (By 16-byte copies of every lane the loads alone took 136 us for the first.)
 //
 // The products run on m16n8k16 instructions.  Codes are exact in f16; a query row is brought to |q| < 2 by a power
 // of two and split into two f16 (22 bits), as the weights 2^(s - m) vs are.  With up to eight rows (the query heads of
@@ -16,8 +17,8 @@
 //   values: lane 4n + c takes piece n of tokens 2c, 2c + 1, 2c + 8, 2c + 9: the tokens whose weights it holds, the
 //           bytes of two tokens paired by permutes.
 // With the copies' 128-byte swizzle neither has bank conflicts.
-// A unit is 32 tokens, two halves of 16 with scales of their own (a page holds whole halves).  All units of all sequences and heads form one line, cut into equal shares, one a
-// warp: lengths may differ as they like.  A row whose units are shared by warps is put together in shared memory,
+// A unit is 32 tokens, two halves of 16 with scales of their own (a page holds whole halves).  All units of all sequences
+// and heads form one line, cut into equal shares, one a warp: lengths may differ as they like.  A row whose units are shared by warps is put together in shared memory,
 // one that is shared by thread blocks through the workspace and a second kernel, in a fixed order.
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -6,7 +6,8 @@
 // of the unrounded ones).
 //
 // The form for any head width up to 256 and rows at any address: a thread block takes 64 tokens of one head, 16 a
-// warp, and goes over the keys in tiles of 32, on m16n8k16 instructions.
+// warp, and goes over the keys in tiles of 32, on m16n8k16 instructions (16384 tokens, 32 heads over 8 of 128: 21.5 ms, 0.1
+// PFLOP/s; bound by its element-wise staging of keys and values).
 // A masked weight is 0, but 0 times an infinity is not: rows of values past the sequence's end are
 // taken as zeros, and a tile that some row sees only in part and that holds an infinity or NaN is added up one key at
 // a time, leaving out what is masked.

@@ -7,6 +7,8 @@
 // read once and every code written once.  Which blocks those are follows from cu and lens on the device: a run of n
 // tokens touches at most floor(n / page) + 2 pages, and at most n; so sequence b's share of the grid starts at
 // floor(cu[b] / page) + 2b, or at cu[b], whichever makes the smaller grid.
+// 8192 tokens, 8 heads of 128, fp32: append 22 us (84 MB, 12.4 at the memory's rate), bound by a block's chain of waits (where
+// it is, positions, rows, maximum); reading them back as bf16 11 us.  One token each of 64 users: 4 us each.
 // The maximum, every product and sum are rounded one by one, so that codes and scales are the same bits whatever
 // the grid or the vector width.
 #include <type_traits>
