@@ -18,8 +18,9 @@
 //           bytes of two tokens paired by permutes.
 // With the copies' 128-byte swizzle neither has bank conflicts.
 // A unit is 32 tokens, two halves of 16 with scales of their own (a page holds whole halves).  All units of all sequences
-// and heads form one line, cut into equal shares, one a warp: lengths may differ as they like.  A row whose units are shared by warps is put together in shared memory,
-// one that is shared by thread blocks through the workspace and a second kernel, in a fixed order.
+// and heads form one line, cut into equal shares, one a warp: lengths may differ as they like.  A row whose units are
+// shared by warps is put together in shared memory, one that is shared by thread blocks through the workspace and a
+// second kernel, in a fixed order.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>

@@ -3,7 +3,8 @@
 // A block of the cache (a page and head) has one scale, so its largest magnitude has to be known before its
 // first code is written, and when a later token raises it the codes that are there follow:
 //   s' = max(s, max |x| / 127),   q' = rint(q * (s / s')) for the old tokens,   q = rint(x * (1 / s')) for the new.
-// A group of threads takes one block of the cache that the call touches (four warps, or one where the sequences have few rows): it keeps the new rows in registers between the maximum and the codes, so every row is
+// A group of threads (256, or a warp where the sequences have few rows) takes one block of the cache that the call
+// touches: it keeps the new rows in registers between the maximum and the codes, so every row is
 // read once and every code written once.  Which blocks those are follows from cu and lens on the device: a run of n
 // tokens touches at most floor(n / page) + 2 pages, and at most n; so sequence b's share of the grid starts at
 // floor(cu[b] / page) + 2b, or at cu[b], whichever makes the smaller grid.
