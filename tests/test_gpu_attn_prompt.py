@@ -169,6 +169,30 @@ def test_many_sequences():
     run(n, n, 2, 1, 64)
 
 
+def test_more_sequences_than_a_warp_finds_in_two_steps():
+    g = np.random.default_rng(2)
+    n = g.integers(0, 4, 2500).tolist()
+    run(n, n, 6, 2, 64, "f16")
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each; both take their pairs from a line of their own."""
+    scale, work = 128 ** -0.5, []
+    for seed, tokens in ((1, [1500, 800]), (2, [3000])):
+        p = Prompt(tokens, tokens, 8, 2, 128, "bf16", seed=seed)
+        q, k, v = (x.reshape(x.shape[0], -1).to(DEV) for x in (p.q, p.k, p.v))
+        n = kq.kq_attn_prompt_workspace_bytes(len(tokens), p.Tq, 8, 2, 128)
+        work.append((p, q, k, v, ints(np.cumsum([0] + tokens)), torch.zeros_like(q), torch.zeros(n, dtype=torch.uint8, device=DEV), n, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for p, q, k, v, cu, y, ws, n, stream in work:
+            kq.kq_attn_prompt(kq.BF16, q, 1024, k, 256, v, 256, cu, cu, len(p.nq), p.Tq, p.Tk, 8, 2, 128, scale, 1, y, 1024, ws, n, stream=stream)
+    torch.cuda.synchronize()
+    for p, _, _, _, _, y, ws, _, _ in work:
+        assert kq.kq_read_device_flag(ws) == 0
+        p.check(y.double().cpu().numpy().reshape(p.Tq, 8, 128), scale, True, rows=40)
+
+
 def test_repeatable_streams_and_graphs():
     p, y = run([500, 77], [500, 77], 4, 2, 128)
     assert np.array_equal(p.call(128 ** -0.5, True, stream=torch.cuda.Stream()), y)
