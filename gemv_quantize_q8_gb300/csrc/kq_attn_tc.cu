@@ -35,9 +35,10 @@ constexpr int PT_MASKED = 3;        // key tiles that some row of a block's (at 
 constexpr float kPtNone = -1.0e30f; // the maximum of no key, in units of log 2
 constexpr float kPtSlack = 8.0f;
 
-template <int DP_>
+template <int DP_, int OW_>
 struct PtCfg {
-    static constexpr int DP = DP_;             // D rounded up to 64 or 128
+    static constexpr int DP = DP_;             // D rounded up to 64 or 128: what is loaded
+    static constexpr int OW = OW_;             // D rounded up to 64, 96 or 128: columns of the sums
     static constexpr int CH = DP / 64;         // boxes of 64 elements
     static constexpr int BOX = PT * 128;       // bytes of one
     static constexpr int TILE = CH * BOX;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             const bool one = pt_elect();
             constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u;
             const uint32_t id_s = idesc_f16_f32(PT, PT) | type | (X.negate ? 1u << 13 : 0u);
-            constexpr uint32_t id_o = idesc_f16_f32(PT, C::DP) | type | (1u << 16);  // V: [token][d]
+            constexpr uint32_t id_o = idesc_f16_f32(PT, C::OW) | type | (1u << 16);  // V: [token][d]
             const uint64_t dQ = smem_desc(smem_u32(sm), 1024, 2), dK = smem_desc(smem_u32(sKV), 1024, 2);
             // 64 elements of d a box, boxes BOX apart; eight tokens 1024 bytes apart
             const uint64_t dV = (dK & ~((uint64_t)0x3FFF << 16)) | (uint64_t)(C::BOX >> 4) << 16;
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                             if (one) {
 #pragma unroll
                                 for (int k = 0; k < PT / 16; ++k)
-                                    mma_f16_ts(C::O_COL + q * C::DP, q * 128 + k * 8, dV + (uint64_t)(sv * (C::TILE >> 4) + k * (2048 >> 4)),
+                                    mma_f16_ts(C::O_COL + q * C::OW, q * 128 + k * 8, dV + (uint64_t)(sv * (C::TILE >> 4) + k * (2048 >> 4)),
                                                id_o, at > 0 || k > 0);
                                 mma_commit(&o_full[q]);
                             }
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         // ------------------------------------------------------------ weights and results, one row a thread
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int q = warp >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16, ts = lane_base + q * 128, to = lane_base + C::O_COL + q * C::DP;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16, ts = lane_base + q * 128, to = lane_base + C::O_COL + q * C::OW;
         unsigned t = 0;  // this row tile's key tiles so far
         walk([&](const PtWork &w, int kv_head) {
             const int first = of(w.first, q), token = first + row, limit = first < w.t.n_q ? pa_limit(P, w.t, token) : 0, n = of(w.tiles, q);
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                     if (i > 0) {
                         if (!wait(&o_full[q], (t - 1) & 1)) break;
 #pragma unroll 1
-                        for (int c = 0; c < C::DP; c += 32) {
+                        for (int c = 0; c < C::OW; c += 32) {
                             float o[32];
                             uint32_t r[32];
                             tmem_ld32(to + c, o);
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             T *y = static_cast<T *>(P.y) + (w.t.q_row + token) * P.ldy + (int64_t)(kv_head * P.G + of(w.head, q)) * P.D;
             // (not unrolled: code that runs once a pair comes from memory)
 #pragma unroll 1
-            for (int c = 0; c < C::DP; c += 32) {
+            for (int c = 0; c < C::OW; c += 32) {
                 float o[32];
                 if (n) {
                     tmem_ld32(to + c, o);
@@ -703,7 +704,8 @@ kq_status pa_tc(const char *fn, kq_dtype xt, const PaParams &P, unsigned long lo
     X.p.scale = P.scale == 0.0f ? 1e-35f : fabsf(P.scale);
     auto go = [&](auto t) {
         using T = decltype(t);
-        return P.D <= 64 ? pt_launch<T, PtCfg<64>>(fn, X, st) : pt_launch<T, PtCfg<128>>(fn, X, st);
+        if (P.D <= 64) return pt_launch<T, PtCfg<64, 64>>(fn, X, st);
+        return P.D <= 96 ? pt_launch<T, PtCfg<128, 96>>(fn, X, st) : pt_launch<T, PtCfg<128, 128>>(fn, X, st);
     };
     return xt == KQ_F16 ? go(__half{}) : go(__nv_bfloat16{});
 }
