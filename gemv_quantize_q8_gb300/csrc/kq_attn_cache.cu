@@ -4,8 +4,8 @@
 // K, V and their blocks' scales ks, vs:
 //   m = max s_j,  l = sum 2^(s_j - m),  y = (sum 2^(s_j - m) vs V_j) / l       (s in units of log 2)
 // Bound by the cache's bytes: each is read once, by TMA, into a ring of the warp that needs it (2 or 4 KB a copy, two
-// units under way; a warp waits for nobody else).  Two sequences of 131072 tokens, 32 heads over 8 of 128, 537 MB: 89.6
-// us, 6.0 TB/s, of which the start, the parts and their join take 10; 64 users of up to 8192 tokens, 516 MB, 100.8; one user of
+// units under way; a warp waits for nobody else).  Two sequences of 131072 tokens, 32 heads over 8 of 128, 537 MB: 87.7
+// us, 6.1 TB/s, of which the start, the parts and their join take 10; 64 users of up to 8192 tokens, 516 MB, 88.4; one user of
 // 900 tokens 9.7, all of it latency.  (By 16-byte copies of every lane the loads alone took 136 us for the first.)
 //
 // The products run on m16n8k16 instructions.  Codes are exact in f16; a query row is brought to |q| < 2 by a power
@@ -18,9 +18,9 @@
 //           bytes of two tokens paired by permutes.
 // With the copies' 128-byte swizzle neither has bank conflicts.
 // A unit is 32 tokens, two halves of 16 with scales of their own (a page holds whole halves).  All units of all sequences
-// and heads form one line, cut into equal shares, one a warp: lengths may differ as they like.  A row whose units are
-// shared by warps is put together in shared memory, one that is shared by thread blocks through the workspace and a
-// second kernel, in a fixed order.
+// and heads form one line, cut into equal shares, one a warp (an item's beginning counts as units, too): lengths may differ
+// as they like.  A row whose units are shared by warps is put together in shared memory, one that is shared by thread
+// blocks through the workspace and a second kernel, in a fixed order.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -34,6 +34,11 @@ namespace kq {
 
 constexpr int kAcUnit = 32;           // tokens
 constexpr int kAcLeast = 1;           // units of a warp
+// What an item's beginning (its queries are loaded and split) costs a warp, in units, where the line is cut into shares; 64
+// users of up to 8192 tokens: 98.5 us without it, 91.0 with 1, 88.4 with 2 and 3.  Not for shares of fewer than two units
+// with it: their borders then fall less evenly (16 users of up to 512 tokens 13.2 us without, 13.6 with it; 32 users,
+// whose shares have two: 18.9 and 15.5).
+constexpr int kAcStart = 2;
 constexpr int kAcMaxBlocks = 152;     // one an SM
 constexpr unsigned long long kAcWaitNs = 2000000000ull;  // limit of every wait
 constexpr float kAcLift = 128.0f;     // weights are held times this: f16 keeps their low bits, with room for kAcSlack
@@ -92,58 +97,80 @@ __device__ __forceinline__ int ac_blocks(const AcParams &P, int64_t total, int w
     return n < 1 ? 1 : n < P.blocks ? (int)n : P.blocks;
 }
 
-// Where the sequences lie on the line: thread t of the block sums up `per` of them, and end[t] is where they end.
+// Where the sequences lie on the line: thread t of the block sums up `per` of them; units and places up to their end.
 template <int THREADS>
 struct AcLine {
-    int64_t end[THREADS], warps[THREADS / 32];
+    int64_t units[THREADS], places[THREADS], warps[THREADS / 32];
+    int full[THREADS / 32];
 };
-// All threads of the block; the line's length, in units of all heads and row tiles.
+// Its length.  Every item begins with `start` places without units.
+struct AcTotal {
+    int64_t units, places;
+    int blocks, start;
+};
+// All threads of the block.
 template <int THREADS>
-__device__ __forceinline__ int64_t ac_line(const AcParams &P, AcLine<THREADS> &line) {
+__device__ __forceinline__ AcTotal ac_line(const AcParams &P, AcLine<THREADS> &line, int warps) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t per = (P.c.B + THREADS - 1) / THREADS, b0 = threadIdx.x * per;
+    const int64_t items = (int64_t)P.c.n_kv * P.tiles;  // of a sequence
     int64_t n = 0;
-    for (int64_t b = b0; b < b0 + per && b < P.c.B; ++b) n += ac_units(P, b);
-    n *= P.c.n_kv * P.tiles;
+    int full = 0;  // sequences with units
+    for (int64_t b = b0; b < b0 + per && b < P.c.B; ++b) {
+        const int units = ac_units(P, b);
+        n += units;
+        full += units > 0;
+    }
+    n *= items;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
         const int64_t o = __shfl_up_sync(~0u, n, s);
-        if (lane >= s) n += o;
+        const int f = __shfl_up_sync(~0u, full, s);
+        if (lane >= s) n += o, full += f;
     }
-    if (lane == 31) line.warps[warp] = n;
+    if (lane == 31) line.warps[warp] = n, line.full[warp] = full;
     __syncthreads();
     int64_t total = 0;
+    int all = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w == warp) n += total;
+        if (w == warp) n += total, full += all;
         total += line.warps[w];
+        all += line.full[w];
     }
-    line.end[threadIdx.x] = n;
+    AcTotal r;
+    r.units = total;
+    r.blocks = ac_blocks(P, total, warps);
+    r.places = total + kAcStart * items * all;
+    r.start = r.places >= 2ll * r.blocks * warps ? kAcStart : 0;
+    if (!r.start) r.places = total;
+    line.units[threadIdx.x] = n;
+    line.places[threadIdx.x] = n + r.start * items * full;
     __syncthreads();
-    return total;
+    return r;
 }
-// The item that unit u (below the line's length) lies in, and its place in it.
+// The item that place u (below the line's length) lies in, and its place in it; returns the units of the line before it.
 template <int THREADS>
-__device__ __forceinline__ AcItem ac_find(const AcParams &P, const AcLine<THREADS> &line, int64_t u, int &at) {
+__device__ __forceinline__ int64_t ac_find(const AcParams &P, const AcLine<THREADS> &line, int start, int64_t u, AcItem &it, int &at) {
     int lo = 0;  // threads whose sequences end at or before u
 #pragma unroll
     for (int s = THREADS / 2; s; s >>= 1)
-        if (line.end[lo + s - 1] <= u) lo += s;
-    u -= lo ? line.end[lo - 1] : 0;
+        if (line.places[lo + s - 1] <= u) lo += s;
+    int64_t before = 0;
+    if (lo) before = line.units[lo - 1], u -= line.places[lo - 1];
     const int64_t per = (P.c.B + THREADS - 1) / THREADS;
-    AcItem it;
-    it.b = lo * per;
-    for (;; ++it.b) {
+    for (it.b = lo * per;; ++it.b) {
         it.units = ac_units(P, it.b);
-        const int64_t mine = (int64_t)it.units * P.c.n_kv * P.tiles;
+        const int64_t items = it.units ? (int64_t)P.c.n_kv * P.tiles : 0, mine = items * (it.units + start);
         if (u < mine) break;
         u -= mine;
+        before += items * it.units;
     }
-    const int64_t i = ac_div(u, it.units);
-    at = (int)(u - i * it.units);
+    const int64_t i = ac_div(u, it.units + start);
+    at = (int)(u - i * (it.units + start));
     it.h = (int)((uint32_t)i / (uint32_t)P.tiles);
     it.tile = (int)i - it.h * P.tiles;
-    return it;
+    return before + i * it.units;
 }
 // The next item that has units (there is one).
 __device__ __forceinline__ void ac_next(const AcParams &P, AcItem &it) {
@@ -660,7 +687,7 @@ __global__ void __launch_bounds__(NW * 64, 1)
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
     if (blockIdx.x == 0 && tid == 0) *P.err = 0ull;  // (an error is counted two seconds later at the earliest)
-    const int64_t total = ac_line(P, line);
+    const AcTotal total = ac_line(P, line, NW);
     // rows of sequences without tokens
     for (int64_t b = blockIdx.x; b < P.c.B; b += gridDim.x)
         if (P.c.lens[b] <= 0)
@@ -668,23 +695,30 @@ __global__ void __launch_bounds__(NW * 64, 1)
                 const int t = i / (P.n_q * D);
                 ac_store(P.y, P.yt, (b * P.n_new + t) * P.ldy + i - t * (P.n_q * D), 0.0f);
             }
-    const int blocks = ac_blocks(P, total, NW);
-    if ((int)blockIdx.x >= blocks) return;
-    const AcShares shares(total, blocks);
-    const int64_t first = shares(blockIdx.x), last = shares(blockIdx.x + 1);
-    if (first >= last) return;
-    const AcShares mine(last - first, NW);
+    if ((int)blockIdx.x >= total.blocks || !total.units) return;
+    const AcShares shares(total.places, total.blocks);
+    const int64_t first_place = shares(blockIdx.x), last_place = shares(blockIdx.x + 1);
+    const AcShares mine(last_place - first_place, NW);
     const int mate = warp % NW;  // the first warps work on what the others bring
-    const int64_t u0 = first + mine(mate), u1 = first + mine(mate + 1);
+    // where the warp's units begin (lane 0) and end, and the block's: a lane each
     AcItem it;
     int at = 0;
-    if (u0 < u1) it = ac_find(P, line, u0, at);
+    int64_t unit = total.units;
+    {
+        const int64_t place = lane & 2 ? (lane & 1 ? last_place : first_place) : first_place + mine(mate + (lane & 1));
+        if (place < total.places) {
+            unit = ac_find(P, line, total.start, place, it, at);
+            at = max(at - total.start, 0);
+            unit += at;
+        }
+    }
+    const int64_t u1 = __shfl_sync(~0u, unit, 1);
     if (warp >= NW) {
         // ------------------------------------------------------------ one lane brings the units of one of the first warps
         // (one warp for all, its lanes in turns, could not keep up, nor could two lanes a warp)
         if (NW == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (lane == 0) {
-            AcFetch<DP> f{it, at, u1 - u0};
+            AcFetch<DP> f{it, at, u1 - unit};
             if (f.left > 0) f.start(P), f.look(P);
             int stage = 0;
             uint32_t phase = 1;
@@ -708,7 +742,12 @@ __global__ void __launch_bounds__(NW * 64, 1)
         __syncwarp();
     } else {
         if (NW == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        if (u0 < u1) {
+        const int64_t u0 = __shfl_sync(~0u, unit, 0), first = __shfl_sync(~0u, unit, 2), last = __shfl_sync(~0u, unit, 3);
+        it.b = __shfl_sync(~0u, it.b, 0);
+        it.h = __shfl_sync(~0u, it.h, 0);
+        it.tile = __shfl_sync(~0u, it.tile, 0);
+        it.units = __shfl_sync(~0u, it.units, 0);
+        at = __shfl_sync(~0u, at, 0);
         AcWarp<DP, MT> w;
         int stage = 0;
         uint32_t phase = 0;
@@ -736,7 +775,6 @@ __global__ void __launch_bounds__(NW * 64, 1)
             u += n;
             at = 0;
             if (u < u1) ac_next(P, it);
-        }
         }
         // the first warps meet: what they share is in place
         asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
@@ -806,20 +844,19 @@ __global__ void __launch_bounds__(256) ac_join_kernel(AcParams P) {
     __shared__ float weight[kAcMaxBlocks][MT], sum[MT];
     const int c = blockIdx.x + 1, D = P.c.D;
     constexpr int size = kAcPart<DP, MT>;
-    const int64_t total = ac_line(P, line);
-    const int blocks = ac_blocks(P, total, P.warps);
-    bool cut = c < blocks;
-    const AcShares shares(total, blocks);
-    const int64_t border = cut ? shares(c) : 0, before = cut ? shares(c - 1) : 0;
+    const AcTotal total = ac_line(P, line, P.warps);
+    bool cut = c < total.blocks;
+    const AcShares shares(total.places, total.blocks);
     AcItem it;
     int parts = 0;
     if (cut) {
-        int at;
-        it = ac_find(P, line, border, at);
-        const int64_t start = border - at, end = start + it.units;
-        cut = at > 0 && before <= start;  // (else the border cuts nothing, or an earlier one cuts the item)
+        const int64_t border = shares(c);
+        int in;
+        ac_find(P, line, total.start, border, it, in);
+        const int64_t begin = border - in + total.start, end = begin + it.units;  // of its units
+        cut = border > begin && shares(c - 1) <= begin;  // (else the border cuts nothing, or an earlier one cuts the item)
         // the shares up to the one that the item ends in; none of them is empty
-        for (parts = 2; c - 1 + parts < blocks && shares(c - 1 + parts) < end;) ++parts;
+        for (parts = 2; c - 1 + parts < total.blocks && shares(c - 1 + parts) < end;) ++parts;
     }
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
@@ -898,7 +935,7 @@ static kq_status launch_ac(const char *fn, AcParams P, cudaStream_t st) {
     constexpr int NW = DP == 256 ? 4 : 8, NS = 2;
     using Ring = AcRing<DP>;
     const int smem = NW * (NS * Ring::BYTES + kAcPart<DP, MT> * 4);
-    static_assert(NW * (NS * Ring::BYTES + kAcPart<DP, MT> * 4) <= 224 * 1024 + 512, "shared memory");
+    static_assert(NW * (NS * Ring::BYTES + kAcPart<DP, MT> * 4) <= 216 * 1024, "shared memory");
     auto encode = ac_encoder();
     if (!encode) return fail(KQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", fn);
     CUtensorMap tm[2];

@@ -77,6 +77,35 @@ def test_lengths(lens):
     run(lens, 1, 4, 2, 64, 64)
 
 
+@pytest.mark.parametrize("B,n_kv,D,longest", [(6000, 2, 64, 40), (1300, 1, 256, 70), (200, 2, 64, 3000), (140, 1, 256, 3000), (90, 2, 128, 5000)])
+def test_more_sequences_than_threads_and_full_shares(B, n_kv, D, longest):
+    """A thread sums up several sequences; many items, of one unit or of about a hundred, in every warp's share."""
+    lens = np.random.default_rng(B).integers(0, longest, B).tolist()
+    run(lens, 1, 2 * n_kv, n_kv, D, 32)
+
+
+def test_rows_of_sixteen_in_full_shares():
+    lens = np.random.default_rng(2).integers(0, 4000, 120).tolist()
+    run(lens, 4, 6, 2, 64, 64, "f16", "f16")
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each."""
+    work = []
+    for seed, lens in ((1, [4000, 900, 0, 7]), (2, [2500, 2500, 31])):
+        c = Cache(lens, 2, 128, 64, seed=seed, fill=True)
+        q = torch.randn((c.B, 8 * 128), generator=torch.Generator().manual_seed(seed))
+        n = kq.kq_attn_cache_i8_workspace_bytes(c.B, 1, 8, 2, 128)
+        work.append((c, lens, q, q.to(DEV), torch.zeros_like(q, device=DEV), torch.zeros(n, dtype=torch.uint8, device=DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, _, _, dq, y, ws, stream in work:
+            call(c, dq, 1, 8, 128 ** -0.5, out=y, ws=ws, stream=stream)
+    torch.cuda.synchronize()
+    for c, lens, q, _, y, _, _ in work:
+        check(y, c, q, lens, 1, 8, 128 ** -0.5, "f32")
+
+
 def test_long_rows_of_sixteen():
     run([6000, 1000], 4, 8, 2, 128, 64, "bf16", "f32")
 
