@@ -10,7 +10,7 @@
 //
 // The products run on m16n8k16 instructions.  Codes are exact in f16; a query row is brought to |q| < 2 by a power
 // of two and split into two f16 (22 bits), as the weights 2^(s - m) vs are.  With up to eight rows (the query heads of
-// one key head) the second parts fill the tile's other eight rows, so they cost nothing; 9 to 16 rows take twice
+// one key head) the second parts fill the tile's other eight rows, so they cost nothing; tiles of 16 rows take twice
 // the instructions.  Which of its elements a lane holds is free where both operands agree, so it follows the loads:
 //   keys:   lane 4n + c of an eight-token tile takes the 16-byte pieces 2c and 2c + 1 of token n; 4 bytes make the two
 //           registers of one step.
@@ -908,10 +908,22 @@ __global__ void __launch_bounds__(256) ac_join_kernel(AcParams P) {
 }
 
 // ---------------------------------------------------------------- host
-static int ac_row_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
 static int ac_width(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+// Tiles of 16 rows fetch a unit half as often for the same instructions, but double what a warp begins, keeps and hands
+// over; with heads of 256 that does not fit the registers.
+static bool ac_may_be_wide(int64_t rows, int64_t D) { return rows > 8 && D <= 128; }
+// They are taken where the tables have room for kAcWideFrom units a warp and more (the lengths are known on the device only; both
+// kinds in one kernel, chosen there, cost the short calls 2.5 us).  24 rows of 128: 5 sequences of up to 5001 tokens 20.4 us
+// with 16 rows, 15.5 with 8; 16 of up to 7500 (six units a warp) 23.1 and 22.3, of up to 20001 32.5 and 35.2; 64 of up to 8192
+// with 8 heads 133 and 175.  Heads of 256: 38.0 and 21.6, 100.0 and 72.4.
+constexpr int kAcWideFrom = 6;
+static int ac_row_tile(const AcParams &P) {
+    if (!ac_may_be_wide(P.rows, P.c.D)) return 8;
+    const double units = (double)P.c.B * P.c.ldt * (1 << P.c.lp) / kAcUnit * P.c.n_kv * ((P.rows + 15) / 16);
+    return units >= (double)kAcWideFrom * kAcMaxBlocks * 8 ? 16 : 8;
+}
 static size_t ac_workspace(int64_t rows, int64_t D) {
-    return 256 + (size_t)kAcMaxBlocks * 2 * ac_row_tile(rows) * (ac_width(D) + 2) * 4;
+    return 256 + (size_t)kAcMaxBlocks * 2 * (ac_may_be_wide(rows, D) ? 16 : 8) * (ac_width(D) + 2) * 4;
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 ac_encoder() {
@@ -995,7 +1007,7 @@ static kq_status ac_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq
     P.yvec = aligned(y, 16) && ldy * (int64_t)value_bytes(yt) % 16 == 0;
     P.n_new = (int)n_new; P.n_q = (int)n_q; P.G = (int)(n_q / n_kv);
     P.rows = P.n_new * P.G;
-    const int mt = ac_row_tile(P.rows);
+    const int mt = ac_row_tile(P);
     P.tiles = (P.rows + mt - 1) / mt;
     P.scale = scale * 1.44269504f;
     P.err = static_cast<unsigned long long *>(workspace);
@@ -1004,8 +1016,9 @@ static kq_status ac_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq
     P.wait_ns = wait_ns;
     P.idle = idle;
     const cudaStream_t st = (cudaStream_t)stream;
-    if (mt == 8) return D <= 64 ? launch_ac<64, 8>(fn, P, st) : D <= 128 ? launch_ac<128, 8>(fn, P, st) : launch_ac<256, 8>(fn, P, st);
-    return D <= 64 ? launch_ac<64, 16>(fn, P, st) : D <= 128 ? launch_ac<128, 16>(fn, P, st) : launch_ac<256, 16>(fn, P, st);
+    if (D > 128) return launch_ac<256, 8>(fn, P, st);
+    if (mt == 8) return D <= 64 ? launch_ac<64, 8>(fn, P, st) : launch_ac<128, 8>(fn, P, st);
+    return D <= 64 ? launch_ac<64, 16>(fn, P, st) : launch_ac<128, 16>(fn, P, st);
 }
 
 }  // namespace kq

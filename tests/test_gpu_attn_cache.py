@@ -41,8 +41,12 @@ def check(y, c, q, lens, n_new, n_q, scale, yt, only=None):
         assert not bad.any(), (b, t, np.abs(y[b] - ref)[bad].max(), tol.max())
 
 
-def run(lens, n_new, n_q, n_kv, D, page, xt="f32", yt="f32", scale=None, seed=0, amp=1.0):
+def run(lens, n_new, n_q, n_kv, D, page, xt="f32", yt="f32", scale=None, seed=0, amp=1.0, room=0):
     c = Cache(lens, n_kv, D, page, seed=seed, fill=True)
+    if room:  # tables of `room` pages: long sequences may come
+        c.table_host = np.pad(c.table_host, ((0, 0), (0, room - c.ldt)), constant_values=-7)
+        c.ldt = room
+        c.upload()
     g = torch.Generator().manual_seed(seed)
     q = (torch.randn((c.B * n_new, n_q * D), generator=g) * amp).to(TYPES[xt][1])
     scale = D ** -0.5 if scale is None else scale
@@ -75,6 +79,15 @@ def test_types(xt, yt):
 def test_lengths(lens):
     """One long sequence over every warp, ragged ones, many short ones, one among empty ones."""
     run(lens, 1, 4, 2, 64, 64)
+
+
+@pytest.mark.parametrize("n_new,n_q,n_kv", [(1, 20, 1), (3, 14, 2), (1, 32, 2), (9, 4, 2), (2, 9, 1), (4, 4, 1), (8, 8, 2)])
+@pytest.mark.parametrize("D", [16, 64, 80, 128, 256])
+def test_many_rows_and_tables_with_room(n_new, n_q, n_kv, D):
+    """More than eight rows of a key head, in tables that have room for much longer sequences and in those that have not."""
+    lens = [37, 0, 1, 16, 200, 1500, 8]
+    run(lens, n_new, n_q, n_kv, D, 16, room=3000)
+    run(lens, n_new, n_q, n_kv, D, 16)
 
 
 @pytest.mark.parametrize("B,n_kv,D,longest", [(6000, 2, 64, 40), (1300, 1, 256, 70), (200, 2, 64, 3000), (140, 1, 256, 3000), (90, 2, 128, 5000)])
