@@ -30,14 +30,15 @@ __device__ __forceinline__ int64_t pa_row(const int32_t *cu, int64_t b, int64_t 
 // All threads of the block call it; false where there is no such tile.
 template <int THREADS>
 __device__ __forceinline__ bool pa_tile(const PaParams &P, int64_t unit, int size, PaTile &t) {
-    int64_t b = -1;
-    for (int64_t b0 = 0; b0 < P.B; b0 += THREADS) {
-        const int64_t i = b0 + threadIdx.x;
-        const int n = __syncthreads_count(i < P.B && pa_row(P.cu_q, i, P.Tq) / size + i <= unit);
-        b += n;
-        if (n < THREADS) break;
+    int64_t b = 0;
+    for (int64_t n = P.B;;) {  // the sequence is one of n from b on
+        const int64_t step = (n + THREADS - 1) / THREADS, at = threadIdx.x * step;
+        const int k = __syncthreads_count(at < n && pa_row(P.cu_q, b + at, P.Tq) / size + b + at <= unit) - 1;
+        if (k < 0) return false;
+        b += k * step;
+        if (step == 1) break;
+        n = min(step, n - k * step);
     }
-    if (b < 0) return false;
     t.q_row = pa_row(P.cu_q, b, P.Tq);
     t.k_row = pa_row(P.cu_k, b, P.Tk);
     const int64_t first = (unit - t.q_row / size - b) * size;

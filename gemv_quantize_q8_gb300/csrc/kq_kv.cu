@@ -46,18 +46,19 @@ struct KvPart {
     int64_t page, row;
     int lo, hi;  // none: lo = hi
 };
-// All threads of the block call it; false where there is nothing to do.  (One warp finds it out for all: the block's
+// All threads of the block call it; false where there is nothing to do.  (One thread finds it out for all: the block's
 // instructions count.)
 __device__ __forceinline__ KvPart kv_find(const KvCache &c, const KvRows &r, int64_t unit, int64_t b);
 __device__ __forceinline__ bool kv_part(const KvCache &c, const KvRows &r, int64_t unit, KvPart &p) {
     __shared__ KvPart shared;
     // the last sequence whose share starts at or before the unit; shares start in rising order
-    int64_t b = -1;
-    for (int64_t b0 = 0; b0 < c.B; b0 += kKvThreads) {
-        const int64_t i = b0 + threadIdx.x;
-        const int n = __syncthreads_count(i < c.B && kv_start(r, c, kv_row(r.cu, i, c.B, r.T), i) <= unit);
-        b += n;
-        if (n < kKvThreads) break;
+    int64_t b = 0;
+    for (int64_t n = c.B; b >= 0;) {  // it is one of n from b on
+        const int64_t step = (n + kKvThreads - 1) / kKvThreads, at = threadIdx.x * step;
+        const int k = __syncthreads_count(at < n && kv_start(r, c, kv_row(r.cu, b + at, c.B, r.T), b + at) <= unit) - 1;
+        b = k < 0 ? -1 : b + k * step;
+        if (step == 1) break;
+        n = min(step, n - k * step);
     }
     if (threadIdx.x == 0) shared = kv_find(c, r, unit, b);
     __syncthreads();

@@ -175,6 +175,14 @@ def test_more_sequences_than_a_warp_finds_in_two_steps():
     run(n, n, 6, 2, 64, "f16")
 
 
+@pytest.mark.parametrize("offset", [0, 1])
+def test_very_many_sequences_of_one_token(offset):
+    """A token that sees itself alone gives its value."""
+    n = [0 if b % 5 == 3 else 1 for b in range(70000)]
+    p = Prompt(n, n, 1, 1, 8, "bf16", offset=offset)
+    assert np.array_equal(p.call(0.3, True), p.v.double().numpy())
+
+
 def test_two_calls_at_once():
     """Two streams, a workspace each; both take their pairs from a line of their own."""
     scale, work = 128 ** -0.5, []

@@ -214,3 +214,11 @@ def test_many_sequences_and_pages():
     for got, want in ((k, x[:, :D]), (v, x[:, D:])):  # a code is off by half a step of amax / 127
         assert bool(((got - want).abs() <= want.abs().amax(1, keepdim=True) / 127 * 0.5001).all())
     assert int((codes != 0).any(-1).sum()) == 4
+
+
+def test_very_many_sequences():
+    """More than two steps of the search for a row's sequence find; every third without tokens."""
+    new = [0 if b % 3 == 2 else 1 for b in range(70000)]
+    c = Cache(new, 1, 16, 16)
+    append(c, new, new, "bf16")
+    same(c)
