@@ -396,7 +396,7 @@ struct AcWarp {
                 x[r][i] = (MT == 8 ? s[t][e] + s[t][2 + e] : s[t][2 * r + e]) * f[t >> 1];
             }
         }
-        if (t0 + kAcUnit > sure) {  // not every row sees all of the unit
+        if (t0 > sure - kAcUnit) {  // not every row sees all of the unit
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
