@@ -205,8 +205,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     if (!X.next && blockIdx.x == 0 && tid == 0) *P.err = 0ull;  // (an error is counted two seconds later at the earliest)
 
     // Every role walks the same pairs: f(w, key head), false to stop.  The warp that brings tiles asks for the next place on the
-    // line and passes it on.
-    auto walk = [&](auto f) {
+    // line and passes it on.  `patience`: the role is through with a pair long before its last tiles have been sent for.
+    auto walk = [&](auto f, unsigned long long patience = 0) {
+        unsigned long long limit = X.wait_ns;
         const unsigned items = (unsigned)(X.pairs * X.n_kv);
         unsigned ahead = blockIdx.x;
         for (unsigned r = 0;; ++r) {
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 i = __shfl_sync(~0u, i, 0);
                 if (!__shfl_sync(~0u, (int)ok, 0)) return;
             } else {
-                if (!__all_sync(~0u, mbar_wait_sleep(&turn_full[s], r >> 1 & 1, abort_flag, X.wait_ns))) return;
+                if (!__all_sync(~0u, mbar_wait_sleep(&turn_full[s], r >> 1 & 1, abort_flag, limit))) return;
                 i = turns[s];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&turn_empty[s]);
@@ -232,7 +233,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             // the longest first: later tokens of a sequence see more keys
             const unsigned turn = i / (unsigned)X.n_kv;
             PtWork w;
+            w.n = 0;
             if (pt_work(P, X.order ? X.order[turn] : X.pairs - 1 - turn, w) && !f(w, (int)(i - turn * X.n_kv))) return;
+            limit = X.wait_ns + patience * w.n;
             // (asked for when the pair's last tiles have been sent for, not before: a place taken early waits behind a long pair)
             if (warp == 9 && lane == 0) ahead = X.next ? gridDim.x + atomicAdd(X.next, 1u) : items;
         }
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 g += 2 * w.n;
                 masked_done(w);
                 return ok;
-            });
+            }, 20000ull);  // (a pair of key tiles takes 2 us)
         }
     } else {
         // ------------------------------------------------------------ weights and results, one row a thread
