@@ -995,7 +995,7 @@ static kq_status ac_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq
                     fn, (long long)n_new, (long long)n_q, (long long)n_kv);
     if (ldq < n_q * D || ldy < n_q * D)
         return fail(KQ_ERR_INVALID_ARG, "%s: ldq=%lld or ldy=%lld is less than n_q*D", fn, (long long)ldq, (long long)ldy);
-    if (!(fabsf(scale) <= 3.0e38f)) return fail(KQ_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    if (!(fabsf(scale) <= 2.0e38f)) return fail(KQ_ERR_INVALID_ARG, "%s: scale must be finite, up to 2e38", fn);  // (times log2 e, too)
     if (!aligned(q, value_bytes(xt)) || !aligned(y, value_bytes(yt)))
         return fail(KQ_ERR_ALIGNMENT, "%s: a pointer is not aligned to its elements", fn);
     const size_t need = ac_workspace(n_new * (n_q / n_kv), D);

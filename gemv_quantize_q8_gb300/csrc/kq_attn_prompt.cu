@@ -203,7 +203,7 @@ static kq_status pa_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq
         return fail(KQ_ERR_INVALID_ARG, "%s: a row stride is less than its heads (ldq=%lld ldk=%lld ldv=%lld ldy=%lld)", fn, (long long)ldq,
                     (long long)ldk, (long long)ldv, (long long)ldy);
     if (causal != 0 && causal != 1) return fail(KQ_ERR_INVALID_ARG, "%s: causal=%d is not 0 or 1", fn, causal);
-    if (!(fabsf(scale) <= 3.0e38f)) return fail(KQ_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    if (!(fabsf(scale) <= 2.0e38f)) return fail(KQ_ERR_INVALID_ARG, "%s: scale must be finite, up to 2e38", fn);  // (times log2 e, too)
     if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(y, 2) || !aligned(cu_q, 4) || !aligned(cu_k, 4))
         return fail(KQ_ERR_ALIGNMENT, "%s: a pointer is not aligned to its elements", fn);
     const size_t need = pa_tc_workspace(B, Tq, n_q / n_kv);

@@ -444,7 +444,7 @@ KQ_API kq_status kq_kv_read_i8(const int8_t *k_cache, const int8_t *v_cache, con
  *   y = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * (q . k_j) - max)
  * q: [B*n_new][ldq] of type xt, n_q heads of D elements; query head h reads key head h / (n_q / n_kv), n_q a multiple of
  * n_kv.  y: [B*n_new][ldy] of type yt.  q and y are element-aligned; y may be q itself (same type and stride).  n_new*n_q is
- * at most 65536; scale is finite.  Queries and weights are carried in 22 bits, sums in fp32, so fp32 rows come out
+ * at most 65536; |scale| is up to 2e38.  Queries and weights are carried in 22 bits, sums in fp32, so fp32 rows come out
  * with about fp32's accuracy.  Where a long sum is cut follows from the lengths of the whole batch and the tables' width, so the
  * same call gives the same bits, but a row's last bits may change with its neighbours' lengths.  A token that sees nothing
  * (lens[b] = 0, or a row before token 0) gives 0.  A page
@@ -464,11 +464,12 @@ KQ_API kq_status kq_attn_cache_i8(kq_dtype xt, const void *q, int64_t ldq, int64
  * last of its keys (token i of n_q sees the first n_k - n_q + 1 + i keys); causal = 0: every token sees every key.
  * The formula is kq_attn_cache_i8's.  q: [Tq][ldq], k: [Tk][ldk], v: [Tk][ldv], y: [Tq][ldy], all of
  * type xt (KQ_F16 or KQ_BF16), element-aligned; n_q heads of D elements over n_kv, a multiple; D a multiple of 8 up
- * to 256; Tq and Tk up to 2^31 - 256, B up to 2^24, n_q up to 65535; scale is finite.  y may be q itself (same stride).
+ * to 256; Tq and Tk up to 2^31 - 256, B up to 2^24, n_q up to 65535; |scale| is up to 2e38.  y may be q itself (same stride).
  * Scores and sums are fp32; the weights are rounded to xt for the second product.  A token that sees no key gives 0; what a
  * token does not see has no influence on it, infinities and NaN included.  Rows behind cu_q[B] are left as they were.
  * workspace: kq_attn_prompt_workspace_bytes(...) bytes (0: a shape that the call refuses), 256-byte aligned; its content does
- * not matter before the call, and calls that share it must not overlap; kq_read_device_flag applies to it (a tensor-core pipeline wait that timed out). */
+ * not matter before the call, and calls that share it must not overlap; kq_read_device_flag applies to it (a tensor-core
+ * pipeline wait that timed out). */
 KQ_API size_t kq_attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv, int64_t D);
 KQ_API kq_status kq_attn_prompt(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                                 const int32_t *cu_q, const int32_t *cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t n_q,

@@ -73,3 +73,11 @@ def test_workspace_bytes(lib):
     assert kq.kq_attn_prompt_workspace_bytes(1, 1, 1, 1, 8) >= 8
     for shape in ((0, 1, 4, 2, 128), (1, 0, 4, 2, 128), (1, 1, 3, 2, 128), (1, 1, 4, 2, 4), (1, 1, 4, 2, 320)):
         assert kq.kq_attn_prompt_workspace_bytes(*shape) == 0
+
+
+@pytest.mark.parametrize("name,args", [("kq_attn_cache_i8", CACHE), ("kq_attn_prompt", PROMPT)])
+@pytest.mark.parametrize("scale", [3e38, -2.1e38, float("-inf")])
+def test_scales_that_leave_fp32(lib, name, args, scale):
+    """The exponent's base is 2: the scale times log2 e has to be finite, too."""
+    assert getattr(lib, name)(*{**args, "scale": scale}.values(), None) == BAD
+    assert "scale" in lib.kq_last_error().decode()
