@@ -4,7 +4,7 @@
 // K, V and their blocks' scales ks, vs:
 //   m = max s_j,  l = sum 2^(s_j - m),  y = (sum 2^(s_j - m) vs V_j) / l       (s in units of log 2)
 // Bound by the cache's bytes: each is read once, by TMA, into a ring of the warp that needs it (2 or 4 KB a copy, two
-// units under way; a warp waits for nobody else).  Two sequences of 131072 tokens, 32 heads over 8 of 128, 537 MB: 87.7
+// or three units under way; a warp waits for nobody else).  Two sequences of 131072 tokens, 32 heads over 8 of 128, 537 MB: 87.7
 // us, 6.1 TB/s, of which the start, the parts and their join take 10; 64 users of up to 8192 tokens, 516 MB, 88.4; one user of
 // 900 tokens 9.7, all of it latency.  (By 16-byte copies of every lane the loads alone took 136 us for the first.)
 //
@@ -943,8 +943,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 ac_encoder() {
 template <int DP, int MT>
 static kq_status launch_ac(const char *fn, AcParams P, cudaStream_t st) {
     // 8 KB a unit of 128 elements, two a warp: more under way only makes everything queue longer (64 users of up to
-    // 8192 tokens: three 106 us, two 102)
-    constexpr int NW = DP == 256 ? 4 : 8, NS = 2;
+    // 8192 tokens: three 106 us, two 102).  4 KB with 64 elements: three 60.6, two 64.0, four 60.9.
+    constexpr int NW = DP == 256 ? 4 : 8, NS = DP == 64 ? 3 : 2;
     using Ring = AcRing<DP>;
     const int smem = NW * (NS * Ring::BYTES + kAcPart<DP, MT> * 4);
     static_assert(NW * (NS * Ring::BYTES + kAcPart<DP, MT> * 4) <= 216 * 1024, "shared memory");
