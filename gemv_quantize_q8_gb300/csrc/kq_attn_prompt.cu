@@ -6,8 +6,10 @@
 // of the unrounded ones).
 //
 // The form for any head width up to 256 and rows at any address: a thread block takes 64 tokens of one head, 16 a
-// warp, and goes over the keys in tiles of 32, on m16n8k16 instructions (16384 tokens, 32 heads over 8 of 128: 21.5 ms, 0.1
-// PFLOP/s; bound by its element-wise staging of keys and values).
+// warp, and goes over the keys in tiles of 32, on m16n8k16 instructions.  Rows on 16 bytes (heads of over 128; the narrower ones
+// take kq_attn_tc.cu's form) come by 16-byte copies, the next tile while this one's products run, and both products take
+// their operands by ldmatrix: 4096 tokens, 32 heads over 8 of 256, causal, 1190 us, 0.23 PFLOP/s, bound by the instructions' rate
+// and their operands' loads.  Other rows are staged element by element: 12.4 ms.
 // A masked weight is 0, but 0 times an infinity is not: rows of values past the sequence's end are
 // taken as zeros, and a tile that some row sees only in part and that holds an infinity or NaN is added up one key at
 // a time, leaving out what is masked.
@@ -38,15 +40,34 @@ __device__ __forceinline__ uint32_t pa_pair(float x, float y) {
 }
 __device__ __forceinline__ uint32_t pa_word(const void *p) { return *static_cast<const uint32_t *>(p); }
 
-template <int DP>
-constexpr int pa_smem() { return (kPaRows * (DP + kPaPad) + kPaKeys * (DP + kPaPad) + DP * (kPaKeys + kPaPad)) * 2; }
+// Four 8 x 8 tiles of 16-bit elements; lane i gives row i % 8 of tile i / 8.
+template <bool TRANS>
+__device__ __forceinline__ void pa_matrices(const void *row, uint32_t (&r)[4]) {
+    const uint32_t at = sm100::smem_u32(row);
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+// 16 bytes, or 16 zeros where `in` is false.
+__device__ __forceinline__ void pa_copy(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
 
-// DP: the head's width rounded up to 64, 128 or 256.
-template <typename T, int DP>
+template <int DP, bool VEC>
+constexpr int pa_smem() {
+    return (kPaRows * (DP + kPaPad) + (VEC ? 4 * kPaKeys * (DP + kPaPad) : kPaKeys * (DP + kPaPad) + DP * (kPaKeys + kPaPad))) * 2;
+}
+
+// DP: the head's width rounded up to 64, 128 or 256.  VEC: rows on 16 bytes; then the next tile's keys and values are
+// copied while this one's products run, and values stay as they lie (ldmatrix transposes them).
+template <typename T, int DP, bool VEC>
 __global__ void __launch_bounds__(128) pa_kernel(PaParams P) {
     extern __shared__ uint4 pa_sm[];
     constexpr int LD = DP + kPaPad, LV = kPaKeys + kPaPad;
-    T *sq = reinterpret_cast<T *>(pa_sm), *sk = sq + kPaRows * LD, *sv = sk + kPaKeys * LD;  // values transposed: [d][key]
+    T *sq = reinterpret_cast<T *>(pa_sm), *sk = sq + kPaRows * LD, *sv = sk + kPaKeys * LD;  // values transposed: [d][key], unless VEC
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3, D = P.D;
@@ -59,9 +80,28 @@ __global__ void __launch_bounds__(128) pa_kernel(PaParams P) {
     const T *v = static_cast<const T *>(P.v) + t.k_row * P.ldv + (int64_t)(head / P.G) * D;
     const int rows = min(kPaRows, t.n_q - t.first);
     const T zero = from_f32<T>(0.0f);
-    for (int i = tid; i < kPaRows * DP; i += 128) {
-        const int r = i / DP, d = i % DP;
-        sq[r * LD + d] = r < rows && d < D ? q[r * P.ldq + d] : zero;
+    // (VEC) the tile from key j0 on into one of two buffers
+    constexpr int TILE = 2 * kPaKeys * LD, PIECES = DP / 8;
+    auto stage = [&](int j0, int buffer) {
+        for (int i = tid; i < kPaKeys * PIECES; i += 128) {
+            const int r = i / PIECES, d = i % PIECES * 8;
+            const bool in = j0 + r < t.n_k && d < D;
+            T *to = sk + buffer * TILE + r * LD + d;
+            pa_copy(to, in ? k + (j0 + r) * P.ldk + d : k, in);
+            pa_copy(to + kPaKeys * LD, in ? v + (j0 + r) * P.ldv + d : v, in);
+        }
+    };
+    if constexpr (VEC) {
+        for (int i = tid; i < kPaRows * PIECES; i += 128) {
+            const int r = i / PIECES, d = i % PIECES * 8;
+            const bool in = r < rows && d < D;
+            pa_copy(sq + r * LD + d, in ? q + r * P.ldq + d : q, in);
+        }
+    } else {
+        for (int i = tid; i < kPaRows * DP; i += 128) {
+            const int r = i / DP, d = i % DP;
+            sq[r * LD + d] = r < rows && d < D ? q[r * P.ldq + d] : zero;
+        }
     }
     // row r of this lane (0, 1): token first + 16 * warp + g + 8r, which sees the keys below its limit
     int limit[2];
@@ -69,28 +109,56 @@ __global__ void __launch_bounds__(128) pa_kernel(PaParams P) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) limit[r] = pa_limit(P, t, t.first + 16 * warp + g + 8 * r);
     const int lowest = pa_limit(P, t, t.first), highest = pa_limit(P, t, t.first + rows - 1);
+    if (VEC && highest > 0) stage(0, 0);
+    if (VEC) asm volatile("cp.async.commit_group;" ::: "memory");
     for (int j0 = 0; j0 < highest; j0 += kPaKeys) {
         __syncthreads();
         bool odd = false;
-        for (int i = tid; i < kPaKeys * DP; i += 128) {
-            const int r = i / DP, d = i % DP;
-            const bool in = j0 + r < t.n_k && d < D;
-            const T kv = in ? k[(j0 + r) * P.ldk + d] : zero, vv = in ? v[(j0 + r) * P.ldv + d] : zero;
-            sk[r * LD + d] = kv;
-            sv[d * LV + r] = vv;
-            odd |= !(fabsf(to_f32(vv)) < INFINITY);
+        if constexpr (VEC) {
+            const int buffer = j0 / kPaKeys & 1;
+            sk = sq + kPaRows * LD;
+            if (j0 + kPaKeys < highest) stage(j0 + kPaKeys, buffer ^ 1);
+            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
+            sk += buffer * TILE;
+            sv = sk + kPaKeys * LD;
+            if (j0 + kPaKeys > lowest)  // (each thread looks at what it has copied)
+                for (int i = tid; i < kPaKeys * PIECES; i += 128) {
+                    const T *at = sv + i / PIECES * LD + i % PIECES * 8;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) odd |= !(fabsf(to_f32(at[x])) < INFINITY);
+                }
+        } else {
+            for (int i = tid; i < kPaKeys * DP; i += 128) {
+                const int r = i / DP, d = i % DP;
+                const bool in = j0 + r < t.n_k && d < D;
+                const T kv = in ? k[(j0 + r) * P.ldk + d] : zero, vv = in ? v[(j0 + r) * P.ldv + d] : zero;
+                sk[r * LD + d] = kv;
+                sv[d * LV + r] = vv;
+                odd |= !(fabsf(to_f32(vv)) < INFINITY);
+            }
         }
         // (part of the tile masked for some row, and not finite)
         odd = __syncthreads_or(odd && j0 + kPaKeys > lowest);
         float s[kPaKeys / 8][4] = {};
 #pragma unroll
         for (int x = 0; x < DP / 16; ++x) {
-            const T *a = sq + (16 * warp + g) * LD + 16 * x + 2 * c;
-            const uint32_t af[4] = {pa_word(a), pa_word(a + 8 * LD), pa_word(a + 8), pa_word(a + 8 * LD + 8)};
+            if constexpr (VEC) {
+                uint32_t af[4], b[4];
+                pa_matrices<false>(sq + (16 * warp + (lane & 15)) * LD + 16 * x + (lane >> 4) * 8, af);
 #pragma unroll
-            for (int n = 0; n < kPaKeys / 8; ++n) {
-                const T *b = sk + (8 * n + g) * LD + 16 * x + 2 * c;
-                pa_mma(s[n], af, pa_word(b), pa_word(b + 8), T{});
+                for (int n = 0; n < kPaKeys / 8; n += 2) {
+                    pa_matrices<false>(sk + (8 * (n + (lane >> 4)) + (lane & 7)) * LD + 16 * x + (lane >> 3 & 1) * 8, b);
+                    pa_mma(s[n], af, b[0], b[1], T{});
+                    pa_mma(s[n + 1], af, b[2], b[3], T{});
+                }
+            } else {
+                const T *a = sq + (16 * warp + g) * LD + 16 * x + 2 * c;
+                const uint32_t af[4] = {pa_word(a), pa_word(a + 8 * LD), pa_word(a + 8), pa_word(a + 8 * LD + 8)};
+#pragma unroll
+                for (int n = 0; n < kPaKeys / 8; ++n) {
+                    const T *b = sk + (8 * n + g) * LD + 16 * x + 2 * c;
+                    pa_mma(s[n], af, pa_word(b), pa_word(b + 8), T{});
+                }
             }
         }
         float f[2];
@@ -128,10 +196,20 @@ __global__ void __launch_bounds__(128) pa_kernel(PaParams P) {
             for (int x = 0; x < kPaKeys / 16; ++x) {
                 const uint32_t af[4] = {pa_pair<T>(s[2 * x][0], s[2 * x][1]), pa_pair<T>(s[2 * x][2], s[2 * x][3]),
                                         pa_pair<T>(s[2 * x + 1][0], s[2 * x + 1][1]), pa_pair<T>(s[2 * x + 1][2], s[2 * x + 1][3])};
+                if constexpr (VEC) {
 #pragma unroll
-                for (int j = 0; j < DP / 8; ++j) {
-                    const T *b = sv + (8 * j + g) * LV + 16 * x + 2 * c;
-                    pa_mma(o[j], af, pa_word(b), pa_word(b + 8), T{});
+                    for (int j = 0; j < DP / 8; j += 2) {
+                        uint32_t b[4];
+                        pa_matrices<true>(sv + (16 * x + (lane & 15)) * LD + 8 * (j + (lane >> 4)), b);
+                        pa_mma(o[j], af, b[0], b[1], T{});
+                        pa_mma(o[j + 1], af, b[2], b[3], T{});
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < DP / 8; ++j) {
+                        const T *b = sv + (8 * j + g) * LV + 16 * x + 2 * c;
+                        pa_mma(o[j], af, pa_word(b), pa_word(b + 8), T{});
+                    }
                 }
             }
         } else {
@@ -146,13 +224,14 @@ __global__ void __launch_bounds__(128) pa_kernel(PaParams P) {
                         for (int j = 0; j < DP / 8; ++j)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const float x = to_f32(sv[(8 * j + 2 * c + i) * LV + key]);
+                                const float x = to_f32(VEC ? sv[key * LD + 8 * j + 2 * c + i] : sv[(8 * j + 2 * c + i) * LV + key]);
                                 if (j0 + key < limit[0]) o[j][i] += to_f32(from_f32<T>(p0)) * x;
                                 if (j0 + key < limit[1]) o[j][2 + i] += to_f32(from_f32<T>(p1)) * x;
                             }
                     }
         }
     }
+    if (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");  // (queries of rows that see nothing)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(~0u, l[r], 1);
@@ -170,12 +249,12 @@ __global__ void __launch_bounds__(128) pa_kernel(PaParams P) {
     }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool VEC>
 static kq_status launch_pa(const char *fn, const PaParams &P, cudaStream_t st) {
-    auto kern = pa_kernel<T, DP>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pa_smem<DP>());
+    auto kern = pa_kernel<T, DP, VEC>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pa_smem<DP, VEC>());
     const unsigned tiles = (unsigned)(P.Tq / kPaRows + P.B);
-    if (e == cudaSuccess) e = launch_beside(kern, dim3(tiles, P.n_q), dim3(128), pa_smem<DP>(), dim3(1), st, P);
+    if (e == cudaSuccess) e = launch_beside(kern, dim3(tiles, P.n_q), dim3(128), pa_smem<DP, VEC>(), dim3(1), st, P);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
     count_launch(R_ATTN);
     return KQ_OK;
@@ -217,7 +296,8 @@ static kq_status pa_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq
     if (idle) return fail(KQ_ERR_INVALID_ARG, "%s: these rows do not take the tensor-core path", fn);
     auto go = [&](auto t) {
         using T = decltype(t);
-        return D <= 64 ? launch_pa<T, 64>(fn, P, st) : D <= 128 ? launch_pa<T, 128>(fn, P, st) : launch_pa<T, 256>(fn, P, st);
+        if (D <= 128) return D <= 64 ? launch_pa<T, 64, false>(fn, P, st) : launch_pa<T, 128, false>(fn, P, st);
+        return pa_aligned(P) ? launch_pa<T, 256, true>(fn, P, st) : launch_pa<T, 256, false>(fn, P, st);
     };
     return xt == KQ_F16 ? go(__half{}) : go(__nv_bfloat16{});
 }

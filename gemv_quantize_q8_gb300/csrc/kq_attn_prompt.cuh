@@ -60,6 +60,7 @@ __device__ __forceinline__ int pa_limit(const PaParams &P, const PaTile &t, int 
 // The tensor-core form (kq_attn_tc.cu): which rows it takes, and the launch.  wait_ns limits every wait of its pipeline;
 // idle names a role that does nothing (test hook: 1 what brings tiles, 2 what issues the products, 0 none).
 constexpr unsigned long long kPtWaitNs = 2000000000ull;
+bool pa_aligned(const PaParams &P);  // all rows on 16 bytes
 bool pa_takes_tc(const PaParams &P);
 size_t pa_tc_workspace(int64_t B, int64_t Tq, int64_t G);
 kq_status pa_tc(const char *fn, kq_dtype xt, const PaParams &P, unsigned long long wait_ns, int idle, cudaStream_t st);

@@ -659,10 +659,11 @@ static PFN_cuTensorMapEncodeTiled_v12000 pt_encoder() {
 static int64_t pt_pairs(int64_t B, int64_t Tq, int64_t G) { return ((Tq / PT + B) * G >> 1) + B; }
 size_t pa_tc_workspace(int64_t B, int64_t Tq, int64_t G) { return 256 + (size_t)(pt_pairs(B, Tq, G) * 4 + 255) / 256 * 256; }
 
-bool pa_takes_tc(const PaParams &P) {
-    return P.D <= 128 && P.D % 8 == 0 && aligned(P.q, 16) && aligned(P.k, 16) && aligned(P.v, 16) && aligned(P.y, 16) && P.ldq % 8 == 0 &&
+bool pa_aligned(const PaParams &P) {
+    return P.D % 8 == 0 && aligned(P.q, 16) && aligned(P.k, 16) && aligned(P.v, 16) && aligned(P.y, 16) && P.ldq % 8 == 0 &&
            P.ldk % 8 == 0 && P.ldv % 8 == 0 && P.ldy % 8 == 0;
 }
+bool pa_takes_tc(const PaParams &P) { return P.D <= 128 && pa_aligned(P); }
 
 template <typename T, typename C>
 static kq_status pt_launch(const char *fn, PtParams X, cudaStream_t st) {

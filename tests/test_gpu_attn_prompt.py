@@ -108,6 +108,14 @@ def test_long(D, xt):
     run([300], [5000], 2, 1, D, xt, rows=40)
 
 
+@pytest.mark.parametrize("D", [136, 192, 256])
+@pytest.mark.parametrize("xt,causal", [("bf16", True), ("f16", False)])
+@pytest.mark.parametrize("offset,pad", [(0, 0), (8, 8), (2, 0), (0, 4)])
+def test_wide_heads(D, xt, causal, offset, pad):
+    """Rows on 16 bytes and others; tiles that end inside, keys without queries' tiles and the other way round."""
+    run([33, 64, 1, 200, 5, 0], [33, 100, 32, 170, 0, 7], 4, 2, D, xt, causal, offset=offset, pad=pad, behind=2)
+
+
 @pytest.mark.parametrize("offset,pad", [(1, 0), (0, 3), (8, 8), (3, 5), (4, 4)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_addresses_strides_and_rows_behind(offset, pad, D):
