@@ -8,7 +8,7 @@
 // The form for any head width up to 256 and rows at any address: a thread block takes 64 tokens of one head, 16 a
 // warp, and goes over the keys in tiles of 32, on m16n8k16 instructions.  Rows on 16 bytes (heads of over 128; the narrower ones
 // take kq_attn_tc.cu's form) come by 16-byte copies, the next tile while this one's products run, and both products take
-// their operands by ldmatrix: 4096 tokens, 32 heads over 8 of 256, causal, 1190 us, 0.23 PFLOP/s, bound by the instructions' rate
+// their operands by ldmatrix: 4096 tokens, 32 heads over 8 of 256, causal, 1033 us, 0.27 PFLOP/s, bound by the instructions' rate
 // and their operands' loads.  Other rows are staged element by element: 12.4 ms.
 // A masked weight is 0, but 0 times an infinity is not: rows of values past the sequence's end are
 // taken as zeros, and a tile that some row sees only in part and that holds an infinity or NaN is added up one key at
@@ -71,10 +71,12 @@ __global__ void __launch_bounds__(128) pa_kernel(PaParams P) {
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3, D = P.D;
-    if (P.err && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *P.err = 0ull;
+    if (P.err && blockIdx.x == 0 && tid == 0) *P.err = 0ull;
     PaTile t;
-    if (!pa_tile<128>(P, blockIdx.x, kPaRows, t)) return;
-    const int head = blockIdx.y;
+    // heads side by side (their keys meet in the L2), the last tokens, which see the most, first: 1033 us for 1190
+    const unsigned unit = blockIdx.x / (unsigned)P.n_q;
+    const int head = (int)(blockIdx.x - unit * (unsigned)P.n_q);
+    if (!pa_tile<128>(P, gridDim.x / (unsigned)P.n_q - 1 - unit, kPaRows, t)) return;
     const T *q = static_cast<const T *>(P.q) + (t.q_row + t.first) * P.ldq + (int64_t)head * D;
     const T *k = static_cast<const T *>(P.k) + t.k_row * P.ldk + (int64_t)(head / P.G) * D;
     const T *v = static_cast<const T *>(P.v) + t.k_row * P.ldv + (int64_t)(head / P.G) * D;
@@ -253,8 +255,9 @@ template <typename T, int DP, bool VEC>
 static kq_status launch_pa(const char *fn, const PaParams &P, cudaStream_t st) {
     auto kern = pa_kernel<T, DP, VEC>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pa_smem<DP, VEC>());
-    const unsigned tiles = (unsigned)(P.Tq / kPaRows + P.B);
-    if (e == cudaSuccess) e = launch_beside(kern, dim3(tiles, P.n_q), dim3(128), pa_smem<DP, VEC>(), dim3(1), st, P);
+    const int64_t tiles = (P.Tq / kPaRows + P.B) * P.n_q;
+    if (tiles > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: too many row tiles", fn);
+    if (e == cudaSuccess) e = launch_beside(kern, dim3((unsigned)tiles), dim3(128), pa_smem<DP, VEC>(), dim3(1), st, P);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
     count_launch(R_ATTN);
     return KQ_OK;

@@ -66,6 +66,12 @@ def test_refused(lib, name, args, changes, status, text):
     assert kq.launch_count() == before
 
 
+def test_too_many_row_tiles(lib):
+    changes = dict(B=1 << 24, n_q=256, D=256, ldq=1 << 16, ldk=512, ldv=512, ldy=1 << 16, n=1 << 40)
+    assert getattr(lib, "kq_attn_prompt")(*{**PROMPT, **changes}.values(), None) == BAD
+    assert "row tiles" in lib.kq_last_error().decode()
+
+
 def test_workspace_bytes(lib):
     assert kq.kq_attn_cache_i8_workspace_bytes(1, 1, 32, 8, 128) > 256
     for shape in ((0, 1, 32, 8, 128), (1, 0, 32, 8, 128), (1, 1, 30, 8, 128), (1, 1, 32, 8, 120), (1, 1, 32, 8, 512)):
