@@ -413,8 +413,9 @@ struct AcWarp {
             // bring the sums to a new maximum and a new reference of the value scales
             float ref = vref;
             if (vtop > vref) {
+                // (2^-119 at least: kAcLift over it is finite)
                 const uint32_t e = __float_as_uint(vtop) & 0x7f800000u;
-                ref = e < 0x00800000u ? 2.3509887e-38f : e >= 0x7f000000u ? vtop : __uint_as_float(e + 0x00800000u);
+                ref = e >= 0x7f000000u ? vtop : fmaxf(__uint_as_float(e + 0x00800000u), 0x1p-119f);
             }
             const float fv = vref > 0.0f ? vref / ref : 0.0f;
             vref = ref;
