@@ -62,7 +62,7 @@ struct AcParams {
     bool idle;            // test hook: nothing is fetched
 };
 
-// What a warp (or a block) hands over: m and l of its rows, then their sums relative to 2^m, in the order in which a
+// What a warp (or a block) hands over: m and l of its rows, then their weighted averages, in the order in which a
 // warp's lanes hold them (32 lanes side by side, 16 bytes each: no bank conflicts).
 template <int DP, int MT> constexpr int kAcPart = MT * (DP + 2);
 
@@ -206,6 +206,9 @@ __device__ __forceinline__ float ac_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 1/l of a sum of weights.  A part of an item's tokens may have none that a row sees: 0.  (All of them: 0 * infinity, which
+// is NaN where a row sees tokens, all of scores below fp32, and is not written where it sees none.)
+__device__ __forceinline__ float ac_inverse(float l, bool all) { return l == 0.0f && !all ? 0.0f : 1.0f / l; }
 __device__ __forceinline__ void ac_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -489,14 +492,18 @@ struct AcWarp {
             }
     }
 
-    // The item's sums so far: m, l, and D values a row that stand relative to 2^m.
-    __device__ __forceinline__ void end() {
+    // The item's results so far: m, l, and D values a row, which are weighted averages already: sums relative to 2^m could
+    // leave fp32 where the values do not.
+    __device__ __forceinline__ void end(bool all) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             l[r] += __shfl_xor_sync(~0u, l[r], 1);
             l[r] += __shfl_xor_sync(~0u, l[r], 2);
         }
         const float back = vref / kAcLift;
+        float inv[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) inv[r] = ac_inverse(l[r], all);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             if (MT == 8) {
@@ -504,7 +511,7 @@ struct AcWarp {
                 o[j][1] += o[j][3];
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[j][i] = o[j][i] * back;
+            for (int i = 0; i < 4; ++i) o[j][i] = o[j][i] * inv[i / 2 * (R - 1)] * back;
         }
     }
     // What a lane holds of a row lies in runs: f(r, d0, run) for the RUN elements from d0 on of its row r.
@@ -550,16 +557,15 @@ __device__ __forceinline__ void ac_place(int x, int &row, int &d) {
 
 // A run of row `row` (of the item's tile) of the output; a token that sees nothing gives 0.
 template <int N>
-__device__ __forceinline__ void ac_write_run(const AcParams &P, const AcItem &it, int MT, int row, int d0, const float (&v)[N], float l) {
+__device__ __forceinline__ void ac_write_run(const AcParams &P, const AcItem &it, int MT, int row, int d0, const float (&v)[N]) {
     const int i = it.tile * MT + row;
     if (i >= P.rows) return;
     const int token = i / P.G, head = it.h * P.G + i - token * P.G;
     const bool sees = ac_len(P, it.b) - P.n_new + token >= 0;
     const int64_t at = (it.b * P.n_new + token) * P.ldy + (int64_t)head * P.c.D + d0;
-    const float inv = 1.0f / l;
     float x[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = sees ? v[j] * inv : 0.0f;
+    for (int j = 0; j < N; ++j) x[j] = sees ? v[j] : 0.0f;
     if (!P.yvec) {
 #pragma unroll
         for (int j = 0; j < N; ++j) ac_store(P.y, P.yt, at + j, x[j]);
@@ -584,9 +590,9 @@ __device__ __forceinline__ void ac_write_run(const AcParams &P, const AcItem &it
         }
     }
 }
-__device__ __forceinline__ void ac_write4(const AcParams &P, const AcItem &it, int MT, int row, int d0, float4 v, float l) {
+__device__ __forceinline__ void ac_write4(const AcParams &P, const AcItem &it, int MT, int row, int d0, float4 v) {
     const float x[4] = {v.x, v.y, v.z, v.w};
-    ac_write_run(P, it, MT, row, d0, x, l);
+    ac_write_run(P, it, MT, row, d0, x);
 }
 
 __device__ __forceinline__ void ac_copy4(float *dst, const float *src) {
@@ -764,9 +770,10 @@ __global__ void __launch_bounds__(NW * 64, 1)
                 if (lane == 0) sm100::mbar_arrive(&empty[warp][stage]);
                 if (++stage == NS) stage = 0, phase ^= 1;
             }
-            w.end();
-            if (at == 0 && n == it.units) {
-                w.runs(D, [&](int r, int d0, const auto &v) { ac_write_run(P, it, MT, (lane >> 2) + 8 * r, d0, v, w.l[r]); });
+            const bool all = at == 0 && n == it.units;
+            w.end(all);
+            if (all) {
+                w.runs(D, [&](int r, int d0, const auto &v) { ac_write_run(P, it, MT, (lane >> 2) + 8 * r, d0, v); });
             } else {
                 const int slot = u == u0 ? 0 : 1;
                 __syncwarp();
@@ -809,10 +816,15 @@ __global__ void __launch_bounds__(NW * 64, 1)
                 for (int s = 0; s < 2 * NW; ++s) m = fmaxf(m, pm[s]);
                 float4 o[2] = {};
 #pragma unroll
+                for (int s = 0; s < 2 * NW; ++s) {
+                    pm[s] = group >> s & 1 ? part(s)[MT + row] * ac_exp2(pm[s] - m) : 0.0f;
+                    l += pm[s];
+                }
+                const float inv = ac_inverse(l, whole);
+#pragma unroll
                 for (int s = 0; s < 2 * NW; ++s)
                     if (group >> s & 1) {
-                        const float f = ac_exp2(pm[s] - m);
-                        l += part(s)[MT + row] * f;
+                        const float f = pm[s] * inv;
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const float4 v = reinterpret_cast<const float4 *>(part(s) + 2 * MT)[(2 * n + k) * 32 + lane];
@@ -829,7 +841,7 @@ __global__ void __launch_bounds__(NW * 64, 1)
                     int at_row, d;
                     ac_place<DP>(x, at_row, d);
                     if (!whole) reinterpret_cast<float4 *>(out + 2 * MT)[x] = o[k];
-                    else if (d < D) ac_write4(P, item, MT, row, d, o[k], l);
+                    else if (d < D) ac_write4(P, item, MT, row, d, o[k]);
                 }
             }
         }
@@ -842,7 +854,7 @@ __global__ void __launch_bounds__(NW * 64, 1)
 template <int DP, int MT>
 __global__ void __launch_bounds__(256) ac_join_kernel(AcParams P) {
     __shared__ AcLine<256> line;
-    __shared__ float weight[kAcMaxBlocks][MT], sum[MT];
+    __shared__ float weight[kAcMaxBlocks][MT];
     const int c = blockIdx.x + 1, D = P.c.D;
     constexpr int size = kAcPart<DP, MT>;
     const AcTotal total = ac_line(P, line, P.warps);
@@ -876,13 +888,14 @@ __global__ void __launch_bounds__(256) ac_join_kernel(AcParams P) {
 #pragma unroll
         for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
         for (int s = lane; s < parts; s += 32) {
-            const float f = ac_exp2(weight[s][row] - top);
+            const float f = part(s)[MT + row] * ac_exp2(weight[s][row] - top);
             weight[s][row] = f;
-            l += part(s)[MT + row] * f;
+            l += f;
         }
 #pragma unroll
         for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(~0u, l, x);
-        if (lane == 0) sum[row] = l;
+        const float inv = ac_inverse(l, true);
+        for (int s = lane; s < parts; s += 32) weight[s][row] *= inv;
     }
     __syncthreads();
 #pragma unroll
@@ -904,7 +917,7 @@ __global__ void __launch_bounds__(256) ac_join_kernel(AcParams P) {
             if (s < parts) add(k == 0 ? ahead[s] : __ldcg(reinterpret_cast<const float4 *>(part(s) + 2 * MT) + x), s);
 #pragma unroll 4
         for (int s = AHEAD; s < parts; ++s) add(__ldcg(reinterpret_cast<const float4 *>(part(s) + 2 * MT) + x), s);
-        if (d < D) ac_write4(P, it, MT, row, d, o, sum[row]);
+        if (d < D) ac_write4(P, it, MT, row, d, o);
     }
 }
 

@@ -59,3 +59,17 @@ def test_tiny_values_appended(size):
         y = call(c, q.to(DEV), 1, 4, D ** -0.5)
         torch.cuda.synchronize()
         check(y, c, q, [b], 1, 4, D ** -0.5)
+
+
+@pytest.mark.parametrize("n_new,n_q,D", [(1, 4, 64), (1, 2, 128), (3, 8, 64), (1, 4, 256)])
+def test_values_near_the_end_of_fp32(n_new, n_q, D):
+    """Values of one sign up to 3.3e38: their average is finite, their sum is not."""
+    lens = [3, 700, 6000]
+    c = Cache(lens, 1, D, 16, fill=True)
+    c.codes_host[1] = c.codes_host[1] // 10 + 114
+    c.scale_host[1] = 2.6e36
+    c.upload()
+    q = torch.randn((c.B * n_new, n_q * D), generator=torch.Generator().manual_seed(D))
+    y = call(c, q.to(DEV), n_new, n_q, D ** -0.5)
+    torch.cuda.synchronize()
+    check(y, c, q, lens, n_new, n_q, D ** -0.5)
