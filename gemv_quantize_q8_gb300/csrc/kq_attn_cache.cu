@@ -41,8 +41,10 @@ constexpr int kAcLeast = 1;           // units of a warp
 constexpr int kAcStart = 2;
 constexpr int kAcMaxBlocks = 152;     // one an SM
 constexpr unsigned long long kAcWaitNs = 2000000000ull;  // limit of every wait
-constexpr float kAcLift = 128.0f;     // weights are held times this: f16 keeps their low bits, with room for kAcSlack
 constexpr float kAcSlack = 8.0f;      // a weight may grow to 2^8 before the sums are brought to a new maximum
+// Weights are held times this power of two: f16 keeps their low bits, with room for kAcSlack.
+constexpr float kAcLift = 7.0f;
+constexpr float kAcLeastRef = -119.0f;  // the least reference that they are held against: 2^(kAcLift + 119) is finite
 constexpr float kAcNone = -3.0e38f;   // the maximum of no token
 
 struct AcParams {
@@ -206,6 +208,12 @@ __device__ __forceinline__ float ac_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2^x for whole numbers -126 .. 127.
+__device__ __forceinline__ float ac_pow2(float x) { return __uint_as_float((uint32_t)(127 + (int)x) << 23); }
+// A whole number above log2 |x|, -126 below the normal numbers.
+__device__ __forceinline__ float ac_size(float x) {
+    return __uint_as_float(0x4b000000u | (__float_as_uint(x) >> 23 & 255u)) - (8388608.0f + 126.0f);
+}
 // 1/l of a sum of weights.  A part of an item's tokens may have none that a row sees: 0.  (All of them: 0 * infinity, which
 // is NaN where a row sees tokens, all of scores below fp32, and is not written where it sees none.)
 __device__ __forceinline__ float ac_inverse(float l, bool all) { return l == 0.0f && !all ? 0.0f : 1.0f / l; }
@@ -296,7 +304,11 @@ struct AcWarp {
     static constexpr int R = MT / 8;     // rows of a lane: g and, with 16, g + 8
     float m[R], l[R], factor[R];
     int limit[R], sure;                  // tokens that a row sees, and that all rows see
-    float vref, lift;                    // a power of two above the value scales so far; kAcLift over it
+    // A row's weights times their blocks' value scales are held against a power of two of its own, 2^ref, that is above
+    // the largest of them so far and not far above: blocks that a row does not see, or weighs next to nothing, cost
+    // the others no bits, however large their scales.  They are held times down * up = 2^(kAcLift - ref); down is at
+    // most 1 and goes with the scale, up is at least 1 and comes last, so that nothing overflows on the way.
+    float ref[R], down[R], up[R];
 
     __device__ __forceinline__ void begin(const AcParams &P, const AcItem &it) {
         const int g = (threadIdx.x & 31) >> 2;
@@ -343,12 +355,17 @@ struct AcWarp {
             }
             m[r] = kAcNone;
             l[r] = 0.0f;
+            refer(r, kAcLeastRef);
         }
-        vref = 0.0f;
-        lift = 0.0f;
         sure = (int)max(len - P.n_new + 1, (int64_t)0);  // (rows past the tile's end are not kept)
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+    }
+
+    __device__ __forceinline__ void refer(int r, float to) {
+        ref[r] = to;
+        down[r] = ac_pow2(fminf(kAcLift - to, 0.0f));
+        up[r] = ac_pow2(fmaxf(kAcLift - to, 0.0f));
     }
 
     // A unit: tokens t0 .. t0 + 31, of which a row sees those below its limit.
@@ -357,13 +374,17 @@ struct AcWarp {
         using Ring = AcRing<DP>;
         const int c = threadIdx.x & 3;
         uint32_t k[KP][4][4];
+        constexpr int AHEAD = KP < 2 ? KP : 2;  // (all four pieces of heads of 256 do not fit the registers)
 #pragma unroll
-        for (int i = 0; i < KP; ++i)
+        for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
             for (int t = 0; t < 4; ++t) Ring::get_key(stage, t, i, k[i][t]);
         float s[4][4] = {};
 #pragma unroll
-        for (int i = 0; i < KP; ++i)
+        for (int i = 0; i < KP; ++i) {
+            if (i + 1 >= AHEAD && i + 1 < KP)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) Ring::get_key(stage, t, i + 1, k[i + 1][t]);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
 #pragma unroll
@@ -379,6 +400,7 @@ struct AcWarp {
                     }
                 }
             }
+        }
         uint32_t v[VW / Ring::VWORDS][2][4][Ring::VWORDS];
         auto values = [&](int i) {
 #pragma unroll
@@ -388,7 +410,7 @@ struct AcWarp {
         };
         values(0);
         // x[r][2t + e]: a row's logits for tokens 8t + 2c + e, in units of log 2
-        float x[R][8], top[R];
+        float x[R][8], top[R][2];
         bool grows = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -406,33 +428,42 @@ struct AcWarp {
                 for (int i = 0; i < 8; ++i)
                     if (t0 + (i >> 1) * 8 + 2 * c + (i & 1) >= limit[r]) x[r][i] = -INFINITY;
         }
+        float vs[2] = {scales.y, scales.w};
+        const float size[2] = {ac_size(vs[0]), ac_size(vs[1])};
+        // what the unit's halves would be held as: the largest weight, and the largest times its block's scale
+        auto heights = [&](int r, float base, float &p, float &pv) {
+            p = fmaxf(top[r][0], top[r][1]) - base;
+            pv = fmaxf(top[r][0] - base + size[0], top[r][1] - base + size[1]);
+        };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            top[r] = fmaxf(fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3])), fmaxf(fmaxf(x[r][4], x[r][5]), fmaxf(x[r][6], x[r][7])));
-            grows |= top[r] > m[r] + kAcSlack;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                top[r][h] = fmaxf(fmaxf(x[r][4 * h], x[r][4 * h + 1]), fmaxf(x[r][4 * h + 2], x[r][4 * h + 3]));
+            float p, pv;
+            heights(r, m[r], p, pv);
+            grows |= p > kAcSlack || pv > ref[r] + kAcSlack;
         }
-        const float vtop = fmaxf(scales.y < INFINITY ? scales.y : 0.0f, scales.w < INFINITY ? scales.w : 0.0f);
-        if (__any_sync(~0u, grows || vtop > vref)) {
-            // bring the sums to a new maximum and a new reference of the value scales
-            float ref = vref;
-            if (vtop > vref) {
-                // (2^-119 at least: kAcLift over it is finite)
-                const uint32_t e = __float_as_uint(vtop) & 0x7f800000u;
-                ref = e >= 0x7f000000u ? vtop : fmaxf(__uint_as_float(e + 0x00800000u), 0x1p-119f);
-            }
-            const float fv = vref > 0.0f ? vref / ref : 0.0f;
-            vref = ref;
-            lift = ref > 0.0f ? kAcLift / ref : 0.0f;
+        if (__any_sync(~0u, grows)) {
+            // bring the sums of the rows that grow to a new maximum and a new reference
             float f[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float mx = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                mx = fmaxf(mx, m[r]);
-                f[r] = ac_exp2(m[r] - mx);
-                l[r] *= f[r];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    top[r][h] = fmaxf(top[r][h], __shfl_xor_sync(~0u, top[r][h], 1));
+                    top[r][h] = fmaxf(top[r][h], __shfl_xor_sync(~0u, top[r][h], 2));
+                }
+                f[r] = 1.0f;
+                float p, pv;
+                heights(r, m[r], p, pv);
+                if (!(p > kAcSlack || pv > ref[r] + kAcSlack)) continue;
+                const float mx = fmaxf(m[r], fmaxf(top[r][0], top[r][1])), by = m[r] - mx, was = ref[r];
+                heights(r, mx, p, pv);
+                refer(r, fmaxf(fmaxf(floorf(was + by), ceilf(pv)), kAcLeastRef));
+                l[r] *= ac_exp2(by);
+                f[r] = ac_exp2(by + (was - ref[r]));
                 m[r] = mx;
-                f[r] *= fv;
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -442,9 +473,8 @@ struct AcWarp {
                 o[j][3] *= f[R - 1];
             }
         }
-        float by[2] = {scales.y * lift, scales.w * lift};
-        const bool poison = !(by[0] <= kAcLift && by[1] <= kAcLift);
-        if (poison) poisoned(x, by);
+        const bool poison = !(fabsf(vs[0]) < INFINITY && fabsf(vs[1]) < INFINITY);
+        if (poison) poisoned(x, vs);
         uint32_t ph[R][4], pl[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -452,8 +482,12 @@ struct AcWarp {
 #pragma unroll
             for (int i = 0; i < 8; ++i) p[i] = ac_exp2(x[r][i] - m[r]);
             l[r] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+            const float by[2] = {vs[0] * down[r], vs[1] * down[r]};
 #pragma unroll
-            for (int t = 0; t < 4; ++t) ac_split(p[2 * t] * by[t >> 1], p[2 * t + 1] * by[t >> 1], ph[r][t], pl[r][t]);
+            for (int t = 0; t < 4; ++t) {
+                const float2 w = mul2(mul2(make_float2(p[2 * t], p[2 * t + 1]), make_float2(by[t >> 1], by[t >> 1])), make_float2(up[r], up[r]));
+                ac_split(w.x, w.y, ph[r][t], pl[r][t]);
+            }
         }
 #pragma unroll
         for (int n = 0; n < VW / Ring::VWORDS; ++n) {
@@ -479,11 +513,11 @@ struct AcWarp {
         }
     }
     // A block of values with an infinity: NaN for the rows that see it, for them alone.
-    __device__ __forceinline__ void poisoned(const float (&x)[R][8], float (&by)[2]) {
+    __device__ __forceinline__ void poisoned(const float (&x)[R][8], float (&vs)[2]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (!(by[h] <= kAcLift)) {
-                by[h] = 0.0f;
+            if (!(fabsf(vs[h]) < INFINITY)) {
+                vs[h] = 0.0f;
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -500,7 +534,9 @@ struct AcWarp {
             l[r] += __shfl_xor_sync(~0u, l[r], 1);
             l[r] += __shfl_xor_sync(~0u, l[r], 2);
         }
-        const float back = vref / kAcLift;
+        float back[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) back[r] = ac_pow2(ref[r] - kAcLift);
         float inv[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) inv[r] = ac_inverse(l[r], all);
@@ -511,7 +547,7 @@ struct AcWarp {
                 o[j][1] += o[j][3];
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[j][i] = o[j][i] * inv[i / 2 * (R - 1)] * back;
+            for (int i = 0; i < 4; ++i) o[j][i] = o[j][i] * inv[i / 2 * (R - 1)] * back[i / 2 * (R - 1)];
         }
     }
     // What a lane holds of a row lies in runs: f(r, d0, run) for the RUN elements from d0 on of its row r.

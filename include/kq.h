@@ -444,8 +444,9 @@ KQ_API kq_status kq_kv_read_i8(const int8_t *k_cache, const int8_t *v_cache, con
  *   y = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * (q . k_j) - max)
  * q: [B*n_new][ldq] of type xt, n_q heads of D elements; query head h reads key head h / (n_q / n_kv), n_q a multiple of
  * n_kv.  y: [B*n_new][ldy] of type yt.  q and y are element-aligned; y may be q itself (same type and stride).  n_new*n_q is
- * at most 65536; |scale| is up to 2e38.  Queries and weights are carried in 22 bits, sums in fp32, so fp32 rows come out
- * with about fp32's accuracy.  Where a long sum is cut follows from the lengths of the whole batch and the tables' width, so the
+ * at most 65536; |scale| is up to 2e38.  Queries are carried in 22 bits of a row's largest element, weights times value scales
+ * in 22 bits of a row's largest such product (of no other row's), sums in fp32, so fp32 rows come out with about fp32's
+ * accuracy.  Where a long sum is cut follows from the lengths of the whole batch and the tables' width, so the
  * same call gives the same bits, but a row's last bits may change with its neighbours' lengths.  A token that sees nothing
  * (lens[b] = 0, or a row before token 0) gives 0.  A page
  * outside [0, n_pages), or a length past ldt pages, gives NaN.
