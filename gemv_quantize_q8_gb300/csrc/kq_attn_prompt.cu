@@ -1,6 +1,6 @@
 // kq_attn_prompt.cu -- attention over whole prompts: packed sequences, grouped heads, causal or not.
 //
-//   y_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = 2^(s_ij - m_i),   s_ij = scale * log2 e * (q_i . k_j)
+//   y_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = 2^(scale * log2 e * (s_ij - m_i)),   s_ij = q_i . k_j
 // over the keys that token i sees, with a running maximum m_i and fp32 sums; weights are rounded to the rows' type for
 // the second product (their errors are independent and average out over the keys; the sum below the line is
 // of the unrounded ones).
@@ -21,7 +21,6 @@
 namespace kq {
 
 constexpr int kPaRows = 64, kPaKeys = 32, kPaPad = 8;
-constexpr float kPaNone = -3.0e38f;  // the maximum of no key
 
 __device__ __forceinline__ void pa_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -172,12 +171,12 @@ __global__ void __launch_bounds__(128) pa_kernel(PaParams P) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float &x = s[n][2 * r + e];
-                    x = j0 + 8 * n + 2 * c + e < limit[r] ? x * P.scale : -INFINITY;
+                    x = j0 + 8 * n + 2 * c + e < limit[r] ? (P.negate ? -x : x) : -INFINITY;
                     top = fmaxf(top, x);
                 }
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            f[r] = exp2f(m[r] - top);
+            f[r] = exp2f((m[r] - top) * P.scale);
             m[r] = top;
             l[r] *= f[r];
 #pragma unroll
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(128) pa_kernel(PaParams P) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float &x = s[n][2 * r + e];
-                    x = exp2f(x - top);
+                    x = exp2f((x - top) * P.scale);
                     l[r] += x;
                 }
         }
@@ -292,8 +291,10 @@ static kq_status pa_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq
     if (!workspace || ws_bytes < need)
         return fail(KQ_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace ? ws_bytes : (size_t)0, need);
     if (!aligned(workspace, 256)) return fail(KQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", fn);
+    // (a scale of 0 weighs all keys alike, as the smallest one does, which keeps -inf times it -inf)
+    const float magnitude = fmaxf(fabsf(scale * 1.44269504f), 1.4e-45f);
     const PaParams P{q, k, v, y, ldq, ldk, ldv, ldy, cu_q, cu_k, B, Tq, Tk, (int)n_q, (int)(n_q / n_kv), (int)D,
-                     scale * 1.44269504f, causal != 0, static_cast<unsigned long long *>(workspace)};
+                     magnitude, scale < 0.0f, causal != 0, static_cast<unsigned long long *>(workspace)};
     const cudaStream_t st = (cudaStream_t)stream;
     if (pa_takes_tc(P)) return pa_tc(fn, xt, P, wait_ns, idle, st);
     if (idle) return fail(KQ_ERR_INVALID_ARG, "%s: these rows do not take the tensor-core path", fn);

@@ -11,10 +11,15 @@ struct PaParams {
     const int32_t *cu_q, *cu_k;  // [B + 1]
     int64_t B, Tq, Tk;
     int n_q, G, D;               // query heads, those of a key head, elements
-    float scale;                 // times log2 e
+    float scale;                 // its magnitude times log2 e, above 0
+    bool negate;                 // it is negative: the scores' signs turn
     bool causal;
     unsigned long long *err;     // device flag, cleared by the call
 };
+
+// Running maxima are those of the scores as the products give them (their signs turned where the scale is negative), and
+// weights are 2^((s - m) * scale): at any scale a row's largest weight is then 1, and nothing but s itself can leave fp32.
+constexpr float kPaNone = -3.402823466e38f;  // the maximum of no key: no finite score is below it
 
 // Some tokens of one sequence: `first` on of its n_q, with its n_k keys.
 struct PaTile {

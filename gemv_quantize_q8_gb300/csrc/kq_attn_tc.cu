@@ -7,7 +7,7 @@
 // key and value tile that is brought in serves 256 rows and one tile's products run while the other's weights
 // are made:
 //   S = Q K^T   128 x 128, fp32 in tensor memory, both operands in shared memory
-//   P = 2^(S - m), one row a thread; written over S as the rows' type
+//   P = 2^(scale (S - m)), one row a thread; written over S as the rows' type
 //   O += P V    P from tensor memory, V in shared memory as it lies there ([token][d]: the transposed form of the operand)
 // The sums stay relative to an old maximum until a row's grows by more than 2^8: then its warp scales O in place.
 // Key tiles go from the last to the first, so the masked ones come first.
@@ -32,8 +32,10 @@ using namespace sm100;
 constexpr int PT = 128;             // rows of a tile, keys of a tile
 constexpr int PT_THREADS = 384;
 constexpr int PT_MASKED = 3;        // key tiles that some row of a block's (at most 256 tokens) sees only in part
-constexpr float kPtNone = -1.0e30f; // the maximum of no key, in units of log 2
-constexpr float kPtSlack = 8.0f;
+constexpr float kPtSlack = 8.0f;    // in units of log 2
+// Up to this |m * scale| weights are 2^(S scale - m scale), one fused operation each: m * scale, rounded, is off by less than
+// a sixteenth.  Beyond it the rounding would make weights of any size, so S - m is formed first.
+constexpr float kPtFused = 1048576.0f;
 
 template <int DP_, int OW_>
 struct PtCfg {
@@ -57,7 +59,6 @@ struct PtParams {
     PaParams p;
     int64_t pairs;        // for one key head
     int n_kv;
-    bool negate;          // the scale is negative: -Q K^T and |scale|
     unsigned long long wait_ns;
     int idle;
     bool wide;            // output rows on 32 bytes, and whole heads of them
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             // ------------------------------------------------------------ products
             const bool one = pt_elect();
             constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u;
-            const uint32_t id_s = idesc_f16_f32(PT, PT) | type | (X.negate ? 1u << 13 : 0u);
+            const uint32_t id_s = idesc_f16_f32(PT, PT) | type | (P.negate ? 1u << 13 : 0u);
             constexpr uint32_t id_o = idesc_f16_f32(PT, C::OW) | type | (1u << 16);  // V: [token][d]
             const uint64_t dQ = smem_desc(smem_u32(sm), 1024, 2), dK = smem_desc(smem_u32(sKV), 1024, 2);
             // 64 elements of d a box, boxes BOX apart; eight tokens 1024 bytes apart
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         unsigned t = 0;  // this row tile's key tiles so far
         walk([&](const PtWork &w, int kv_head) {
             const int first = of(w.first, q), token = first + row, limit = first < w.t.n_q ? pa_limit(P, w.t, token) : 0, n = of(w.tiles, q);
-            float mc = kPtNone, l = 0.0f;  // the maximum times the scale; this row's sum
+            float m = -INFINITY, mc = 0.0f, l = 0.0f;  // the maximum, and times the scale (0 without keys); this row's sum
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 ok = __all_sync(~0u, mbar_wait(bar, parity, abort_flag, X.wait_ns));
@@ -472,10 +473,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int c = 4; c < PT; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
-                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.scale;
-                if (__any_sync(~0u, mx > mc + kPtSlack)) {
-                    const float m2 = fmaxf(mc, mx), f = pt_exp2(mc - m2);
-                    mc = m2;
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                float less = mc;
+                if (__any_sync(~0u, (mx - m) * P.scale > kPtSlack || (fabsf(mc) > kPtFused && mx > -INFINITY))) {
+                    const float f = mx > m ? pt_exp2((m - mx) * P.scale) : 1.0f;
+                    if (mx > m) m = mx, less = mc = fmaxf(m * P.scale, kPaNone);
                     l *= f;
                     if (i > 0) {
                         if (!wait(&o_full[q], (t - 1) & 1)) break;
@@ -490,8 +492,18 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                             tmem_st32(to + c, r);
                         }
                     }
+                    if (__any_sync(~0u, fabsf(mc) > kPtFused)) {
+                        const bool far = fabsf(mc) > kPtFused;
+                        const float at = far ? m : 0.0f;
+                        if (far) less = 0.0f;
+#pragma unroll
+                        for (int c = 0; c < PT; c += 2) {
+                            const float2 x = fma2(make_float2(s[c], s[c + 1]), make_float2(1.0f, 1.0f), make_float2(-at, -at));
+                            s[c] = x.x, s[c + 1] = x.y;
+                        }
+                    }
                 }
-                const float2 sc = make_float2(P.scale, P.scale), off = make_float2(-mc, -mc);
+                const float2 sc = make_float2(P.scale, P.scale), off = make_float2(-less, -less);
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                 for (int c = 0; c < PT; c += 64) {
@@ -535,7 +547,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                         const T *k = static_cast<const T *>(P.k) + (w.t.k_row + key0 + r) * P.ldk + (int64_t)kv_head * P.D;
                         float dot = 0.0f;
                         for (int d = 0; d < P.D; ++d) dot += to_f32(x[d]) * to_f32(k[d]);
-                        none = (X.negate ? -dot : dot) == -INFINITY;
+                        none = (P.negate ? -dot : dot) == -INFINITY;
                     }
 #pragma unroll
                     for (int k = 0; k < C::DP / 32; ++k) {
@@ -703,9 +715,7 @@ static kq_status pt_launch(const char *fn, PtParams X, cudaStream_t st) {
 }
 
 kq_status pa_tc(const char *fn, kq_dtype xt, const PaParams &P, unsigned long long wait_ns, int idle, cudaStream_t st) {
-    PtParams X{P, 0, P.n_q / P.G, P.scale < 0.0f, wait_ns, idle, aligned(P.y, 32) && P.ldy % 16 == 0 && P.D % 16 == 0, nullptr, nullptr};
-    // (a scale of 0 weighs all keys alike, as any tiny one does, which keeps -inf times it -inf)
-    X.p.scale = P.scale == 0.0f ? 1e-35f : fabsf(P.scale);
+    PtParams X{P, 0, P.n_q / P.G, wait_ns, idle, aligned(P.y, 32) && P.ldy % 16 == 0 && P.D % 16 == 0, nullptr, nullptr};
     auto go = [&](auto t) {
         using T = decltype(t);
         if (P.D <= 64) return pt_launch<T, PtCfg<64, 64>>(fn, X, st);
