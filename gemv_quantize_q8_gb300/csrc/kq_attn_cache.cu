@@ -45,7 +45,7 @@ constexpr float kAcSlack = 8.0f;      // a weight may grow to 2^8 before the sum
 // Weights are held times this power of two: f16 keeps their low bits, with room for kAcSlack.
 constexpr float kAcLift = 7.0f;
 constexpr float kAcLeastRef = -119.0f;  // the least reference that they are held against: 2^(kAcLift + 119) is finite
-constexpr float kAcNone = -3.0e38f;   // the maximum of no token
+constexpr float kAcNone = -3.402823466e38f;  // the maximum of no token: no finite score is below it
 
 struct AcParams {
     KvCache c;
@@ -302,7 +302,7 @@ struct AcWarp {
     uint32_t qh[KS][MT == 8 ? 2 : 4], ql[KS][MT == 8 ? 2 : 4];
     float o[NT][4];
     static constexpr int R = MT / 8;     // rows of a lane: g and, with 16, g + 8
-    float m[R], l[R], factor[R];
+    float m[R], l[R], factor[R];         // (factor: the power of two that the row was brought down by)
     int limit[R], sure;                  // tokens that a row sees, and that all rows see
     // A row's weights times their blocks' value scales are held against a power of two of its own, 2^ref, that is above
     // the largest of them so far and not far above: blocks that a row does not see, or weighs next to nothing, cost
@@ -347,7 +347,7 @@ struct AcWarp {
             if (e == 0x7f800000u || e == 0u) e = 0x3f800000u;
             if (e > 0x7e800000u) e = 0x7e800000u;
             const float down = __uint_as_float(0x7f000000u - e);
-            factor[r] = P.scale * __uint_as_float(e);
+            factor[r] = __uint_as_float(e);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 ac_split(v[s][0] * down, v[s][1] * down, qh[s][r * 2], ql[s][r * 2]);
@@ -370,7 +370,7 @@ struct AcWarp {
 
     // A unit: tokens t0 .. t0 + 31, of which a row sees those below its limit.
     // scales: of keys and values, of its first and second half.
-    __device__ __forceinline__ void unit(uint32_t stage, float4 scales, int t0) {
+    __device__ __forceinline__ void unit(uint32_t stage, float4 scales, int t0, float scale) {
         using Ring = AcRing<DP>;
         const int c = threadIdx.x & 3;
         uint32_t k[KP][4][4];
@@ -414,11 +414,14 @@ struct AcWarp {
         bool grows = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            // the product first and the scale last, each rounded: the scale alone may be as large as fp32
             const float f[2] = {factor[r] * scales.x, factor[r] * scales.z};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int t = i >> 1, e = i & 1;
-                x[r][i] = (MT == 8 ? s[t][e] + s[t][2 + e] : s[t][2 * r + e]) * f[t >> 1];
+            for (int t = 0; t < 4; ++t) {
+                const float2 sum = MT == 8 ? make_float2(s[t][0] + s[t][2], s[t][1] + s[t][3]) : make_float2(s[t][2 * r], s[t][2 * r + 1]);
+                const float2 v = mul2(mul2(sum, make_float2(f[t >> 1], f[t >> 1])), make_float2(scale, scale));
+                x[r][2 * t] = v.x;
+                x[r][2 * t + 1] = v.y;
             }
         }
         if (t0 > sure - kAcUnit) {  // not every row sees all of the unit
@@ -801,7 +804,7 @@ __global__ void __launch_bounds__(NW * 64, 1)
             for (int i = 0; i < n; ++i) {
                 // (a wait that runs out spoils the result, which the device flag tells)
                 if (!sm100::mbar_wait(&full[warp][stage], phase, &aborted, P.wait_ns)) aborted = 1;
-                w.unit(sm100::smem_u32(ring + stage * Ring::BYTES), scales[warp][stage], (at + i) * kAcUnit);
+                w.unit(sm100::smem_u32(ring + stage * Ring::BYTES), scales[warp][stage], (at + i) * kAcUnit, P.scale);
                 __syncwarp();
                 if (lane == 0) sm100::mbar_arrive(&empty[warp][stage]);
                 if (++stage == NS) stage = 0, phase ^= 1;
