@@ -271,7 +271,7 @@ static bool pa_shape(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv, int64_t D
 static kq_status pa_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                          const int32_t *cu_q, const int32_t *cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t n_q, int64_t n_kv,
                          int64_t D, float scale, int causal, void *y, int64_t ldy, void *workspace, size_t ws_bytes, kq_stream_t stream,
-                         int idle = 0, unsigned long long wait_ns = kPtWaitNs) {
+                         int idle = -1, unsigned long long wait_ns = kPtWaitNs) {
     if (xt != KQ_F16 && xt != KQ_BF16) return fail(KQ_ERR_UNSUPPORTED_DTYPE, "%s: row type %s is not F16 or BF16", fn, dtype_name(xt));
     if (!q || !k || !v || !y) return fail(KQ_ERR_INVALID_ARG, "%s: null rows", fn);
     if (!cu_q || !cu_k) return fail(KQ_ERR_INVALID_ARG, "%s: null %s", fn, cu_q ? "cu_k" : "cu_q");
@@ -297,7 +297,7 @@ static kq_status pa_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq
                      magnitude, scale < 0.0f, causal != 0, static_cast<unsigned long long *>(workspace)};
     const cudaStream_t st = (cudaStream_t)stream;
     if (pa_takes_tc(P)) return pa_tc(fn, xt, P, wait_ns, idle, st);
-    if (idle) return fail(KQ_ERR_INVALID_ARG, "%s: these rows do not take the tensor-core path", fn);
+    if (idle >= 0) return fail(KQ_ERR_INVALID_ARG, "%s: these rows do not take the tensor-core path", fn);
     auto go = [&](auto t) {
         using T = decltype(t);
         if (D <= 128) return D <= 64 ? launch_pa<T, 64, false>(fn, P, st) : launch_pa<T, 128, false>(fn, P, st);
@@ -329,7 +329,7 @@ kq_status kq_debug_attn_prompt_wait_timeout(kq_dtype xt, const void *q, int64_t 
                                             int64_t n_kv, int64_t D, float scale, int causal, void *y, int64_t ldy, int idle,
                                             int64_t wait_limit_ns, void *workspace, size_t ws_bytes, kq_stream_t stream) {
     const char *fn = "kq_debug_attn_prompt_wait_timeout";
-    if (idle != 1 && idle != 2) return fail(KQ_ERR_INVALID_ARG, "%s: idle=%d is not 1 or 2", fn, idle);
+    if (idle < 0 || idle > 2) return fail(KQ_ERR_INVALID_ARG, "%s: idle=%d is not in 0..2", fn, idle);
     if (wait_limit_ns < 1000 || wait_limit_ns > 1000000000)
         return fail(KQ_ERR_INVALID_ARG, "%s: wait_limit_ns must be in [1e3, 1e9]", fn);
     return pa_call(fn, xt, q, ldq, k, ldk, v, ldv, cu_q, cu_k, B, Tq, Tk, n_q, n_kv, D, scale, causal, y, ldy, workspace, ws_bytes, stream,

@@ -32,6 +32,7 @@ using namespace sm100;
 constexpr int PT = 128;             // rows of a tile, keys of a tile
 constexpr int PT_THREADS = 384;
 constexpr int PT_MASKED = 3;        // key tiles that some row of a block's (at most 256 tokens) sees only in part
+constexpr unsigned long long kPtPairNs = 20000;  // far longer than a pair of key tiles takes (2 us)
 constexpr float kPtSlack = 8.0f;    // in units of log 2
 // Up to this |m * scale| weights are 2^(S scale - m scale), one fused operation each: m * scale, rounded, is off by less than
 // a sixteenth.  Beyond it the rounding would make weights of any size, so S - m is formed first.
@@ -206,8 +207,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     if (!X.next && blockIdx.x == 0 && tid == 0) *P.err = 0ull;  // (an error is counted two seconds later at the earliest)
 
     // Every role walks the same pairs: f(w, key head), false to stop.  The warp that brings tiles asks for the next place on the
-    // line and passes it on.  `patience`: the role is through with a pair long before its last tiles have been sent for.
-    auto walk = [&](auto f, unsigned long long patience = 0) {
+    // line and passes it on when it has sent for a pair's last tiles, which a role may wait for that is through with the pair
+    // long before (what looks through the values; a row tile that is not there): the longer the pair, the longer.
+    auto walk = [&](auto f) {
         unsigned long long limit = X.wait_ns;
         const unsigned items = (unsigned)(X.pairs * X.n_kv);
         unsigned ahead = blockIdx.x;
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             PtWork w;
             w.n = 0;
             if (pt_work(P, X.order ? X.order[turn] : X.pairs - 1 - turn, w) && !f(w, (int)(i - turn * X.n_kv))) return;
-            limit = X.wait_ns + patience * w.n;
+            limit = X.wait_ns + kPtPairNs * w.n;
             // (asked for when the pair's last tiles have been sent for, not before: a place taken early waits behind a long pair)
             if (warp == 9 && lane == 0) ahead = X.next ? gridDim.x + atomicAdd(X.next, 1u) : items;
         }
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                 g += 2 * w.n;
                 masked_done(w);
                 return ok;
-            }, 20000ull);  // (a pair of key tiles takes 2 us)
+            });
         }
     } else {
         // ------------------------------------------------------------ weights and results, one row a thread
