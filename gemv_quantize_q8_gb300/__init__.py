@@ -405,7 +405,7 @@ def kq_debug_i8_wait_timeout(q, ldq, sx, w, ldw, sw, M, N, K, y, ldy, idle, wait
 
 def kq_debug_attn_prompt_wait_timeout(xt, q, ldq, k, ldk, v, ldv, cu_q, cu_k, B, Tq, Tk, n_q, n_kv, D, scale, causal, y, ldy, idle,
                                       wait_limit_ns, workspace, ws_bytes, stream=None):
-    """kq_attn_prompt's tensor-core kernel with a role idle (1: tiles, 2: products, 0: none) and every wait limited to wait_limit_ns."""
+    """kq_attn_prompt's tensor-core kernel with a role idle (1: tiles, 2: products, 4: the second row tile's second ones, 0: none) and every wait limited to wait_limit_ns."""
     _check(lib().kq_debug_attn_prompt_wait_timeout(xt, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, n_q,
                                                    n_kv, D, float(scale), int(causal), _ptr(y), ldy, idle, wait_limit_ns,
                                                    _ptr(workspace), ws_bytes, _stream(stream)))

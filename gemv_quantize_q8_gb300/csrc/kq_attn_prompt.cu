@@ -329,7 +329,7 @@ kq_status kq_debug_attn_prompt_wait_timeout(kq_dtype xt, const void *q, int64_t 
                                             int64_t n_kv, int64_t D, float scale, int causal, void *y, int64_t ldy, int idle,
                                             int64_t wait_limit_ns, void *workspace, size_t ws_bytes, kq_stream_t stream) {
     const char *fn = "kq_debug_attn_prompt_wait_timeout";
-    if (idle < 0 || idle > 2) return fail(KQ_ERR_INVALID_ARG, "%s: idle=%d is not in 0..2", fn, idle);
+    if (idle < 0 || idle == 3 || idle > 4) return fail(KQ_ERR_INVALID_ARG, "%s: idle=%d is not 0, 1, 2 or 4", fn, idle);
     if (wait_limit_ns < 1000 || wait_limit_ns > 1000000000)
         return fail(KQ_ERR_INVALID_ARG, "%s: wait_limit_ns must be in [1e3, 1e9]", fn);
     return pa_call(fn, xt, q, ldq, k, ldk, v, ldv, cu_q, cu_k, B, Tq, Tk, n_q, n_kv, D, scale, causal, y, ldy, workspace, ws_bytes, stream,

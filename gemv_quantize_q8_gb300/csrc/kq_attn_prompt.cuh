@@ -63,7 +63,8 @@ __device__ __forceinline__ int pa_limit(const PaParams &P, const PaTile &t, int 
 }
 
 // The tensor-core form (kq_attn_tc.cu): which rows it takes, and the launch.  wait_ns limits every wait of its pipeline;
-// idle names a role that does nothing (test hook: 1 what brings tiles, 2 what issues the products, others none).
+// idle names a role that does nothing (test hook: 1 what brings tiles, 2 what issues the products, 4 the second row
+// tile's second ones alone, others none).
 constexpr unsigned long long kPtWaitNs = 2000000000ull;
 bool pa_aligned(const PaParams &P);  // all rows on 16 bytes
 bool pa_takes_tc(const PaParams &P);

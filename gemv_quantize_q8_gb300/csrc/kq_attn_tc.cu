@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
                         if (ok && at >= 0 && wait(&p_full[q], p_phase[q])) {
                             p_phase[q] ^= 1;
                             tc_fence_after();
-                            if (one) {
+                            if (one && !(q && X.idle == 4)) {
 #pragma unroll
                                 for (int k = 0; k < PT / 16; ++k)
                                     mma_f16_ts(C::O_COL + q * C::OW, q * 128 + k * 8, dV + (uint64_t)(sv * (C::TILE >> 4) + k * (2048 >> 4)),
@@ -603,9 +603,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             return true;
         });
     }
-    if (tid == 0 && *abort_flag) atomicAdd(P.err, 1ull);
     tc_fence_before();
     __syncthreads();
+    if (tid == 0 && *abort_flag) atomicAdd(P.err, 1ull);  // (here: any role may have given up last)
     if (warp == 8) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*tmem_holder) : "memory");

@@ -546,7 +546,8 @@ KQ_API kq_status kq_debug_i8_wait_timeout(const int8_t *q, int64_t ldq, const fl
 
 /* Test hooks of the attention kernels' bounded waits: the calls of the same names with one role kept idle and every wait limited
  * to wait_limit_ns (1e3 .. 1e9; the calls use 2 s).  Prompts: idle = 1 what brings the tiles, 2 what issues the products,
- * 0 none: the call as it is (rows that take the tensor-core path); cache: nothing is fetched.  The waits run out, the thread blocks count it in
+ * 4 the products with the values for every second row tile alone, 0 none: the call as it is (rows that take the tensor-core
+ * path); cache: nothing is fetched.  The waits run out, the thread blocks count it in
  * the device flag (kq_read_device_flag), let their copies and MMAs in flight end, and return; y is not written or
  * incomplete. */
 KQ_API kq_status kq_debug_attn_prompt_wait_timeout(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,

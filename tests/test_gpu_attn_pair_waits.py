@@ -26,3 +26,23 @@ def test_pairs_longer_than_the_limit(heads):
     assert kq.kq_read_device_flag(ws) == 0
     kq.kq_debug_attn_prompt_wait_timeout(*args, again, heads * D, 0, 2_000_000, ws, n)
     assert kq.kq_read_device_flag(ws) == 0 and torch.equal(again, y)
+
+
+@pytest.mark.parametrize("tokens", [100, 700])
+def test_a_row_tile_that_waits_alone(tokens):
+    """The first row tile of a pair finishes, the second one's products never come: the flag tells it all the same."""
+    H, D = 2, 128
+    g = torch.Generator(device=DEV).manual_seed(0)
+    q = torch.randn((tokens, H * D), generator=g, device=DEV).to(torch.bfloat16)
+    k, v = (torch.randn((tokens, D), generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    cu = ints([0, tokens])
+    n = kq.kq_attn_prompt_workspace_bytes(1, tokens, H, 1, D)
+    ws = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    y, again = torch.zeros_like(q), torch.zeros_like(q)
+    args = (kq.BF16, q, H * D, k, D, v, D, cu, cu, 1, tokens, tokens, H, 1, D, D ** -0.5, 1)
+    kq.kq_attn_prompt(*args, y, H * D, ws, n)
+    assert kq.kq_read_device_flag(ws) == 0
+    kq.kq_debug_attn_prompt_wait_timeout(*args, again, H * D, 4, 2_000_000, ws, n)
+    assert kq.kq_read_device_flag(ws) > 0
+    kq.kq_attn_prompt(*args, again, H * D, ws, n)
+    assert kq.kq_read_device_flag(ws) == 0 and torch.equal(again, y)
