@@ -85,6 +85,7 @@ __device__ __forceinline__ KvPart kv_find(const KvCache &c, const KvRows &r, int
 template <int G>
 __device__ __forceinline__ void kv_sync() {
     if (G > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / G), "n"(G) : "memory");
+    else __syncwarp();
 }
 
 // W elements as fp32; the address is aligned to all of them.
@@ -249,9 +250,9 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv_append_kernel(KvCache c, KvR
         }
 #pragma unroll
         for (int s = 16; s; s >>= 1) amax = max2(amax, __shfl_xor_sync(~0u, amax, s));
+        kv_sync<G>();  // (all have read the old scale, too, before the new one is written)
         if (G > 32) {
             const int w0 = threadIdx.x / G * (G / 32);
-            kv_sync<G>();
             if ((tid & 31) == 0) red[w0 + (tid >> 5)] = amax;
             kv_sync<G>();
             amax = red[w0];
