@@ -654,6 +654,7 @@ struct AcFetch {
         bad = ac_bad(P, it.b);
         table = P.c.table + it.b * P.c.ldt;
     }
+    __device__ __forceinline__ bool valid(const AcParams &P, int number) const { return number >= 0 && number < P.c.n_pages && !bad; }
     __device__ __forceinline__ void look(const AcParams &P) {
         const int t0 = at * kAcUnit;
         page[0] = table[t0 >> P.c.lp];
@@ -666,27 +667,27 @@ struct AcFetch {
         const bool small = P.c.lp == 4;
         // a unit's second half may lie past the last page: weight 0, whatever is there
         const int parts = small && t0 + 16 < len ? 2 : 1;
-        sm100::mbar_arrive_expect_tx(bar, small && parts == 1 ? Ring::BYTES / 2 : Ring::BYTES);
+        const int number[2] = {page[0], small ? page[1] : page[0]};
+        const bool there[2] = {true, parts == 2 || !small}, ok[2] = {valid(P, number[0]), there[1] && valid(P, number[1])};
         float *sc = reinterpret_cast<float *>(scales);
+        // (what is written without a copy comes before the arrival, which releases it)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (!ok[h]) sc[2 * h] = there[h] ? NAN : 0.0f, sc[2 * h + 1] = 0.0f;
+        sm100::mbar_arrive_expect_tx(bar, small && parts == 1 ? Ring::BYTES / 2 : Ring::BYTES);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int number = h && small ? page[1] : page[0];
-            const bool ok = number >= 0 && number < P.c.n_pages && !bad;
             if (h < parts) {
 #pragma unroll
                 for (int i = 0; i < Ring::BOXES; ++i) {
-                    ac_copy(stage + i * Ring::BOX + h * 16 * Ring::W, tmK, bar, i * 128, row, ok ? number : 0);
-                    ac_copy(stage + (Ring::BOXES + i) * Ring::BOX + h * 16 * Ring::W, tmV, bar, i * 128, row, ok ? number : 0);
+                    ac_copy(stage + i * Ring::BOX + h * 16 * Ring::W, tmK, bar, i * 128, row, ok[h] ? number[h] : 0);
+                    ac_copy(stage + (Ring::BOXES + i) * Ring::BOX + h * 16 * Ring::W, tmV, bar, i * 128, row, ok[h] ? number[h] : 0);
                 }
             }
-            const bool there = h < parts || !small;
-            if (there && ok) {
-                const int64_t block = (int64_t)number * P.c.n_kv + it.h;
+            if (ok[h]) {
+                const int64_t block = (int64_t)number[h] * P.c.n_kv + it.h;
                 ac_copy4(sc + 2 * h, P.c.k_scale + block);
                 ac_copy4(sc + 2 * h + 1, P.c.v_scale + block);
-            } else {
-                sc[2 * h] = there ? NAN : 0.0f;
-                sc[2 * h + 1] = 0.0f;
             }
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(bar)) : "memory");
