@@ -250,13 +250,13 @@ __global__ void __launch_bounds__(128) pa_kernel(PaParams P) {
     }
 }
 
+static int64_t pa_units(int64_t B, int64_t Tq, int64_t n_q) { return (Tq / kPaRows + B) * n_q; }
+
 template <typename T, int DP, bool VEC>
 static kq_status launch_pa(const char *fn, const PaParams &P, cudaStream_t st) {
     auto kern = pa_kernel<T, DP, VEC>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pa_smem<DP, VEC>());
-    const int64_t tiles = (P.Tq / kPaRows + P.B) * P.n_q;
-    if (tiles > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: too many row tiles", fn);
-    if (e == cudaSuccess) e = launch_beside(kern, dim3((unsigned)tiles), dim3(128), pa_smem<DP, VEC>(), dim3(1), st, P);
+    if (e == cudaSuccess) e = launch_beside(kern, dim3((unsigned)pa_units(P.B, P.Tq, P.n_q)), dim3(128), pa_smem<DP, VEC>(), dim3(1), st, P);
     if (e != cudaSuccess) return fail(KQ_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
     count_launch(R_ATTN);
     return KQ_OK;
@@ -287,16 +287,19 @@ static kq_status pa_call(const char *fn, kq_dtype xt, const void *q, int64_t ldq
     if (!(fabsf(scale) <= 2.0e38f)) return fail(KQ_ERR_INVALID_ARG, "%s: scale must be finite, up to 2e38", fn);  // (times log2 e, too)
     if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(y, 2) || !aligned(cu_q, 4) || !aligned(cu_k, 4))
         return fail(KQ_ERR_ALIGNMENT, "%s: a pointer is not aligned to its elements", fn);
-    const size_t need = pa_tc_workspace(B, Tq, n_q / n_kv);
-    if (!workspace || ws_bytes < need)
-        return fail(KQ_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace ? ws_bytes : (size_t)0, need);
-    if (!aligned(workspace, 256)) return fail(KQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", fn);
     // (a scale of 0 weighs all keys alike, as the smallest one does, which keeps -inf times it -inf)
     const float magnitude = fmaxf(fabsf(scale * 1.44269504f), 1.4e-45f);
     const PaParams P{q, k, v, y, ldq, ldk, ldv, ldy, cu_q, cu_k, B, Tq, Tk, (int)n_q, (int)(n_q / n_kv), (int)D,
                      magnitude, scale < 0.0f, causal != 0, static_cast<unsigned long long *>(workspace)};
+    const bool tc = pa_takes_tc(P);
+    if ((tc ? pa_tc_units(B, Tq, n_q, n_kv) : pa_units(B, Tq, n_q)) > kPaMaxUnits)
+        return fail(KQ_ERR_INVALID_ARG, "%s: too many row tiles", fn);
+    const size_t need = pa_tc_workspace(B, Tq, n_q / n_kv);
+    if (!workspace || ws_bytes < need)
+        return fail(KQ_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace ? ws_bytes : (size_t)0, need);
+    if (!aligned(workspace, 256)) return fail(KQ_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", fn);
     const cudaStream_t st = (cudaStream_t)stream;
-    if (pa_takes_tc(P)) return pa_tc(fn, xt, P, wait_ns, idle, st);
+    if (tc) return pa_tc(fn, xt, P, wait_ns, idle, st);
     if (idle >= 0) return fail(KQ_ERR_INVALID_ARG, "%s: these rows do not take the tensor-core path", fn);
     auto go = [&](auto t) {
         using T = decltype(t);
@@ -313,7 +316,10 @@ using namespace kq;
 extern "C" {
 
 size_t kq_attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv, int64_t D) {
-    return pa_shape(B, Tq, n_q, n_kv, D) ? pa_tc_workspace(B, Tq, n_q / n_kv) : 0;
+    if (!pa_shape(B, Tq, n_q, n_kv, D)) return 0;
+    // (which form a call takes follows from its addresses as well: 0 where neither would do)
+    const bool tc = D <= 128 && pa_tc_units(B, Tq, n_q, n_kv) <= kPaMaxUnits;
+    return tc || pa_units(B, Tq, n_q) <= kPaMaxUnits ? pa_tc_workspace(B, Tq, n_q / n_kv) : 0;
 }
 
 kq_status kq_attn_prompt(kq_dtype xt, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,

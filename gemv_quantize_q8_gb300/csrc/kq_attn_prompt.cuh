@@ -69,6 +69,9 @@ constexpr unsigned long long kPtWaitNs = 2000000000ull;
 bool pa_aligned(const PaParams &P);  // all rows on 16 bytes
 bool pa_takes_tc(const PaParams &P);
 size_t pa_tc_workspace(int64_t B, int64_t Tq, int64_t G);
+// Either form numbers its units in 32 bits: pairs of row tiles times key heads here, row tiles times heads in the other.
+constexpr int64_t kPaMaxUnits = 0x7fffffff;
+int64_t pa_tc_units(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv);
 kq_status pa_tc(const char *fn, kq_dtype xt, const PaParams &P, unsigned long long wait_ns, int idle, cudaStream_t st);
 
 }  // namespace kq

@@ -673,6 +673,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 pt_encoder() {
 static int64_t pt_pairs(int64_t B, int64_t Tq, int64_t G) { return ((Tq / PT + B) * G >> 1) + B; }
 size_t pa_tc_workspace(int64_t B, int64_t Tq, int64_t G) { return 256 + (size_t)(pt_pairs(B, Tq, G) * 4 + 255) / 256 * 256; }
 
+int64_t pa_tc_units(int64_t B, int64_t Tq, int64_t n_q, int64_t n_kv) { return pt_pairs(B, Tq, n_q / n_kv) * n_kv; }
+
 bool pa_aligned(const PaParams &P) {
     return P.D % 8 == 0 && aligned(P.q, 16) && aligned(P.k, 16) && aligned(P.v, 16) && aligned(P.y, 16) && P.ldq % 8 == 0 &&
            P.ldk % 8 == 0 && P.ldv % 8 == 0 && P.ldy % 8 == 0;
@@ -697,7 +699,6 @@ static kq_status pt_launch(const char *fn, PtParams X, cudaStream_t st) {
         if (e != CUDA_SUCCESS) return fail(KQ_ERR_CUDA, "%s: tensor map %d failed (%d)", fn, i, (int)e);
     }
     X.pairs = pt_pairs(P.B, P.Tq, P.G);
-    if (X.pairs * X.n_kv > 0x7fffffff) return fail(KQ_ERR_INVALID_ARG, "%s: too many row tiles", fn);
     auto kern = pt_kernel<T, C>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TOTAL);
     const int64_t items = X.pairs * X.n_kv;

@@ -465,7 +465,7 @@ KQ_API kq_status kq_attn_cache_i8(kq_dtype xt, const void *q, int64_t ldq, int64
  * last of its keys (token i of n_q sees the first n_k - n_q + 1 + i keys); causal = 0: every token sees every key.
  * The formula is kq_attn_cache_i8's.  q: [Tq][ldq], k: [Tk][ldk], v: [Tk][ldv], y: [Tq][ldy], all of
  * type xt (KQ_F16 or KQ_BF16), element-aligned; n_q heads of D elements over n_kv, a multiple; D a multiple of 8 up
- * to 256; Tq and Tk up to 2^31 - 256, B up to 2^24, n_q up to 65535, (Tq/64 + B)*n_q below 2^31; |scale| is up to 2e38.  y may be
+ * to 256; Tq and Tk up to 2^31 - 256, B up to 2^24, n_q up to 65535, (Tq/64 + B)*n_q + B*n_kv below 2^31; |scale| is up to 2e38.  y may be
  * q itself (same stride).
  * Products q . k and sums are fp32 (a product beyond fp32 is infinite, at any scale of a product within it the weights
  * are right); the weights are rounded to xt for the second product.  A token that sees no key gives 0; what a
