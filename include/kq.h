@@ -467,8 +467,8 @@ KQ_API kq_status kq_attn_cache_i8(kq_dtype xt, const void *q, int64_t ldq, int64
  * type xt (KQ_F16 or KQ_BF16), element-aligned; n_q heads of D elements over n_kv, a multiple; D a multiple of 8 up
  * to 256; Tq and Tk up to 2^31 - 256, B up to 2^24, n_q up to 65535, (Tq/64 + B)*n_q + B*n_kv below 2^31; |scale| is up to 2e38.  y may be
  * q itself (same stride).
- * Products q . k and sums are fp32 (a product beyond fp32 is infinite, at any scale of a product within it the weights
- * are right); the weights are rounded to xt for the second product.  A token that sees no key gives 0; what a
+ * Products q . k and sums are fp32 (a product, or a difference of two, beyond fp32 is infinite; within it the weights
+ * are right at any scale); the weights are rounded to xt for the second product.  A token that sees no key gives 0; what a
  * token does not see has no influence on it, infinities and NaN included.  Rows behind cu_q[B] are left as they were.
  * workspace: kq_attn_prompt_workspace_bytes(...) bytes (0: a shape that the call refuses), 256-byte aligned; its content does
  * not matter before the call, and calls that share it must not overlap; kq_read_device_flag applies to it (a tensor-core
