@@ -33,6 +33,13 @@ class Generator:
         self.scales = torch.zeros((2, n, model.kv_heads), device=DEV)
         self.cache = (self.codes[0], self.codes[1], self.scales[0], self.scales[1], n, page, self.table, self.width)
         self.lens = torch.zeros(batch, dtype=torch.int32, device=DEV)
+        self.room, self.longest = min(self.width * page, model.max_len), 0
+
+    def _grow(self, longest):
+        """A token past the last page would have no place, and one past the tables no angle."""
+        if longest > self.room:
+            raise ValueError(f"{longest} tokens; the cache and the rotation's tables have room for {self.room}")
+        self.longest = longest
 
     def _heads(self, tokens, pos, cu):
         """The residual, rotated queries in bf16; keys and values go to the cache."""
@@ -60,6 +67,9 @@ class Generator:
 
     def prompt(self, prompts):
         m, new = self.m, [len(p) for p in prompts]
+        if len(new) != self.B or min(new) < 1:
+            raise ValueError(f"need {self.B} prompts of a token at least")
+        self._grow(max(new))
         T, nq, nk = sum(new), m.heads * m.D, m.kv_heads * m.D
         cu = _ints([0] + torch.tensor(new).cumsum(0).tolist())
         self.lens.copy_(_ints(new))
@@ -76,6 +86,7 @@ class Generator:
 
     def step(self, tokens):
         m, nq = self.m, self.m.heads * self.m.D
+        self._grow(self.longest + 1)
         pos = self.lens.clone()
         self.lens += 1
         x, q = self._heads(tokens, pos, None)
