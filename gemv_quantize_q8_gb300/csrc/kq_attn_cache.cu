@@ -3,14 +3,15 @@
 // For a query row q (one token and head) over the tokens j that it sees, with s_j = scale * ks * (q . K_j) for codes
 // K, V and their blocks' scales ks, vs:
 //   m = max s_j,  l = sum 2^(s_j - m),  y = (sum 2^(s_j - m) vs V_j) / l       (s in units of log 2)
+// What is handed from warp to warp or block to block is m, l and y of a part: sums that are not divided yet may leave fp32.
 // Bound by the cache's bytes: each is read once, by TMA, into a ring of the warp that needs it (2 or 4 KB a copy, two
-// or three units under way; a warp waits for nobody else).  Two sequences of 131072 tokens, 32 heads over 8 of 128, 537 MB: 87.7
-// us, 6.1 TB/s, of which the start, the parts and their join take 10; 64 users of up to 8192 tokens, 516 MB, 88.4; one user of
-// 900 tokens 9.7, all of it latency.  (By 16-byte copies of every lane the loads alone took 136 us for the first.)
+// or three units under way; a warp waits for nobody else).  Two sequences of 131072 tokens, 32 heads over 8 of 128, 537 MB: 87.8
+// us, 6.1 TB/s, of which the start, the parts and their join take 10; 64 users of up to 8192 tokens, 516 MB, 89.3; one user of
+// 900 tokens 10.1, all of it latency.  (By 16-byte copies of every lane the loads alone took 136 us for the first.)
 //
 // The products run on m16n8k16 instructions.  Codes are exact in f16; a query row is brought to |q| < 2 by a power
-// of two and split into two f16 (22 bits), as the weights 2^(s - m) vs are.  With up to eight rows (the query heads of
-// one key head) the second parts fill the tile's other eight rows, so they cost nothing; tiles of 16 rows take twice
+// of two and split into two f16 (22 bits), as the weights 2^(s - m) vs are, held against the largest of their own row.
+// With up to eight rows (the query heads of one key head) the second parts fill the tile's other eight rows, so they cost nothing; tiles of 16 rows take twice
 // the instructions.  Which of its elements a lane holds is free where both operands agree, so it follows the loads:
 //   keys:   lane 4n + c of an eight-token tile takes the 16-byte pieces 2c and 2c + 1 of token n; 4 bytes make the two
 //           registers of one step.
@@ -969,7 +970,7 @@ static bool ac_may_be_wide(int64_t rows, int64_t D) { return rows > 8 && D <= 12
 // They are taken where the tables have room for kAcWideFrom units a warp and more (the lengths are known on the device only; both
 // kinds in one kernel, chosen there, cost the short calls 2.5 us).  24 rows of 128: 5 sequences of up to 5001 tokens 20.4 us
 // with 16 rows, 15.5 with 8; 16 of up to 7500 (six units a warp) 23.1 and 22.3, of up to 20001 32.5 and 35.2; 64 of up to 8192
-// with 8 heads 133 and 175.  Heads of 256: 38.0 and 21.6, 100.0 and 72.4.
+// with 8 key heads 241 and 249, and with 12 rows of each 134 and 170.  Heads of 256: 38.0 and 21.6, 100.0 and 72.4.
 constexpr int kAcWideFrom = 6;
 static int ac_row_tile(const AcParams &P) {
     if (!ac_may_be_wide(P.rows, P.c.D)) return 8;

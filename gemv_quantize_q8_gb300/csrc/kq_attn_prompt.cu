@@ -8,8 +8,8 @@
 // The form for any head width up to 256 and rows at any address: a thread block takes 64 tokens of one head, 16 a
 // warp, and goes over the keys in tiles of 32, on m16n8k16 instructions.  Rows on 16 bytes (heads of over 128; the narrower ones
 // take kq_attn_tc.cu's form) come by 16-byte copies, the next tile while this one's products run, and both products take
-// their operands by ldmatrix: 4096 tokens, 32 heads over 8 of 256, causal, 1033 us, 0.27 PFLOP/s, bound by the instructions' rate
-// and their operands' loads.  Other rows are staged element by element: 12.4 ms.
+// their operands by ldmatrix: 4096 tokens, 32 heads over 8 of 256, causal, 1045 us, 0.26 PFLOP/s, bound by the instructions' rate
+// and their operands' loads.  Other rows are staged element by element: 7.3 ms (16384 tokens of 128: 22.0 ms for 1468 us).
 // A masked weight is 0, but 0 times an infinity is not: rows of values past the sequence's end are
 // taken as zeros, and a tile that some row sees only in part and that holds an infinity or NaN is added up one key at
 // a time, leaving out what is masked.

@@ -2,7 +2,7 @@
 // boundaries (the other rows take kq_attn_prompt.cu's form).
 //
 // Bound by the two products, 4 D flops a score, and their operands' shared-memory reads: 16384 tokens, 32 heads over 8 of
-// 128, causal, 1452 us, 1.5 PFLOP/s; with nothing done between the products they take 1355.  A thread block takes two row tiles of
+// 128, causal, 1468 us, 1.5 PFLOP/s; with nothing done between the products they take 1355.  A thread block takes two row tiles of
 // one key head, 128 tokens of one query head each (two heads of the same tokens where the group is even), so that every
 // key and value tile that is brought in serves 256 rows and one tile's products run while the other's weights
 // are made:
