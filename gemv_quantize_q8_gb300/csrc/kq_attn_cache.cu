@@ -11,8 +11,8 @@
 //
 // The products run on m16n8k16 instructions.  Codes are exact in f16; a query row is brought to |q| < 2 by a power
 // of two and split into two f16 (22 bits), as the weights 2^(s - m) vs are, held against the largest of their own row.
-// With up to eight rows (the query heads of one key head) the second parts fill the tile's other eight rows, so they cost nothing; tiles of 16 rows take twice
-// the instructions.  Which of its elements a lane holds is free where both operands agree, so it follows the loads:
+// With up to eight rows (the query heads of one key head) the second parts fill the tile's other eight rows, so they cost
+// nothing; tiles of 16 rows take twice the instructions.  Which of its elements a lane holds is free where both operands agree, so it follows the loads:
 //   keys:   lane 4n + c of an eight-token tile takes the 16-byte pieces 2c and 2c + 1 of token n; 4 bytes make the two
 //           registers of one step.
 //   values: lane 4n + c takes piece n of tokens 2c, 2c + 1, 2c + 8, 2c + 9: the tokens whose weights it holds, the
@@ -343,9 +343,10 @@ struct AcWarp {
                 for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fabsf(v[s][i]));
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
-            // the power of two at or below the largest (1 for rows of zeros and of infinities)
+            // the power of two at or below the largest (2^-126 for rows below the normal numbers, 1 for infinities)
             uint32_t e = __float_as_uint(amax) & 0x7f800000u;
-            if (e == 0x7f800000u || e == 0u) e = 0x3f800000u;
+            if (e == 0x7f800000u) e = 0x3f800000u;
+            if (e == 0u) e = 0x00800000u;
             if (e > 0x7e800000u) e = 0x7e800000u;
             const float down = __uint_as_float(0x7f000000u - e);
             factor[r] = __uint_as_float(e);

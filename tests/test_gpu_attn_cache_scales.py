@@ -66,3 +66,22 @@ def test_scores_at_the_lower_end_of_fp32():
     torch.cuda.synchronize()
     want = c.rows(0, 1, 1)[0, 0]
     assert (np.abs(y.double().cpu().numpy()[0] - want) <= 64 * U * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("n_new,n_q,D", SHAPES)
+def test_queries_below_the_normal_numbers(n_new, n_q, D):
+    """Queries of some 1e-39 at a scale of 1e38.  Their products with the keys are as fp32 holds them there: beyond the relative
+    errors of (D + 16) u, a block's scale times 2^-126 is off by 2^-150, and a product once more."""
+    lens, scale = [300, 1, 40], 1e38
+    c = Cache(lens, 1, D, 16, fill=True)
+    q = torch.randn((c.B * n_new, n_q * D), generator=torch.Generator().manual_seed(D)) * 2e-39
+    y = call(c, q.to(DEV), n_new, n_q, scale)
+    torch.cuda.synchronize()
+    q, y = (x.double().cpu().numpy().reshape(c.B, n_new, n_q, D) for x in (q, y))
+    for b, t in enumerate(lens):
+        limits = [max(t - n_new + 1 + i, 0) for i in range(n_new)]
+        k = c.rows(b, t, 0)
+        ref, V, S = attention(q[b], k, c.rows(b, t, 1), float(np.float32(scale)), limits)
+        codes = (np.abs(q[b]) * 2.0 ** 126).sum(-1, keepdims=True) * 128
+        E = (D + 16) * U * S + scale * (2.0 ** -150 * codes + 2.0 ** -149)
+        assert (np.abs(y[b] - ref) <= (2 * E + (t / 4 + 64) * U) * V + U * np.abs(ref)).all()
