@@ -6,11 +6,12 @@
 // A group of threads (256, or a warp where the sequences have few rows) takes one block of the cache that the call
 // touches and keeps its new rows in registers between the maximum and the codes: 8192 elements of 256 threads (64 tokens
 // of 128), 1024 of a warp.  Those are read once; what a block has beyond them (pages of 128 tokens of 128) is read and
-// rotated for the maximum and again for the codes.  Every code is written once.  Which blocks those are follows from cu and lens on the device: a run of n
-// tokens touches at most floor(n / page) + 2 pages, and at most n; so sequence b's share of the grid starts at
-// floor(cu[b] / page) + 2b, or at cu[b], whichever makes the smaller grid.
+// rotated for the maximum and again for the codes.  Every code is written once.  Which blocks those are follows from cu and
+// lens on the device: a run of n tokens touches at most floor(n / page) + 2 pages, and at most n; so sequence b's share of
+// the grid starts at floor(cu[b] / page) + 2b, or at cu[b], whichever makes the smaller grid.
 // 8192 tokens, 8 heads of 128, fp32: append 22 us (84 MB, 12.4 at the memory's rate), bound by a block's chain of waits (where
-// it is, positions, rows, maximum); reading them back as bf16 11 us (two calls one after the other 34).  One token each of 64 users: 8.7 us both.
+// it is, positions, rows, maximum); reading them back as bf16 11 us (one after the other 34).  One token each of 64 users: 8.9
+// us both.
 // The maximum, every product and sum are rounded one by one, so that codes and scales are the same bits whatever
 // the grid or the vector width.
 #include <type_traits>
